@@ -311,14 +311,214 @@ h3attn_status_t h3attn_prefill_window(const void* q, const void* k, const void* 
                                       int Hq, int Hkv, int D, float scale, const h3attn_window_t* win,
                                       const h3attn_mask_t* mask, h3attn_stream_t stream);
 
+/*
+ * Residual add + RMSNorm of transformer hidden rows, beside the modulated
+ * norm above: the step between two layers of a block that generates.  For
+ * every row of C channels:
+ *   h   = bf16(x + residual)                  (h = x when residual is NULL)
+ *   r   = 1 / sqrt(mean_c(h_c^2) + eps)
+ *   y_c = (h_c * w_c) * r                     (w_c = 1 when w is NULL)
+ * in float32, and y is written in one of three formats:
+ *   H3ATTN_Y_BF16        bf16(y)
+ *   H3ATTN_Y_E4M3_ROW    e4m3(y / s), s = max_c |y_c| / 448 of each row (at
+ *                        least 2^-126), float32
+ *   H3ATTN_Y_E4M3_MX32   e4m3(y / s) with s the least power of two that is at
+ *                        least max |y| / 448 (and at least 2^-126), of each 32
+ *                        neighbouring channels, as an 8-bit exponent biased by
+ *                        127 (e8m0)
+ * 448 is the largest e4m3 value, so nothing saturates.  An all-zero row or
+ * group has s = 1.  NaN stays NaN, and an infinite h makes its row NaN and
+ * zeros as the formula does.
+ *
+ * x: [T, C] bf16; residual: [T, C] bf16 or NULL; h: [T, C] bf16 output,
+ *    present exactly when residual is, may be x or residual itself.
+ * y: [T, C] bf16 or e4m3 output; in bf16 it may be x or residual itself (then
+ *    not h).  w: [C] float32 or NULL.
+ * y_scale: [T] float32 (ROW), [T, C / 32] bytes (MX32), NULL (BF16).
+ * C a multiple of 8 (MX32: of 32), 8 <= C <= 16384; eps >= 0 and finite;
+ * T == 0 is a no-op.  x, residual, h, y, w 16-byte aligned, a float32 y_scale
+ * 4-byte aligned; no other overlap of an output with an input or output.
+ * Stream order as for h3attn_rmsnorm_modulate().
+ * Errors: INVALID_ARG, MISALIGNED, UNSUPPORTED_DEVICE, LAUNCH.
+ */
+typedef enum {
+  H3ATTN_Y_BF16 = 0,
+  H3ATTN_Y_E4M3_ROW = 1,
+  H3ATTN_Y_E4M3_MX32 = 2
+} h3attn_y_format_t;
+h3attn_status_t h3attn_add_rmsnorm(const void* x, const void* residual, void* h, void* y, const float* w,
+                                   void* y_scale, int T, int C, int y_format, float eps,
+                                   h3attn_stream_t stream);
+
+/*
+ * Scaling of rotary frequencies for sequences longer than a model was
+ * trained on.  With f_i = theta^(-2 i / rotary_dim), i < rotary_dim / 2:
+ *   H3ATTN_ROPE_LINEAR    f_i / factor (positions interpolated)
+ *   H3ATTN_ROPE_NTK       theta replaced by theta * factor^(rotary_dim / (rotary_dim - 2)):
+ *                         the slowest pair is stretched by factor, the fastest not at all
+ *   H3ATTN_ROPE_BY_PARTS  by the turns that a pair makes over original_len positions,
+ *                         n_i = original_len f_i / (2 pi): keep = clamp((n_i - low_turns) /
+ *                         (high_turns - low_turns), 0, 1), (1 - keep) f_i / factor + keep f_i
+ *                         (the "NTK-by-parts" interpolation of Peng, Quesnelle, Fan and Shippole,
+ *                         "YaRN: Efficient Context Window Extension of Large Language Models", 2023)
+ * amplitude multiplies every cosine and sine (the paper's attention
+ * temperature is amplitude = 0.1 ln(factor) + 1); 1 for none.
+ */
+typedef enum {
+  H3ATTN_ROPE_NONE = 0,
+  H3ATTN_ROPE_LINEAR = 1,
+  H3ATTN_ROPE_NTK = 2,
+  H3ATTN_ROPE_BY_PARTS = 3
+} h3attn_rope_kind_t;
+typedef struct {
+  int kind;            /* h3attn_rope_kind_t */
+  int original_len;    /* >= 1 (BY_PARTS) */
+  double factor;       /* >= 1 and finite */
+  double low_turns;    /* >= 0 (BY_PARTS) */
+  double high_turns;   /* > low_turns and finite (BY_PARTS) */
+  double amplitude;    /* > 0 and finite */
+} h3attn_rope_scaling_t;
+
+/*
+ * The cos / sin tables that h3attn_qk_norm_rope(), its _out form and
+ * h3attn_qk_norm_rope_append() take: row n is position p_n, with
+ *   cos[n, i] = amplitude * cos(p_n f_i),  sin[n, i] = amplitude * sin(p_n f_i).
+ * Angles are kept in 64-bit fractions of a turn, so a row is as exact at
+ * position 2^31 as at position 1 (two float32 roundings).
+ *
+ * cos, sin: [N, rotary_dim / 2] float32 outputs (device, 16-byte aligned, no overlap).
+ * pos: [N] int32 positions (device, 4-byte aligned; negative ones turn
+ *    backwards), or NULL: p_n = first + n, with 0 <= first and
+ *    first + N <= 2^31.  first must be 0 when pos is given.
+ * rotary_dim even, 2 <= rotary_dim <= 256 (NTK: from 4 on); theta >= 1 and
+ * finite; scaling NULL for none.  N == 0 is a no-op.
+ * Frequencies are computed on the host in double precision during the call
+ * and travel with the launch.  Stream order as for h3attn_rmsnorm_modulate().
+ * Errors: INVALID_ARG, MISALIGNED, UNSUPPORTED_DEVICE, LAUNCH.
+ */
+h3attn_status_t h3attn_rope_table(float* cos, float* sin, const int32_t* pos, int64_t first, int N,
+                                  int rotary_dim, double theta, const h3attn_rope_scaling_t* scaling,
+                                  h3attn_stream_t stream);
+
+/*
+ * A paged key-value cache: pages of page_size tokens in BSHD order, and for
+ * each sequence the list of its pages.  Token j of sequence b is row
+ * j % page_size of page page_table[b, j / page_size].  Pointers are device
+ * pointers, owned by the caller.
+ *
+ * kv_len[b] counts the tokens that the cache holds of sequence b: values
+ * <= 0 mean none, values above the capacity max_pages * page_size mean the
+ * capacity.  Entries of page_table past a sequence's last page are not read.
+ * An entry outside [0, num_pages) that is needed is an error of the data:
+ * nothing outside the cache is read or written, and
+ * h3attn_check_device_status() then reports H3ATTN_ERR_INVALID_ARG (what
+ * the call does with the token is said there).
+ * Two sequences may share pages (a common prefix); two tokens appended to
+ * the same row in one call race.
+ */
+typedef struct {
+  void* k_pages;             /* [num_pages, page_size, Hkv, D] bf16, 16-byte aligned */
+  void* v_pages;             /* the same */
+  const int32_t* page_table; /* [B, max_pages], 4-byte aligned */
+  const int32_t* kv_len;     /* [B], 4-byte aligned */
+  int B;
+  int num_pages;             /* >= 1; num_pages * page_size < 2^31 */
+  int page_size;             /* >= 1 */
+  int max_pages;             /* >= 1; max_pages * page_size <= 2^31 - 64 */
+  int Hkv;
+  int D;                     /* 64, 128 or 256 */
+} h3attn_paged_kv_t;
+
+/*
+ * The fused Q/K RMSNorm -> bf16 boundary -> partial RoPE of S new tokens of
+ * each sequence, with K and V appended to a paged cache and Q written to
+ * q_out: the paged counterpart of h3attn_qk_norm_rope_out().  In the half
+ * layout a normed row is bit-identical to that call's.
+ *   n       = bf16((x * r) * w), r as in h3attn_qk_norm_rope(); n = x without weights
+ *   half layout:        y_i = n_i c_i - n_{i+h} t_i,      y_{i+h} = n_{i+h} c_i + n_i t_i
+ *   interleaved layout: y_{2i} = n_{2i} c_i - n_{2i+1} t_i,  y_{2i+1} = n_{2i+1} c_i + n_{2i} t_i
+ *   with h = rotary_dim / 2, i < h, (c, t) the table row of the token's
+ *   position; channels from rotary_dim on pass through.  V is copied.
+ * Token s of sequence b is new when s < new_len[b] (NULL: all S are).  It is
+ * stored as the sequence's token kv_len[b] + s (a negative kv_len counts as
+ * 0); its position is pos[b, s], or that place when pos is NULL.  Tokens that
+ * are not new are padding: nothing of them is written, q_out keeps their rows.
+ * The caller provides the pages beforehand, and kv_len is not changed:
+ * len_out receives kv_len + new_len (at most the capacity), the lengths
+ * that h3attn_paged_decode() takes next.
+ * A new token without a row in the cache (past the capacity, or a page
+ * outside [0, num_pages)) is not stored; one whose position is outside
+ * [0, table_rows) gets zeros in q_out and K.  Both are reported by
+ * h3attn_check_device_status() as H3ATTN_ERR_INVALID_ARG.
+ *
+ * q: [B, S, Hq, D] bf16 or NULL with Hq == 0; k, v: [B, S, Hkv, D] bf16.
+ *    Token b * S + s starts stride elements after the one before it, its
+ *    heads lie behind one another: slices of one fused projection are taken as
+ *    they are.  Strides are multiples of 8 and at least heads * D.
+ * q_out: [B, S, Hq, D] bf16, contiguous; may be q itself when q_stride is Hq * D.
+ * wq, wk: [D] float32 or NULL (no norm; each for itself).
+ * cos, sin: [table_rows, rotary_dim / 2] float32; NULL when rotary_dim == 0.
+ * pos: [B, S] int32 or NULL.  new_len: [B] int32 or NULL; values are clamped
+ *    to [0, S].  len_out: [B] int32 or NULL, not kv_len or new_len.
+ * rotary_dim even, 0 <= rotary_dim <= D; eps >= 0 and finite;
+ * B * S * (Hq + 2 Hkv) < 2^31; B * S == 0 is a no-op.  q, k, v, q_out, pages, weights and
+ * tables 16-byte aligned, int32 arrays 4-byte aligned.  q_out and the pages
+ * overlap nothing else.
+ * Stream order as for h3attn_rmsnorm_modulate().
+ * Errors: INVALID_ARG, MISALIGNED, UNSUPPORTED_HEAD_DIM, UNSUPPORTED_DEVICE, LAUNCH.
+ */
+h3attn_status_t h3attn_qk_norm_rope_append(const void* q, const void* k, const void* v, void* q_out,
+                                           const h3attn_paged_kv_t* cache, const float* wq, const float* wk,
+                                           const float* cos, const float* sin, const int32_t* pos,
+                                           const int32_t* new_len, int32_t* len_out, int S, int Hq,
+                                           int64_t q_stride, int64_t k_stride, int64_t v_stride, int table_rows,
+                                           int rotary_dim, int interleaved, float eps, h3attn_stream_t stream);
+
+/*
+ * Attention of one new token per sequence over its paged cache, the decode
+ * counterpart of h3attn_prefill():
+ *   o[b, h] = sum_j softmax_j(scale * q[b, h] . k_j) v_j,   j < kv_len[b],
+ * query head h reading key-value head h / (Hq / Hkv).  The new token's own
+ * key and value are in the cache already (appended before the call).  A
+ * sequence without a key gets a zero row.  Rows of the last page past kv_len
+ * may hold anything.  Keys of a page outside [0, num_pages) are not attended
+ * (and reported).
+ *
+ * q, o: [B, Hq, D] bf16 (a [B, 1, Hq, D] tensor), o overlapping nothing else;
+ * scale finite and > 0; Hq a multiple of cache->Hkv; B, Hq <= 65535,
+ * B * Hkv * ceil(Hq / Hkv / 16) < 2^31; B == 0 is a no-op.
+ * workspace: device memory of at least h3attn_paged_decode_workspace_size()
+ *    bytes for the same cache geometry and Hq, 16-byte aligned, overlapping
+ *    nothing else; its contents on entry do not matter.  The tiles of all
+ *    sequences are then dealt evenly to the SMs whatever the lengths are, and
+ *    the parts of a sequence that several SMs hold are joined by a second
+ *    kernel.  NULL: one CTA walks each sequence (no second kernel).  Calls
+ *    that share a workspace must be ordered.
+ * Products on the tensor cores with float32 accumulation, softmax in float32
+ * with exp2, weights rounded to bf16 before the second product, the output
+ * rounded once to bf16.  Results do not depend on timing.
+ * Stream order as for h3attn_rmsnorm_modulate().
+ * Errors: INVALID_ARG, MISALIGNED, UNSUPPORTED_HEAD_DIM, UNSUPPORTED_DEVICE, LAUNCH.
+ */
+h3attn_status_t h3attn_paged_decode(const void* q, void* o, const h3attn_paged_kv_t* cache, int Hq, float scale,
+                                    void* workspace, size_t workspace_bytes, h3attn_stream_t stream);
+
+/*
+ * Workspace bytes of h3attn_paged_decode() on the current device for this
+ * cache geometry (its pointers are not looked at) and Hq, written to *bytes;
+ * 0 when the call does not split.
+ * Errors: INVALID_ARG, UNSUPPORTED_HEAD_DIM, UNSUPPORTED_DEVICE, LAUNCH.
+ */
+h3attn_status_t h3attn_paged_decode_workspace_size(const h3attn_paged_kv_t* cache, int Hq, size_t* bytes);
+
 /* Static English description of a status code (never NULL). */
 const char* h3attn_status_string(h3attn_status_t status);
 
 /*
  * Synchronises `stream`, then reads the current device's status word and
  * clears it.  Returns H3ATTN_ERR_TIMEOUT if a kernel gave up on a bounded wait
- * (H3ATTN_ERR_INVALID_ARG for an out-of-range modulation index) since the
- * last check, H3ATTN_ERR_LAUNCH if the stream reports a CUDA error, else
+ * (H3ATTN_ERR_INVALID_ARG for an out-of-range modulation index, cache page or
+ * position) since the last check, H3ATTN_ERR_LAUNCH if the stream reports a CUDA error, else
  * H3ATTN_OK.
  * The status word is one per device, shared by every stream and host thread
  * on it: a kernel on any stream can set it, and a check on any stream reports

@@ -26,6 +26,17 @@ The entry points mirror the C ABI in ``include/h3attn.h``:
   prefill attention on BSHD bf16 tensors with GQA, cross-attention, causal
   and boolean-mask variants (FastVideo PR #1799 "Add opt-in FlashInfer
   attention backend for Wan", section "Implementation").
+
+Generation over a paged key-value cache (``PagedKV``), one step of a block:
+
+* ``h3attn_add_rmsnorm(x, residual, h, y, w, eps, y_scale, stream)`` --
+  residual add and RMSNorm, in bf16 or in e4m3 with scales.
+* ``h3attn_qk_norm_rope_append(q, k, v, q_out, cache, ...)`` -- the fused
+  Q/K norm and RoPE of new tokens, K and V appended to the cache.
+* ``h3attn_paged_decode(q, o, cache, scale, workspace, stream)`` -- attention
+  of one new token per sequence over the cache.
+* ``h3attn_rope_table(cos, sin, rotary_dim, theta, scaling, pos, first,
+  stream)`` -- rotary tables, also scaled for long contexts.
 """
 from __future__ import annotations
 
@@ -49,7 +60,8 @@ H3ATTN_ERR_TIMEOUT = 7
 # Every symbol include/h3attn.h declares.
 EXPORTED = ("h3attn_qk_norm_rope", "h3attn_qk_norm_rope_out", "h3attn_prefill", "h3attn_prefill_ws",
             "h3attn_prefill_workspace_size", "h3attn_prefill_noalloc", "h3attn_prefill_window",
-            "h3attn_rmsnorm_modulate",
+            "h3attn_rmsnorm_modulate", "h3attn_add_rmsnorm", "h3attn_rope_table", "h3attn_qk_norm_rope_append",
+            "h3attn_paged_decode", "h3attn_paged_decode_workspace_size",
             "h3attn_status_string", "h3attn_check_device_status", "h3attn_version")
 
 
@@ -69,6 +81,21 @@ class h3attn_window_t(ctypes.Structure):
     _fields_ = [("frame_tokens", ctypes.c_int), ("anchor_frames", ctypes.c_int),
                 ("chunk_frames", ctypes.c_int), ("radius", ctypes.c_int)]
 
+
+class h3attn_paged_kv_t(ctypes.Structure):
+    _fields_ = [("k_pages", ctypes.c_void_p), ("v_pages", ctypes.c_void_p), ("page_table", ctypes.c_void_p),
+                ("kv_len", ctypes.c_void_p), ("B", ctypes.c_int), ("num_pages", ctypes.c_int),
+                ("page_size", ctypes.c_int), ("max_pages", ctypes.c_int), ("Hkv", ctypes.c_int), ("D", ctypes.c_int)]
+
+
+class h3attn_rope_scaling_t(ctypes.Structure):
+    _fields_ = [("kind", ctypes.c_int), ("original_len", ctypes.c_int), ("factor", ctypes.c_double),
+                ("low_turns", ctypes.c_double), ("high_turns", ctypes.c_double), ("amplitude", ctypes.c_double)]
+
+
+# h3attn_y_format_t and h3attn_rope_kind_t
+H3ATTN_Y_BF16, H3ATTN_Y_E4M3_ROW, H3ATTN_Y_E4M3_MX32 = 0, 1, 2
+H3ATTN_ROPE_NONE, H3ATTN_ROPE_LINEAR, H3ATTN_ROPE_NTK, H3ATTN_ROPE_BY_PARTS = 0, 1, 2, 3
 
 _lock = threading.Lock()
 _lib = None
@@ -110,6 +137,19 @@ def load(path: str = LIB_PATH):
             lib.h3attn_prefill_window.argtypes = [P, P, P, P, I, I, I, I, I, F, ctypes.POINTER(h3attn_window_t),
                                                   ctypes.POINTER(h3attn_mask_t), P]
             lib.h3attn_prefill_window.restype = I
+            cache = ctypes.POINTER(h3attn_paged_kv_t)
+            lib.h3attn_add_rmsnorm.argtypes = [P, P, P, P, P, P, I, I, I, F, P]
+            lib.h3attn_add_rmsnorm.restype = I
+            lib.h3attn_rope_table.argtypes = [P, P, P, ctypes.c_int64, I, I, ctypes.c_double,
+                                              ctypes.POINTER(h3attn_rope_scaling_t), P]
+            lib.h3attn_rope_table.restype = I
+            lib.h3attn_qk_norm_rope_append.argtypes = [P, P, P, P, cache, P, P, P, P, P, P, P, I, I, ctypes.c_int64,
+                                                       ctypes.c_int64, ctypes.c_int64, I, I, I, F, P]
+            lib.h3attn_qk_norm_rope_append.restype = I
+            lib.h3attn_paged_decode.argtypes = [P, P, cache, I, F, P, ctypes.c_size_t, P]
+            lib.h3attn_paged_decode.restype = I
+            lib.h3attn_paged_decode_workspace_size.argtypes = [cache, I, ctypes.POINTER(ctypes.c_size_t)]
+            lib.h3attn_paged_decode_workspace_size.restype = I
             lib.h3attn_status_string.argtypes = [I]
             lib.h3attn_status_string.restype = ctypes.c_char_p
             lib.h3attn_check_device_status.argtypes = [P]
@@ -381,6 +421,267 @@ def h3attn_prefill_window(q, k, v, o, window: Window, scale=None, mask: Mask | N
                                     ctypes.pointer(w), mptr, _stream_handle(stream))
     _raise_if(st, "h3attn_prefill_window")
     return o
+
+
+def _check(name, t, dtype, shape):
+    """A contiguous CUDA tensor of this dtype and shape on the current device,
+    without a gradient; the message names what is expected."""
+    import torch
+    if t.dtype != dtype or not t.is_cuda or not t.is_contiguous() or tuple(t.shape) != shape:
+        raise H3AttnError(H3ATTN_ERR_INVALID_ARG, f"{name} must be a contiguous {list(shape)} {dtype} CUDA tensor")
+    if t.get_device() != torch.cuda.current_device():
+        raise H3AttnError(H3ATTN_ERR_INVALID_ARG, f"{name} must be on the current device")
+    if t.requires_grad:
+        raise H3AttnError(H3ATTN_ERR_INVALID_ARG, f"{name}: inference only, grad-enabled inputs are rejected")
+
+
+def h3attn_add_rmsnorm(x, residual, h, y, w=None, eps=1e-6, y_scale=None, stream=None):
+    """h <- bf16(x + residual); y <- rmsnorm(h) * w, in bf16 or in e4m3 with scales.
+
+    x, residual, h: [T, C] bf16 CUDA tensors (residual and h may both be None:
+    the norm is then of x; h may be x or residual); w: [C] float32 or None.
+    y: [T, C], bfloat16, or float8_e4m3fn with y_scale [T] float32 (one scale a
+    row) or [T, C / 32] float8_e8m0fnu or uint8 (a power of two for each 32
+    channels).
+    """
+    import torch
+    load()
+    if x.dim() != 2:
+        raise H3AttnError(H3ATTN_ERR_INVALID_ARG, "x must be a [T, C] bf16 CUDA tensor")
+    shape = T, C = tuple(x.shape)
+    bf16 = torch.bfloat16
+    _check("x", x, bf16, shape)
+    if (residual is None) != (h is None):
+        raise H3AttnError(H3ATTN_ERR_INVALID_ARG, "residual and h must be given together")
+    if residual is not None:
+        _check("residual", residual, bf16, shape)
+        _check("h", h, bf16, shape)
+    if w is not None:
+        _check("w", w, torch.float32, (C,))
+    if y.dtype == bf16:
+        if y_scale is not None:
+            raise H3AttnError(H3ATTN_ERR_INVALID_ARG, "a bf16 y takes no y_scale")
+        _check("y", y, bf16, shape)
+        fmt = H3ATTN_Y_BF16
+    else:
+        _check("y", y, torch.float8_e4m3fn, shape)
+        if y_scale is None:
+            raise H3AttnError(H3ATTN_ERR_INVALID_ARG, "an e4m3 y needs y_scale")
+        if y_scale.dtype == torch.float32:
+            _check("y_scale", y_scale, torch.float32, (T,))
+            fmt = H3ATTN_Y_E4M3_ROW
+        else:
+            _check("y_scale", y_scale, torch.uint8 if y_scale.dtype == torch.uint8 else torch.float8_e8m0fnu,
+                   (T, C // 32))
+            fmt = H3ATTN_Y_E4M3_MX32
+    st = _lib.h3attn_add_rmsnorm(x.data_ptr(), _ptr(residual), _ptr(h), y.data_ptr(), _ptr(w), _ptr(y_scale), T, C, fmt,
+                                 eps, _stream_handle(stream))
+    _raise_if(st, "h3attn_add_rmsnorm")
+    return y
+
+
+_ROPE_KINDS = {"none": H3ATTN_ROPE_NONE, "linear": H3ATTN_ROPE_LINEAR, "ntk": H3ATTN_ROPE_NTK,
+               "by_parts": H3ATTN_ROPE_BY_PARTS}
+
+
+@dataclass(frozen=True)
+class RopeScaling:
+    """Rotary frequencies for long contexts: see h3attn_rope_scaling_t.  kind
+    is "none", "linear", "ntk" or "by_parts"."""
+    kind: str
+    factor: float = 1.0
+    original_len: int = 1
+    low_turns: float = 1.0
+    high_turns: float = 32.0
+    amplitude: float = 1.0
+
+
+def h3attn_rope_table(cos, sin, rotary_dim, theta=10000.0, scaling: RopeScaling | None = None, pos=None, first=0,
+                      stream=None):
+    """cos, sin <- the rotary table of positions pos, or first, first + 1, ...
+
+    cos, sin: [N, rotary_dim / 2] float32 CUDA tensors (preallocated); pos: [N]
+    int32 or None.  Returns (cos, sin).
+    """
+    import torch
+    load()
+    shape = (cos.shape[0] if cos.dim() else 0, rotary_dim // 2)
+    _check("cos", cos, torch.float32, shape)
+    _check("sin", sin, torch.float32, shape)
+    if pos is not None:
+        _check("pos", pos, torch.int32, shape[:1])
+    ref = None
+    if scaling is not None:
+        if scaling.kind not in _ROPE_KINDS:
+            raise H3AttnError(H3ATTN_ERR_INVALID_ARG, f"unknown scaling {scaling.kind!r}")
+        ref = ctypes.byref(h3attn_rope_scaling_t(_ROPE_KINDS[scaling.kind], scaling.original_len, scaling.factor,
+                                                 scaling.low_turns, scaling.high_turns, scaling.amplitude))
+    st = _lib.h3attn_rope_table(cos.data_ptr(), sin.data_ptr(), _ptr(pos), first, shape[0], rotary_dim, theta, ref,
+                                _stream_handle(stream))
+    _raise_if(st, "h3attn_rope_table")
+    return cos, sin
+
+
+class PagedKV:
+    """A paged key-value cache: see h3attn_paged_kv_t.
+
+    k_pages, v_pages: [num_pages, page_size, Hkv, D] bf16; page_table:
+    [B, max_pages] int32; kv_len: [B] int32, the tokens the cache holds of each
+    sequence.  All CUDA tensors, kept by reference: their contents may change
+    between calls, their storage not.
+    """
+    __slots__ = ("k_pages", "v_pages", "page_table", "kv_len", "_struct", "_ref", "_device")
+
+    def __init__(self, k_pages, v_pages, page_table, kv_len):
+        import torch
+        if k_pages.dim() != 4 or page_table.dim() != 2:
+            raise H3AttnError(H3ATTN_ERR_INVALID_ARG, "pages must be [num_pages, page_size, Hkv, D], page_table [B, max_pages]")
+        num_pages, page_size, Hkv, D = k_pages.shape
+        B, max_pages = page_table.shape
+        _check("k_pages", k_pages, torch.bfloat16, (num_pages, page_size, Hkv, D))
+        _check("v_pages", v_pages, torch.bfloat16, (num_pages, page_size, Hkv, D))
+        _check("page_table", page_table, torch.int32, (B, max_pages))
+        _check("kv_len", kv_len, torch.int32, (B,))
+        self.k_pages, self.v_pages, self.page_table, self.kv_len = k_pages, v_pages, page_table, kv_len
+        self._struct = h3attn_paged_kv_t(k_pages.data_ptr(), v_pages.data_ptr(), page_table.data_ptr(),
+                                         kv_len.data_ptr(), B, num_pages, page_size, max_pages, Hkv, D)
+        self._ref = ctypes.byref(self._struct)
+        self._device = k_pages.get_device()
+
+    def with_lengths(self, kv_len):
+        """The same cache with another lengths tensor (len_out of an append)."""
+        return PagedKV(self.k_pages, self.v_pages, self.page_table, kv_len)
+
+    def _check_device(self):
+        import torch
+        if self._device != torch.cuda.current_device():
+            raise H3AttnError(H3ATTN_ERR_INVALID_ARG, "the cache must be on the current device")
+
+
+def _token_stride(name, t, B, S, H, D):
+    """Elements from one token to the next of a [B, S, H, D] bf16 tensor whose
+    heads lie behind one another (a slice of a fused projection, say)."""
+    import torch
+    if t.dtype != torch.bfloat16 or not t.is_cuda or tuple(t.shape) != (B, S, H, D):
+        raise H3AttnError(H3ATTN_ERR_INVALID_ARG, f"{name} must be a {[B, S, H, D]} bf16 CUDA tensor")
+    if t.get_device() != torch.cuda.current_device():
+        raise H3AttnError(H3ATTN_ERR_INVALID_ARG, f"{name} must be on the current device")
+    if t.requires_grad:
+        raise H3AttnError(H3ATTN_ERR_INVALID_ARG, f"{name}: inference only, grad-enabled inputs are rejected")
+    if B * S * H == 0:
+        return H * D
+    sb, ss, sh, sd = t.stride()
+    stride = ss if S > 1 else sb if B > 1 else H * D
+    if sd != 1 or (H > 1 and sh != D) or (S > 1 and B > 1 and sb != S * ss):
+        raise H3AttnError(H3ATTN_ERR_INVALID_ARG, f"{name} must have contiguous heads and one stride from token to token")
+    return stride
+
+
+def h3attn_qk_norm_rope_append(q, k, v, q_out, cache: PagedKV, wq, wk, cos, sin, rotary_dim=96, eps=1e-6,
+                               interleaved=False, pos=None, new_len=None, len_out=None, stream=None):
+    """Q/K RMSNorm + bf16 boundary + partial RoPE of new tokens; K and V go to
+    the cache behind its kv_len tokens, Q to q_out.
+
+    q: [B, S, Hq, D] bf16 or None, k, v: [B, S, Hkv, D] bf16 (slices of one
+    projection are taken as they are); q_out: contiguous [B, S, Hq, D], or None
+    with q; wq, wk: [D] float32 or None (no norm); cos, sin: [rows,
+    rotary_dim / 2] float32; pos: [B, S] int32 or None (the place in the cache);
+    new_len: [B] int32 or None (all S); len_out: [B] int32 or None, receives the
+    new lengths.  Returns q_out.
+    """
+    import torch
+    load()
+    c = cache._struct
+    B, Hkv, D = c.B, c.Hkv, c.D
+    if k.dim() != 4:
+        raise H3AttnError(H3ATTN_ERR_INVALID_ARG, "k must be a [B, S, Hkv, D] bf16 CUDA tensor")
+    cache._check_device()
+    S = k.shape[1]
+    ks = _token_stride("k", k, B, S, Hkv, D)
+    vs = _token_stride("v", v, B, S, Hkv, D)
+    Hq = qs = 0
+    if (q is None) != (q_out is None):
+        raise H3AttnError(H3ATTN_ERR_INVALID_ARG, "q_out must be given exactly when q is")
+    if q is not None:
+        if q.dim() != 4:
+            raise H3AttnError(H3ATTN_ERR_INVALID_ARG, "q must be a [B, S, Hq, D] bf16 CUDA tensor")
+        Hq = q.shape[2]
+        qs = _token_stride("q", q, B, S, Hq, D)
+        _check("q_out", q_out, torch.bfloat16, (B, S, Hq, D))
+    f32, i32 = torch.float32, torch.int32
+    if wq is not None:
+        _check("wq", wq, f32, (D,))
+    if wk is not None:
+        _check("wk", wk, f32, (D,))
+    rows = 0
+    if rotary_dim > 0:
+        if cos is None or sin is None:
+            raise H3AttnError(H3ATTN_ERR_INVALID_ARG, "cos and sin are required when rotary_dim > 0")
+        rows = cos.shape[0] if cos.dim() else 0
+        _check("cos", cos, f32, (rows, rotary_dim // 2))
+        _check("sin", sin, f32, (rows, rotary_dim // 2))
+    if pos is not None:
+        _check("pos", pos, i32, (B, S))
+    if new_len is not None:
+        _check("new_len", new_len, i32, (B,))
+    if len_out is not None:
+        _check("len_out", len_out, i32, (B,))
+    st = _lib.h3attn_qk_norm_rope_append(_ptr(q), k.data_ptr(), v.data_ptr(), _ptr(q_out), cache._ref, _ptr(wq), _ptr(wk),
+                                         _ptr(cos), _ptr(sin), _ptr(pos), _ptr(new_len), _ptr(len_out), S, Hq, qs, ks,
+                                         vs, rows, rotary_dim, int(bool(interleaved)), eps, _stream_handle(stream))
+    _raise_if(st, "h3attn_qk_norm_rope_append")
+    return q_out
+
+
+def h3attn_paged_decode(q, o, cache: PagedKV, scale=None, workspace=None, stream=None):
+    """o <- attention of one new token per sequence over its paged cache.
+
+    q, o: [B, 1, Hq, D] or [B, Hq, D] bf16 (o preallocated); the token's own key
+    and value are in the cache.  workspace: None (one CTA walks a sequence), or
+    a CUDA tensor from paged_decode_workspace(): the sequences are then split
+    over the GPU.
+    """
+    import torch
+    load()
+    c = cache._struct
+    cache._check_device()
+    shape = tuple(q.shape)
+    if len(shape) == 4 and shape[1] == 1:
+        B, _, Hq, D = shape
+    elif len(shape) == 3:
+        B, Hq, D = shape
+    else:
+        raise H3AttnError(H3ATTN_ERR_INVALID_ARG, "q must be [B, 1, Hq, D] or [B, Hq, D]: one new token per sequence")
+    if B != c.B or D != c.D:
+        raise H3AttnError(H3ATTN_ERR_INVALID_ARG, "shape mismatch between q and the cache")
+    _check("q", q, torch.bfloat16, shape)
+    _check("o", o, torch.bfloat16, shape)
+    ws, nbytes = None, 0
+    if workspace is not None:
+        if not workspace.is_cuda or not workspace.is_contiguous() or workspace.get_device() != q.get_device():
+            raise H3AttnError(H3ATTN_ERR_INVALID_ARG, "workspace must be a contiguous CUDA tensor on the current device")
+        ws, nbytes = workspace.data_ptr(), workspace.numel() * workspace.element_size()
+    st = _lib.h3attn_paged_decode(q.data_ptr(), o.data_ptr(), cache._ref, Hq, D ** -0.5 if scale is None else scale, ws,
+                                  nbytes, _stream_handle(stream))
+    _raise_if(st, "h3attn_paged_decode")
+    return o
+
+
+def h3attn_paged_decode_workspace_size(cache: PagedKV, Hq) -> int:
+    """Bytes of workspace h3attn_paged_decode takes for this cache and Hq query heads (0: no split)."""
+    load()
+    out = ctypes.c_size_t(0)
+    st = _lib.h3attn_paged_decode_workspace_size(cache._ref, int(Hq), ctypes.byref(out))
+    _raise_if(st, "h3attn_paged_decode_workspace_size")
+    return int(out.value)
+
+
+def paged_decode_workspace(q, cache: PagedKV):
+    """A workspace tensor for h3attn_paged_decode(q, ..., cache) on the current
+    device, or None when the call does not split (allocated by torch)."""
+    import torch
+    n = h3attn_paged_decode_workspace_size(cache, q.shape[-2])
+    return torch.empty(n, dtype=torch.uint8, device=q.device) if n else None
 
 
 def h3attn_check_device_status(stream=None) -> int:

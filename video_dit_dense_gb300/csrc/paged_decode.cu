@@ -1,0 +1,648 @@
+// Attention of one new token per sequence over a paged key-value cache.
+//
+//   o_h = sum_j softmax_j(scale q_h . k_j) v_j,   j < kv_len[b]
+//
+// Memory-bound: every cached K and V row is read once and used for the
+// G = Hq / Hkv query heads that share it, 2 G multiply-adds per element read.
+// From G = 4 on that is more than the CUDA cores do at the memory's rate, so
+// both products are tensor-core products of a warp (mma.sync m16n8k16: a
+// tcgen05 tile has 128 rows at least, and a decode step has G).  The cache
+// side is the 16-row operand, the query heads the 8 columns:
+//   S^T[16 tokens, 8 heads] = K[16, D] q^T[D, 8]
+//   O^T[16 channels, 8 heads] += V^T[16, 16 tokens] P^T[16 tokens, 8 heads]
+// so that up to 8 heads cost one pass, and P^T is S^T's accumulator with each
+// 8x8 block transposed (movmatrix).  Groups of 9 to 16 heads take two column
+// tiles; larger groups are cut into tiles of 16 that read the cache again
+// (from L2, as they run side by side).
+//
+// Work.  Lengths are known on the device only, and are unlike.  A "unit head"
+// is a key-value head (and a tile of 16 query heads of its group).  A CTA
+// takes WH neighbouring unit heads, so that its warps read one contiguous
+// stretch of the pages, and its other factor WT = warps / WH splits the
+// tokens.  All sequences' tiles of TILE tokens are numbered through; range r
+// of R takes tiles [r T / R, (r + 1) T / R), so CTAs differ by one tile
+// however unlike the lengths are.  A range that holds all of a sequence
+// writes its output; of a sequence that ranges share, each range writes its
+// unnormalised O, its running max and sum to the workspace, and a second
+// kernel joins them in the order of the ranges (results do not depend on
+// timing).  Every warp streams its own tiles through its own ring of
+// shared-memory stages with cp.async, ahead over sequence borders.
+//
+// Softmax in float32 with exp2, running max over the tiles; P is rounded to
+// bf16 for the second product (as in prefill: its relative error of 2^-9 per
+// weight averages out over the keys and stays below the output's own
+// rounding), the sum of the weights is taken before that rounding.
+#include <cuda_bf16.h>
+
+#include <algorithm>
+
+#include "generate.h"
+#include "ptx.cuh"
+
+namespace h3 {
+namespace {
+
+constexpr int kMaxSplitBatch = 512;  // sequences whose tile counts fit the CTA's shared memory
+
+__device__ __forceinline__ uint32_t fdiv(uint32_t n, const FastDiv& f) {
+  return f.one ? n : static_cast<uint32_t>(__umul64hi(f.M, static_cast<uint64_t>(n)));
+}
+__device__ __forceinline__ uint32_t pack_bf16(float lo, float hi) {
+  __nv_bfloat162 v = __floats2bfloat162_rn(lo, hi);
+  return *reinterpret_cast<uint32_t*>(&v);
+}
+__device__ __forceinline__ float ex2(float x) {
+  float y;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
+// 16 bytes global -> shared; zeros when !valid (the source is not read).
+__device__ __forceinline__ void cp_async16(uint32_t dst, const void* src, bool valid) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(valid ? 16 : 0) : "memory");
+}
+__device__ __forceinline__ void cp_async_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+template <int N>
+__device__ __forceinline__ void cp_async_wait() {
+  asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
+}
+__device__ __forceinline__ void ldmatrix4(uint32_t (&r)[4], uint32_t addr) {
+  asm volatile("ldmatrix.sync.aligned.m8n8.x4.shared.b16 {%0, %1, %2, %3}, [%4];"
+               : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
+               : "r"(addr)
+               : "memory");
+}
+__device__ __forceinline__ void ldmatrix4_trans(uint32_t (&r)[4], uint32_t addr) {
+  asm volatile("ldmatrix.sync.aligned.m8n8.x4.trans.shared.b16 {%0, %1, %2, %3}, [%4];"
+               : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
+               : "r"(addr)
+               : "memory");
+}
+// The transpose of an 8x8 block of 16-bit values held as an accumulator fragment.
+__device__ __forceinline__ uint32_t transpose8x8(uint32_t v) {
+  uint32_t d;
+  asm volatile("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(d) : "r"(v));
+  return d;
+}
+__device__ __forceinline__ void mma16816(float (&c)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
+  asm volatile(
+      "mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, "
+      "{%0, %1, %2, %3};"
+      : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
+      : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+}
+
+// NT: tiles of 8 query heads (1 or 2).
+template <int D, int NT>
+struct DecodeCfg {
+  static constexpr int kTile = D == 64 ? 32 : 16;  // tokens a warp takes at a time: 8 KB of K and V at D 64 and 128
+  static constexpr int kWarps = D == 256 ? 4 : 8;
+  static constexpr int kStages = 3;
+  static constexpr int kTileBytes = kTile * D * 2;    // of K, and the same of V
+  static constexpr int kRing = kWarps * kStages * 2 * kTileBytes;
+  static constexpr int kHeads = NT * 8;
+  // joining the warps of a unit head: accumulators, max and sum of every second warp
+  static constexpr int kJoin = kWarps / 2 * kHeads * D * 4;
+  static constexpr int kStats = kWarps / 2 * kHeads * 2 * 4;
+  static constexpr int kSmem = kRing + kJoin + kStats + kWarps * kStages * 4 + kMaxSplitBatch * 4 + 16;
+  static_assert(kSmem <= 232448, "shared memory of one CTA");
+};
+
+// Unit heads and the shape of the launch, the same on the host and in both kernels.
+struct DecodePlan {
+  int unit_heads;  // Hkv * tiles of query heads
+  int q_tiles;     // tiles of at most 16 query heads in a group
+  int WH, WT;      // warps of a CTA: unit heads x token splits
+  int groups;      // CTAs across the unit heads
+  int ranges;      // ranges of tiles, 0: one range per sequence (no split)
+  int min_tiles;   // tiles that a range has at least
+};
+
+struct Kernelargs {
+  DecodeArgs a;
+  DecodePlan p;
+};
+
+__device__ __forceinline__ int tiles_of(const DecodeArgs& a, int b, int tile) {
+  const int64_t capacity = static_cast<int64_t>(a.max_pages) * a.page_size;
+  const int n = static_cast<int>(min(static_cast<int64_t>(max(a.kv_len[b], 0)), capacity));
+  return (n + tile - 1) / tile;
+}
+__device__ __forceinline__ int len_of(const DecodeArgs& a, int b) {
+  const int64_t capacity = static_cast<int64_t>(a.max_pages) * a.page_size;
+  return static_cast<int>(min(static_cast<int64_t>(max(__ldg(a.kv_len + b), 0)), capacity));
+}
+// Ranges that T tiles are cut into.
+__device__ __forceinline__ int ranges_of(const DecodePlan& p, int T) {
+  return max(1, min(p.ranges, (T + p.min_tiles - 1) / p.min_tiles));
+}
+__device__ __forceinline__ int range_begin(int r, int R, int T) {
+  return static_cast<int>(static_cast<int64_t>(r) * T / R);
+}
+
+// end[b] = tiles of sequences 0 .. b, for all b < B, in shared memory.
+// Every thread of the block takes part; returns the total.
+__device__ __forceinline__ int scan_tiles(const DecodeArgs& a, int tile, int* end) {
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  if (warp == 0) {
+    int carry = 0;
+    for (int b0 = 0; b0 < a.B; b0 += 32) {
+      int n = b0 + lane < a.B ? tiles_of(a, b0 + lane, tile) : 0;
+#pragma unroll
+      for (int off = 1; off < 32; off <<= 1) {
+        const int m = __shfl_up_sync(0xFFFFFFFFu, n, off);
+        if (lane >= off) n += m;
+      }
+      if (b0 + lane < a.B) end[b0 + lane] = carry + n;
+      carry += __shfl_sync(0xFFFFFFFFu, n, 31);
+    }
+  }
+  __syncthreads();
+  return end[a.B - 1];
+}
+// First sequence whose tiles end after tile t.
+__device__ __forceinline__ int sequence_at(const int* end, int B, int t) {
+  int lo = 0, hi = B - 1;
+  while (lo < hi) {
+    const int mid = (lo + hi) >> 1;
+    if (end[mid] > t)
+      hi = mid;
+    else
+      lo = mid + 1;
+  }
+  return lo;
+}
+
+// A partial: max and sum of each head, padded to 16 bytes, then O of each head.
+__host__ __device__ constexpr int partial_o(int heads) { return (2 * heads + 3) / 4 * 4; }
+__host__ __device__ constexpr int64_t partial_floats(int heads, int D) { return partial_o(heads) + static_cast<int64_t>(heads) * D; }
+
+template <int D, int NT>
+__global__ void __launch_bounds__(DecodeCfg<D, NT>::kWarps * 32, 1) decode_kernel(const __grid_constant__ Kernelargs k) {
+  using C = DecodeCfg<D, NT>;
+  constexpr int TILE = C::kTile, MT = TILE / 16, STAGES = C::kStages;
+  constexpr int CH = D / 8;  // 16-byte pieces of a row
+  const DecodeArgs& a = k.a;
+  const DecodePlan& p = k.p;
+  extern __shared__ __align__(128) uint8_t smem[];
+  float* join = reinterpret_cast<float*>(smem + C::kRing);
+  float* stats = reinterpret_cast<float*>(smem + C::kRing + C::kJoin);
+  uint32_t* masks = reinterpret_cast<uint32_t*>(smem + C::kRing + C::kJoin + C::kStats);
+  int* end = reinterpret_cast<int*>(masks + C::kWarps * STAGES);
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+  asm volatile("griddepcontrol.wait;" ::: "memory");
+
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int wh = warp % p.WH, wt = warp / p.WH;
+  const int r = blockIdx.x / p.groups;
+  const int unit = (blockIdx.x - r * p.groups) * p.WH + wh;
+  const int kvh = unit / p.q_tiles, qt = unit - kvh * p.q_tiles;
+  const int G = a.Hq / a.Hkv;
+  const int head0 = kvh * G + qt * 16;            // first query head of the unit
+  const int heads = min(G - qt * 16, C::kHeads);  // its query heads
+
+  // This CTA's tiles [t0, t1) of all sequences' tiles.  Without a split the range is sequence r.
+  int t0, t1, b0;
+  if (p.ranges > 0) {
+    const int T = scan_tiles(a, TILE, end);
+    const int R = ranges_of(p, T);
+    if (r >= R) return;
+    t0 = range_begin(r, R, T);
+    t1 = range_begin(r + 1, R, T);
+    if (t0 >= t1) return;
+    b0 = sequence_at(end, a.B, t0);
+  } else {
+    t0 = 0;
+    t1 = tiles_of(a, r, TILE);
+    b0 = r;
+  }
+  auto seq_begin = [&](int b) { return p.ranges > 0 && b > 0 ? end[b - 1] : 0; };
+  auto seq_end = [&](int b) { return p.ranges > 0 ? end[b] : t1; };
+
+  // The tiles that this warp loads, in the order it uses them, over sequence borders.
+  struct Walk {
+    int b, tile, stop, len;  // sequence, tile of the sequence, the range's end in it
+  };
+  auto enter = [&](Walk& w) {  // to the first tile at or after the present one that is there
+    while (w.tile >= w.stop) {
+      if (p.ranges == 0 || seq_end(w.b) >= t1) {
+        w.b = -1;
+        return;
+      }
+      ++w.b;
+      w.stop = min(t1, seq_end(w.b)) - seq_begin(w.b);
+      w.tile = wt;
+    }
+    w.len = len_of(a, w.b);
+  };
+  Walk ld;
+  ld.b = b0;
+  ld.tile = t0 - seq_begin(b0) + wt;
+  ld.stop = min(t1, seq_end(b0)) - seq_begin(b0);
+  enter(ld);
+
+  const uint32_t ring = smem_u32(smem) + warp * (STAGES * 2 * C::kTileBytes);
+  uint32_t* mask_ring = masks + warp * STAGES;
+  const int64_t row_stride = static_cast<int64_t>(a.Hkv) * D;
+  const uint16_t* kbase = a.k_pages + kvh * D;
+  const uint16_t* vbase = a.v_pages + kvh * D;
+
+  // Cache row of the lane's token of the tile to be loaded next, -1: none.
+  auto lookup = [&]() {
+    int row = -1;
+    if (ld.b >= 0) {
+      const int token = ld.tile * TILE + (lane % TILE);
+      if (token < ld.len) {
+        const uint32_t pg = fdiv(static_cast<uint32_t>(token), a.div_page);
+        const int page = __ldg(a.page_table + static_cast<int64_t>(ld.b) * a.max_pages + pg);
+        if (page >= 0 && page < a.num_pages)
+          row = page * a.page_size + (token - static_cast<int>(pg) * a.page_size);
+        else
+          atomicExch(a.status, static_cast<int>(H3ATTN_ERR_INVALID_ARG));  // its keys are not attended
+      }
+    }
+    return row;
+  };
+  int row_next = lookup();
+  auto load = [&](int st) {
+    const int row = row_next;
+    const uint32_t ks = ring + st * 2 * C::kTileBytes, vs = ks + C::kTileBytes;
+    const uint32_t mask = __ballot_sync(0xFFFFFFFFu, row >= 0);
+    if (lane == 0) mask_ring[st] = mask;
+    if (ld.b >= 0) {
+#pragma unroll
+      for (int i = 0; i < TILE * CH / 32; ++i) {
+        const int c = i * 32 + lane, tr = c / CH, col = c % CH;
+        const int src_row = __shfl_sync(0xFFFFFFFFu, row, tr);
+        const int64_t off = static_cast<int64_t>(max(src_row, 0)) * row_stride + col * 8;
+        const uint32_t dst = tr * (D * 2) + ((col ^ (tr & 7)) << 4);
+        cp_async16(ks + dst, kbase + off, src_row >= 0);
+        cp_async16(vs + dst, vbase + off, src_row >= 0);
+      }
+      ld.tile += p.WT;
+      enter(ld);
+      row_next = lookup();
+    }
+    cp_async_commit();
+  };
+#pragma unroll
+  for (int st = 0; st < STAGES - 1; ++st) load(st);
+
+  int st = 0, st_load = STAGES - 1;
+  int b = b0;
+  bool first_segment = true;
+  const int g = lane >> 2, t = lane & 3;
+  while (true) {
+    const int s0 = max(t0 - seq_begin(b), 0), s1 = min(t1, seq_end(b)) - seq_begin(b);
+    if (s0 < s1 || p.ranges == 0) {
+      // ---- one sequence's tiles [s0, s1) ----
+      uint32_t qf[NT][D / 16][2];
+#pragma unroll
+      for (int n = 0; n < NT; ++n) {
+        const bool there = n * 8 + g < heads;
+        const uint16_t* qp = a.q + (static_cast<int64_t>(b) * a.Hq + head0 + (there ? n * 8 + g : 0)) * D + 2 * t;
+#pragma unroll
+        for (int ks = 0; ks < D / 16; ++ks) {
+          qf[n][ks][0] = there ? __ldg(reinterpret_cast<const uint32_t*>(qp + ks * 16)) : 0u;
+          qf[n][ks][1] = there ? __ldg(reinterpret_cast<const uint32_t*>(qp + ks * 16 + 8)) : 0u;
+        }
+      }
+      float o[NT][D / 16][4];
+      float m[NT][2], l[NT][2];
+#pragma unroll
+      for (int n = 0; n < NT; ++n) {
+        m[n][0] = m[n][1] = -INFINITY;
+        l[n][0] = l[n][1] = 0.0f;
+#pragma unroll
+        for (int dt = 0; dt < D / 16; ++dt) o[n][dt][0] = o[n][dt][1] = o[n][dt][2] = o[n][dt][3] = 0.0f;
+      }
+      for (int tile = s0 + wt; tile < s1; tile += p.WT) {
+        cp_async_wait<STAGES - 2>();
+        __syncwarp();
+        const uint32_t ks_base = ring + st * 2 * C::kTileBytes, vs_base = ks_base + C::kTileBytes;
+        const uint32_t mask = mask_ring[st];
+        load(st_load);
+        float s[NT][MT][4];
+#pragma unroll
+        for (int n = 0; n < NT; ++n)
+#pragma unroll
+          for (int mt = 0; mt < MT; ++mt) s[n][mt][0] = s[n][mt][1] = s[n][mt][2] = s[n][mt][3] = 0.0f;
+#pragma unroll
+        for (int ks = 0; ks < D / 16; ++ks) {
+#pragma unroll
+          for (int mt = 0; mt < MT; ++mt) {
+            uint32_t kf[4];
+            const int row = mt * 16 + (lane & 15), col = ks * 2 + (lane >> 4);
+            ldmatrix4(kf, ks_base + row * (D * 2) + ((col ^ (row & 7)) << 4));
+#pragma unroll
+            for (int n = 0; n < NT; ++n) mma16816(s[n][mt], kf, qf[n][ks][0], qf[n][ks][1]);
+          }
+        }
+        // lane: tokens g and g + 8 of each 16, heads 2 t and 2 t + 1 of each 8
+        uint32_t pf[NT][MT][2];
+#pragma unroll
+        for (int n = 0; n < NT; ++n) {
+          float top[2] = {m[n][0], m[n][1]};
+#pragma unroll
+          for (int mt = 0; mt < MT; ++mt) {
+            const bool in0 = (mask >> (mt * 16 + g)) & 1u, in1 = (mask >> (mt * 16 + g + 8)) & 1u;
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+              s[n][mt][e] = ((e < 2) ? in0 : in1) ? s[n][mt][e] * a.scale_log2 : -INFINITY;
+              top[e & 1] = fmaxf(top[e & 1], s[n][mt][e]);
+            }
+          }
+          float base[2];
+#pragma unroll
+          for (int c = 0; c < 2; ++c) {
+            top[c] = fmaxf(top[c], __shfl_xor_sync(0xFFFFFFFFu, top[c], 4));
+            top[c] = fmaxf(top[c], __shfl_xor_sync(0xFFFFFFFFu, top[c], 8));
+            top[c] = fmaxf(top[c], __shfl_xor_sync(0xFFFFFFFFu, top[c], 16));
+            base[c] = top[c] == -INFINITY ? 0.0f : top[c];  // nothing attended yet
+            const float fix = ex2(m[n][c] - base[c]);
+            m[n][c] = top[c];
+            l[n][c] *= fix;
+#pragma unroll
+            for (int dt = 0; dt < D / 16; ++dt) {
+              o[n][dt][c] *= fix;
+              o[n][dt][c + 2] *= fix;
+            }
+          }
+#pragma unroll
+          for (int mt = 0; mt < MT; ++mt) {
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+              s[n][mt][e] = ex2(s[n][mt][e] - base[e & 1]);
+              l[n][e & 1] += s[n][mt][e];
+            }
+            pf[n][mt][0] = transpose8x8(pack_bf16(s[n][mt][0], s[n][mt][1]));
+            pf[n][mt][1] = transpose8x8(pack_bf16(s[n][mt][2], s[n][mt][3]));
+          }
+        }
+#pragma unroll
+        for (int mt = 0; mt < MT; ++mt) {
+#pragma unroll
+          for (int dt = 0; dt < D / 16; ++dt) {
+            uint32_t vf[4];
+            const int row = mt * 16 + (lane >> 4) * 8 + (lane & 7), col = dt * 2 + ((lane >> 3) & 1);
+            ldmatrix4_trans(vf, vs_base + row * (D * 2) + ((col ^ (row & 7)) << 4));
+#pragma unroll
+            for (int n = 0; n < NT; ++n) mma16816(o[n][dt], vf, pf[n][mt][0], pf[n][mt][1]);
+          }
+        }
+        __syncwarp();  // the stage is read; the next turn's load may fill it
+        st = st + 1 == STAGES ? 0 : st + 1;
+        st_load = st_load + 1 == STAGES ? 0 : st_load + 1;
+      }
+#pragma unroll
+      for (int n = 0; n < NT; ++n)
+#pragma unroll
+        for (int c = 0; c < 2; ++c) {
+          l[n][c] += __shfl_xor_sync(0xFFFFFFFFu, l[n][c], 4);
+          l[n][c] += __shfl_xor_sync(0xFFFFFFFFu, l[n][c], 8);
+          l[n][c] += __shfl_xor_sync(0xFFFFFFFFu, l[n][c], 16);
+        }
+      // ---- the warps of a unit head are joined, halving their number ----
+      for (int step = p.WT >> 1; step >= 1; step >>= 1) {
+        __syncthreads();  // the buffers are free
+        if (wt >= step && wt < 2 * step) {
+          const int at = (wt - step) * p.WH + wh;
+          float4* dst = reinterpret_cast<float4*>(join + at * (C::kHeads * D));
+#pragma unroll
+          for (int n = 0; n < NT; ++n)
+#pragma unroll
+            for (int dt = 0; dt < D / 16; ++dt)
+              dst[(n * (D / 16) + dt) * 32 + lane] = make_float4(o[n][dt][0], o[n][dt][1], o[n][dt][2], o[n][dt][3]);
+          if (lane < 4) {
+#pragma unroll
+            for (int n = 0; n < NT; ++n)
+#pragma unroll
+              for (int c = 0; c < 2; ++c) {
+                stats[(at * C::kHeads + n * 8 + 2 * t + c) * 2] = m[n][c];
+                stats[(at * C::kHeads + n * 8 + 2 * t + c) * 2 + 1] = l[n][c];
+              }
+          }
+        }
+        __syncthreads();
+        if (wt < step) {
+          const int at = wt * p.WH + wh;
+          const float4* src = reinterpret_cast<const float4*>(join + at * (C::kHeads * D));
+#pragma unroll
+          for (int n = 0; n < NT; ++n) {
+            float mine[2], theirs[2];
+#pragma unroll
+            for (int c = 0; c < 2; ++c) {
+              const float mo = stats[(at * C::kHeads + n * 8 + 2 * t + c) * 2];
+              const float lo = stats[(at * C::kHeads + n * 8 + 2 * t + c) * 2 + 1];
+              const float top = fmaxf(m[n][c], mo), base = top == -INFINITY ? 0.0f : top;
+              mine[c] = ex2(m[n][c] - base);
+              theirs[c] = ex2(mo - base);
+              m[n][c] = top;
+              l[n][c] = l[n][c] * mine[c] + lo * theirs[c];
+            }
+#pragma unroll
+            for (int dt = 0; dt < D / 16; ++dt) {
+              const float4 v = src[(n * (D / 16) + dt) * 32 + lane];
+              o[n][dt][0] = o[n][dt][0] * mine[0] + v.x * theirs[0];
+              o[n][dt][1] = o[n][dt][1] * mine[1] + v.y * theirs[1];
+              o[n][dt][2] = o[n][dt][2] * mine[0] + v.z * theirs[0];
+              o[n][dt][3] = o[n][dt][3] * mine[1] + v.w * theirs[1];
+            }
+          }
+        }
+      }
+      if (wt == 0) {
+        const bool whole = s0 == 0 && s1 == seq_end(b) - seq_begin(b);
+        if (whole) {
+#pragma unroll
+          for (int n = 0; n < NT; ++n)
+#pragma unroll
+            for (int c = 0; c < 2; ++c) {
+              const int h = n * 8 + 2 * t + c;
+              if (h < heads) {
+                const float inv = l[n][c] == 0.0f ? 0.0f : 1.0f / l[n][c];  // no key: zeros
+                __nv_bfloat16* op = reinterpret_cast<__nv_bfloat16*>(a.o) +
+                                    (static_cast<int64_t>(b) * a.Hq + head0 + h) * D + g;
+#pragma unroll
+                for (int dt = 0; dt < D / 16; ++dt) {
+                  op[dt * 16] = __float2bfloat16_rn(o[n][dt][c] * inv);
+                  op[dt * 16 + 8] = __float2bfloat16_rn(o[n][dt][c + 2] * inv);
+                }
+              }
+            }
+        } else {
+          // slot 0: the range's first sequence, slot 1: its last
+          float* part = a.ws + ((static_cast<int64_t>(r) * 2 + (first_segment ? 0 : 1)) * p.unit_heads + unit) *
+                                   partial_floats(min(G, C::kHeads), D);
+#pragma unroll
+          for (int n = 0; n < NT; ++n)
+#pragma unroll
+            for (int c = 0; c < 2; ++c) {
+              const int h = n * 8 + 2 * t + c;
+              if (h < heads) {
+                if (g == 0) {
+                  part[2 * h] = m[n][c];
+                  part[2 * h + 1] = l[n][c];
+                }
+                float* op = part + partial_o(min(G, C::kHeads)) + h * D + g;
+#pragma unroll
+                for (int dt = 0; dt < D / 16; ++dt) {
+                  op[dt * 16] = o[n][dt][c];
+                  op[dt * 16 + 8] = o[n][dt][c + 2];
+                }
+              }
+            }
+        }
+      }
+      first_segment = false;
+    }
+    if (p.ranges == 0 || seq_end(b) >= t1) break;
+    ++b;
+  }
+  cp_async_wait<0>();
+}
+
+constexpr int kCombineThreads = 256;
+
+// One CTA joins the partials of one sequence and query head, in the order of
+// the ranges.  Sequences that one range held whole are written already;
+// sequences without a key get zeros here.
+template <int D>
+__global__ void __launch_bounds__(kCombineThreads) decode_join_kernel(const __grid_constant__ Kernelargs k, int tile,
+                                                                      int tile_heads) {
+  constexpr int LANES = D / 4, ROWS = kCombineThreads / LANES;  // threads on a partial's O, partials at a time
+  const DecodeArgs& a = k.a;
+  const DecodePlan& p = k.p;
+  __shared__ int end[kMaxSplitBatch];
+  __shared__ float4 sum[ROWS][LANES];
+  __shared__ float2 ml[ROWS];
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+  asm volatile("griddepcontrol.wait;" ::: "memory");
+  const int b = blockIdx.x / a.Hq, h = blockIdx.x - b * a.Hq;
+  const int T = scan_tiles(a, tile, end);
+  const int R = ranges_of(p, T);
+  const int begin = b > 0 ? end[b - 1] : 0, stop = end[b];
+  uint16_t* out = a.o + (static_cast<int64_t>(b) * a.Hq + h) * D;
+  const int lane = threadIdx.x % LANES, row = threadIdx.x / LANES;
+  if (begin == stop) {
+    if (row == 0) *reinterpret_cast<uint2*>(out + 4 * lane) = make_uint2(0u, 0u);
+    return;
+  }
+  // the ranges that hold tiles begin and stop - 1: range r begins at floor(r T / R)
+  int r0 = static_cast<int>((static_cast<int64_t>(begin) * R) / T), r1 = static_cast<int>((static_cast<int64_t>(stop - 1) * R) / T);
+  while (r0 + 1 < R && range_begin(r0 + 1, R, T) <= begin) ++r0;
+  while (r1 + 1 < R && range_begin(r1 + 1, R, T) <= stop - 1) ++r1;
+  if (r0 == r1) return;
+  const int G = a.Hq / a.Hkv, kvh = h / G, in_group = h - kvh * G, qt = in_group / 16;
+  const int unit = kvh * p.q_tiles + qt, hh = in_group - qt * 16;
+  float m = -INFINITY, l = 0.0f;
+  float4 o = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+  for (int r = r0 + row; r <= r1; r += ROWS) {
+    const int which = range_begin(r, R, T) >= begin ? 0 : 1;  // slot 0 where the range begins in this sequence
+    const float* part = a.ws + ((static_cast<int64_t>(r) * 2 + which) * p.unit_heads + unit) * partial_floats(tile_heads, D);
+    const float mr = part[2 * hh], lr = part[2 * hh + 1];
+    const float4 v = *reinterpret_cast<const float4*>(part + partial_o(tile_heads) + hh * D + 4 * lane);
+    const float top = fmaxf(m, mr), base = top == -INFINITY ? 0.0f : top;
+    const float mine = ex2(m - base), theirs = ex2(mr - base);
+    m = top;
+    l = l * mine + lr * theirs;
+    o.x = o.x * mine + v.x * theirs;
+    o.y = o.y * mine + v.y * theirs;
+    o.z = o.z * mine + v.z * theirs;
+    o.w = o.w * mine + v.w * theirs;
+  }
+  sum[row][lane] = o;
+  if (lane == 0) ml[row] = make_float2(m, l);
+  __syncthreads();
+  if (row != 0) return;
+  float top = -INFINITY;
+#pragma unroll
+  for (int i = 0; i < ROWS; ++i) top = fmaxf(top, ml[i].x);
+  const float base = top == -INFINITY ? 0.0f : top;
+  float total = 0.0f;
+  o = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+#pragma unroll
+  for (int i = 0; i < ROWS; ++i) {
+    const float w = ex2(ml[i].x - base);
+    const float4 v = sum[i][lane];
+    total += ml[i].y * w;
+    o.x += v.x * w;
+    o.y += v.y * w;
+    o.z += v.z * w;
+    o.w += v.w * w;
+  }
+  const float inv = total == 0.0f ? 0.0f : 1.0f / total;
+  *reinterpret_cast<uint2*>(out + 4 * lane) = make_uint2(pack_bf16(o.x * inv, o.y * inv), pack_bf16(o.z * inv, o.w * inv));
+}
+
+cudaError_t sm_count(int* sms) {
+  int dev = 0;
+  cudaError_t e = cudaGetDevice(&dev);
+  return e != cudaSuccess ? e : cudaDeviceGetAttribute(sms, cudaDevAttrMultiProcessorCount, dev);
+}
+
+DecodePlan make_plan(const DecodeArgs& a, int sms, bool split) {
+  DecodePlan p;
+  const int G = a.Hq / a.Hkv, warps = a.D == 256 ? 4 : 8;
+  p.q_tiles = (G + 15) / 16;
+  p.unit_heads = a.Hkv * p.q_tiles;
+  p.WH = 1;
+  while (p.WH < warps && p.unit_heads % (2 * p.WH) == 0) p.WH *= 2;
+  p.WT = warps / p.WH;
+  p.groups = p.unit_heads / p.WH;
+  // one CTA an SM; a batch too long for the shared-memory scan has sequences enough to fill the GPU, and tiles
+  // are counted in 32 bits
+  const int64_t most_tiles = (static_cast<int64_t>(a.max_pages) * a.page_size / 16 + 1) * a.B;
+  p.ranges = split && a.B <= kMaxSplitBatch && most_tiles <= INT32_MAX ? std::max(1, sms / p.groups) : 0;
+  p.min_tiles = 2 * p.WT;
+  return p;
+}
+
+template <int D, int NT>
+cudaError_t launch_d(const Kernelargs& k, cudaStream_t stream) {
+  using C = DecodeCfg<D, NT>;
+  static bool attr_set[64] = {};
+  int dev = 0;
+  cudaError_t e = cudaGetDevice(&dev);
+  if (e != cudaSuccess) return e;
+  if (dev < 0 || dev >= 64) return cudaErrorInvalidDevice;
+  if (!attr_set[dev]) {
+    e = cudaFuncSetAttribute(decode_kernel<D, NT>, cudaFuncAttributeMaxDynamicSharedMemorySize, C::kSmem);
+    if (e != cudaSuccess) return e;
+    attr_set[dev] = true;
+  }
+  const int64_t ranges = k.p.ranges > 0 ? k.p.ranges : k.a.B;
+  e = launch_dependent(decode_kernel<D, NT>, dim3(static_cast<unsigned>(ranges * k.p.groups)), C::kWarps * 32, C::kSmem,
+                       stream, k);
+  if (e != cudaSuccess || k.p.ranges == 0) return e;
+  const int G = k.a.Hq / k.a.Hkv;
+  return launch_dependent(decode_join_kernel<D>, dim3(static_cast<unsigned>(k.a.B) * k.a.Hq), kCombineThreads, 0, stream, k,
+                          C::kTile, std::min(G, C::kHeads));
+}
+
+}  // namespace
+
+cudaError_t decode_workspace(const DecodeArgs& a, size_t* bytes) {
+  int sms = 0;
+  cudaError_t e = sm_count(&sms);
+  if (e != cudaSuccess) return e;
+  const DecodePlan p = make_plan(a, sms, true);
+  const int heads = std::min(a.Hq / a.Hkv, 16);
+  *bytes = static_cast<size_t>(p.ranges) * 2 * p.unit_heads * partial_floats(heads, a.D) * sizeof(float);
+  return cudaSuccess;
+}
+
+cudaError_t launch_decode(const DecodeArgs& a, cudaStream_t stream) {
+  int sms = 0;
+  cudaError_t e = sm_count(&sms);
+  if (e != cudaSuccess) return e;
+  Kernelargs k{a, make_plan(a, sms, a.ws != nullptr)};
+  const bool wide = a.Hq / a.Hkv > 8;
+  switch (a.D) {
+    case 64: return wide ? launch_d<64, 2>(k, stream) : launch_d<64, 1>(k, stream);
+    case 128: return wide ? launch_d<128, 2>(k, stream) : launch_d<128, 1>(k, stream);
+    case 256: return wide ? launch_d<256, 2>(k, stream) : launch_d<256, 1>(k, stream);
+    default: return cudaErrorInvalidValue;
+  }
+}
+
+}  // namespace h3
