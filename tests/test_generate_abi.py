@@ -148,17 +148,16 @@ class _Cuda:
         return 0
 
 
-def test_token_strides(monkeypatch):
-    monkeypatch.setattr(torch.cuda, "current_device", lambda: 0)
+def test_token_strides():
+    h3._get_torch()
     B, S, H, D = 2, 5, 3, 64
-    assert h3._token_stride("k", _Cuda((B, S, H, D), (S * 1000, 1000, D, 1)), B, S, H, D) == 1000
-    assert h3._token_stride("k", _Cuda((B, 1, H, D), (1000, 7, D, 1)), B, 1, H, D) == 1000   # one token a sequence
-    assert h3._token_stride("k", _Cuda((1, S, H, D), (7, 1000, D, 1)), 1, S, H, D) == 1000
-    assert h3._token_stride("k", _Cuda((1, 1, H, D), (7, 7, D, 1)), 1, 1, H, D) == H * D
-    assert h3._token_stride("k", _Cuda((1, S, 1, D), (7, 1000, 9, 1)), 1, S, 1, D) == 1000   # one head
+    assert h3._token_stride("k", _Cuda((B, S, H, D), (S * 1000, 1000, D, 1)), B, S, H, D, 0) == 1000
+    assert h3._token_stride("k", _Cuda((B, 1, H, D), (1000, 7, D, 1)), B, 1, H, D, 0) == 1000   # one token a sequence
+    assert h3._token_stride("k", _Cuda((1, S, H, D), (7, 1000, D, 1)), 1, S, H, D, 0) == 1000
+    assert h3._token_stride("k", _Cuda((1, 1, H, D), (7, 7, D, 1)), 1, 1, H, D, 0) == H * D
+    assert h3._token_stride("k", _Cuda((1, S, 1, D), (7, 1000, 9, 1)), 1, S, 1, D, 0) == 1000   # one head
     for strides in ((S * 1000 + 64, 1000, D, 1), (S * 1000, 1000, D + 8, 1), (S * 1000, 1000, D, 2)):
         with pytest.raises(h3.H3AttnError, match="stride"):
-            h3._token_stride("k", _Cuda((B, S, H, D), strides), B, S, H, D)
+            h3._token_stride("k", _Cuda((B, S, H, D), strides), B, S, H, D, 0)
     with pytest.raises(h3.H3AttnError, match="current device"):
-        monkeypatch.setattr(torch.cuda, "current_device", lambda: 1)
-        h3._token_stride("k", _Cuda((B, S, H, D), (S * 1000, 1000, D, 1)), B, S, H, D)
+        h3._token_stride("k", _Cuda((B, S, H, D), (S * 1000, 1000, D, 1)), B, S, H, D, 1)

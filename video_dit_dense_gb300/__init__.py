@@ -423,16 +423,49 @@ def h3attn_prefill_window(q, k, v, o, window: Window, scale=None, mask: Mask | N
     return o
 
 
-def _check(name, t, dtype, shape):
-    """A contiguous CUDA tensor of this dtype and shape on the current device,
-    without a gradient; the message names what is expected."""
-    import torch
+# A step of generation is a few microseconds of kernels, so these calls keep the
+# host's part short: torch is looked up once, a tensor's checks are one
+# expression, and the current stream's handle is read without making a Stream
+# object where torch offers that.
+_torch = None
+
+
+def _get_torch():
+    global _torch
+    if _torch is None:
+        import torch
+        _torch = torch
+    return _torch
+
+
+def _current_device(name, t):
+    """The device of t, which has to be the current one (the library launches there)."""
+    dev = t.get_device()
+    if dev < 0:
+        raise H3AttnError(H3ATTN_ERR_INVALID_ARG, f"{name} must be a CUDA tensor")
+    if dev != _torch.cuda.current_device():
+        raise H3AttnError(H3ATTN_ERR_INVALID_ARG, f"{name} must be on the current device")
+    return dev
+
+
+def _stream_on(stream, dev):
+    """Handle of the stream, by default device dev's current one."""
+    if stream is not None:
+        return _stream_handle(stream)
+    raw = getattr(_torch._C, "_cuda_getCurrentRawStream", None)
+    return raw(dev) if raw is not None else _torch.cuda.current_stream(dev).cuda_stream
+
+
+def _check(name, t, dtype, shape, dev):
+    """A contiguous tensor of this dtype and shape on CUDA device dev, without a
+    gradient; the message names what is expected."""
+    if t.dtype is dtype and t.shape == shape and t.get_device() == dev and t.is_contiguous() and not t.requires_grad:
+        return
     if t.dtype != dtype or not t.is_cuda or not t.is_contiguous() or tuple(t.shape) != shape:
         raise H3AttnError(H3ATTN_ERR_INVALID_ARG, f"{name} must be a contiguous {list(shape)} {dtype} CUDA tensor")
-    if t.get_device() != torch.cuda.current_device():
-        raise H3AttnError(H3ATTN_ERR_INVALID_ARG, f"{name} must be on the current device")
     if t.requires_grad:
         raise H3AttnError(H3ATTN_ERR_INVALID_ARG, f"{name}: inference only, grad-enabled inputs are rejected")
+    raise H3AttnError(H3ATTN_ERR_INVALID_ARG, f"{name} must be on the current device")
 
 
 def h3attn_add_rmsnorm(x, residual, h, y, w=None, eps=1e-6, y_scale=None, stream=None):
@@ -444,39 +477,44 @@ def h3attn_add_rmsnorm(x, residual, h, y, w=None, eps=1e-6, y_scale=None, stream
     row) or [T, C / 32] float8_e8m0fnu or uint8 (a power of two for each 32
     channels).
     """
-    import torch
-    load()
-    if x.dim() != 2:
+    _lib or load()
+    torch = _torch or _get_torch()
+    shape = x.shape
+    if len(shape) != 2:
         raise H3AttnError(H3ATTN_ERR_INVALID_ARG, "x must be a [T, C] bf16 CUDA tensor")
-    shape = T, C = tuple(x.shape)
-    bf16 = torch.bfloat16
-    _check("x", x, bf16, shape)
-    if (residual is None) != (h is None):
+    T, C = shape
+    bf16, dev = torch.bfloat16, _current_device("x", x)
+    _check("x", x, bf16, shape, dev)
+    rp = hp = wp = sp = None
+    if residual is not None and h is not None:
+        _check("residual", residual, bf16, shape, dev)
+        _check("h", h, bf16, shape, dev)
+        rp, hp = residual.data_ptr(), h.data_ptr()
+    elif residual is not None or h is not None:
         raise H3AttnError(H3ATTN_ERR_INVALID_ARG, "residual and h must be given together")
-    if residual is not None:
-        _check("residual", residual, bf16, shape)
-        _check("h", h, bf16, shape)
     if w is not None:
-        _check("w", w, torch.float32, (C,))
-    if y.dtype == bf16:
+        _check("w", w, torch.float32, (C,), dev)
+        wp = w.data_ptr()
+    if y.dtype is bf16:
         if y_scale is not None:
             raise H3AttnError(H3ATTN_ERR_INVALID_ARG, "a bf16 y takes no y_scale")
-        _check("y", y, bf16, shape)
+        _check("y", y, bf16, shape, dev)
         fmt = H3ATTN_Y_BF16
     else:
-        _check("y", y, torch.float8_e4m3fn, shape)
+        _check("y", y, torch.float8_e4m3fn, shape, dev)
         if y_scale is None:
             raise H3AttnError(H3ATTN_ERR_INVALID_ARG, "an e4m3 y needs y_scale")
-        if y_scale.dtype == torch.float32:
-            _check("y_scale", y_scale, torch.float32, (T,))
+        if y_scale.dtype is torch.float32:
+            _check("y_scale", y_scale, torch.float32, (T,), dev)
             fmt = H3ATTN_Y_E4M3_ROW
         else:
-            _check("y_scale", y_scale, torch.uint8 if y_scale.dtype == torch.uint8 else torch.float8_e8m0fnu,
-                   (T, C // 32))
+            _check("y_scale", y_scale, torch.uint8 if y_scale.dtype is torch.uint8 else torch.float8_e8m0fnu,
+                   (T, C // 32), dev)
             fmt = H3ATTN_Y_E4M3_MX32
-    st = _lib.h3attn_add_rmsnorm(x.data_ptr(), _ptr(residual), _ptr(h), y.data_ptr(), _ptr(w), _ptr(y_scale), T, C, fmt,
-                                 eps, _stream_handle(stream))
-    _raise_if(st, "h3attn_add_rmsnorm")
+        sp = y_scale.data_ptr()
+    st = _lib.h3attn_add_rmsnorm(x.data_ptr(), rp, hp, y.data_ptr(), wp, sp, T, C, fmt, eps, _stream_on(stream, dev))
+    if st:
+        raise H3AttnError(st, "h3attn_add_rmsnorm")
     return y
 
 
@@ -503,13 +541,14 @@ def h3attn_rope_table(cos, sin, rotary_dim, theta=10000.0, scaling: RopeScaling 
     cos, sin: [N, rotary_dim / 2] float32 CUDA tensors (preallocated); pos: [N]
     int32 or None.  Returns (cos, sin).
     """
-    import torch
-    load()
+    _lib or load()
+    torch = _torch or _get_torch()
+    dev = _current_device("cos", cos)
     shape = (cos.shape[0] if cos.dim() else 0, rotary_dim // 2)
-    _check("cos", cos, torch.float32, shape)
-    _check("sin", sin, torch.float32, shape)
+    _check("cos", cos, torch.float32, shape, dev)
+    _check("sin", sin, torch.float32, shape, dev)
     if pos is not None:
-        _check("pos", pos, torch.int32, shape[:1])
+        _check("pos", pos, torch.int32, shape[:1], dev)
     ref = None
     if scaling is not None:
         if scaling.kind not in _ROPE_KINDS:
@@ -517,8 +556,9 @@ def h3attn_rope_table(cos, sin, rotary_dim, theta=10000.0, scaling: RopeScaling 
         ref = ctypes.byref(h3attn_rope_scaling_t(_ROPE_KINDS[scaling.kind], scaling.original_len, scaling.factor,
                                                  scaling.low_turns, scaling.high_turns, scaling.amplitude))
     st = _lib.h3attn_rope_table(cos.data_ptr(), sin.data_ptr(), _ptr(pos), first, shape[0], rotary_dim, theta, ref,
-                                _stream_handle(stream))
-    _raise_if(st, "h3attn_rope_table")
+                                _stream_on(stream, dev))
+    if st:
+        raise H3AttnError(st, "h3attn_rope_table")
     return cos, sin
 
 
@@ -527,44 +567,44 @@ class PagedKV:
 
     k_pages, v_pages: [num_pages, page_size, Hkv, D] bf16; page_table:
     [B, max_pages] int32; kv_len: [B] int32, the tokens the cache holds of each
-    sequence.  All CUDA tensors, kept by reference: their contents may change
-    between calls, their storage not.
+    sequence.  All CUDA tensors on the current device, kept by reference: their
+    contents may change between calls, their storage not.
     """
-    __slots__ = ("k_pages", "v_pages", "page_table", "kv_len", "_struct", "_ref", "_device")
+    __slots__ = ("_tensors", "_struct", "_ref", "_device")
 
     def __init__(self, k_pages, v_pages, page_table, kv_len):
-        import torch
+        torch = _get_torch()
         if k_pages.dim() != 4 or page_table.dim() != 2:
             raise H3AttnError(H3ATTN_ERR_INVALID_ARG, "pages must be [num_pages, page_size, Hkv, D], page_table [B, max_pages]")
         num_pages, page_size, Hkv, D = k_pages.shape
         B, max_pages = page_table.shape
-        _check("k_pages", k_pages, torch.bfloat16, (num_pages, page_size, Hkv, D))
-        _check("v_pages", v_pages, torch.bfloat16, (num_pages, page_size, Hkv, D))
-        _check("page_table", page_table, torch.int32, (B, max_pages))
-        _check("kv_len", kv_len, torch.int32, (B,))
-        self.k_pages, self.v_pages, self.page_table, self.kv_len = k_pages, v_pages, page_table, kv_len
+        dev = _current_device("k_pages", k_pages)
+        _check("k_pages", k_pages, torch.bfloat16, (num_pages, page_size, Hkv, D), dev)
+        _check("v_pages", v_pages, torch.bfloat16, (num_pages, page_size, Hkv, D), dev)
+        _check("page_table", page_table, torch.int32, (B, max_pages), dev)
+        _check("kv_len", kv_len, torch.int32, (B,), dev)
+        self._tensors = (k_pages, v_pages, page_table, kv_len)
         self._struct = h3attn_paged_kv_t(k_pages.data_ptr(), v_pages.data_ptr(), page_table.data_ptr(),
                                          kv_len.data_ptr(), B, num_pages, page_size, max_pages, Hkv, D)
         self._ref = ctypes.byref(self._struct)
-        self._device = k_pages.get_device()
+        self._device = dev
+
+    k_pages = property(lambda self: self._tensors[0])
+    v_pages = property(lambda self: self._tensors[1])
+    page_table = property(lambda self: self._tensors[2])
+    kv_len = property(lambda self: self._tensors[3])
 
     def with_lengths(self, kv_len):
         """The same cache with another lengths tensor (len_out of an append)."""
         return PagedKV(self.k_pages, self.v_pages, self.page_table, kv_len)
 
-    def _check_device(self):
-        import torch
-        if self._device != torch.cuda.current_device():
-            raise H3AttnError(H3ATTN_ERR_INVALID_ARG, "the cache must be on the current device")
 
-
-def _token_stride(name, t, B, S, H, D):
+def _token_stride(name, t, B, S, H, D, dev):
     """Elements from one token to the next of a [B, S, H, D] bf16 tensor whose
     heads lie behind one another (a slice of a fused projection, say)."""
-    import torch
-    if t.dtype != torch.bfloat16 or not t.is_cuda or tuple(t.shape) != (B, S, H, D):
+    if t.dtype is not _torch.bfloat16 or t.shape != (B, S, H, D) or t.get_device() < 0:
         raise H3AttnError(H3ATTN_ERR_INVALID_ARG, f"{name} must be a {[B, S, H, D]} bf16 CUDA tensor")
-    if t.get_device() != torch.cuda.current_device():
+    if t.get_device() != dev:
         raise H3AttnError(H3ATTN_ERR_INVALID_ARG, f"{name} must be on the current device")
     if t.requires_grad:
         raise H3AttnError(H3ATTN_ERR_INVALID_ARG, f"{name}: inference only, grad-enabled inputs are rejected")
@@ -589,47 +629,58 @@ def h3attn_qk_norm_rope_append(q, k, v, q_out, cache: PagedKV, wq, wk, cos, sin,
     new_len: [B] int32 or None (all S); len_out: [B] int32 or None, receives the
     new lengths.  Returns q_out.
     """
-    import torch
-    load()
+    _lib or load()
+    torch = _torch or _get_torch()
     c = cache._struct
     B, Hkv, D = c.B, c.Hkv, c.D
     if k.dim() != 4:
         raise H3AttnError(H3ATTN_ERR_INVALID_ARG, "k must be a [B, S, Hkv, D] bf16 CUDA tensor")
-    cache._check_device()
+    dev = _current_device("k", k)
+    if cache._device != dev:
+        raise H3AttnError(H3ATTN_ERR_INVALID_ARG, "the cache must be on the current device")
     S = k.shape[1]
-    ks = _token_stride("k", k, B, S, Hkv, D)
-    vs = _token_stride("v", v, B, S, Hkv, D)
-    Hq = qs = 0
-    if (q is None) != (q_out is None):
-        raise H3AttnError(H3ATTN_ERR_INVALID_ARG, "q_out must be given exactly when q is")
-    if q is not None:
+    ks = _token_stride("k", k, B, S, Hkv, D, dev)
+    vs = _token_stride("v", v, B, S, Hkv, D, dev)
+    Hq = qs = rows = 0
+    qp = op = wqp = wkp = cp = sp = pp = np = lp = None
+    if q is not None and q_out is not None:
         if q.dim() != 4:
             raise H3AttnError(H3ATTN_ERR_INVALID_ARG, "q must be a [B, S, Hq, D] bf16 CUDA tensor")
         Hq = q.shape[2]
-        qs = _token_stride("q", q, B, S, Hq, D)
-        _check("q_out", q_out, torch.bfloat16, (B, S, Hq, D))
+        qs = _token_stride("q", q, B, S, Hq, D, dev)
+        _check("q_out", q_out, torch.bfloat16, (B, S, Hq, D), dev)
+        qp, op = q.data_ptr(), q_out.data_ptr()
+    elif q is not None or q_out is not None:
+        raise H3AttnError(H3ATTN_ERR_INVALID_ARG, "q_out must be given exactly when q is")
     f32, i32 = torch.float32, torch.int32
     if wq is not None:
-        _check("wq", wq, f32, (D,))
+        _check("wq", wq, f32, (D,), dev)
+        wqp = wq.data_ptr()
     if wk is not None:
-        _check("wk", wk, f32, (D,))
-    rows = 0
+        _check("wk", wk, f32, (D,), dev)
+        wkp = wk.data_ptr()
     if rotary_dim > 0:
         if cos is None or sin is None:
             raise H3AttnError(H3ATTN_ERR_INVALID_ARG, "cos and sin are required when rotary_dim > 0")
         rows = cos.shape[0] if cos.dim() else 0
-        _check("cos", cos, f32, (rows, rotary_dim // 2))
-        _check("sin", sin, f32, (rows, rotary_dim // 2))
+        shape = (rows, rotary_dim // 2)
+        _check("cos", cos, f32, shape, dev)
+        _check("sin", sin, f32, shape, dev)
+        cp, sp = cos.data_ptr(), sin.data_ptr()
     if pos is not None:
-        _check("pos", pos, i32, (B, S))
+        _check("pos", pos, i32, (B, S), dev)
+        pp = pos.data_ptr()
     if new_len is not None:
-        _check("new_len", new_len, i32, (B,))
+        _check("new_len", new_len, i32, (B,), dev)
+        np = new_len.data_ptr()
     if len_out is not None:
-        _check("len_out", len_out, i32, (B,))
-    st = _lib.h3attn_qk_norm_rope_append(_ptr(q), k.data_ptr(), v.data_ptr(), _ptr(q_out), cache._ref, _ptr(wq), _ptr(wk),
-                                         _ptr(cos), _ptr(sin), _ptr(pos), _ptr(new_len), _ptr(len_out), S, Hq, qs, ks,
-                                         vs, rows, rotary_dim, int(bool(interleaved)), eps, _stream_handle(stream))
-    _raise_if(st, "h3attn_qk_norm_rope_append")
+        _check("len_out", len_out, i32, (B,), dev)
+        lp = len_out.data_ptr()
+    st = _lib.h3attn_qk_norm_rope_append(qp, k.data_ptr(), v.data_ptr(), op, cache._ref, wqp, wkp, cp, sp, pp, np, lp, S, Hq,
+                                         qs, ks, vs, rows, rotary_dim, 1 if interleaved else 0, eps,
+                                         _stream_on(stream, dev))
+    if st:
+        raise H3AttnError(st, "h3attn_qk_norm_rope_append")
     return q_out
 
 
@@ -641,11 +692,10 @@ def h3attn_paged_decode(q, o, cache: PagedKV, scale=None, workspace=None, stream
     a CUDA tensor from paged_decode_workspace(): the sequences are then split
     over the GPU.
     """
-    import torch
-    load()
+    _lib or load()
+    torch = _torch or _get_torch()
     c = cache._struct
-    cache._check_device()
-    shape = tuple(q.shape)
+    shape = q.shape
     if len(shape) == 4 and shape[1] == 1:
         B, _, Hq, D = shape
     elif len(shape) == 3:
@@ -654,16 +704,20 @@ def h3attn_paged_decode(q, o, cache: PagedKV, scale=None, workspace=None, stream
         raise H3AttnError(H3ATTN_ERR_INVALID_ARG, "q must be [B, 1, Hq, D] or [B, Hq, D]: one new token per sequence")
     if B != c.B or D != c.D:
         raise H3AttnError(H3ATTN_ERR_INVALID_ARG, "shape mismatch between q and the cache")
-    _check("q", q, torch.bfloat16, shape)
-    _check("o", o, torch.bfloat16, shape)
+    dev = _current_device("q", q)
+    if cache._device != dev:
+        raise H3AttnError(H3ATTN_ERR_INVALID_ARG, "the cache must be on the current device")
+    _check("q", q, torch.bfloat16, shape, dev)
+    _check("o", o, torch.bfloat16, shape, dev)
     ws, nbytes = None, 0
     if workspace is not None:
-        if not workspace.is_cuda or not workspace.is_contiguous() or workspace.get_device() != q.get_device():
+        if workspace.get_device() != dev or not workspace.is_contiguous():
             raise H3AttnError(H3ATTN_ERR_INVALID_ARG, "workspace must be a contiguous CUDA tensor on the current device")
-        ws, nbytes = workspace.data_ptr(), workspace.numel() * workspace.element_size()
+        ws, nbytes = workspace.data_ptr(), workspace.nbytes
     st = _lib.h3attn_paged_decode(q.data_ptr(), o.data_ptr(), cache._ref, Hq, D ** -0.5 if scale is None else scale, ws,
-                                  nbytes, _stream_handle(stream))
-    _raise_if(st, "h3attn_paged_decode")
+                                  nbytes, _stream_on(stream, dev))
+    if st:
+        raise H3AttnError(st, "h3attn_paged_decode")
     return o
 
 
@@ -679,8 +733,8 @@ def h3attn_paged_decode_workspace_size(cache: PagedKV, Hq) -> int:
 def paged_decode_workspace(q, cache: PagedKV):
     """A workspace tensor for h3attn_paged_decode(q, ..., cache) on the current
     device, or None when the call does not split (allocated by torch)."""
-    import torch
     n = h3attn_paged_decode_workspace_size(cache, q.shape[-2])
+    torch = _get_torch()
     return torch.empty(n, dtype=torch.uint8, device=q.device) if n else None
 
 

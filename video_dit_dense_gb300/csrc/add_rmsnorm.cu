@@ -81,8 +81,8 @@ __global__ void __launch_bounds__(TPR > kThreads ? TPR : kThreads) add_rmsnorm_k
     const int v = k * TPR + t;
     const bool in = live && v < V;
     const float4 one = make_float4(1.0f, 1.0f, 1.0f, 1.0f);
-    *reinterpret_cast<float4*>(&wv[k][0]) = in && a.w ? __ldg(reinterpret_cast<const float4*>(a.w + 8 * v)) : one;
-    *reinterpret_cast<float4*>(&wv[k][4]) = in && a.w ? __ldg(reinterpret_cast<const float4*>(a.w + 8 * v + 4)) : one;
+    *reinterpret_cast<float4*>(&wv[k][0]) = in && a.w ? *reinterpret_cast<const float4*>(a.w + 8 * v) : one;
+    *reinterpret_cast<float4*>(&wv[k][4]) = in && a.w ? *reinterpret_cast<const float4*>(a.w + 8 * v + 4) : one;
     xv[k] = in ? *reinterpret_cast<const uint4*>(a.x + base + 8 * v) : make_uint4(0u, 0u, 0u, 0u);
     rv[k] = in && a.residual ? *reinterpret_cast<const uint4*>(a.residual + base + 8 * v) : make_uint4(0u, 0u, 0u, 0u);
   }

@@ -14,7 +14,9 @@ namespace h3 {
 // Launch with programmatic stream serialization: the kernel's CTAs may be
 // placed while the kernel before it in the stream drains; every kernel
 // launched this way executes griddepcontrol.wait before it touches global
-// memory.
+// memory.  What the kernels before may have written (lengths, page tables,
+// rotary tables) is read with ordinary loads, not through the read-only path,
+// which is for data that stays as it is for the whole life of a kernel.
 template <class... P, class... A>
 inline cudaError_t launch_dependent(void (*kernel)(P...), dim3 grid, unsigned threads, size_t smem,
                                     cudaStream_t stream, const A&... args) {
@@ -97,6 +99,7 @@ struct DecodeArgs {
   float scale_log2;  // scale * log2(e)
   float* ws;         // partials, or nullptr: each sequence is walked by one CTA
   int* status;
+  uint64_t wait_limit_ns;
 };
 // Workspace bytes of a call on the current device (0: the call does not split).
 cudaError_t decode_workspace(const DecodeArgs& a, size_t* bytes);

@@ -144,7 +144,7 @@ __global__ void __launch_bounds__(kThreads) append_kernel(const __grid_constant_
       const float r = __fdiv_rn(1.0f, __fsqrt_rn(__fadd_rn(__fmul_rn(acc, kInvD), a.eps)));
 #pragma unroll
       for (int e = 0; e < 4; ++e) {
-        const float4 wv = __ldg(reinterpret_cast<const float4*>(w + (e < 2 ? g0 : g1) * 8 + (e & 1) * 4));
+        const float4 wv = *reinterpret_cast<const float4*>(w + (e < 2 ? g0 : g1) * 8 + (e & 1) * 4);
         n[2 * e] = pack_bf16(__fmul_rn(__fmul_rn(bf16lo(xw[2 * e]), r), wv.x),
                              __fmul_rn(__fmul_rn(bf16hi(xw[2 * e]), r), wv.y));
         n[2 * e + 1] = pack_bf16(__fmul_rn(__fmul_rn(bf16lo(xw[2 * e + 1]), r), wv.z),
@@ -169,7 +169,7 @@ __global__ void __launch_bounds__(kThreads) append_kernel(const __grid_constant_
             const int i = d < half ? d : d - half;
             const float na = __uint_as_float(static_cast<uint32_t>(buf[i]) << 16);
             const float nb = __uint_as_float(static_cast<uint32_t>(buf[i + half]) << 16);
-            const float c = __ldg(a.cos + at + i), s = __ldg(a.sin + at + i);
+            const float c = a.cos[at + i], s = a.sin[at + i];
             const float t = d < half ? __fmaf_rn(na, c, -__fmul_rn(nb, s)) : __fmaf_rn(nb, c, __fmul_rn(na, s));
             const uint32_t tb = pack_bf16(t, 0.0f) & 0xFFFFu;
             y[e >> 1] = (e & 1) ? ((y[e >> 1] & 0xFFFFu) | (tb << 16)) : ((y[e >> 1] & 0xFFFF0000u) | tb);
@@ -183,7 +183,7 @@ __global__ void __launch_bounds__(kThreads) append_kernel(const __grid_constant_
         for (int e = 0; e < 8; ++e) {  // pair of word e: channels 2 i and 2 i + 1
           const int i = static_cast<int>((e < 4 ? g0 : g1) * 4) + (e & 3);
           if (i < half) {
-            const float c = __ldg(a.cos + at + i), s = __ldg(a.sin + at + i);
+            const float c = a.cos[at + i], s = a.sin[at + i];
             const float na = bf16lo(n[e]), nb = bf16hi(n[e]);
             y[e] = pack_bf16(__fmaf_rn(na, c, -__fmul_rn(nb, s)), __fmaf_rn(nb, c, __fmul_rn(na, s)));
           }
@@ -192,8 +192,8 @@ __global__ void __launch_bounds__(kThreads) append_kernel(const __grid_constant_
     } else if (turn && rotating) {
 #pragma unroll
       for (int q = 0; q < 2; ++q) {
-        const float4 c = __ldg(reinterpret_cast<const float4*>(a.cos + at + lr * 8 + 4 * q));
-        const float4 s = __ldg(reinterpret_cast<const float4*>(a.sin + at + lr * 8 + 4 * q));
+        const float4 c = *reinterpret_cast<const float4*>(a.cos + at + lr * 8 + 4 * q);
+        const float4 s = *reinterpret_cast<const float4*>(a.sin + at + lr * 8 + 4 * q);
         const float cv[4] = {c.x, c.y, c.z, c.w}, sv[4] = {s.x, s.y, s.z, s.w};
 #pragma unroll
         for (int j = 0; j < 2; ++j) {

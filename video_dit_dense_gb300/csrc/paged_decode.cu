@@ -33,6 +33,7 @@
 // weight averages out over the keys and stays below the output's own
 // rounding), the sum of the weights is taken before that rounding.
 #include <cuda_bf16.h>
+#include <float.h>
 
 #include <algorithm>
 
@@ -42,6 +43,7 @@
 namespace h3 {
 namespace {
 
+constexpr float kSlack = 8.0f;  // in exponents of two: how far a maximum may grow before the sums are rescaled
 constexpr int kMaxSplitBatch = 512;  // sequences whose tile counts fit the CTA's shared memory
 
 __device__ __forceinline__ uint32_t fdiv(uint32_t n, const FastDiv& f) {
@@ -97,13 +99,13 @@ struct DecodeCfg {
   static constexpr int kTile = D == 64 ? 32 : 16;  // tokens a warp takes at a time: 8 KB of K and V at D 64 and 128
   static constexpr int kWarps = D == 256 ? 4 : 8;
   static constexpr int kStages = 3;
-  static constexpr int kTileBytes = kTile * D * 2;    // of K, and the same of V
+  static constexpr int kTileBytes = kTile * D * 2;  // of K, and the same of V
   static constexpr int kRing = kWarps * kStages * 2 * kTileBytes;
+  // joining the warps of a unit head: accumulators, max and sum of every second warp, 8 heads at a time
+  static constexpr int kJoin = kWarps / 2 * 8 * D * 4;
+  static constexpr int kStats = kWarps / 2 * 8 * 2 * 4;
+  static constexpr int kSmem = kRing + kJoin + kStats + kMaxSplitBatch * 4;
   static constexpr int kHeads = NT * 8;
-  // joining the warps of a unit head: accumulators, max and sum of every second warp
-  static constexpr int kJoin = kWarps / 2 * kHeads * D * 4;
-  static constexpr int kStats = kWarps / 2 * kHeads * 2 * 4;
-  static constexpr int kSmem = kRing + kJoin + kStats + kWarps * kStages * 4 + kMaxSplitBatch * 4 + 16;
   static_assert(kSmem <= 232448, "shared memory of one CTA");
 };
 
@@ -122,15 +124,11 @@ struct Kernelargs {
   DecodePlan p;
 };
 
-__device__ __forceinline__ int tiles_of(const DecodeArgs& a, int b, int tile) {
-  const int64_t capacity = static_cast<int64_t>(a.max_pages) * a.page_size;
-  const int n = static_cast<int>(min(static_cast<int64_t>(max(a.kv_len[b], 0)), capacity));
-  return (n + tile - 1) / tile;
-}
+// Tokens attended of sequence b.  From L2: the joining kernel looks before its own wait.
 __device__ __forceinline__ int len_of(const DecodeArgs& a, int b) {
-  const int64_t capacity = static_cast<int64_t>(a.max_pages) * a.page_size;
-  return static_cast<int>(min(static_cast<int64_t>(max(__ldg(a.kv_len + b), 0)), capacity));
+  return min(max(__ldcg(a.kv_len + b), 0), a.max_pages * a.page_size);
 }
+__device__ __forceinline__ int tiles_of(const DecodeArgs& a, int b, int tile) { return (len_of(a, b) + tile - 1) / tile; }
 // Ranges that T tiles are cut into.
 __device__ __forceinline__ int ranges_of(const DecodePlan& p, int T) {
   return max(1, min(p.ranges, (T + p.min_tiles - 1) / p.min_tiles));
@@ -141,23 +139,32 @@ __device__ __forceinline__ int range_begin(int r, int R, int T) {
 
 // end[b] = tiles of sequences 0 .. b, for all b < B, in shared memory.
 // Every thread of the block takes part; returns the total.
+template <int THREADS>
 __device__ __forceinline__ int scan_tiles(const DecodeArgs& a, int tile, int* end) {
+  __shared__ int warp_sum[THREADS / 32];
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  if (warp == 0) {
-    int carry = 0;
-    for (int b0 = 0; b0 < a.B; b0 += 32) {
-      int n = b0 + lane < a.B ? tiles_of(a, b0 + lane, tile) : 0;
+  int carry = 0;
+  for (int b0 = 0; b0 < a.B; b0 += THREADS) {
+    const int b = b0 + static_cast<int>(threadIdx.x);
+    int n = b < a.B ? tiles_of(a, b, tile) : 0;
 #pragma unroll
-      for (int off = 1; off < 32; off <<= 1) {
-        const int m = __shfl_up_sync(0xFFFFFFFFu, n, off);
-        if (lane >= off) n += m;
-      }
-      if (b0 + lane < a.B) end[b0 + lane] = carry + n;
-      carry += __shfl_sync(0xFFFFFFFFu, n, 31);
+    for (int off = 1; off < 32; off <<= 1) {
+      const int m = __shfl_up_sync(0xFFFFFFFFu, n, off);
+      if (lane >= off) n += m;
     }
+    if (b0 > 0) __syncthreads();  // the sums of the last turn are read
+    if (lane == 31) warp_sum[warp] = n;
+    __syncthreads();
+    int before = carry;
+#pragma unroll
+    for (int w = 0; w < THREADS / 32; ++w) {
+      if (w < warp) before += warp_sum[w];
+      carry += warp_sum[w];
+    }
+    if (b < a.B) end[b] = before + n;
   }
   __syncthreads();
-  return end[a.B - 1];
+  return carry;
 }
 // First sequence whose tiles end after tile t.
 __device__ __forceinline__ int sequence_at(const int* end, int B, int t) {
@@ -186,10 +193,10 @@ __global__ void __launch_bounds__(DecodeCfg<D, NT>::kWarps * 32, 1) decode_kerne
   extern __shared__ __align__(128) uint8_t smem[];
   float* join = reinterpret_cast<float*>(smem + C::kRing);
   float* stats = reinterpret_cast<float*>(smem + C::kRing + C::kJoin);
-  uint32_t* masks = reinterpret_cast<uint32_t*>(smem + C::kRing + C::kJoin + C::kStats);
-  int* end = reinterpret_cast<int*>(masks + C::kWarps * STAGES);
-  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+  int* end = reinterpret_cast<int*>(smem + C::kRing + C::kJoin + C::kStats);
+  // The joining kernel may start once every CTA is past its wait: it reads the lengths before its own.
   asm volatile("griddepcontrol.wait;" ::: "memory");
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
 
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int wh = warp % p.WH, wt = warp / p.WH;
@@ -203,7 +210,7 @@ __global__ void __launch_bounds__(DecodeCfg<D, NT>::kWarps * 32, 1) decode_kerne
   // This CTA's tiles [t0, t1) of all sequences' tiles.  Without a split the range is sequence r.
   int t0, t1, b0;
   if (p.ranges > 0) {
-    const int T = scan_tiles(a, TILE, end);
+    const int T = scan_tiles<C::kWarps * 32>(a, TILE, end);
     const int R = ranges_of(p, T);
     if (r >= R) return;
     t0 = range_begin(r, R, T);
@@ -231,63 +238,66 @@ __global__ void __launch_bounds__(DecodeCfg<D, NT>::kWarps * 32, 1) decode_kerne
       ++w.b;
       w.stop = min(t1, seq_end(w.b)) - seq_begin(w.b);
       w.tile = wt;
+      w.len = len_of(a, w.b);
     }
-    w.len = len_of(a, w.b);
   };
   Walk ld;
   ld.b = b0;
   ld.tile = t0 - seq_begin(b0) + wt;
   ld.stop = min(t1, seq_end(b0)) - seq_begin(b0);
+  ld.len = len_of(a, b0);
   enter(ld);
 
   const uint32_t ring = smem_u32(smem) + warp * (STAGES * 2 * C::kTileBytes);
-  uint32_t* mask_ring = masks + warp * STAGES;
   const int64_t row_stride = static_cast<int64_t>(a.Hkv) * D;
-  const uint16_t* kbase = a.k_pages + kvh * D;
-  const uint16_t* vbase = a.v_pages + kvh * D;
 
-  // Cache row of the lane's token of the tile to be loaded next, -1: none.
-  auto lookup = [&]() {
-    int row = -1;
+  // The lane's token of the tile to be loaded next: its page, asked for a turn ahead and looked at only when its rows
+  // are loaded, and its row in the page.  token_row < 0: no such token.
+  int page = -1, token_row = -1;
+  auto look_ahead = [&]() {
+    const int token = ld.tile * TILE + lane % TILE;
+    token_row = -1;
+    if (ld.b >= 0 && token < ld.len) {
+      const uint32_t pg = fdiv(static_cast<uint32_t>(token), a.div_page);
+      page = a.page_table[static_cast<int64_t>(ld.b) * a.max_pages + pg];
+      token_row = token - static_cast<int>(pg) * a.page_size;
+    }
+  };
+  look_ahead();
+  uint32_t mask_of[STAGES];  // tokens of each stage's tile that are attended
+  const uint16_t* kbase = a.k_pages + kvh * D + (lane % CH) * 8;
+  const uint16_t* vbase = a.v_pages + kvh * D + (lane % CH) * 8;
+  // Fills stage `at` with the next tile; rows that are not attended are zeros.
+  auto load = [&](int at, uint32_t& mask) {
     if (ld.b >= 0) {
-      const int token = ld.tile * TILE + (lane % TILE);
-      if (token < ld.len) {
-        const uint32_t pg = fdiv(static_cast<uint32_t>(token), a.div_page);
-        const int page = __ldg(a.page_table + static_cast<int64_t>(ld.b) * a.max_pages + pg);
+      int row = -1;  // of the whole cache
+      if (token_row >= 0) {
         if (page >= 0 && page < a.num_pages)
-          row = page * a.page_size + (token - static_cast<int>(pg) * a.page_size);
+          row = page * a.page_size + token_row;
         else
           atomicExch(a.status, static_cast<int>(H3ATTN_ERR_INVALID_ARG));  // its keys are not attended
       }
-    }
-    return row;
-  };
-  int row_next = lookup();
-  auto load = [&](int st) {
-    const int row = row_next;
-    const uint32_t ks = ring + st * 2 * C::kTileBytes, vs = ks + C::kTileBytes;
-    const uint32_t mask = __ballot_sync(0xFFFFFFFFu, row >= 0);
-    if (lane == 0) mask_ring[st] = mask;
-    if (ld.b >= 0) {
+      mask = __ballot_sync(0xFFFFFFFFu, row >= 0);
+      const uint32_t ks = ring + at * (2 * C::kTileBytes), vs = ks + C::kTileBytes;
 #pragma unroll
       for (int i = 0; i < TILE * CH / 32; ++i) {
-        const int c = i * 32 + lane, tr = c / CH, col = c % CH;
+        const int tr = (i * 32 + lane) / CH, col = lane % CH;
         const int src_row = __shfl_sync(0xFFFFFFFFu, row, tr);
-        const int64_t off = static_cast<int64_t>(max(src_row, 0)) * row_stride + col * 8;
+        const int64_t off = max(src_row, 0) * row_stride;
         const uint32_t dst = tr * (D * 2) + ((col ^ (tr & 7)) << 4);
         cp_async16(ks + dst, kbase + off, src_row >= 0);
         cp_async16(vs + dst, vbase + off, src_row >= 0);
       }
       ld.tile += p.WT;
       enter(ld);
-      row_next = lookup();
+      look_ahead();
     }
     cp_async_commit();
   };
 #pragma unroll
-  for (int st = 0; st < STAGES - 1; ++st) load(st);
+  for (int i = 0; i < STAGES - 1; ++i) load(i, mask_of[i]);
 
-  int st = 0, st_load = STAGES - 1;
+  int turn = 0;  // tiles used by this warp
   int b = b0;
   bool first_segment = true;
   const int g = lane >> 2, t = lane & 3;
@@ -302,30 +312,42 @@ __global__ void __launch_bounds__(DecodeCfg<D, NT>::kWarps * 32, 1) decode_kerne
         const uint16_t* qp = a.q + (static_cast<int64_t>(b) * a.Hq + head0 + (there ? n * 8 + g : 0)) * D + 2 * t;
 #pragma unroll
         for (int ks = 0; ks < D / 16; ++ks) {
-          qf[n][ks][0] = there ? __ldg(reinterpret_cast<const uint32_t*>(qp + ks * 16)) : 0u;
-          qf[n][ks][1] = there ? __ldg(reinterpret_cast<const uint32_t*>(qp + ks * 16 + 8)) : 0u;
+          qf[n][ks][0] = there ? *reinterpret_cast<const uint32_t*>(qp + ks * 16) : 0u;
+          qf[n][ks][1] = there ? *reinterpret_cast<const uint32_t*>(qp + ks * 16 + 8) : 0u;
         }
       }
       float o[NT][D / 16][4];
+      // m: what the exponents are taken against, within 8 of the running maximum; l: the lane's part of the sum
       float m[NT][2], l[NT][2];
 #pragma unroll
       for (int n = 0; n < NT; ++n) {
-        m[n][0] = m[n][1] = -INFINITY;
+        m[n][0] = m[n][1] = -FLT_MAX;
         l[n][0] = l[n][1] = 0.0f;
 #pragma unroll
         for (int dt = 0; dt < D / 16; ++dt) o[n][dt][0] = o[n][dt][1] = o[n][dt][2] = o[n][dt][3] = 0.0f;
       }
       for (int tile = s0 + wt; tile < s1; tile += p.WT) {
+        const int st = turn % STAGES;
         cp_async_wait<STAGES - 2>();
         __syncwarp();
+        const uint32_t mask = st == 0 ? mask_of[0] : st == 1 ? mask_of[1] : mask_of[2];
+        {
+          const int at = (turn + STAGES - 1) % STAGES;
+          uint32_t fresh = 0;
+          load(at, fresh);
+#pragma unroll
+          for (int i = 0; i < STAGES; ++i) mask_of[i] = i == at ? fresh : mask_of[i];
+        }
+        ++turn;
         const uint32_t ks_base = ring + st * 2 * C::kTileBytes, vs_base = ks_base + C::kTileBytes;
-        const uint32_t mask = mask_ring[st];
-        load(st_load);
-        float s[NT][MT][4];
+        // two accumulators a product: a chain of tensor-core products waits for each of its links
+        float s[NT][MT][4], s2[NT][MT][4];
 #pragma unroll
         for (int n = 0; n < NT; ++n)
 #pragma unroll
-          for (int mt = 0; mt < MT; ++mt) s[n][mt][0] = s[n][mt][1] = s[n][mt][2] = s[n][mt][3] = 0.0f;
+          for (int mt = 0; mt < MT; ++mt)
+#pragma unroll
+            for (int e = 0; e < 4; ++e) s[n][mt][e] = s2[n][mt][e] = 0.0f;
 #pragma unroll
         for (int ks = 0; ks < D / 16; ++ks) {
 #pragma unroll
@@ -334,64 +356,91 @@ __global__ void __launch_bounds__(DecodeCfg<D, NT>::kWarps * 32, 1) decode_kerne
             const int row = mt * 16 + (lane & 15), col = ks * 2 + (lane >> 4);
             ldmatrix4(kf, ks_base + row * (D * 2) + ((col ^ (row & 7)) << 4));
 #pragma unroll
-            for (int n = 0; n < NT; ++n) mma16816(s[n][mt], kf, qf[n][ks][0], qf[n][ks][1]);
+            for (int n = 0; n < NT; ++n) mma16816(ks & 1 ? s2[n][mt] : s[n][mt], kf, qf[n][ks][0], qf[n][ks][1]);
           }
         }
         // lane: tokens g and g + 8 of each 16, heads 2 t and 2 t + 1 of each 8
-        uint32_t pf[NT][MT][2];
+#pragma unroll
+        for (int n = 0; n < NT; ++n)
+#pragma unroll
+          for (int mt = 0; mt < MT; ++mt)
+#pragma unroll
+            for (int e = 0; e < 4; ++e) s[n][mt][e] += s2[n][mt][e];
+        constexpr uint32_t kAll = TILE == 32 ? 0xFFFFFFFFu : 0xFFFFu;
+        if ((mask & kAll) != kAll) {
+#pragma unroll
+          for (int n = 0; n < NT; ++n)
+#pragma unroll
+            for (int mt = 0; mt < MT; ++mt)
+#pragma unroll
+              for (int e = 0; e < 4; ++e)
+                if (!((mask >> (mt * 16 + g + (e < 2 ? 0 : 8))) & 1u)) s[n][mt][e] = -INFINITY;
+        }
+        uint32_t pf[NT][MT][2], pr[NT][MT][2];  // P and what its rounding left
 #pragma unroll
         for (int n = 0; n < NT; ++n) {
-          float top[2] = {m[n][0], m[n][1]};
+          float top[2] = {-INFINITY, -INFINITY};
 #pragma unroll
-          for (int mt = 0; mt < MT; ++mt) {
-            const bool in0 = (mask >> (mt * 16 + g)) & 1u, in1 = (mask >> (mt * 16 + g + 8)) & 1u;
+          for (int mt = 0; mt < MT; ++mt)
 #pragma unroll
-            for (int e = 0; e < 4; ++e) {
-              s[n][mt][e] = ((e < 2) ? in0 : in1) ? s[n][mt][e] * a.scale_log2 : -INFINITY;
-              top[e & 1] = fmaxf(top[e & 1], s[n][mt][e]);
-            }
-          }
-          float base[2];
+            for (int e = 0; e < 4; ++e) top[e & 1] = fmaxf(top[e & 1], s[n][mt][e]);
+          const bool over = top[0] * a.scale_log2 > m[n][0] + kSlack || top[1] * a.scale_log2 > m[n][1] + kSlack;
+          if (__any_sync(0xFFFFFFFFu, over)) {
 #pragma unroll
-          for (int c = 0; c < 2; ++c) {
-            top[c] = fmaxf(top[c], __shfl_xor_sync(0xFFFFFFFFu, top[c], 4));
-            top[c] = fmaxf(top[c], __shfl_xor_sync(0xFFFFFFFFu, top[c], 8));
-            top[c] = fmaxf(top[c], __shfl_xor_sync(0xFFFFFFFFu, top[c], 16));
-            base[c] = top[c] == -INFINITY ? 0.0f : top[c];  // nothing attended yet
-            const float fix = ex2(m[n][c] - base[c]);
-            m[n][c] = top[c];
-            l[n][c] *= fix;
+            for (int c = 0; c < 2; ++c) {
+              top[c] = fmaxf(top[c], __shfl_xor_sync(0xFFFFFFFFu, top[c], 4));
+              top[c] = fmaxf(top[c], __shfl_xor_sync(0xFFFFFFFFu, top[c], 8));
+              top[c] = fmaxf(top[c], __shfl_xor_sync(0xFFFFFFFFu, top[c], 16));
+              const float to = fmaxf(m[n][c], top[c] * a.scale_log2);
+              const float fix = ex2(m[n][c] - to);
+              m[n][c] = to;
+              l[n][c] *= fix;
 #pragma unroll
-            for (int dt = 0; dt < D / 16; ++dt) {
-              o[n][dt][c] *= fix;
-              o[n][dt][c + 2] *= fix;
+              for (int dt = 0; dt < D / 16; ++dt) {
+                o[n][dt][c] *= fix;
+                o[n][dt][c + 2] *= fix;
+              }
             }
           }
 #pragma unroll
           for (int mt = 0; mt < MT; ++mt) {
 #pragma unroll
             for (int e = 0; e < 4; ++e) {
-              s[n][mt][e] = ex2(s[n][mt][e] - base[e & 1]);
+              s[n][mt][e] = ex2(fmaf(s[n][mt][e], a.scale_log2, -m[n][e & 1]));
               l[n][e & 1] += s[n][mt][e];
             }
-            pf[n][mt][0] = transpose8x8(pack_bf16(s[n][mt][0], s[n][mt][1]));
-            pf[n][mt][1] = transpose8x8(pack_bf16(s[n][mt][2], s[n][mt][3]));
+#pragma unroll
+            for (int half = 0; half < 2; ++half) {
+              const float p0 = s[n][mt][2 * half], p1 = s[n][mt][2 * half + 1];
+              const uint32_t hi = pack_bf16(p0, p1);
+              pf[n][mt][half] = transpose8x8(hi);
+              pr[n][mt][half] =
+                  transpose8x8(pack_bf16(p0 - __uint_as_float(hi << 16), p1 - __uint_as_float(hi & 0xFFFF0000u)));
+            }
           }
         }
+        constexpr int DB = 4;  // channel tiles whose products are interleaved
 #pragma unroll
         for (int mt = 0; mt < MT; ++mt) {
 #pragma unroll
-          for (int dt = 0; dt < D / 16; ++dt) {
-            uint32_t vf[4];
-            const int row = mt * 16 + (lane >> 4) * 8 + (lane & 7), col = dt * 2 + ((lane >> 3) & 1);
-            ldmatrix4_trans(vf, vs_base + row * (D * 2) + ((col ^ (row & 7)) << 4));
+          for (int d0 = 0; d0 < D / 16; d0 += DB) {
+            uint32_t vf[DB][4];
 #pragma unroll
-            for (int n = 0; n < NT; ++n) mma16816(o[n][dt], vf, pf[n][mt][0], pf[n][mt][1]);
+            for (int i = 0; i < DB; ++i) {
+              const int row = mt * 16 + (lane >> 4) * 8 + (lane & 7), col = (d0 + i) * 2 + ((lane >> 3) & 1);
+              ldmatrix4_trans(vf[i], vs_base + row * (D * 2) + ((col ^ (row & 7)) << 4));
+            }
+#pragma unroll
+            for (int n = 0; n < NT; ++n)
+#pragma unroll
+              for (int i = 0; i < DB; ++i) mma16816(o[n][d0 + i], vf[i], pf[n][mt][0], pf[n][mt][1]);
+#pragma unroll
+            for (int n = 0; n < NT; ++n)
+#pragma unroll
+              for (int i = 0; i < DB; ++i) mma16816(o[n][d0 + i], vf[i], pr[n][mt][0], pr[n][mt][1]);
           }
         }
         __syncwarp();  // the stage is read; the next turn's load may fill it
-        st = st + 1 == STAGES ? 0 : st + 1;
-        st_load = st_load + 1 == STAGES ? 0 : st_load + 1;
       }
 #pragma unroll
       for (int n = 0; n < NT; ++n)
@@ -403,45 +452,40 @@ __global__ void __launch_bounds__(DecodeCfg<D, NT>::kWarps * 32, 1) decode_kerne
         }
       // ---- the warps of a unit head are joined, halving their number ----
       for (int step = p.WT >> 1; step >= 1; step >>= 1) {
-        __syncthreads();  // the buffers are free
-        if (wt >= step && wt < 2 * step) {
-          const int at = (wt - step) * p.WH + wh;
-          float4* dst = reinterpret_cast<float4*>(join + at * (C::kHeads * D));
 #pragma unroll
-          for (int n = 0; n < NT; ++n)
+        for (int n = 0; n < NT; ++n) {
+          __syncthreads();  // the buffers are free
+          if (wt >= step && wt < 2 * step) {
+            const int at = (wt - step) * p.WH + wh;
+            float4* dst = reinterpret_cast<float4*>(join + at * (8 * D));
 #pragma unroll
             for (int dt = 0; dt < D / 16; ++dt)
-              dst[(n * (D / 16) + dt) * 32 + lane] = make_float4(o[n][dt][0], o[n][dt][1], o[n][dt][2], o[n][dt][3]);
-          if (lane < 4) {
-#pragma unroll
-            for (int n = 0; n < NT; ++n)
+              dst[dt * 32 + lane] = make_float4(o[n][dt][0], o[n][dt][1], o[n][dt][2], o[n][dt][3]);
+            if (lane < 4) {
 #pragma unroll
               for (int c = 0; c < 2; ++c) {
-                stats[(at * C::kHeads + n * 8 + 2 * t + c) * 2] = m[n][c];
-                stats[(at * C::kHeads + n * 8 + 2 * t + c) * 2 + 1] = l[n][c];
+                stats[(at * 8 + 2 * t + c) * 2] = m[n][c];
+                stats[(at * 8 + 2 * t + c) * 2 + 1] = l[n][c];
               }
+            }
           }
-        }
-        __syncthreads();
-        if (wt < step) {
-          const int at = wt * p.WH + wh;
-          const float4* src = reinterpret_cast<const float4*>(join + at * (C::kHeads * D));
-#pragma unroll
-          for (int n = 0; n < NT; ++n) {
+          __syncthreads();
+          if (wt < step) {
+            const int at = wt * p.WH + wh;
+            const float4* src = reinterpret_cast<const float4*>(join + at * (8 * D));
             float mine[2], theirs[2];
 #pragma unroll
             for (int c = 0; c < 2; ++c) {
-              const float mo = stats[(at * C::kHeads + n * 8 + 2 * t + c) * 2];
-              const float lo = stats[(at * C::kHeads + n * 8 + 2 * t + c) * 2 + 1];
-              const float top = fmaxf(m[n][c], mo), base = top == -INFINITY ? 0.0f : top;
-              mine[c] = ex2(m[n][c] - base);
-              theirs[c] = ex2(mo - base);
-              m[n][c] = top;
+              const float mo = stats[(at * 8 + 2 * t + c) * 2], lo = stats[(at * 8 + 2 * t + c) * 2 + 1];
+              const float to = fmaxf(m[n][c], mo);
+              mine[c] = ex2(m[n][c] - to);
+              theirs[c] = ex2(mo - to);
+              m[n][c] = to;
               l[n][c] = l[n][c] * mine[c] + lo * theirs[c];
             }
 #pragma unroll
             for (int dt = 0; dt < D / 16; ++dt) {
-              const float4 v = src[(n * (D / 16) + dt) * 32 + lane];
+              const float4 v = src[dt * 32 + lane];
               o[n][dt][0] = o[n][dt][0] * mine[0] + v.x * theirs[0];
               o[n][dt][1] = o[n][dt][1] * mine[1] + v.y * theirs[1];
               o[n][dt][2] = o[n][dt][2] * mine[0] + v.z * theirs[0];
@@ -515,14 +559,16 @@ __global__ void __launch_bounds__(kCombineThreads) decode_join_kernel(const __gr
   __shared__ int end[kMaxSplitBatch];
   __shared__ float4 sum[ROWS][LANES];
   __shared__ float2 ml[ROWS];
-  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
-  asm volatile("griddepcontrol.wait;" ::: "memory");
+  // The decode kernel lets this one start after its own wait, so the lengths
+  // are final: only its partials, and the output rows, have to be waited for.
   const int b = blockIdx.x / a.Hq, h = blockIdx.x - b * a.Hq;
-  const int T = scan_tiles(a, tile, end);
+  const int T = scan_tiles<kCombineThreads>(a, tile, end);
   const int R = ranges_of(p, T);
   const int begin = b > 0 ? end[b - 1] : 0, stop = end[b];
   uint16_t* out = a.o + (static_cast<int64_t>(b) * a.Hq + h) * D;
   const int lane = threadIdx.x % LANES, row = threadIdx.x / LANES;
+  asm volatile("griddepcontrol.wait;" ::: "memory");
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
   if (begin == stop) {
     if (row == 0) *reinterpret_cast<uint2*>(out + 4 * lane) = make_uint2(0u, 0u);
     return;
@@ -534,15 +580,15 @@ __global__ void __launch_bounds__(kCombineThreads) decode_join_kernel(const __gr
   if (r0 == r1) return;
   const int G = a.Hq / a.Hkv, kvh = h / G, in_group = h - kvh * G, qt = in_group / 16;
   const int unit = kvh * p.q_tiles + qt, hh = in_group - qt * 16;
-  float m = -INFINITY, l = 0.0f;
+  float m = -FLT_MAX, l = 0.0f;
   float4 o = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
   for (int r = r0 + row; r <= r1; r += ROWS) {
     const int which = range_begin(r, R, T) >= begin ? 0 : 1;  // slot 0 where the range begins in this sequence
     const float* part = a.ws + ((static_cast<int64_t>(r) * 2 + which) * p.unit_heads + unit) * partial_floats(tile_heads, D);
     const float mr = part[2 * hh], lr = part[2 * hh + 1];
     const float4 v = *reinterpret_cast<const float4*>(part + partial_o(tile_heads) + hh * D + 4 * lane);
-    const float top = fmaxf(m, mr), base = top == -INFINITY ? 0.0f : top;
-    const float mine = ex2(m - base), theirs = ex2(mr - base);
+    const float top = fmaxf(m, mr);
+    const float mine = ex2(m - top), theirs = ex2(mr - top);
     m = top;
     l = l * mine + lr * theirs;
     o.x = o.x * mine + v.x * theirs;
@@ -554,15 +600,14 @@ __global__ void __launch_bounds__(kCombineThreads) decode_join_kernel(const __gr
   if (lane == 0) ml[row] = make_float2(m, l);
   __syncthreads();
   if (row != 0) return;
-  float top = -INFINITY;
+  float top = -FLT_MAX;
 #pragma unroll
   for (int i = 0; i < ROWS; ++i) top = fmaxf(top, ml[i].x);
-  const float base = top == -INFINITY ? 0.0f : top;
   float total = 0.0f;
   o = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
 #pragma unroll
   for (int i = 0; i < ROWS; ++i) {
-    const float w = ex2(ml[i].x - base);
+    const float w = ex2(ml[i].x - top);
     const float4 v = sum[i][lane];
     total += ml[i].y * w;
     o.x += v.x * w;

@@ -44,7 +44,7 @@ __global__ void __launch_bounds__(kThreads) rope_table_kernel(const __grid_const
   for (int e = 0; e < VEC; ++e) turn[e] = a.turn[col * VEC + e];
   const int64_t step = static_cast<int64_t>(gridDim.x) * rows;
   for (int64_t n = static_cast<int64_t>(blockIdx.x) * rows + lane_row; n < a.N; n += step) {
-    const int64_t p = a.pos ? static_cast<int64_t>(__ldg(a.pos + n)) : a.first + n;
+    const int64_t p = a.pos ? static_cast<int64_t>(a.pos[n]) : a.first + n;
     float c[VEC], s[VEC];
 #pragma unroll
     for (int e = 0; e < VEC; ++e) {
