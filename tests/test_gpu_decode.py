@@ -60,14 +60,15 @@ def check(h3, c, what=""):
 @pytest.mark.parametrize("D", [64, 128, 256])
 @pytest.mark.parametrize("Hq,Hkv", [(1, 1), (4, 4), (16, 4), (8, 1), (9, 1), (16, 1), (17, 1), (40, 2), (24, 24), (6, 3), (14, 2)])
 def test_heads_and_head_dims(h3, Hq, Hkv, D):
-    check(h3, Case([150, 0, 33, 1], Hq, Hkv, D, 16, seed=D + Hq))
+    check(h3, Case([150, 0, 33, 1], Hq, Hkv, D, 16, capacity=1040, seed=D + Hq))
 
 
 @pytest.mark.gpu
 @pytest.mark.parametrize("page", [1, 3, 16, 24, 64, 1000])
 @pytest.mark.parametrize("D", [64, 128, 256])
 def test_lengths_around_tiles_and_pages(h3, page, D):
-    check(h3, Case([0, 1, 2, 15, 16, 17, 31, 32, 33, 47, 48, 63, 64, 65, 127, 128, 129, 255, 257, 500], 4, 2, D, page, seed=page))
+    check(h3, Case([0, 1, 2, 15, 16, 17, 31, 32, 33, 47, 48, 63, 64, 65, 127, 128, 129, 255, 257, 500], 4, 2, D, page, capacity=1100,
+                   seed=page))
 
 
 @pytest.mark.gpu
@@ -84,7 +85,7 @@ def test_unlike_lengths(h3):
 
 @pytest.mark.gpu
 def test_all_empty(h3):
-    c = Case([0, 0, 0], 4, 2, 128, 16, capacity=40).cuda(h3)
+    c = Case([0, 0, 0], 4, 2, 128, 16, capacity=4000).cuda(h3)
     for split in (True, False):
         assert bool((c.run(h3, split) == 0).all())
 
@@ -108,15 +109,27 @@ def test_peaky_and_flat_softmax(h3, peak, scale):
 def test_many_sequences(h3, B):
     """Up to 512 sequences are split over the GPU, more are walked one a CTA."""
     lens = [(37 * b) % 90 for b in range(B)]
-    c = Case(lens, 4, 2, 64, 16, seed=B).cuda(h3)
+    c = Case(lens, 4, 2, 64, 16, capacity=520, seed=B).cuda(h3)
     assert (h3.paged_decode_workspace(c.dq, c.cache) is None) == (B > 512)
     check(h3, c)
 
 
 @pytest.mark.gpu
+def test_short_caches_take_no_workspace(h3):
+    """A cache without room for more than four tiles a warp is walked whole, with and without a workspace."""
+    for capacity, splits in ((128, False), (144, True)):
+        c = Case([100, 128, 1], 4, 4, 128, 16, capacity=capacity, seed=capacity).cuda(h3)
+        assert (h3.h3attn_paged_decode_workspace_size(c.cache, 4) > 0) == splits
+        o = torch.empty_like(c.dq)
+        h3.h3attn_paged_decode(c.dq, o, c.cache, workspace=torch.empty(1 << 20, dtype=torch.uint8, device="cuda"))
+        torch.cuda.synchronize()
+        close(o, *c.reference())
+
+
+@pytest.mark.gpu
 @pytest.mark.parametrize("D", [64, 128])
 def test_bad_pages_are_not_attended(h3, D):
-    c = Case([100, 40, 64], 4, 2, D, 16, seed=9)
+    c = Case([100, 40, 64], 4, 2, D, 16, capacity=600, seed=9)
     c.table[0, 2] = -1
     c.table[0, 6] = c.k.shape[0]
     c.table[1, 0] = c.table[1, 1] = c.table[1, 2] = 2 ** 31 - 1   # nothing is left of this one
@@ -132,7 +145,7 @@ def test_bad_pages_are_not_attended(h3, D):
 
 @pytest.mark.gpu
 def test_nan_in_an_attended_row_stays_in_its_sequence(h3):
-    c = Case([50, 60], 4, 2, 128, 16, seed=2)
+    c = Case([50, 60], 4, 2, 128, 16, capacity=400, seed=2)
     c.k[c.table[0, 1].long(), 3, 0, 5] = float("nan")
     c.cuda(h3)
     o = c.run(h3).float()
@@ -151,7 +164,7 @@ def test_repeatable(h3):
 @pytest.mark.gpu
 def test_shared_pages(h3):
     """Two sequences with a common prefix."""
-    c = Case([64, 80], 4, 2, 128, 16, poison=False, seed=6)
+    c = Case([64, 80], 4, 2, 128, 16, capacity=400, poison=False, seed=6)
     c.table[1, :4] = c.table[0, :4]
     check(h3, c)
 
@@ -216,3 +229,32 @@ def test_pages_past_32_bits(h3):
     h3.h3attn_paged_decode(dq, o, cache, workspace=h3.paged_decode_workspace(dq, cache))
     torch.cuda.synchronize()
     close(o, *c.reference())
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("n,rest", [(17 * 32, 40), (33 * 32, 2000), (200 * 32, 0), (16 * 32, 600), (2432 * 4, 31)])
+def test_sequences_that_end_where_another_begins(h3, n, rest):
+    """One unit head, so as many ranges as there are SMs: sequences over more and fewer of them than are joined at a
+    time, whose last range another sequence begins in."""
+    check(h3, Case([n, rest, 1, n // 2, 7, rest, n], 4, 1, 128, 16, seed=n))
+
+
+@pytest.mark.gpu
+def test_workspaces_that_hold_anything(h3):
+    """Zeros, ones, small numbers, what another geometry's call left, and its own call's: each gives the same output."""
+    c = Case([3000, 5, 2100], 8, 2, 128, 16, seed=30).cuda(h3)
+    other = Case([900, 4000], 4, 4, 64, 24, seed=31).cuda(h3)
+    need = max(h3.h3attn_paged_decode_workspace_size(x.cache, x.q.shape[1]) for x in (c, other))
+    ws = torch.zeros(need, dtype=torch.uint8, device="cuda")
+    want = c.run(h3)
+    o, o2 = torch.empty_like(c.dq), torch.empty_like(other.dq)
+    for fill in (0, 1, 255, None, "small", "self"):
+        if fill == "small":
+            ws[:need // 8 * 8].view(torch.int64).copy_(torch.arange(need // 8))
+        elif fill is None:
+            h3.h3attn_paged_decode(other.dq, o2, other.cache, workspace=ws)
+        elif fill != "self":
+            ws.fill_(fill)
+        o.fill_(float("nan"))
+        h3.h3attn_paged_decode(c.dq, o, c.cache, workspace=ws)
+        assert torch.equal(o, want), fill

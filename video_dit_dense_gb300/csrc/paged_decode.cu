@@ -20,7 +20,7 @@
 // takes WH neighbouring unit heads, so that its warps read one contiguous
 // stretch of the pages, and its other factor WT = warps / WH splits the
 // tokens.  All sequences' tiles of TILE tokens are numbered through; range r
-// of R takes tiles [r T / R, (r + 1) T / R), so CTAs differ by one tile
+// of R takes T / R of them, so CTAs differ by one tile
 // however unlike the lengths are.  A range that holds all of a sequence
 // writes its output; of a sequence that ranges share, each range writes its
 // unnormalised O, its running max and sum to the workspace, and a second
@@ -79,6 +79,7 @@ __device__ __forceinline__ void ldmatrix4_trans(uint32_t (&r)[4], uint32_t addr)
                : "r"(addr)
                : "memory");
 }
+__device__ __forceinline__ void prefetch_l2(const void* p) { asm volatile("prefetch.global.L2 [%0];" ::"l"(p)); }
 // The transpose of an 8x8 block of 16-bit values held as an accumulator fragment.
 __device__ __forceinline__ uint32_t transpose8x8(uint32_t v) {
   uint32_t d;
@@ -104,7 +105,7 @@ struct DecodeCfg {
   // joining the warps of a unit head: accumulators, max and sum of every second warp, 8 heads at a time
   static constexpr int kJoin = kWarps / 2 * 8 * D * 4;
   static constexpr int kStats = kWarps / 2 * 8 * 2 * 4;
-  static constexpr int kSmem = kRing + kJoin + kStats + kMaxSplitBatch * 4;
+  static constexpr int kSmem = kRing + kJoin + kStats + 2 * kMaxSplitBatch * 4;
   static constexpr int kHeads = NT * 8;
   static_assert(kSmem <= 232448, "shared memory of one CTA");
 };
@@ -128,43 +129,61 @@ struct Kernelargs {
 __device__ __forceinline__ int len_of(const DecodeArgs& a, int b) {
   return min(max(__ldcg(a.kv_len + b), 0), a.max_pages * a.page_size);
 }
-__device__ __forceinline__ int tiles_of(const DecodeArgs& a, int b, int tile) { return (len_of(a, b) + tile - 1) / tile; }
-// Ranges that T tiles are cut into.
-__device__ __forceinline__ int ranges_of(const DecodePlan& p, int T) {
-  return max(1, min(p.ranges, (T + p.min_tiles - 1) / p.min_tiles));
-}
-__device__ __forceinline__ int range_begin(int r, int R, int T) {
-  return static_cast<int>(static_cast<int64_t>(r) * T / R);
+// T tiles cut into `count` ranges of `each` tiles, the first `longer` of them one longer.
+struct Ranges {
+  int count, each, longer;
+  __device__ __forceinline__ int begin(int r) const { return r * each + min(r, longer); }
+  __device__ __forceinline__ int of(int tile) const {
+    const int in_longer = longer * (each + 1);
+    return tile < in_longer ? tile / (each + 1) : longer + (tile - in_longer) / each;
+  }
+};
+// Ranges of at least min_tiles, but no fewer than there are sequences: a CTA
+// that walks several short ones joins its warps once for each.
+__device__ __forceinline__ Ranges cut(const DecodePlan& p, int T, int sequences) {
+  Ranges c;
+  c.count = max(1, min(p.ranges, max((T + p.min_tiles - 1) / p.min_tiles, sequences)));
+  c.each = T / c.count;
+  c.longer = T - c.each * c.count;
+  return c;
 }
 
-// end[b] = tiles of sequences 0 .. b, for all b < B, in shared memory.
-// Every thread of the block takes part; returns the total.
+// end[b] = tiles of sequences 0 .. b and len[b] (unless null) their tokens, for
+// all b < B, in shared memory.  Every thread of the block takes part; returns
+// the ranges that the tiles are cut into.
 template <int THREADS>
-__device__ __forceinline__ int scan_tiles(const DecodeArgs& a, int tile, int* end) {
-  __shared__ int warp_sum[THREADS / 32];
+__device__ __forceinline__ Ranges scan_tiles(const DecodeArgs& a, const DecodePlan& p, int tile, int* end, int* len) {
+  __shared__ int2 warp_sum[THREADS / 32];  // tiles, sequences with a tile
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  int carry = 0;
+  int carry = 0, sequences = 0;
   for (int b0 = 0; b0 < a.B; b0 += THREADS) {
     const int b = b0 + static_cast<int>(threadIdx.x);
-    int n = b < a.B ? tiles_of(a, b, tile) : 0;
+    const int tokens = b < a.B ? len_of(a, b) : 0;
+    int n = (tokens + tile - 1) / tile;
+    const int there = __popc(__ballot_sync(0xFFFFFFFFu, n > 0));
 #pragma unroll
     for (int off = 1; off < 32; off <<= 1) {
       const int m = __shfl_up_sync(0xFFFFFFFFu, n, off);
       if (lane >= off) n += m;
     }
     if (b0 > 0) __syncthreads();  // the sums of the last turn are read
-    if (lane == 31) warp_sum[warp] = n;
+    if (lane == 31) warp_sum[warp] = make_int2(n, there);
     __syncthreads();
     int before = carry;
 #pragma unroll
     for (int w = 0; w < THREADS / 32; ++w) {
-      if (w < warp) before += warp_sum[w];
-      carry += warp_sum[w];
+      const int2 of_warp = warp_sum[w];
+      if (w < warp) before += of_warp.x;
+      carry += of_warp.x;
+      sequences += of_warp.y;
     }
-    if (b < a.B) end[b] = before + n;
+    if (b < a.B) {
+      end[b] = before + n;
+      if (len) len[b] = tokens;
+    }
   }
   __syncthreads();
-  return carry;
+  return cut(p, carry, sequences);
 }
 // First sequence whose tiles end after tile t.
 __device__ __forceinline__ int sequence_at(const int* end, int B, int t) {
@@ -194,6 +213,15 @@ __global__ void __launch_bounds__(DecodeCfg<D, NT>::kWarps * 32, 1) decode_kerne
   float* join = reinterpret_cast<float*>(smem + C::kRing);
   float* stats = reinterpret_cast<float*>(smem + C::kRing + C::kJoin);
   int* end = reinterpret_cast<int*>(smem + C::kRing + C::kJoin + C::kStats);
+  int* lens = end + kMaxSplitBatch;  // without a split: of the one sequence
+  // The lengths and the page table are the first two links of the chain to the first K and V row, and the last
+  // step's cache has pushed them out of L2: they are brought back while the kernel before this one drains.  (L2 is
+  // where all SMs' writes meet, so what that kernel still writes is not missed.)
+  if (threadIdx.x * 32 < static_cast<unsigned>(a.B)) prefetch_l2(a.kv_len + threadIdx.x * 32);
+  {
+    const int64_t line = (static_cast<int64_t>(blockIdx.x) * (C::kWarps * 32) + threadIdx.x) * 32;
+    if (line < static_cast<int64_t>(a.B) * a.max_pages) prefetch_l2(a.page_table + line);
+  }
   // The joining kernel may start once every CTA is past its wait: it reads the lengths before its own.
   asm volatile("griddepcontrol.wait;" ::: "memory");
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
@@ -210,20 +238,22 @@ __global__ void __launch_bounds__(DecodeCfg<D, NT>::kWarps * 32, 1) decode_kerne
   // This CTA's tiles [t0, t1) of all sequences' tiles.  Without a split the range is sequence r.
   int t0, t1, b0;
   if (p.ranges > 0) {
-    const int T = scan_tiles<C::kWarps * 32>(a, TILE, end);
-    const int R = ranges_of(p, T);
-    if (r >= R) return;
-    t0 = range_begin(r, R, T);
-    t1 = range_begin(r + 1, R, T);
+    const Ranges ranges = scan_tiles<C::kWarps * 32>(a, p, TILE, end, lens);
+    if (r >= ranges.count) return;
+    t0 = ranges.begin(r);
+    t1 = ranges.begin(r + 1);
     if (t0 >= t1) return;
     b0 = sequence_at(end, a.B, t0);
   } else {
     t0 = 0;
-    t1 = tiles_of(a, r, TILE);
     b0 = r;
+    if (threadIdx.x == 0) lens[0] = len_of(a, r);
+    __syncthreads();
+    t1 = (lens[0] + TILE - 1) / TILE;
   }
   auto seq_begin = [&](int b) { return p.ranges > 0 && b > 0 ? end[b - 1] : 0; };
   auto seq_end = [&](int b) { return p.ranges > 0 ? end[b] : t1; };
+  auto seq_len = [&](int b) { return lens[p.ranges > 0 ? b : 0]; };
 
   // The tiles that this warp loads, in the order it uses them, over sequence borders.
   struct Walk {
@@ -238,14 +268,14 @@ __global__ void __launch_bounds__(DecodeCfg<D, NT>::kWarps * 32, 1) decode_kerne
       ++w.b;
       w.stop = min(t1, seq_end(w.b)) - seq_begin(w.b);
       w.tile = wt;
-      w.len = len_of(a, w.b);
+      w.len = seq_len(w.b);
     }
   };
   Walk ld;
   ld.b = b0;
   ld.tile = t0 - seq_begin(b0) + wt;
   ld.stop = min(t1, seq_end(b0)) - seq_begin(b0);
-  ld.len = len_of(a, b0);
+  ld.len = seq_len(b0);
   enter(ld);
 
   const uint32_t ring = smem_u32(smem) + warp * (STAGES * 2 * C::kTileBytes);
@@ -545,78 +575,158 @@ __global__ void __launch_bounds__(DecodeCfg<D, NT>::kWarps * 32, 1) decode_kerne
   cp_async_wait<0>();
 }
 
-constexpr int kCombineThreads = 256;
+constexpr int kJoinThreads = 256;
+constexpr int kMaxRanges = kJoinThreads;  // a thread looks at a range, 8 bits number it
+constexpr int kFewParts = 4;  // partials that a warp asks for at a time: a head in no more of them takes one warp
 
-// One CTA joins the partials of one sequence and query head, in the order of
-// the ranges.  Sequences that one range held whole are written already;
-// sequences without a key get zeros here.
+// Joins the partials of the sequences that several ranges hold, each in the
+// order of its ranges.  Which sequences those are follows from the lengths, as
+// in the decode kernel, and is worked out while that one runs: it lets this
+// one start after its own wait, so the lengths are final, and only the partials
+// have to be waited for.  Sequences that one range held are written already;
+// sequences without a key get their zeros here.  One CTA an SM, small enough to
+// sit beside a decode CTA.
 template <int D>
-__global__ void __launch_bounds__(kCombineThreads) decode_join_kernel(const __grid_constant__ Kernelargs k, int tile,
-                                                                      int tile_heads) {
-  constexpr int LANES = D / 4, ROWS = kCombineThreads / LANES;  // threads on a partial's O, partials at a time
+__global__ void __launch_bounds__(kJoinThreads) __maxnreg__(D == 256 ? 64 : 56) decode_join_kernel(const __grid_constant__ Kernelargs k, int tile,
+                                                                   int tile_heads) {
+  constexpr int VEC = D / 32, WARPS = kJoinThreads / 32;
   const DecodeArgs& a = k.a;
   const DecodePlan& p = k.p;
   __shared__ int end[kMaxSplitBatch];
-  __shared__ float4 sum[ROWS][LANES];
-  __shared__ float2 ml[ROWS];
-  // The decode kernel lets this one start after its own wait, so the lengths
-  // are final: only its partials, and the output rows, have to be waited for.
-  const int b = blockIdx.x / a.Hq, h = blockIdx.x - b * a.Hq;
-  const int T = scan_tiles<kCombineThreads>(a, tile, end);
-  const int R = ranges_of(p, T);
-  const int begin = b > 0 ? end[b - 1] : 0, stop = end[b];
-  uint16_t* out = a.o + (static_cast<int64_t>(b) * a.Hq + h) * D;
-  const int lane = threadIdx.x % LANES, row = threadIdx.x / LANES;
+  __shared__ uint32_t split[2][kMaxRanges];  // sequence << 16 | first range << 8 | last: of many ranges, of a few
+  __shared__ int in_warp[2][WARPS];
+  __shared__ float part_o[WARPS][D];
+  __shared__ float2 part_ml[WARPS];
+  const Ranges ranges = scan_tiles<kJoinThreads>(a, p, tile, end, nullptr);
+  // The ranges cut a sequence in the middle where one begins inside it: the
+  // first such range speaks for it.  The lists are in the order of the ranges,
+  // so that every CTA has the same ones.
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  uint32_t mine = 0;
+  int kind = -1;
+  if (const int r = threadIdx.x; r > 0 && r < ranges.count) {
+    const int t = ranges.begin(r), b = sequence_at(end, a.B, t), begin = b > 0 ? end[b - 1] : 0;
+    if (begin < t && ranges.begin(r - 1) <= begin) {
+      const int last = ranges.of(end[b] - 1);
+      kind = last - r + 2 > kFewParts ? 0 : 1;
+      mine = static_cast<uint32_t>(b) << 16 | static_cast<uint32_t>(r - 1) << 8 | static_cast<uint32_t>(last);
+    }
+  }
+  const uint32_t same[2] = {__ballot_sync(0xFFFFFFFFu, kind == 0), __ballot_sync(0xFFFFFFFFu, kind == 1)};
+  if (lane < 2) in_warp[lane][warp] = __popc(same[lane]);
+  __syncthreads();
+  int n_split[2] = {0, 0}, at = 0;
+#pragma unroll
+  for (int i = 0; i < 2; ++i) {
+#pragma unroll
+    for (int w = 0; w < WARPS; ++w) {
+      if (i == kind && w < warp) at += in_warp[i][w];
+      n_split[i] += in_warp[i][w];
+    }
+  }
+  if (kind >= 0) split[kind][at + __popc(same[kind] & ((1u << lane) - 1u))] = mine;
+  __syncthreads();
   asm volatile("griddepcontrol.wait;" ::: "memory");
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
-  if (begin == stop) {
-    if (row == 0) *reinterpret_cast<uint2*>(out + 4 * lane) = make_uint2(0u, 0u);
-    return;
+
+  for (int b = blockIdx.x; b < a.B; b += gridDim.x) {
+    if (end[b] == (b > 0 ? end[b - 1] : 0)) {
+      uint2* row = reinterpret_cast<uint2*>(a.o + static_cast<int64_t>(b) * a.Hq * D);
+      for (int i = threadIdx.x; i < a.Hq * (D / 4); i += kJoinThreads) row[i] = make_uint2(0u, 0u);
+    }
   }
-  // the ranges that hold tiles begin and stop - 1: range r begins at floor(r T / R)
-  int r0 = static_cast<int>((static_cast<int64_t>(begin) * R) / T), r1 = static_cast<int>((static_cast<int64_t>(stop - 1) * R) / T);
-  while (r0 + 1 < R && range_begin(r0 + 1, R, T) <= begin) ++r0;
-  while (r1 + 1 < R && range_begin(r1 + 1, R, T) <= stop - 1) ++r1;
-  if (r0 == r1) return;
-  const int G = a.Hq / a.Hkv, kvh = h / G, in_group = h - kvh * G, qt = in_group / 16;
-  const int unit = kvh * p.q_tiles + qt, hh = in_group - qt * 16;
-  float m = -FLT_MAX, l = 0.0f;
-  float4 o = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
-  for (int r = r0 + row; r <= r1; r += ROWS) {
-    const int which = range_begin(r, R, T) >= begin ? 0 : 1;  // slot 0 where the range begins in this sequence
-    const float* part = a.ws + ((static_cast<int64_t>(r) * 2 + which) * p.unit_heads + unit) * partial_floats(tile_heads, D);
-    const float mr = part[2 * hh], lr = part[2 * hh + 1];
-    const float4 v = *reinterpret_cast<const float4*>(part + partial_o(tile_heads) + hh * D + 4 * lane);
-    const float top = fmaxf(m, mr);
-    const float mine = ex2(m - top), theirs = ex2(mr - top);
-    m = top;
-    l = l * mine + lr * theirs;
-    o.x = o.x * mine + v.x * theirs;
-    o.y = o.y * mine + v.y * theirs;
-    o.z = o.z * mine + v.z * theirs;
-    o.w = o.w * mine + v.w * theirs;
-  }
-  sum[row][lane] = o;
-  if (lane == 0) ml[row] = make_float2(m, l);
-  __syncthreads();
-  if (row != 0) return;
-  float top = -FLT_MAX;
+  const int G = a.Hq / a.Hkv;
+  float m, l, o[VEC];
+  // Adds up the ranges first, first + step, ... of a head of a sequence: four partials are asked for at a time.
+  auto gather = [&](uint32_t which_split, int h, int first, int step) {
+    const int b = which_split >> 16, r0 = (which_split >> 8) & 255, last = which_split & 255;
+    const int kvh = h / G, in_group = h - kvh * G, qt = in_group / 16, hh = in_group - qt * 16;
+    const int begin = b > 0 ? end[b - 1] : 0;
+    m = -FLT_MAX;
+    l = 0.0f;
 #pragma unroll
-  for (int i = 0; i < ROWS; ++i) top = fmaxf(top, ml[i].x);
-  float total = 0.0f;
-  o = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+    for (int e = 0; e < VEC; ++e) o[e] = 0.0f;
+    for (int r = r0 + first; r <= last; r += 4 * step) {
+      float mr[4], lr[4], v[4][VEC];
 #pragma unroll
-  for (int i = 0; i < ROWS; ++i) {
-    const float w = ex2(ml[i].x - top);
-    const float4 v = sum[i][lane];
-    total += ml[i].y * w;
-    o.x += v.x * w;
-    o.y += v.y * w;
-    o.z += v.z * w;
-    o.w += v.w * w;
+      for (int i = 0; i < 4; ++i) {
+        const int ri = r + i * step;
+        mr[i] = -FLT_MAX;
+        lr[i] = 0.0f;
+#pragma unroll
+        for (int e = 0; e < VEC; ++e) v[i][e] = 0.0f;
+        if (ri <= last) {
+          const int which = ranges.begin(ri) >= begin ? 0 : 1;  // slot 0 where the range begins in this sequence
+          const float* part = a.ws + ((static_cast<int64_t>(ri) * 2 + which) * p.unit_heads + kvh * p.q_tiles + qt) *
+                                         partial_floats(tile_heads, D);
+          mr[i] = part[2 * hh];
+          lr[i] = part[2 * hh + 1];
+          const float* po = part + partial_o(tile_heads) + hh * D + lane * VEC;
+#pragma unroll
+          for (int e = 0; e < VEC; e += 2) {
+            const float2 two = *reinterpret_cast<const float2*>(po + e);
+            v[i][e] = two.x;
+            v[i][e + 1] = two.y;
+          }
+        }
+      }
+      const float to = fmaxf(fmaxf(fmaxf(mr[0], mr[1]), fmaxf(mr[2], mr[3])), m);
+      const float mine = ex2(m - to);
+      l *= mine;
+#pragma unroll
+      for (int e = 0; e < VEC; ++e) o[e] *= mine;
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        const float theirs = ex2(mr[i] - to);
+        l = fmaf(lr[i], theirs, l);
+#pragma unroll
+        for (int e = 0; e < VEC; ++e) o[e] = fmaf(v[i][e], theirs, o[e]);
+      }
+      m = to;
+    }
+  };
+  auto write = [&](int b, int h) {
+    const float inv = l == 0.0f ? 0.0f : 1.0f / l;  // no key was attended: zeros
+    uint32_t* out = reinterpret_cast<uint32_t*>(a.o + (static_cast<int64_t>(b) * a.Hq + h) * D + lane * VEC);
+#pragma unroll
+    for (int e = 0; e < VEC; e += 2) out[e >> 1] = pack_bf16(o[e] * inv, o[e + 1] * inv);
+  };
+  for (int i = blockIdx.x * WARPS + warp; i < n_split[1] * a.Hq; i += gridDim.x * WARPS) {
+    const uint32_t q = split[1][i / a.Hq];
+    gather(q, i % a.Hq, 0, 1);
+    write(q >> 16, i % a.Hq);
   }
-  const float inv = total == 0.0f ? 0.0f : 1.0f / total;
-  *reinterpret_cast<uint2*>(out + 4 * lane) = make_uint2(pack_bf16(o.x * inv, o.y * inv), pack_bf16(o.z * inv, o.w * inv));
+  // as many warps on a head of a long sequence as there are for all of them
+  int per = WARPS;
+  while (per > 2 && n_split[0] * a.Hq * per > static_cast<int>(gridDim.x) * WARPS) per >>= 1;
+  const int first = warp / per * per, items = WARPS / per;  // first warp of this one's head, heads a CTA takes at a time
+  for (int i0 = blockIdx.x * items; i0 < n_split[0] * a.Hq; i0 += gridDim.x * items) {
+    const int i = i0 + warp / per;
+    const bool there = i < n_split[0] * a.Hq;
+    const uint32_t q = split[0][there ? i / a.Hq : 0];
+    if (there) {
+      gather(q, i % a.Hq, warp - first, per);
+#pragma unroll
+      for (int e = 0; e < VEC; ++e) part_o[warp][lane * VEC + e] = o[e];
+      if (lane == 0) part_ml[warp] = make_float2(m, l);
+    }
+    __syncthreads();
+    if (there && warp == first) {
+      m = -FLT_MAX;
+      for (int w = first; w < first + per; ++w) m = fmaxf(m, part_ml[w].x);
+      l = 0.0f;
+#pragma unroll
+      for (int e = 0; e < VEC; ++e) o[e] = 0.0f;
+      for (int w = first; w < first + per; ++w) {
+        const float weight = ex2(part_ml[w].x - m);
+        l = fmaf(part_ml[w].y, weight, l);
+#pragma unroll
+        for (int e = 0; e < VEC; ++e) o[e] = fmaf(part_o[w][lane * VEC + e], weight, o[e]);
+      }
+      write(q >> 16, i % a.Hq);
+    }
+    __syncthreads();
+  }
 }
 
 cudaError_t sm_count(int* sms) {
@@ -634,11 +744,18 @@ DecodePlan make_plan(const DecodeArgs& a, int sms, bool split) {
   while (p.WH < warps && p.unit_heads % (2 * p.WH) == 0) p.WH *= 2;
   p.WT = warps / p.WH;
   p.groups = p.unit_heads / p.WH;
-  // one CTA an SM; a batch too long for the shared-memory scan has sequences enough to fill the GPU, and tiles
-  // are counted in 32 bits
-  const int64_t most_tiles = (static_cast<int64_t>(a.max_pages) * a.page_size / 16 + 1) * a.B;
-  p.ranges = split && a.B <= kMaxSplitBatch && most_tiles <= INT32_MAX ? std::max(1, sms / p.groups) : 0;
-  p.min_tiles = 2 * p.WT;
+  // Split into one range an SM, unless
+  // - the cache has no room for sequences of more than four tiles a warp: one CTA walks them in less time than the
+  //   second kernel takes (16 query and 4 key-value heads of 128, one sequence: 6.1 us against 6.9 at 128 tokens, 9.0
+  //   against 7.2 at 256; 24 heads of each: 5.6 against 6.6 at 64, 8.5 against 6.8 at 128; 8 and 1: 6.8 against 7.7 at
+  //   512, 9.7 against 7.8 at 1024);
+  // - the batch is too long for the tables in shared memory: it has sequences enough to fill the GPU;
+  // - tiles do not fit 32 bits.
+  const int tile = a.D == 64 ? 32 : 16;
+  const int64_t capacity = static_cast<int64_t>(a.max_pages) * a.page_size;
+  const bool whole = capacity <= 4 * p.WT * tile || a.B > kMaxSplitBatch || (capacity / 16 + 1) * a.B > INT32_MAX;
+  p.ranges = split && !whole ? std::max(1, std::min(sms / p.groups, kMaxRanges)) : 0;
+  p.min_tiles = p.WT;  // one a warp: two or more take longer than their partials (7.6 us against 7.0 at 1024 tokens)
   return p;
 }
 
@@ -660,8 +777,8 @@ cudaError_t launch_d(const Kernelargs& k, cudaStream_t stream) {
                        stream, k);
   if (e != cudaSuccess || k.p.ranges == 0) return e;
   const int G = k.a.Hq / k.a.Hkv;
-  return launch_dependent(decode_join_kernel<D>, dim3(static_cast<unsigned>(k.a.B) * k.a.Hq), kCombineThreads, 0, stream, k,
-                          C::kTile, std::min(G, C::kHeads));
+  return launch_dependent(decode_join_kernel<D>, dim3(k.p.ranges * k.p.groups), kJoinThreads, 0, stream, k, C::kTile,
+                          std::min(G, C::kHeads));
 }
 
 }  // namespace
