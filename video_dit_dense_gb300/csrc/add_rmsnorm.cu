@@ -16,7 +16,15 @@
 //
 // Memory-bound: x and residual are read once, h and y written once; a row
 // stays in registers (VPT vectors of 8 channels a thread) between the sum and
-// the scaling.
+// the scaling.  One row a CTA of as many warps as the row fills, or a warp a
+// row; no ring and no second row in flight, the other CTAs of the SM keep the
+// memory busy.  At 32760 rows with residual, e4m3 and row scales: 5120 channels
+// 168 us, 8192 channels 265 us, 7.0 and 7.1 TB/s (a copy reaches 6.8).
+// CTAs that stay on their SM and ask for their next row ahead took 184 us
+// (registers) and 186 us and more (shared memory).  Threads without a
+// vector cost as much as they leave idle: 256 threads for the 640 vectors of
+// 5120 channels took 195 us.  So does a register too many: 82 a thread instead of 80
+// took 318 us instead of 261 at 8192 channels, two CTAs an SM instead of three.
 #include <cuda_bf16.h>
 #include <cuda_fp8.h>
 
@@ -25,7 +33,7 @@
 namespace h3 {
 namespace {
 
-constexpr int kThreads = 256;
+constexpr int kShortRows = 8;  // short rows that a CTA takes, a warp each
 
 __device__ __forceinline__ float lo16(uint32_t w) { return __uint_as_float(w << 16); }
 __device__ __forceinline__ float hi16(uint32_t w) { return __uint_as_float(w & 0xFFFF0000u); }
@@ -39,50 +47,69 @@ __device__ __forceinline__ uint32_t pack_e4m3x4(float a, float b, float c, float
   return lo | (hi << 16);
 }
 
-// Sum and maximum over the TPR threads of a row (TPR <= 32: within a warp).
-template <int TPR>
+// Sum and maximum over the threads of a row: a warp (WARPS == 1), or the whole
+// block of at most WARPS warps.  A row's time is a chain of latencies, so the
+// warps' parts are read side by side and added as a tree.
+template <int WARPS>
 __device__ __forceinline__ void row_reduce(float& sum, float& top) {
 #pragma unroll
-  for (int off = (TPR < 32 ? TPR : 32) / 2; off >= 1; off >>= 1) {
+  for (int off = 16; off >= 1; off >>= 1) {
     sum += __shfl_xor_sync(0xFFFFFFFFu, sum, off);
     top = fmaxf(top, __shfl_xor_sync(0xFFFFFFFFu, top, off));
   }
-  if constexpr (TPR > 32) {
-    constexpr int kWarps = TPR / 32;
-    __shared__ float2 part[(TPR > kThreads ? TPR : kThreads) / 32];
-    const int warp = threadIdx.x >> 5, first = warp / kWarps * kWarps;
-    if ((threadIdx.x & 31) == 0) part[warp] = make_float2(sum, top);
+  if constexpr (WARPS > 1) {
+    __shared__ __align__(16) float2 part[WARPS];
+    if ((threadIdx.x & 31) == 0) part[threadIdx.x >> 5] = make_float2(sum, top);
+    if (threadIdx.x < WARPS && threadIdx.x >= (blockDim.x >> 5)) part[threadIdx.x] = make_float2(0.0f, 0.0f);
     __syncthreads();
-    sum = 0.0f;
-    top = 0.0f;
+    float s[WARPS / 2], m[WARPS / 2];
 #pragma unroll
-    for (int i = 0; i < kWarps; ++i) {  // the same order in every thread of the row
-      sum += part[first + i].x;
-      top = fmaxf(top, part[first + i].y);
+    for (int i = 0; i < WARPS / 2; ++i) {
+      const float4 two = *reinterpret_cast<const float4*>(&part[2 * i]);
+      s[i] = two.x + two.z;
+      m[i] = fmaxf(two.y, two.w);
     }
+#pragma unroll
+    for (int n = WARPS / 4; n >= 1; n >>= 1) {
+#pragma unroll
+      for (int i = 0; i < n; ++i) {
+        s[i] += s[i + n];
+        m[i] = fmaxf(m[i], m[i + n]);
+      }
+    }
+    sum = s[0];
+    top = m[0];
   }
 }
 
-// TPR threads hold a row, VPT vectors of 8 channels each (vector k * TPR + thread).
-template <int TPR, int VPT, int FORMAT>
-__global__ void __launch_bounds__(TPR > kThreads ? TPR : kThreads) add_rmsnorm_kernel(const __grid_constant__ AddNormArgs a) {
-  constexpr int kBlock = TPR > kThreads ? TPR : kThreads;
-  constexpr int kRows = kBlock / TPR;
+// Vector k * threads + thread of the row is the thread's k-th.
+template <int WARPS, int VPT, int FORMAT>
+__global__ void __launch_bounds__(WARPS == 1 ? kShortRows * 32 : WARPS * 32) __maxnreg__(VPT == 2 ? 48 : WARPS == 1 ? 80 : 56)
+    add_rmsnorm_kernel(const __grid_constant__ AddNormArgs a) {
+  constexpr bool SHORT = WARPS == 1;
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
   asm volatile("griddepcontrol.wait;" ::: "memory");
-  const int t = threadIdx.x % TPR, V = a.C >> 3;
-  const int64_t row = static_cast<int64_t>(blockIdx.x) * kRows + threadIdx.x / TPR;
-  const bool live = row < a.T;
+  const int TPR = SHORT ? 32 : blockDim.x;
+  const int t = SHORT ? threadIdx.x & 31 : threadIdx.x, V = a.C >> 3;
+  const int64_t row = SHORT ? static_cast<int64_t>(blockIdx.x) * kShortRows + (threadIdx.x >> 5) : blockIdx.x;
+  const bool live = !SHORT || row < a.T;
   const int64_t base = live ? row * a.C : 0;
   uint4 xv[VPT], rv[VPT];
-  float wv[VPT][8];
+  // The weights of a vector: kept from the first use to the second, or, where they would take registers that another
+  // CTA needs, read again from L1.
+  constexpr bool kKeepWeights = SHORT || VPT == 2;
+  auto weights = [&](int v, float (&to)[8]) {
+    const float4* wp = reinterpret_cast<const float4*>(a.w + 8 * v);
+    const float4 one = make_float4(1.0f, 1.0f, 1.0f, 1.0f);
+    *reinterpret_cast<float4*>(&to[0]) = v < V && a.w ? wp[0] : one;
+    *reinterpret_cast<float4*>(&to[4]) = v < V && a.w ? wp[1] : one;
+  };
+  float kept[kKeepWeights ? VPT : 1][8];
 #pragma unroll
   for (int k = 0; k < VPT; ++k) {
     const int v = k * TPR + t;
     const bool in = live && v < V;
-    const float4 one = make_float4(1.0f, 1.0f, 1.0f, 1.0f);
-    *reinterpret_cast<float4*>(&wv[k][0]) = in && a.w ? *reinterpret_cast<const float4*>(a.w + 8 * v) : one;
-    *reinterpret_cast<float4*>(&wv[k][4]) = in && a.w ? *reinterpret_cast<const float4*>(a.w + 8 * v + 4) : one;
+    if constexpr (kKeepWeights) weights(v, kept[k]);
     xv[k] = in ? *reinterpret_cast<const uint4*>(a.x + base + 8 * v) : make_uint4(0u, 0u, 0u, 0u);
     rv[k] = in && a.residual ? *reinterpret_cast<const uint4*>(a.residual + base + 8 * v) : make_uint4(0u, 0u, 0u, 0u);
   }
@@ -104,12 +131,15 @@ __global__ void __launch_bounds__(TPR > kThreads ? TPR : kThreads) add_rmsnorm_k
       sum = fmaf(hi16(x[e]), hi16(x[e]), sum);
     }
     if constexpr (FORMAT == H3ATTN_Y_E4M3_ROW) {
+      float w8[8];
+      if constexpr (!kKeepWeights) weights(v, w8);
+      const float(&wv)[8] = kKeepWeights ? kept[kKeepWeights ? k : 0] : w8;
 #pragma unroll
       for (int e = 0; e < 4; ++e)
-        top = fmaxf(top, fmaxf(fabsf(lo16(x[e]) * wv[k][2 * e]), fabsf(hi16(x[e]) * wv[k][2 * e + 1])));
+        top = fmaxf(top, fmaxf(fabsf(lo16(x[e]) * wv[2 * e]), fabsf(hi16(x[e]) * wv[2 * e + 1])));
     }
   }
-  row_reduce<TPR>(sum, top);
+  row_reduce<WARPS>(sum, top);
   const float r = __frsqrt_rn(__fdiv_rn(sum, static_cast<float>(a.C)) + a.eps);
   float inv = 1.0f;
   if constexpr (FORMAT == H3ATTN_Y_E4M3_ROW) {
@@ -124,9 +154,12 @@ __global__ void __launch_bounds__(TPR > kThreads ? TPR : kThreads) add_rmsnorm_k
     const int v = k * TPR + t;
     const bool in = live && v < V;
     const uint32_t x[4] = {xv[k].x, xv[k].y, xv[k].z, xv[k].w};
+    float w8[8];
+    if constexpr (!kKeepWeights) weights(v, w8);
+    const float(&wv)[8] = kKeepWeights ? kept[kKeepWeights ? k : 0] : w8;
     float y[8];
 #pragma unroll
-    for (int e = 0; e < 8; ++e) y[e] = (((e & 1) ? hi16(x[e >> 1]) : lo16(x[e >> 1])) * wv[k][e]) * r;
+    for (int e = 0; e < 8; ++e) y[e] = (((e & 1) ? hi16(x[e >> 1]) : lo16(x[e >> 1])) * wv[e]) * r;
     if constexpr (FORMAT == H3ATTN_Y_BF16) {
       if (in)
         *reinterpret_cast<uint4*>(static_cast<uint16_t*>(a.y) + base + 8 * v) =
@@ -154,16 +187,17 @@ __global__ void __launch_bounds__(TPR > kThreads ? TPR : kThreads) add_rmsnorm_k
   }
 }
 
-template <int TPR, int VPT>
+// WARPS 1: a warp a row; else a block of up to so many warps.
+template <int WARPS, int VPT>
 cudaError_t launch_rows(const AddNormArgs& a, cudaStream_t stream) {
-  constexpr int kBlock = TPR > kThreads ? TPR : kThreads;
-  const int64_t rows = kBlock / TPR;
-  const dim3 grid(static_cast<unsigned>((a.T + rows - 1) / rows));
+  const unsigned threads = WARPS == 1 ? kShortRows * 32 : ((a.C >> 3) + VPT * 32 - 1) / (VPT * 32) * 32;
+  const dim3 grid(WARPS == 1 ? (static_cast<unsigned>(a.T) + kShortRows - 1) / kShortRows : a.T);
   switch (a.format) {
-    case H3ATTN_Y_BF16: return launch_dependent(add_rmsnorm_kernel<TPR, VPT, H3ATTN_Y_BF16>, grid, kBlock, 0, stream, a);
+    case H3ATTN_Y_BF16:
+      return launch_dependent(add_rmsnorm_kernel<WARPS, VPT, H3ATTN_Y_BF16>, grid, threads, 0, stream, a);
     case H3ATTN_Y_E4M3_ROW:
-      return launch_dependent(add_rmsnorm_kernel<TPR, VPT, H3ATTN_Y_E4M3_ROW>, grid, kBlock, 0, stream, a);
-    default: return launch_dependent(add_rmsnorm_kernel<TPR, VPT, H3ATTN_Y_E4M3_MX32>, grid, kBlock, 0, stream, a);
+      return launch_dependent(add_rmsnorm_kernel<WARPS, VPT, H3ATTN_Y_E4M3_ROW>, grid, threads, 0, stream, a);
+    default: return launch_dependent(add_rmsnorm_kernel<WARPS, VPT, H3ATTN_Y_E4M3_MX32>, grid, threads, 0, stream, a);
   }
 }
 
@@ -171,12 +205,17 @@ cudaError_t launch_rows(const AddNormArgs& a, cudaStream_t stream) {
 
 cudaError_t launch_add_rmsnorm(const AddNormArgs& a, cudaStream_t stream) {
   const int V = a.C >> 3;
-  if (V <= 32 * 2) return launch_rows<32, 2>(a, stream);
-  if (V <= 64 * 2) return launch_rows<64, 2>(a, stream);
-  if (V <= 128 * 2) return launch_rows<128, 2>(a, stream);
-  if (V <= 256 * 2) return launch_rows<256, 2>(a, stream);
-  if (V <= 256 * 4) return launch_rows<256, 4>(a, stream);
-  return launch_rows<512, 4>(a, stream);
+  // A warp a row for short rows: at 32760 rows of 520 channels 24 us, two warps a row 33.  From 65 vectors on only when
+  // there are many: one row of 1024 channels takes 1.6 us by a warp, 1.3 by a block.
+  if (V <= 64) return launch_rows<1, 2>(a, stream);
+  if (V <= 128 && a.T >= 512) return launch_rows<1, 4>(a, stream);
+  // Two vectors a thread while the rows are short or few (one row of 5120 channels 1.7 us, with four 2.4; 1200 rows 8.5
+  // and 11.1), four with weights read twice where the memory is what counts (32760 rows 168 us, with two 174; of 8192 channels
+  // 265 and 313).
+  if (V <= 512) return launch_rows<8, 2>(a, stream);
+  if (V <= 1024 && a.T < 2048) return launch_rows<16, 2>(a, stream);
+  if (V <= 1024) return launch_rows<8, 4>(a, stream);
+  return launch_rows<16, 4>(a, stream);
 }
 
 }  // namespace h3

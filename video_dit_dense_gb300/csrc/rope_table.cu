@@ -8,25 +8,71 @@
 // p is p * u_i mod 2^64, exact integer arithmetic that drops whole turns by
 // itself, off by at most |p| / 2 units of 2^-64 turn (2^-34 turn at 2^31).
 // The two top bits (after adding an eighth) name the quadrant; the rest, a
-// signed angle of at most an eighth of a turn, is converted to float32 with
-// its leading bits intact.
+// signed angle x of at most an eighth of a turn, is rounded to float32 once,
+// small ones with all their bits, and its sine and cosine are the Taylor
+// polynomials of sin(2 pi x) and cos(2 pi x), whose next terms are below
+// 2^-28 and 2^-32 there.
 //
-// Bound by the stores: 8 bytes for each sine and cosine pair.
+// Bound by the stores, 8 bytes for each sine and cosine, as long as the
+// arithmetic takes less than 40 instructions a pair: the phase is two 32-bit
+// multiplications, and the polynomials run on two pairs at a time (packed
+// float32 operations).  524291 rows of 64 pairs: 40 us, 6.7 TB/s (66 us
+// with the library's sincospif).
 #include "generate.h"
+#include "ptx.cuh"
 
 namespace h3 {
 namespace {
 
 constexpr int kThreads = 256;
 
-__device__ __forceinline__ void sincos_turn(uint64_t phase, float* s, float* c) {
-  const uint32_t quadrant = static_cast<uint32_t>((phase + (1ull << 61)) >> 62);
-  const int64_t rest = static_cast<int64_t>(phase - (static_cast<uint64_t>(quadrant) << 62));
-  float sn, cs;
-  sincospif(__ll2float_rn(rest) * 0x1p-63f, &sn, &cs);  // 2 * turns = angle / pi
-  const float a = (quadrant & 1) ? cs : sn, b = (quadrant & 1) ? sn : cs;
-  *s = (quadrant & 2) ? -a : a;
-  *c = ((quadrant + 1) & 2) ? -b : b;
+// sin(2 pi x) = sum kSin[k] x^(2 k + 1) and cos(2 pi x) = 1 + sum kCos[k] x^(2 k + 2): (2 pi)^n / n! with alternating
+// signs; the first of the sine's is in two parts.
+constexpr double k2Pi = 6.283185307179586;
+constexpr double power2pi(int n) { return n == 0 ? 1.0 : power2pi(n - 1) * k2Pi / n; }  // (2 pi)^n / n!
+// The angle of position p: its quadrant, and the rest in turns.
+__device__ __forceinline__ float reduce(int p, uint64_t turn, uint32_t& quadrant) {
+  const uint32_t pu = static_cast<uint32_t>(p), t_lo = static_cast<uint32_t>(turn), t_hi = static_cast<uint32_t>(turn >> 32);
+  const uint64_t low = static_cast<uint64_t>(pu) * t_lo;
+  uint32_t hi = static_cast<uint32_t>(low >> 32) + pu * t_hi;
+  if (p < 0) hi -= t_lo;  // pu is p + 2^32
+  quadrant = (hi + (1u << 29)) >> 30;
+  const int rest = static_cast<int>(hi - (quadrant << 30));
+  return fmaf(static_cast<float>(static_cast<uint32_t>(low)), 0x1p-64f, static_cast<float>(rest) * 0x1p-32f);
+}
+
+// Sines and cosines of two angles (in turns, at most an eighth), scaled.
+__device__ __forceinline__ void sincos2(const float (&x)[2], const uint32_t (&quadrant)[2], float amplitude, float* sn, float* cs) {
+  constexpr float kSinHi = static_cast<float>(power2pi(1));
+  constexpr float kSinLo = static_cast<float>(power2pi(1) - static_cast<double>(kSinHi));
+  constexpr float kSin[4] = {static_cast<float>(-power2pi(3)), static_cast<float>(power2pi(5)),
+                             static_cast<float>(-power2pi(7)), static_cast<float>(power2pi(9))};
+  constexpr float kCos[5] = {static_cast<float>(-power2pi(2)), static_cast<float>(power2pi(4)),
+                             static_cast<float>(-power2pi(6)), static_cast<float>(power2pi(8)),
+                             static_cast<float>(-power2pi(10))};
+  float z0, z1, s0, s1, c0, c1, t0, t1;
+  fmul2(z0, z1, x[0], x[1], x[0], x[1]);
+  s0 = s1 = kSin[3];
+  c0 = c1 = kCos[4];
+#pragma unroll
+  for (int k = 2; k >= 0; --k) ffma2(s0, s1, s0, s1, z0, z1, kSin[k], kSin[k]);
+#pragma unroll
+  for (int k = 3; k >= 0; --k) ffma2(c0, c1, c0, c1, z0, z1, kCos[k], kCos[k]);
+  ffma2(c0, c1, c0, c1, z0, z1, 1.0f, 1.0f);
+  ffma2(s0, s1, s0, s1, z0, z1, kSinLo, kSinLo);
+  fmul2(t0, t1, s0, s1, x[0], x[1]);
+  ffma2(s0, s1, x[0], x[1], kSinHi, kSinHi, t0, t1);
+  fmul2(s0, s1, s0, s1, amplitude, amplitude);
+  fmul2(c0, c1, c0, c1, amplitude, amplitude);
+  const float s[2] = {s0, s1}, c[2] = {c0, c1};
+#pragma unroll
+  for (int i = 0; i < 2; ++i) {
+    // a quarter turn more: sine from cosine, cosine from minus sine
+    const bool odd = quadrant[i] & 1;
+    const float a = odd ? c[i] : s[i], b = odd ? s[i] : c[i];
+    sn[i] = __uint_as_float(__float_as_uint(a) ^ ((quadrant[i] & 2) << 30));
+    cs[i] = __uint_as_float(__float_as_uint(b) ^ (((quadrant[i] + 1) & 2) << 30));
+  }
 }
 
 // A thread keeps VEC neighbouring pairs of a row and walks down the rows, so
@@ -44,13 +90,17 @@ __global__ void __launch_bounds__(kThreads) rope_table_kernel(const __grid_const
   for (int e = 0; e < VEC; ++e) turn[e] = a.turn[col * VEC + e];
   const int64_t step = static_cast<int64_t>(gridDim.x) * rows;
   for (int64_t n = static_cast<int64_t>(blockIdx.x) * rows + lane_row; n < a.N; n += step) {
-    const int64_t p = a.pos ? static_cast<int64_t>(a.pos[n]) : a.first + n;
-    float c[VEC], s[VEC];
+    const int p = a.pos ? a.pos[n] : static_cast<int>(a.first + n);
+    constexpr int PAIRS = VEC == 1 ? 2 : VEC;  // the polynomials take two at a time
+    float x[PAIRS], c[PAIRS], s[PAIRS];
+    uint32_t q[PAIRS];
 #pragma unroll
-    for (int e = 0; e < VEC; ++e) {
-      sincos_turn(static_cast<uint64_t>(p) * turn[e], &s[e], &c[e]);
-      c[e] *= a.amplitude;
-      s[e] *= a.amplitude;
+    for (int e = 0; e < PAIRS; ++e) x[e] = reduce(p, turn[VEC == 1 ? 0 : e], q[e]);
+#pragma unroll
+    for (int e = 0; e < PAIRS; e += 2) {
+      const float x2[2] = {x[e], x[e + 1]};
+      const uint32_t q2[2] = {q[e], q[e + 1]};
+      sincos2(x2, q2, a.amplitude, s + e, c + e);
     }
     const int64_t at = n * a.half + col * VEC;
     if constexpr (VEC == 4) {
