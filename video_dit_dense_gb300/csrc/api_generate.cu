@@ -250,8 +250,7 @@ h3attn_status_t h3attn_qk_norm_rope_append(const void* q, const void* k, const v
   a.q_stride = q_stride;
   a.k_stride = k_stride;
   a.v_stride = v_stride;
-  a.rows = static_cast<uint32_t>(tokens * (Hq + 2 * Hkv));
-  a.div_heads = h3::make_fastdiv(static_cast<uint32_t>(Hq + 2 * Hkv));
+  a.tokens = static_cast<uint32_t>(tokens);
   a.div_s = h3::make_fastdiv(static_cast<uint32_t>(S));
   a.div_page = h3::make_fastdiv(static_cast<uint32_t>(cache->page_size));
   a.B = B;

@@ -78,8 +78,12 @@ struct AppendArgs {
   const int32_t* new_len;     // [B] or nullptr: S new tokens each
   int32_t* len_out;           // [B] or nullptr
   int64_t q_stride, k_stride, v_stride;
-  uint32_t rows;              // B * S * (Hq + 2 Hkv)
-  FastDiv div_heads, div_s, div_page;
+  FastDiv div_s, div_page;
+  uint32_t tokens;  // B * S
+  // set by the launcher: warps' worth of work (some tokens, some heads of each), and the heads of one
+  uint32_t items;
+  FastDiv div_parts;
+  int heads_per_part, heads_log2;
   int B, S, Hq, Hkv, D, page_size, max_pages, num_pages, table_rows, rotary_dim, interleaved;
   float eps;
   int* status;
