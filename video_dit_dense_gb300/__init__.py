@@ -570,7 +570,7 @@ class PagedKV:
     sequence.  All CUDA tensors on the current device, kept by reference: their
     contents may change between calls, their storage not.
     """
-    __slots__ = ("_tensors", "_struct", "_ref", "_device")
+    __slots__ = ("_tensors", "_struct", "_ref", "_device", "_shape")
 
     def __init__(self, k_pages, v_pages, page_table, kv_len):
         torch = _get_torch()
@@ -587,7 +587,7 @@ class PagedKV:
         self._struct = h3attn_paged_kv_t(k_pages.data_ptr(), v_pages.data_ptr(), page_table.data_ptr(),
                                          kv_len.data_ptr(), B, num_pages, page_size, max_pages, Hkv, D)
         self._ref = ctypes.byref(self._struct)
-        self._device = dev
+        self._device, self._shape = dev, (B, Hkv, D)
 
     k_pages = property(lambda self: self._tensors[0])
     v_pages = property(lambda self: self._tensors[1])
@@ -602,7 +602,7 @@ class PagedKV:
 def _token_stride(name, t, B, S, H, D, dev):
     """Elements from one token to the next of a [B, S, H, D] bf16 tensor whose
     heads lie behind one another (a slice of a fused projection, say)."""
-    if t.dtype is not _torch.bfloat16 or t.shape != (B, S, H, D) or t.get_device() < 0:
+    if t.dtype is not _torch.bfloat16 or t.shape != (B, S, H, D):
         raise H3AttnError(H3ATTN_ERR_INVALID_ARG, f"{name} must be a {[B, S, H, D]} bf16 CUDA tensor")
     if t.get_device() != dev:
         raise H3AttnError(H3ATTN_ERR_INVALID_ARG, f"{name} must be on the current device")
@@ -611,6 +611,8 @@ def _token_stride(name, t, B, S, H, D, dev):
     if B * S * H == 0:
         return H * D
     sb, ss, sh, sd = t.stride()
+    if sd == 1 and sh == D and S > 1 and sb == S * ss:
+        return ss
     stride = ss if S > 1 else sb if B > 1 else H * D
     if sd != 1 or (H > 1 and sh != D) or (S > 1 and B > 1 and sb != S * ss):
         raise H3AttnError(H3ATTN_ERR_INVALID_ARG, f"{name} must have contiguous heads and one stride from token to token")
@@ -631,8 +633,7 @@ def h3attn_qk_norm_rope_append(q, k, v, q_out, cache: PagedKV, wq, wk, cos, sin,
     """
     _lib or load()
     torch = _torch or _get_torch()
-    c = cache._struct
-    B, Hkv, D = c.B, c.Hkv, c.D
+    B, Hkv, D = cache._shape
     if k.dim() != 4:
         raise H3AttnError(H3ATTN_ERR_INVALID_ARG, "k must be a [B, S, Hkv, D] bf16 CUDA tensor")
     dev = _current_device("k", k)
@@ -694,7 +695,6 @@ def h3attn_paged_decode(q, o, cache: PagedKV, scale=None, workspace=None, stream
     """
     _lib or load()
     torch = _torch or _get_torch()
-    c = cache._struct
     shape = q.shape
     if len(shape) == 4 and shape[1] == 1:
         B, _, Hq, D = shape
@@ -702,7 +702,7 @@ def h3attn_paged_decode(q, o, cache: PagedKV, scale=None, workspace=None, stream
         B, Hq, D = shape
     else:
         raise H3AttnError(H3ATTN_ERR_INVALID_ARG, "q must be [B, 1, Hq, D] or [B, Hq, D]: one new token per sequence")
-    if B != c.B or D != c.D:
+    if (B, D) != cache._shape[::2]:
         raise H3AttnError(H3ATTN_ERR_INVALID_ARG, "shape mismatch between q and the cache")
     dev = _current_device("q", q)
     if cache._device != dev:

@@ -281,29 +281,34 @@ __global__ void __launch_bounds__(DecodeCfg<D, NT>::kWarps * 32, 1) decode_kerne
   const uint32_t ring = smem_u32(smem) + warp * (STAGES * 2 * C::kTileBytes);
   const int64_t row_stride = static_cast<int64_t>(a.Hkv) * D;
 
-  // The lane's token of the tile to be loaded next: its page, asked for a turn ahead and looked at only when its rows
-  // are loaded, and its row in the page.  token_row < 0: no such token.
-  int page = -1, token_row = -1;
-  auto look_ahead = [&]() {
+  // The lane's tokens of the next two tiles to be loaded: their pages, asked for two turns ahead and looked at only when
+  // the rows are loaded, and their rows in the pages.  token_row < 0: no such token.  -2: no such tile.
+  int page[2], token_row[2];
+  auto look_ahead = [&](int i) {
+    token_row[i] = -2;
+    if (ld.b < 0) return;
     const int token = ld.tile * TILE + lane % TILE;
-    token_row = -1;
-    if (ld.b >= 0 && token < ld.len) {
+    token_row[i] = -1;
+    if (token < ld.len) {
       const uint32_t pg = fdiv(static_cast<uint32_t>(token), a.div_page);
-      page = a.page_table[static_cast<int64_t>(ld.b) * a.max_pages + pg];
-      token_row = token - static_cast<int>(pg) * a.page_size;
+      page[i] = a.page_table[static_cast<int64_t>(ld.b) * a.max_pages + pg];
+      token_row[i] = token - static_cast<int>(pg) * a.page_size;
     }
+    ld.tile += p.WT;
+    enter(ld);
   };
-  look_ahead();
+  look_ahead(0);
+  look_ahead(1);
   uint32_t mask_of[STAGES];  // tokens of each stage's tile that are attended
   const uint16_t* kbase = a.k_pages + kvh * D + (lane % CH) * 8;
   const uint16_t* vbase = a.v_pages + kvh * D + (lane % CH) * 8;
   // Fills stage `at` with the next tile; rows that are not attended are zeros.
   auto load = [&](int at, uint32_t& mask) {
-    if (ld.b >= 0) {
+    if (token_row[0] != -2) {  // the same in all lanes
       int row = -1;  // of the whole cache
-      if (token_row >= 0) {
-        if (page >= 0 && page < a.num_pages)
-          row = page * a.page_size + token_row;
+      if (token_row[0] >= 0) {
+        if (page[0] >= 0 && page[0] < a.num_pages)
+          row = page[0] * a.page_size + token_row[0];
         else
           atomicExch(a.status, static_cast<int>(H3ATTN_ERR_INVALID_ARG));  // its keys are not attended
       }
@@ -318,9 +323,9 @@ __global__ void __launch_bounds__(DecodeCfg<D, NT>::kWarps * 32, 1) decode_kerne
         cp_async16(ks + dst, kbase + off, src_row >= 0);
         cp_async16(vs + dst, vbase + off, src_row >= 0);
       }
-      ld.tile += p.WT;
-      enter(ld);
-      look_ahead();
+      page[0] = page[1];
+      token_row[0] = token_row[1];
+      look_ahead(1);
     }
     cp_async_commit();
   };
@@ -587,7 +592,7 @@ constexpr int kFewParts = 4;  // partials that a warp asks for at a time: a head
 // sequences without a key get their zeros here.  One CTA an SM, small enough to
 // sit beside a decode CTA.
 template <int D>
-__global__ void __launch_bounds__(kJoinThreads) __maxnreg__(D == 256 ? 64 : 56) decode_join_kernel(const __grid_constant__ Kernelargs k, int tile,
+__global__ void __launch_bounds__(kJoinThreads) __maxnreg__(D == 256 ? 96 : 56) decode_join_kernel(const __grid_constant__ Kernelargs k, int tile,
                                                                    int tile_heads) {
   constexpr int VEC = D / 32, WARPS = kJoinThreads / 32;
   const DecodeArgs& a = k.a;
@@ -626,27 +631,37 @@ __global__ void __launch_bounds__(kJoinThreads) __maxnreg__(D == 256 ? 64 : 56) 
   }
   if (kind >= 0) split[kind][at + __popc(same[kind] & ((1u << lane) - 1u))] = mine;
   __syncthreads();
-  asm volatile("griddepcontrol.wait;" ::: "memory");
-  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
-
-  for (int b = blockIdx.x; b < a.B; b += gridDim.x) {
-    if (end[b] == (b > 0 ? end[b - 1] : 0)) {
-      uint2* row = reinterpret_cast<uint2*>(a.o + static_cast<int64_t>(b) * a.Hq * D);
-      for (int i = threadIdx.x; i < a.Hq * (D / 4); i += kJoinThreads) row[i] = make_uint2(0u, 0u);
-    }
-  }
   const int G = a.Hq / a.Hkv;
+  const int64_t unit_floats = partial_floats(tile_heads, D), stride = 2 * p.unit_heads * unit_floats;  // from range to range
+  // A head of a split sequence: its partial of the first range (slot 1 where that range begins in another sequence), the
+  // lane's part of it, and the row it goes to.
+  struct Head {
+    const float *ml, *o;
+    uint16_t* out;
+    int64_t slot1;  // from the others' slot to the first one's
+    int n;          // ranges
+  };
+  auto locate = [&](int list, int i) {
+    const int in_list = i / a.Hq, h = i - in_list * a.Hq;
+    const uint32_t q = split[list][in_list];
+    const int b = q >> 16, r0 = (q >> 8) & 255, kvh = h / G, in_group = h - kvh * G, qt = in_group / 16, hh = in_group - qt * 16;
+    const float* part = a.ws + r0 * stride + (kvh * p.q_tiles + qt) * unit_floats;
+    Head x;
+    x.ml = part + 2 * hh;
+    x.o = part + partial_o(tile_heads) + hh * D + lane * VEC;
+    x.out = a.o + (static_cast<int64_t>(b) * a.Hq + h) * D + lane * VEC;
+    x.slot1 = ranges.begin(r0) >= (b > 0 ? end[b - 1] : 0) ? 0 : stride / 2;
+    x.n = static_cast<int>(q & 255) - r0 + 1;
+    return x;
+  };
   float m, l, o[VEC];
-  // Adds up the ranges first, first + step, ... of a head of a sequence: four partials are asked for at a time.
-  auto gather = [&](uint32_t which_split, int h, int first, int step) {
-    const int b = which_split >> 16, r0 = (which_split >> 8) & 255, last = which_split & 255;
-    const int kvh = h / G, in_group = h - kvh * G, qt = in_group / 16, hh = in_group - qt * 16;
-    const int begin = b > 0 ? end[b - 1] : 0;
+  // Adds up the partials first, first + step, ... of a head: four are asked for at a time.
+  auto gather = [&](const Head& x, int first, int step) {
     m = -FLT_MAX;
     l = 0.0f;
 #pragma unroll
     for (int e = 0; e < VEC; ++e) o[e] = 0.0f;
-    for (int r = r0 + first; r <= last; r += 4 * step) {
+    for (int r = first; r < x.n; r += 4 * step) {
       float mr[4], lr[4], v[4][VEC];
 #pragma unroll
       for (int i = 0; i < 4; ++i) {
@@ -655,16 +670,14 @@ __global__ void __launch_bounds__(kJoinThreads) __maxnreg__(D == 256 ? 64 : 56) 
         lr[i] = 0.0f;
 #pragma unroll
         for (int e = 0; e < VEC; ++e) v[i][e] = 0.0f;
-        if (ri <= last) {
-          const int which = ranges.begin(ri) >= begin ? 0 : 1;  // slot 0 where the range begins in this sequence
-          const float* part = a.ws + ((static_cast<int64_t>(ri) * 2 + which) * p.unit_heads + kvh * p.q_tiles + qt) *
-                                         partial_floats(tile_heads, D);
-          mr[i] = part[2 * hh];
-          lr[i] = part[2 * hh + 1];
-          const float* po = part + partial_o(tile_heads) + hh * D + lane * VEC;
+        if (ri < x.n) {
+          const int64_t off = ri == 0 ? x.slot1 : ri * stride;
+          const float2 ml = *reinterpret_cast<const float2*>(x.ml + off);
+          mr[i] = ml.x;
+          lr[i] = ml.y;
 #pragma unroll
           for (int e = 0; e < VEC; e += 2) {
-            const float2 two = *reinterpret_cast<const float2*>(po + e);
+            const float2 two = *reinterpret_cast<const float2*>(x.o + off + e);
             v[i][e] = two.x;
             v[i][e + 1] = two.y;
           }
@@ -685,47 +698,62 @@ __global__ void __launch_bounds__(kJoinThreads) __maxnreg__(D == 256 ? 64 : 56) 
       m = to;
     }
   };
-  auto write = [&](int b, int h) {
+  auto write = [&](uint16_t* out) {
     const float inv = l == 0.0f ? 0.0f : 1.0f / l;  // no key was attended: zeros
-    uint32_t* out = reinterpret_cast<uint32_t*>(a.o + (static_cast<int64_t>(b) * a.Hq + h) * D + lane * VEC);
 #pragma unroll
-    for (int e = 0; e < VEC; e += 2) out[e >> 1] = pack_bf16(o[e] * inv, o[e + 1] * inv);
+    for (int e = 0; e < VEC; e += 2) reinterpret_cast<uint32_t*>(out)[e >> 1] = pack_bf16(o[e] * inv, o[e + 1] * inv);
   };
-  for (int i = blockIdx.x * WARPS + warp; i < n_split[1] * a.Hq; i += gridDim.x * WARPS) {
-    const uint32_t q = split[1][i / a.Hq];
-    gather(q, i % a.Hq, 0, 1);
-    write(q >> 16, i % a.Hq);
-  }
-  // as many warps on a head of a long sequence as there are for all of them
+  // Heads in few ranges: a warp each.  Heads in many: as many warps on each as there are for all of them.
+  const int few = n_split[1] * a.Hq, many = n_split[0] * a.Hq;
   int per = WARPS;
-  while (per > 2 && n_split[0] * a.Hq * per > static_cast<int>(gridDim.x) * WARPS) per >>= 1;
-  const int first = warp / per * per, items = WARPS / per;  // first warp of this one's head, heads a CTA takes at a time
-  for (int i0 = blockIdx.x * items; i0 < n_split[0] * a.Hq; i0 += gridDim.x * items) {
-    const int i = i0 + warp / per;
-    const bool there = i < n_split[0] * a.Hq;
-    const uint32_t q = split[0][there ? i / a.Hq : 0];
+  while (per > 2 && many * per > static_cast<int>(gridDim.x) * WARPS) per >>= 1;
+  const int lead = warp / per * per, at_once = WARPS / per;  // first warp of this one's head, heads a CTA takes at a time
+  // the first of each is looked up before the wait
+  int i_few = blockIdx.x * WARPS + warp, i_many = blockIdx.x * at_once + warp / per;
+  Head x_few{}, x_many{};
+  if (i_few < few) x_few = locate(1, i_few);
+  if (i_many < many) x_many = locate(0, i_many);
+  asm volatile("griddepcontrol.wait;" ::: "memory");
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+
+  while (i_few < few) {
+    gather(x_few, 0, 1);
+    write(x_few.out);
+    i_few += gridDim.x * WARPS;
+    if (i_few < few) x_few = locate(1, i_few);
+  }
+  for (int i0 = blockIdx.x * at_once; i0 < many; i0 += gridDim.x * at_once) {
+    const bool there = i_many < many;
     if (there) {
-      gather(q, i % a.Hq, warp - first, per);
+      gather(x_many, warp - lead, per);
 #pragma unroll
       for (int e = 0; e < VEC; ++e) part_o[warp][lane * VEC + e] = o[e];
       if (lane == 0) part_ml[warp] = make_float2(m, l);
     }
     __syncthreads();
-    if (there && warp == first) {
+    if (there && warp == lead) {
       m = -FLT_MAX;
-      for (int w = first; w < first + per; ++w) m = fmaxf(m, part_ml[w].x);
+      for (int w = lead; w < lead + per; ++w) m = fmaxf(m, part_ml[w].x);
       l = 0.0f;
 #pragma unroll
       for (int e = 0; e < VEC; ++e) o[e] = 0.0f;
-      for (int w = first; w < first + per; ++w) {
+      for (int w = lead; w < lead + per; ++w) {
         const float weight = ex2(part_ml[w].x - m);
         l = fmaf(part_ml[w].y, weight, l);
 #pragma unroll
         for (int e = 0; e < VEC; ++e) o[e] = fmaf(part_o[w][lane * VEC + e], weight, o[e]);
       }
-      write(q >> 16, i % a.Hq);
+      write(x_many.out);
     }
     __syncthreads();
+    i_many += gridDim.x * at_once;
+    if (i_many < many) x_many = locate(0, i_many);
+  }
+  for (int b = blockIdx.x; b < a.B; b += gridDim.x) {
+    if (end[b] == (b > 0 ? end[b - 1] : 0)) {  // no key: zeros
+      uint2* row = reinterpret_cast<uint2*>(a.o + static_cast<int64_t>(b) * a.Hq * D);
+      for (int i = threadIdx.x; i < a.Hq * (D / 4); i += kJoinThreads) row[i] = make_uint2(0u, 0u);
+    }
   }
 }
 
