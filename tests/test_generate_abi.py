@@ -134,30 +134,17 @@ def test_the_binding_refuses_before_any_call(lib):
         h3.PagedKV(pages[0], pages[0], torch.zeros(1, 2, dtype=torch.int32), torch.zeros(1, dtype=torch.int32))
 
 
-class _Cuda:
-    """Stands in for a CUDA tensor of a given layout (the binding's checks look at nothing else)."""
-    is_cuda, requires_grad = True, False
-
-    def __init__(self, shape, strides, dtype=torch.bfloat16):
-        self.shape, self._strides, self.dtype = torch.Size(shape), strides, dtype
-
-    def stride(self):
-        return self._strides
-
-    def get_device(self):
-        return 0
-
-
-def test_token_strides():
-    h3._get_torch()
-    B, S, H, D = 2, 5, 3, 64
-    assert h3._token_stride("k", _Cuda((B, S, H, D), (S * 1000, 1000, D, 1)), B, S, H, D, 0) == 1000
-    assert h3._token_stride("k", _Cuda((B, 1, H, D), (1000, 7, D, 1)), B, 1, H, D, 0) == 1000   # one token a sequence
-    assert h3._token_stride("k", _Cuda((1, S, H, D), (7, 1000, D, 1)), 1, S, H, D, 0) == 1000
-    assert h3._token_stride("k", _Cuda((1, 1, H, D), (7, 7, D, 1)), 1, 1, H, D, 0) == H * D
-    assert h3._token_stride("k", _Cuda((1, S, 1, D), (7, 1000, 9, 1)), 1, S, 1, D, 0) == 1000   # one head
-    for strides in ((S * 1000 + 64, 1000, D, 1), (S * 1000, 1000, D + 8, 1), (S * 1000, 1000, D, 2)):
-        with pytest.raises(h3.H3AttnError, match="stride"):
-            h3._token_stride("k", _Cuda((B, S, H, D), strides), B, S, H, D, 0)
-    with pytest.raises(h3.H3AttnError, match="current device"):
-        h3._token_stride("k", _Cuda((B, S, H, D), (S * 1000, 1000, D, 1)), B, S, H, D, 1)
+def test_the_compiled_host_path_is_bound_to_the_library(lib):
+    """Wrong counts and kinds of arguments are Python errors, nothing else."""
+    step = h3._get_step()
+    x = torch.zeros(4, 64, dtype=torch.bfloat16)
+    with pytest.raises(TypeError):
+        step.add_rmsnorm(x)
+    with pytest.raises(h3.H3AttnError, match="x must be a tensor"):
+        h3.h3attn_add_rmsnorm(None, None, None, x)
+    with pytest.raises(h3.H3AttnError, match="CUDA tensor"):
+        h3.h3attn_paged_decode(x, x, object())
+    with pytest.raises(h3.H3AttnError, match="CUDA tensor"):
+        h3.h3attn_qk_norm_rope_append(x, x, x, x, object(), None, None, None, None)
+    with pytest.raises(h3.H3AttnError, match="unknown scaling"):
+        h3.RopeScaling("cubic")

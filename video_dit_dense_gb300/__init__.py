@@ -41,6 +41,7 @@ Generation over a paged key-value cache (``PagedKV``), one step of a block:
 from __future__ import annotations
 
 import ctypes
+import importlib
 import os
 import threading
 from dataclasses import dataclass
@@ -423,49 +424,25 @@ def h3attn_prefill_window(q, k, v, o, window: Window, scale=None, mask: Mask | N
     return o
 
 
-# A step of generation is a few microseconds of kernels, so these calls keep the
-# host's part short: torch is looked up once, a tensor's checks are one
-# expression, and the current stream's handle is read without making a Stream
-# object where torch offers that.
-_torch = None
+# The generation operators are called for every token, where a call's kernels
+# take a few microseconds: their argument checks and the call itself are compiled
+# (csrc/step.cpp, _step.so), the functions here give them their names.
+_bound = None
 
 
-def _get_torch():
-    global _torch
-    if _torch is None:
-        import torch
-        _torch = torch
-    return _torch
-
-
-def _current_device(name, t):
-    """The device of t, which has to be the current one (the library launches there)."""
-    dev = t.get_device()
-    if dev < 0:
-        raise H3AttnError(H3ATTN_ERR_INVALID_ARG, f"{name} must be a CUDA tensor")
-    if dev != _torch.cuda.current_device():
-        raise H3AttnError(H3ATTN_ERR_INVALID_ARG, f"{name} must be on the current device")
-    return dev
-
-
-def _stream_on(stream, dev):
-    """Handle of the stream, by default device dev's current one."""
-    if stream is not None:
-        return _stream_handle(stream)
-    raw = getattr(_torch._C, "_cuda_getCurrentRawStream", None)
-    return raw(dev) if raw is not None else _torch.cuda.current_stream(dev).cuda_stream
-
-
-def _check(name, t, dtype, shape, dev):
-    """A contiguous tensor of this dtype and shape on CUDA device dev, without a
-    gradient; the message names what is expected."""
-    if t.dtype is dtype and t.shape == shape and t.get_device() == dev and t.is_contiguous() and not t.requires_grad:
-        return
-    if t.dtype != dtype or not t.is_cuda or not t.is_contiguous() or tuple(t.shape) != shape:
-        raise H3AttnError(H3ATTN_ERR_INVALID_ARG, f"{name} must be a contiguous {list(shape)} {dtype} CUDA tensor")
-    if t.requires_grad:
-        raise H3AttnError(H3ATTN_ERR_INVALID_ARG, f"{name}: inference only, grad-enabled inputs are rejected")
-    raise H3AttnError(H3ATTN_ERR_INVALID_ARG, f"{name} must be on the current device")
+def _get_step():
+    """The compiled host path, given the loaded library's entry points."""
+    global _bound
+    if _bound is None:
+        lib = load()
+        import torch  # noqa: F401  (the module is linked against torch's libraries)
+        if not os.path.exists(os.path.join(HERE, "_step.so")):
+            raise RuntimeError("_step.so is missing: build it with video_dit_dense_gb300.build()")
+        module = importlib.import_module("._step", __name__)
+        module.bind(H3AttnError, PagedKV, *(ctypes.cast(f, ctypes.c_void_p).value for f in (
+            lib.h3attn_add_rmsnorm, lib.h3attn_rope_table, lib.h3attn_qk_norm_rope_append, lib.h3attn_paged_decode)))
+        _bound = module
+    return _bound
 
 
 def h3attn_add_rmsnorm(x, residual, h, y, w=None, eps=1e-6, y_scale=None, stream=None):
@@ -475,47 +452,9 @@ def h3attn_add_rmsnorm(x, residual, h, y, w=None, eps=1e-6, y_scale=None, stream
     the norm is then of x; h may be x or residual); w: [C] float32 or None.
     y: [T, C], bfloat16, or float8_e4m3fn with y_scale [T] float32 (one scale a
     row) or [T, C / 32] float8_e8m0fnu or uint8 (a power of two for each 32
-    channels).
+    channels).  Returns y.
     """
-    _lib or load()
-    torch = _torch or _get_torch()
-    shape = x.shape
-    if len(shape) != 2:
-        raise H3AttnError(H3ATTN_ERR_INVALID_ARG, "x must be a [T, C] bf16 CUDA tensor")
-    T, C = shape
-    bf16, dev = torch.bfloat16, _current_device("x", x)
-    _check("x", x, bf16, shape, dev)
-    rp = hp = wp = sp = None
-    if residual is not None and h is not None:
-        _check("residual", residual, bf16, shape, dev)
-        _check("h", h, bf16, shape, dev)
-        rp, hp = residual.data_ptr(), h.data_ptr()
-    elif residual is not None or h is not None:
-        raise H3AttnError(H3ATTN_ERR_INVALID_ARG, "residual and h must be given together")
-    if w is not None:
-        _check("w", w, torch.float32, (C,), dev)
-        wp = w.data_ptr()
-    if y.dtype is bf16:
-        if y_scale is not None:
-            raise H3AttnError(H3ATTN_ERR_INVALID_ARG, "a bf16 y takes no y_scale")
-        _check("y", y, bf16, shape, dev)
-        fmt = H3ATTN_Y_BF16
-    else:
-        _check("y", y, torch.float8_e4m3fn, shape, dev)
-        if y_scale is None:
-            raise H3AttnError(H3ATTN_ERR_INVALID_ARG, "an e4m3 y needs y_scale")
-        if y_scale.dtype is torch.float32:
-            _check("y_scale", y_scale, torch.float32, (T,), dev)
-            fmt = H3ATTN_Y_E4M3_ROW
-        else:
-            _check("y_scale", y_scale, torch.uint8 if y_scale.dtype is torch.uint8 else torch.float8_e8m0fnu,
-                   (T, C // 32), dev)
-            fmt = H3ATTN_Y_E4M3_MX32
-        sp = y_scale.data_ptr()
-    st = _lib.h3attn_add_rmsnorm(x.data_ptr(), rp, hp, y.data_ptr(), wp, sp, T, C, fmt, eps, _stream_on(stream, dev))
-    if st:
-        raise H3AttnError(st, "h3attn_add_rmsnorm")
-    return y
+    return (_bound or _get_step()).add_rmsnorm(x, residual, h, y, w, eps, y_scale, stream)
 
 
 _ROPE_KINDS = {"none": H3ATTN_ROPE_NONE, "linear": H3ATTN_ROPE_LINEAR, "ntk": H3ATTN_ROPE_NTK,
@@ -533,6 +472,12 @@ class RopeScaling:
     high_turns: float = 32.0
     amplitude: float = 1.0
 
+    def __post_init__(self):
+        if self.kind not in _ROPE_KINDS:
+            raise H3AttnError(H3ATTN_ERR_INVALID_ARG, f"unknown scaling {self.kind!r}")
+        object.__setattr__(self, "_struct", h3attn_rope_scaling_t(_ROPE_KINDS[self.kind], self.original_len, self.factor,
+                                                                  self.low_turns, self.high_turns, self.amplitude))
+
 
 def h3attn_rope_table(cos, sin, rotary_dim, theta=10000.0, scaling: RopeScaling | None = None, pos=None, first=0,
                       stream=None):
@@ -541,25 +486,20 @@ def h3attn_rope_table(cos, sin, rotary_dim, theta=10000.0, scaling: RopeScaling 
     cos, sin: [N, rotary_dim / 2] float32 CUDA tensors (preallocated); pos: [N]
     int32 or None.  Returns (cos, sin).
     """
-    _lib or load()
-    torch = _torch or _get_torch()
-    dev = _current_device("cos", cos)
-    shape = (cos.shape[0] if cos.dim() else 0, rotary_dim // 2)
-    _check("cos", cos, torch.float32, shape, dev)
-    _check("sin", sin, torch.float32, shape, dev)
-    if pos is not None:
-        _check("pos", pos, torch.int32, shape[:1], dev)
-    ref = None
-    if scaling is not None:
-        if scaling.kind not in _ROPE_KINDS:
-            raise H3AttnError(H3ATTN_ERR_INVALID_ARG, f"unknown scaling {scaling.kind!r}")
-        ref = ctypes.byref(h3attn_rope_scaling_t(_ROPE_KINDS[scaling.kind], scaling.original_len, scaling.factor,
-                                                 scaling.low_turns, scaling.high_turns, scaling.amplitude))
-    st = _lib.h3attn_rope_table(cos.data_ptr(), sin.data_ptr(), _ptr(pos), first, shape[0], rotary_dim, theta, ref,
-                                _stream_on(stream, dev))
-    if st:
-        raise H3AttnError(st, "h3attn_rope_table")
+    (_bound or _get_step()).rope_table(cos, sin, rotary_dim, theta,
+                                      0 if scaling is None else ctypes.addressof(scaling._struct), pos, first, stream)
     return cos, sin
+
+
+def _check(name, t, dtype, shape, dev):
+    """A contiguous tensor of this dtype and shape on CUDA device dev, without a
+    gradient."""
+    if t.dtype != dtype or not t.is_cuda or not t.is_contiguous() or tuple(t.shape) != shape:
+        raise H3AttnError(H3ATTN_ERR_INVALID_ARG, f"{name} must be a contiguous {list(shape)} {dtype} CUDA tensor")
+    if t.requires_grad:
+        raise H3AttnError(H3ATTN_ERR_INVALID_ARG, f"{name}: inference only, grad-enabled inputs are rejected")
+    if t.get_device() != dev:
+        raise H3AttnError(H3ATTN_ERR_INVALID_ARG, f"{name} must be on the cache's device")
 
 
 class PagedKV:
@@ -567,27 +507,26 @@ class PagedKV:
 
     k_pages, v_pages: [num_pages, page_size, Hkv, D] bf16; page_table:
     [B, max_pages] int32; kv_len: [B] int32, the tokens the cache holds of each
-    sequence.  All CUDA tensors on the current device, kept by reference: their
+    sequence.  All CUDA tensors on one device, kept by reference: their
     contents may change between calls, their storage not.
     """
-    __slots__ = ("_tensors", "_struct", "_ref", "_device", "_shape")
+    __slots__ = ("_tensors", "_struct", "_address", "_device")
 
     def __init__(self, k_pages, v_pages, page_table, kv_len):
-        torch = _get_torch()
+        import torch
         if k_pages.dim() != 4 or page_table.dim() != 2:
             raise H3AttnError(H3ATTN_ERR_INVALID_ARG, "pages must be [num_pages, page_size, Hkv, D], page_table [B, max_pages]")
         num_pages, page_size, Hkv, D = k_pages.shape
         B, max_pages = page_table.shape
-        dev = _current_device("k_pages", k_pages)
-        _check("k_pages", k_pages, torch.bfloat16, (num_pages, page_size, Hkv, D), dev)
-        _check("v_pages", v_pages, torch.bfloat16, (num_pages, page_size, Hkv, D), dev)
-        _check("page_table", page_table, torch.int32, (B, max_pages), dev)
-        _check("kv_len", kv_len, torch.int32, (B,), dev)
+        self._device = k_pages.get_device()
+        _check("k_pages", k_pages, torch.bfloat16, (num_pages, page_size, Hkv, D), self._device)
+        _check("v_pages", v_pages, torch.bfloat16, (num_pages, page_size, Hkv, D), self._device)
+        _check("page_table", page_table, torch.int32, (B, max_pages), self._device)
+        _check("kv_len", kv_len, torch.int32, (B,), self._device)
         self._tensors = (k_pages, v_pages, page_table, kv_len)
         self._struct = h3attn_paged_kv_t(k_pages.data_ptr(), v_pages.data_ptr(), page_table.data_ptr(),
                                          kv_len.data_ptr(), B, num_pages, page_size, max_pages, Hkv, D)
-        self._ref = ctypes.byref(self._struct)
-        self._device, self._shape = dev, (B, Hkv, D)
+        self._address = ctypes.addressof(self._struct)
 
     k_pages = property(lambda self: self._tensors[0])
     v_pages = property(lambda self: self._tensors[1])
@@ -597,26 +536,6 @@ class PagedKV:
     def with_lengths(self, kv_len):
         """The same cache with another lengths tensor (len_out of an append)."""
         return PagedKV(self.k_pages, self.v_pages, self.page_table, kv_len)
-
-
-def _token_stride(name, t, B, S, H, D, dev):
-    """Elements from one token to the next of a [B, S, H, D] bf16 tensor whose
-    heads lie behind one another (a slice of a fused projection, say)."""
-    if t.dtype is not _torch.bfloat16 or t.shape != (B, S, H, D):
-        raise H3AttnError(H3ATTN_ERR_INVALID_ARG, f"{name} must be a {[B, S, H, D]} bf16 CUDA tensor")
-    if t.get_device() != dev:
-        raise H3AttnError(H3ATTN_ERR_INVALID_ARG, f"{name} must be on the current device")
-    if t.requires_grad:
-        raise H3AttnError(H3ATTN_ERR_INVALID_ARG, f"{name}: inference only, grad-enabled inputs are rejected")
-    if B * S * H == 0:
-        return H * D
-    sb, ss, sh, sd = t.stride()
-    if sd == 1 and sh == D and S > 1 and sb == S * ss:
-        return ss
-    stride = ss if S > 1 else sb if B > 1 else H * D
-    if sd != 1 or (H > 1 and sh != D) or (S > 1 and B > 1 and sb != S * ss):
-        raise H3AttnError(H3ATTN_ERR_INVALID_ARG, f"{name} must have contiguous heads and one stride from token to token")
-    return stride
 
 
 def h3attn_qk_norm_rope_append(q, k, v, q_out, cache: PagedKV, wq, wk, cos, sin, rotary_dim=96, eps=1e-6,
@@ -631,58 +550,8 @@ def h3attn_qk_norm_rope_append(q, k, v, q_out, cache: PagedKV, wq, wk, cos, sin,
     new_len: [B] int32 or None (all S); len_out: [B] int32 or None, receives the
     new lengths.  Returns q_out.
     """
-    _lib or load()
-    torch = _torch or _get_torch()
-    B, Hkv, D = cache._shape
-    if k.dim() != 4:
-        raise H3AttnError(H3ATTN_ERR_INVALID_ARG, "k must be a [B, S, Hkv, D] bf16 CUDA tensor")
-    dev = _current_device("k", k)
-    if cache._device != dev:
-        raise H3AttnError(H3ATTN_ERR_INVALID_ARG, "the cache must be on the current device")
-    S = k.shape[1]
-    ks = _token_stride("k", k, B, S, Hkv, D, dev)
-    vs = _token_stride("v", v, B, S, Hkv, D, dev)
-    Hq = qs = rows = 0
-    qp = op = wqp = wkp = cp = sp = pp = np = lp = None
-    if q is not None and q_out is not None:
-        if q.dim() != 4:
-            raise H3AttnError(H3ATTN_ERR_INVALID_ARG, "q must be a [B, S, Hq, D] bf16 CUDA tensor")
-        Hq = q.shape[2]
-        qs = _token_stride("q", q, B, S, Hq, D, dev)
-        _check("q_out", q_out, torch.bfloat16, (B, S, Hq, D), dev)
-        qp, op = q.data_ptr(), q_out.data_ptr()
-    elif q is not None or q_out is not None:
-        raise H3AttnError(H3ATTN_ERR_INVALID_ARG, "q_out must be given exactly when q is")
-    f32, i32 = torch.float32, torch.int32
-    if wq is not None:
-        _check("wq", wq, f32, (D,), dev)
-        wqp = wq.data_ptr()
-    if wk is not None:
-        _check("wk", wk, f32, (D,), dev)
-        wkp = wk.data_ptr()
-    if rotary_dim > 0:
-        if cos is None or sin is None:
-            raise H3AttnError(H3ATTN_ERR_INVALID_ARG, "cos and sin are required when rotary_dim > 0")
-        rows = cos.shape[0] if cos.dim() else 0
-        shape = (rows, rotary_dim // 2)
-        _check("cos", cos, f32, shape, dev)
-        _check("sin", sin, f32, shape, dev)
-        cp, sp = cos.data_ptr(), sin.data_ptr()
-    if pos is not None:
-        _check("pos", pos, i32, (B, S), dev)
-        pp = pos.data_ptr()
-    if new_len is not None:
-        _check("new_len", new_len, i32, (B,), dev)
-        np = new_len.data_ptr()
-    if len_out is not None:
-        _check("len_out", len_out, i32, (B,), dev)
-        lp = len_out.data_ptr()
-    st = _lib.h3attn_qk_norm_rope_append(qp, k.data_ptr(), v.data_ptr(), op, cache._ref, wqp, wkp, cp, sp, pp, np, lp, S, Hq,
-                                         qs, ks, vs, rows, rotary_dim, 1 if interleaved else 0, eps,
-                                         _stream_on(stream, dev))
-    if st:
-        raise H3AttnError(st, "h3attn_qk_norm_rope_append")
-    return q_out
+    return (_bound or _get_step()).append(q, k, v, q_out, cache, wq, wk, cos, sin, rotary_dim, eps, interleaved, pos, new_len,
+                                         len_out, stream)
 
 
 def h3attn_paged_decode(q, o, cache: PagedKV, scale=None, workspace=None, stream=None):
@@ -691,41 +560,16 @@ def h3attn_paged_decode(q, o, cache: PagedKV, scale=None, workspace=None, stream
     q, o: [B, 1, Hq, D] or [B, Hq, D] bf16 (o preallocated); the token's own key
     and value are in the cache.  workspace: None (one CTA walks a sequence), or
     a CUDA tensor from paged_decode_workspace(): the sequences are then split
-    over the GPU.
+    over the GPU.  Returns o.
     """
-    _lib or load()
-    torch = _torch or _get_torch()
-    shape = q.shape
-    if len(shape) == 4 and shape[1] == 1:
-        B, _, Hq, D = shape
-    elif len(shape) == 3:
-        B, Hq, D = shape
-    else:
-        raise H3AttnError(H3ATTN_ERR_INVALID_ARG, "q must be [B, 1, Hq, D] or [B, Hq, D]: one new token per sequence")
-    if (B, D) != cache._shape[::2]:
-        raise H3AttnError(H3ATTN_ERR_INVALID_ARG, "shape mismatch between q and the cache")
-    dev = _current_device("q", q)
-    if cache._device != dev:
-        raise H3AttnError(H3ATTN_ERR_INVALID_ARG, "the cache must be on the current device")
-    _check("q", q, torch.bfloat16, shape, dev)
-    _check("o", o, torch.bfloat16, shape, dev)
-    ws, nbytes = None, 0
-    if workspace is not None:
-        if workspace.get_device() != dev or not workspace.is_contiguous():
-            raise H3AttnError(H3ATTN_ERR_INVALID_ARG, "workspace must be a contiguous CUDA tensor on the current device")
-        ws, nbytes = workspace.data_ptr(), workspace.nbytes
-    st = _lib.h3attn_paged_decode(q.data_ptr(), o.data_ptr(), cache._ref, Hq, D ** -0.5 if scale is None else scale, ws,
-                                  nbytes, _stream_on(stream, dev))
-    if st:
-        raise H3AttnError(st, "h3attn_paged_decode")
-    return o
+    return (_bound or _get_step()).decode(q, o, cache, scale, workspace, stream)
 
 
 def h3attn_paged_decode_workspace_size(cache: PagedKV, Hq) -> int:
     """Bytes of workspace h3attn_paged_decode takes for this cache and Hq query heads (0: no split)."""
     load()
     out = ctypes.c_size_t(0)
-    st = _lib.h3attn_paged_decode_workspace_size(cache._ref, int(Hq), ctypes.byref(out))
+    st = _lib.h3attn_paged_decode_workspace_size(ctypes.byref(cache._struct), int(Hq), ctypes.byref(out))
     _raise_if(st, "h3attn_paged_decode_workspace_size")
     return int(out.value)
 
@@ -734,7 +578,7 @@ def paged_decode_workspace(q, cache: PagedKV):
     """A workspace tensor for h3attn_paged_decode(q, ..., cache) on the current
     device, or None when the call does not split (allocated by torch)."""
     n = h3attn_paged_decode_workspace_size(cache, q.shape[-2])
-    torch = _get_torch()
+    import torch
     return torch.empty(n, dtype=torch.uint8, device=q.device) if n else None
 
 

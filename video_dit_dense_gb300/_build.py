@@ -1,4 +1,5 @@
-"""Build libh3attn.so in-tree with nvcc for sm_103a.
+"""Build libh3attn.so in-tree with nvcc for sm_103a, and _step.so, the Python
+binding's host path of the generation operators, with g++ against torch.
 
 Translation units compile in parallel; the CUDA runtime is linked
 statically so the library loads without a CUDA toolkit on the library path.
@@ -11,12 +12,16 @@ import hashlib
 import os
 import shutil
 import subprocess
+import sys
+import sysconfig
 
 HERE = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(HERE)
 CSRC = os.path.join(HERE, "csrc")
 INCLUDE = os.path.join(ROOT, "include")
 LIB = os.path.join(HERE, "libh3attn.so")
+STEP_LIB = os.path.join(HERE, "_step.so")
+STEP_SOURCE = "step.cpp"
 BUILD_DIR = os.path.join(HERE, "_build")
 SOURCES = ["api.cu", "api_generate.cu", "qk_norm_rope.cu", "attn_fwd.cu", "rmsnorm_modulate.cu", "add_rmsnorm.cu",
            "rope_table.cu", "norm_rope_append.cu", "paged_decode.cu"]
@@ -44,13 +49,52 @@ def _stamp() -> str:
     return h.hexdigest()[:20]
 
 
+def _step_command(out: str) -> list[str]:
+    import torch
+    root = os.path.dirname(torch.__file__)
+    cuda = os.path.dirname(os.path.dirname(os.path.realpath(_nvcc())))
+    includes = [os.path.join(root, "include"), os.path.join(root, "include", "torch", "csrc", "api", "include"),
+                sysconfig.get_paths()["include"], os.path.join(cuda, "include")]
+    return ["g++", "-O2", "-std=c++17", "-fPIC", "-shared",
+            f"-D_GLIBCXX_USE_CXX11_ABI={int(torch._C._GLIBCXX_USE_CXX11_ABI)}", *(f"-isystem{i}" for i in includes),
+            os.path.join(CSRC, STEP_SOURCE), "-o", out, "-L" + os.path.join(root, "lib"), "-lc10", "-lc10_cuda", "-ltorch_cpu",
+            "-ltorch_python"]
+
+
+def _step_stamp() -> str:
+    import torch
+    h = hashlib.sha256(" ".join(_step_command("") + [torch.__version__, sys.version]).encode())
+    for path in (os.path.join(CSRC, STEP_SOURCE), os.path.join(INCLUDE, "h3attn.h")):
+        with open(path, "rb") as f:
+            h.update(f.read())
+    return h.hexdigest()[:20]
+
+
+def _current(lib: str, stamp: str) -> bool:
+    if not os.path.exists(lib) or not os.path.exists(lib + ".stamp"):
+        return False
+    with open(lib + ".stamp") as f:
+        return f.read().strip() == stamp
+
+
+def _build_step(stamp: str) -> None:
+    tmp = STEP_LIB + f".tmp{os.getpid()}"
+    r = subprocess.run(_step_command(tmp), capture_output=True, text=True)
+    if r.returncode != 0:
+        raise RuntimeError(f"g++ failed on {STEP_SOURCE}:\n{r.stderr}")
+    os.replace(tmp, STEP_LIB)
+    with open(STEP_LIB + ".stamp", "w") as f:
+        f.write(stamp)
+
+
 def build(force: bool = False, verbose: bool = False) -> str:
     stamp_path = LIB + ".stamp"
-    st = _stamp()
-    if not force and os.path.exists(LIB) and os.path.exists(stamp_path):
-        with open(stamp_path) as f:
-            if f.read().strip() == st:
-                return LIB
+    st, step_stamp = _stamp(), _step_stamp()
+    lib_current, step_current = not force and _current(LIB, st), not force and _current(STEP_LIB, step_stamp)
+    if lib_current:
+        if not step_current:
+            _build_step(step_stamp)
+        return LIB
     nvcc = _nvcc()
     os.makedirs(BUILD_DIR, exist_ok=True)
 
@@ -65,8 +109,11 @@ def build(force: bool = False, verbose: bool = False) -> str:
             print(r.stderr)
         return obj
 
-    with cf.ThreadPoolExecutor(max_workers=len(SOURCES)) as ex:
+    with cf.ThreadPoolExecutor(max_workers=len(SOURCES) + 1) as ex:
+        step = None if step_current else ex.submit(_build_step, step_stamp)
         objs = list(ex.map(compile_one, SOURCES))
+        if step is not None:
+            step.result()
     tmp = LIB + f".tmp{os.getpid()}"
     cmd = [nvcc] + ARCH + ["-shared", "-cudart", "static", "-o", tmp] + objs
     r = subprocess.run(cmd, capture_output=True, text=True)
