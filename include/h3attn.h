@@ -327,8 +327,8 @@ h3attn_status_t h3attn_prefill_window(const void* q, const void* k, const void* 
  *                        neighbouring channels, as an 8-bit exponent biased by
  *                        127 (e8m0)
  * 448 is the largest e4m3 value, so nothing saturates.  An all-zero row or
- * group has s = 1.  NaN stays NaN, and an infinite h makes its row NaN and
- * zeros as the formula does.
+ * group has s = 1.  NaN stays NaN, and an infinite h, or squares whose sum
+ * passes float32's range, make their row zeros (and NaN where 0 * infinity).
  *
  * x: [T, C] bf16; residual: [T, C] bf16 or NULL; h: [T, C] bf16 output,
  *    present exactly when residual is, may be x or residual itself.
@@ -481,8 +481,9 @@ h3attn_status_t h3attn_qk_norm_rope_append(const void* q, const void* k, const v
  * query head h reading key-value head h / (Hq / Hkv).  The new token's own
  * key and value are in the cache already (appended before the call).  A
  * sequence without a key gets a zero row.  Rows of the last page past kv_len
- * may hold anything.  Keys of a page outside [0, num_pages) are not attended
- * (and reported).
+ * may hold anything; a NaN or infinity in an attended row reaches its
+ * sequence's heads only.  Keys of a page outside [0, num_pages) are not
+ * attended (and reported).
  *
  * q, o: [B, Hq, D] bf16 (a [B, 1, Hq, D] tensor), o overlapping nothing else;
  * scale finite and > 0; Hq a multiple of cache->Hkv; B, Hq <= 65535,
@@ -492,11 +493,12 @@ h3attn_status_t h3attn_qk_norm_rope_append(const void* q, const void* k, const v
  *    nothing else; its contents on entry do not matter.  The tiles of all
  *    sequences are then dealt evenly to the SMs whatever the lengths are, and
  *    the parts of a sequence that several SMs hold are joined by a second
- *    kernel.  NULL: one CTA walks each sequence (no second kernel).  Calls
- *    that share a workspace must be ordered.
+ *    kernel.  NULL, or a geometry whose size is 0: one CTA walks each sequence
+ *    and group of key-value heads (no second kernel).  Calls that share a
+ *    workspace must be ordered: one stream, events, or graphs replayed in turn.
  * Products on the tensor cores with float32 accumulation, softmax in float32
- * with exp2, weights rounded to bf16 before the second product, the output
- * rounded once to bf16.  Results do not depend on timing.
+ * with exp2, weights kept to 16 bits in the second product, the output rounded
+ * once to bf16.  Results do not depend on timing.
  * Stream order as for h3attn_rmsnorm_modulate().
  * Errors: INVALID_ARG, MISALIGNED, UNSUPPORTED_HEAD_DIM, UNSUPPORTED_DEVICE, LAUNCH.
  */

@@ -19,16 +19,22 @@
 // the scaling.  One row a CTA of as many warps as the row fills, or a warp a
 // row; no ring and no second row in flight, the other CTAs of the SM keep the
 // memory busy.  At 32760 rows with residual, e4m3 and row scales: 5120 channels
-// 168 us, 8192 channels 265 us, 7.0 and 7.1 TB/s (a copy reaches 6.8).
+// 168 us, 4096 channels 132 us, 7.0 and 7.1 TB/s (a copy reaches 6.8).
 // CTAs that stay on their SM and ask for their next row ahead took 184 us
-// (registers) and 186 us and more (shared memory).  Threads without a
+// (registers) and 186 us and more (shared memory) at 5120.  Threads without a
 // vector cost as much as they leave idle: 256 threads for the 640 vectors of
 // 5120 channels took 195 us.  So does a register too many: 82 a thread instead of 80
 // took 318 us instead of 261 at 8192 channels, two CTAs an SM instead of three.
+// Without a residual an e4m3 output moves 3 bytes a channel instead of 7, and
+// the arithmetic is what bounds it (4096 channels: 82 us with row scales, floor 59).
+// Products run on two channels at a time (packed float32 operations); the residual's addition
+// does not: packed, its operands were waited for together, 20.3 us instead of 18.2
+// at 4099 rows of 4096.
 #include <cuda_bf16.h>
 #include <cuda_fp8.h>
 
 #include "generate.h"
+#include "ptx.cuh"
 
 namespace h3 {
 namespace {
@@ -83,8 +89,9 @@ __device__ __forceinline__ void row_reduce(float& sum, float& top) {
 }
 
 // Vector k * threads + thread of the row is the thread's k-th.
-template <int WARPS, int VPT, int FORMAT>
-__global__ void __launch_bounds__(WARPS == 1 ? kShortRows * 32 : WARPS * 32) __maxnreg__(VPT == 2 ? 48 : WARPS == 1 ? 80 : 56)
+template <int WARPS, int VPT, int FORMAT, bool RESIDUAL>
+__global__ void __launch_bounds__(WARPS == 1 ? kShortRows * 32 : WARPS * 32)
+    __maxnreg__(VPT == 2 ? 48 : WARPS == 1 ? 80 : 56)
     add_rmsnorm_kernel(const __grid_constant__ AddNormArgs a) {
   constexpr bool SHORT = WARPS == 1;
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
@@ -111,13 +118,13 @@ __global__ void __launch_bounds__(WARPS == 1 ? kShortRows * 32 : WARPS * 32) __m
     const bool in = live && v < V;
     if constexpr (kKeepWeights) weights(v, kept[k]);
     xv[k] = in ? *reinterpret_cast<const uint4*>(a.x + base + 8 * v) : make_uint4(0u, 0u, 0u, 0u);
-    rv[k] = in && a.residual ? *reinterpret_cast<const uint4*>(a.residual + base + 8 * v) : make_uint4(0u, 0u, 0u, 0u);
+    rv[k] = in && RESIDUAL ? *reinterpret_cast<const uint4*>(a.residual + base + 8 * v) : make_uint4(0u, 0u, 0u, 0u);
   }
-  float sum = 0.0f, top = 0.0f;
+  float even = 0.0f, odd = 0.0f, top = 0.0f;
 #pragma unroll
   for (int k = 0; k < VPT; ++k) {
     const int v = k * TPR + t;
-    if (a.residual) {
+    if constexpr (RESIDUAL) {
       uint32_t* x = &xv[k].x;
       const uint32_t* r = &rv[k].x;
 #pragma unroll
@@ -126,27 +133,28 @@ __global__ void __launch_bounds__(WARPS == 1 ? kShortRows * 32 : WARPS * 32) __m
     }
     const uint32_t x[4] = {xv[k].x, xv[k].y, xv[k].z, xv[k].w};
 #pragma unroll
-    for (int e = 0; e < 4; ++e) {
-      sum = fmaf(lo16(x[e]), lo16(x[e]), sum);
-      sum = fmaf(hi16(x[e]), hi16(x[e]), sum);
-    }
+    for (int e = 0; e < 4; ++e) ffma2(even, odd, lo16(x[e]), hi16(x[e]), lo16(x[e]), hi16(x[e]), even, odd);
     if constexpr (FORMAT == H3ATTN_Y_E4M3_ROW) {
       float w8[8];
       if constexpr (!kKeepWeights) weights(v, w8);
       const float(&wv)[8] = kKeepWeights ? kept[kKeepWeights ? k : 0] : w8;
 #pragma unroll
-      for (int e = 0; e < 4; ++e)
-        top = fmaxf(top, fmaxf(fabsf(lo16(x[e]) * wv[2 * e]), fabsf(hi16(x[e]) * wv[2 * e + 1])));
+      for (int e = 0; e < 4; ++e) {
+        float p0, p1;
+        fmul2(p0, p1, lo16(x[e]), hi16(x[e]), wv[2 * e], wv[2 * e + 1]);
+        top = fmax3(top, fabsf(p0), fabsf(p1));
+      }
     }
   }
+  float sum = even + odd;
   row_reduce<WARPS>(sum, top);
-  const float r = __frsqrt_rn(__fdiv_rn(sum, static_cast<float>(a.C)) + a.eps);
+  const float r = __frsqrt_rn(fmaf(sum, a.inv_C, a.eps));
   float inv = 1.0f;
   if constexpr (FORMAT == H3ATTN_Y_E4M3_ROW) {
     // not below 2^-126, so that 1 / s is finite: such a row is zero or next to it
     const float m = top * r;
-    const float s = m > 0.0f ? fmaxf(__fdiv_rn(m, 448.0f), 1.17549435e-38f) : 1.0f;
-    inv = __fdiv_rn(1.0f, s);
+    const float s = m > 0.0f ? fmaxf(m * (1.0f / 448.0f), 1.17549435e-38f) : 1.0f;
+    inv = __frcp_rn(s);
     if (live && t == 0) static_cast<float*>(a.y_scale)[row] = s;
   }
 #pragma unroll
@@ -159,7 +167,10 @@ __global__ void __launch_bounds__(WARPS == 1 ? kShortRows * 32 : WARPS * 32) __m
     const float(&wv)[8] = kKeepWeights ? kept[kKeepWeights ? k : 0] : w8;
     float y[8];
 #pragma unroll
-    for (int e = 0; e < 8; ++e) y[e] = (((e & 1) ? hi16(x[e >> 1]) : lo16(x[e >> 1])) * wv[e]) * r;
+    for (int e = 0; e < 8; e += 2) {
+      fmul2(y[e], y[e + 1], lo16(x[e >> 1]), hi16(x[e >> 1]), wv[e], wv[e + 1]);
+      fmul2(y[e], y[e + 1], y[e], y[e + 1], r, r);
+    }
     if constexpr (FORMAT == H3ATTN_Y_BF16) {
       if (in)
         *reinterpret_cast<uint4*>(static_cast<uint16_t*>(a.y) + base + 8 * v) =
@@ -169,7 +180,7 @@ __global__ void __launch_bounds__(WARPS == 1 ? kShortRows * 32 : WARPS * 32) __m
         // the four lanes of a 32-channel group hold neighbouring vectors
         float m = 0.0f;
 #pragma unroll
-        for (int e = 0; e < 8; ++e) m = fmaxf(m, fabsf(y[e]));
+        for (int e = 0; e < 8; e += 2) m = fmax3(m, fabsf(y[e]), fabsf(y[e + 1]));
         m = fmaxf(m, __shfl_xor_sync(0xFFFFFFFFu, m, 1));
         m = fmaxf(m, __shfl_xor_sync(0xFFFFFFFFu, m, 2));
         // least e with 448 * 2^e >= m, 448 = 1.75 * 2^8: the exponent of m less 8, and one more above 1.75
@@ -179,25 +190,29 @@ __global__ void __launch_bounds__(WARPS == 1 ? kShortRows * 32 : WARPS * 32) __m
         inv = __uint_as_float(static_cast<uint32_t>(254 - e8) << 23);
         if (in && (v & 3) == 0) static_cast<uint8_t*>(a.y_scale)[row * (a.C >> 5) + (v >> 2)] = static_cast<uint8_t>(e8);
       }
+#pragma unroll
+      for (int e = 0; e < 8; e += 2) fmul2(y[e], y[e + 1], y[e], y[e + 1], inv, inv);
       if (in)
         *reinterpret_cast<uint2*>(static_cast<uint8_t*>(a.y) + base + 8 * v) =
-            make_uint2(pack_e4m3x4(y[0] * inv, y[1] * inv, y[2] * inv, y[3] * inv),
-                       pack_e4m3x4(y[4] * inv, y[5] * inv, y[6] * inv, y[7] * inv));
+            make_uint2(pack_e4m3x4(y[0], y[1], y[2], y[3]), pack_e4m3x4(y[4], y[5], y[6], y[7]));
     }
   }
 }
 
 // WARPS 1: a warp a row; else a block of up to so many warps.
-template <int WARPS, int VPT>
-cudaError_t launch_rows(const AddNormArgs& a, cudaStream_t stream) {
+template <int WARPS, int VPT, int FORMAT>
+cudaError_t launch_format(const AddNormArgs& a, cudaStream_t stream) {
   const unsigned threads = WARPS == 1 ? kShortRows * 32 : ((a.C >> 3) + VPT * 32 - 1) / (VPT * 32) * 32;
   const dim3 grid(WARPS == 1 ? (static_cast<unsigned>(a.T) + kShortRows - 1) / kShortRows : a.T);
+  return a.residual ? launch_dependent(add_rmsnorm_kernel<WARPS, VPT, FORMAT, true>, grid, threads, 0, stream, a)
+                    : launch_dependent(add_rmsnorm_kernel<WARPS, VPT, FORMAT, false>, grid, threads, 0, stream, a);
+}
+template <int WARPS, int VPT>
+cudaError_t launch_rows(const AddNormArgs& a, cudaStream_t stream) {
   switch (a.format) {
-    case H3ATTN_Y_BF16:
-      return launch_dependent(add_rmsnorm_kernel<WARPS, VPT, H3ATTN_Y_BF16>, grid, threads, 0, stream, a);
-    case H3ATTN_Y_E4M3_ROW:
-      return launch_dependent(add_rmsnorm_kernel<WARPS, VPT, H3ATTN_Y_E4M3_ROW>, grid, threads, 0, stream, a);
-    default: return launch_dependent(add_rmsnorm_kernel<WARPS, VPT, H3ATTN_Y_E4M3_MX32>, grid, threads, 0, stream, a);
+    case H3ATTN_Y_BF16: return launch_format<WARPS, VPT, H3ATTN_Y_BF16>(a, stream);
+    case H3ATTN_Y_E4M3_ROW: return launch_format<WARPS, VPT, H3ATTN_Y_E4M3_ROW>(a, stream);
+    default: return launch_format<WARPS, VPT, H3ATTN_Y_E4M3_MX32>(a, stream);
   }
 }
 
@@ -210,8 +225,11 @@ cudaError_t launch_add_rmsnorm(const AddNormArgs& a, cudaStream_t stream) {
   if (V <= 64) return launch_rows<1, 2>(a, stream);
   if (V <= 128 && a.T >= 512) return launch_rows<1, 4>(a, stream);
   // Two vectors a thread while the rows are short or few (one row of 5120 channels 1.7 us, with four 2.4; 1200 rows 8.5
-  // and 11.1), four with weights read twice where the memory is what counts (32760 rows 168 us, with two 174; of 8192 channels
-  // 265 and 313).
+  // and 11.1), four with weights read twice where the memory is what counts (32760 rows 168 us, with two 174; of 8192
+  // channels 265 and 313).
+  // Without a residual the memory leaves less time for a thread's fixed part, and scales of 32 channels cost the most: four
+  // vectors from 257 on (32760 rows of 4096 channels 70 us, with two 89).
+  if (V > 256 && V <= 512 && !a.residual && a.format == H3ATTN_Y_E4M3_MX32) return launch_rows<8, 4>(a, stream);
   if (V <= 512) return launch_rows<8, 2>(a, stream);
   if (V <= 1024 && a.T < 2048) return launch_rows<16, 2>(a, stream);
   if (V <= 1024) return launch_rows<8, 4>(a, stream);

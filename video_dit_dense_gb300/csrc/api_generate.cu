@@ -126,6 +126,7 @@ h3attn_status_t h3attn_add_rmsnorm(const void* x, const void* residual, void* h,
   a.C = C;
   a.format = y_format;
   a.eps = eps;
+  a.inv_C = 1.0f / static_cast<float>(C);
   return h3::launch_add_rmsnorm(a, static_cast<cudaStream_t>(stream)) == cudaSuccess ? H3ATTN_OK : H3ATTN_ERR_LAUNCH;
 }
 

@@ -42,7 +42,7 @@ struct AddNormArgs {
   const float* w;            // [C] or nullptr
   void* y_scale;             // [T] float32 (row), [T, C/32] e8m0 (MX), nullptr (bf16)
   int T, C, format;
-  float eps;
+  float eps, inv_C;
 };
 constexpr int kAddNormMaxChannels = 16384;
 cudaError_t launch_add_rmsnorm(const AddNormArgs& a, cudaStream_t stream);

@@ -59,21 +59,12 @@ __global__ void __launch_bounds__(kThreads, 4) append_kernel(const __grid_consta
   static_assert(LPR >= U, "a lane for each row that shares the square root and the quotient");
   // kStraddling: a row for each row's lanes, 16 bytes apart so that the warp's rows lie in other banks
   __shared__ __align__(16) uint16_t rowbuf[LAYOUT == kStraddling ? kThreads / LPR : 1][LAYOUT == kStraddling ? D + 8 : 8];
-  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
-  asm volatile("griddepcontrol.wait;" ::: "memory");
   const int warp = threadIdx.x >> 5;
   const uint32_t lane = threadIdx.x & 31, lr = lane % LPR, slot = lane / LPR;
-  if (blockIdx.x == 0 && a.len_out) {
-    const int64_t capacity = static_cast<int64_t>(a.max_pages) * a.page_size;
-    for (int b = threadIdx.x; b < a.B; b += kThreads) {
-      const int64_t n = a.new_len ? min(max(a.new_len[b], 0), a.S) : a.S;
-      a.len_out[b] = static_cast<int32_t>(min(static_cast<int64_t>(max(a.kv_len[b], 0)) + n, capacity));
-    }
-  }
   // A row's lanes stay with one token, RPW tokens a warp, and walk over its heads [first, last) of Hq + 2 Hkv.
   const uint32_t item = blockIdx.x * (kThreads / 32) + warp;
-  if (item >= a.items) return;
-  const uint32_t tokens_at = fdiv(item, a.div_parts), part = item - tokens_at * a.div_parts.d;
+  const bool used = item < a.items;
+  const uint32_t tokens_at = fdiv(used ? item : 0u, a.div_parts), part = (used ? item : 0u) - tokens_at * a.div_parts.d;
   const uint32_t hw = 1u << a.heads_log2, head_slot = slot & (hw - 1), token_slot = slot >> a.heads_log2;
   const uint32_t my_token = (tokens_at * RPW >> a.heads_log2) + token_slot;
   const uint32_t token = min(my_token, a.tokens - 1);
@@ -82,6 +73,16 @@ __global__ void __launch_bounds__(kThreads, 4) append_kernel(const __grid_consta
   int first = static_cast<int>(part) * a.heads_per_part;
   const uint32_t b = fdiv(token, a.div_s);
   const int s = static_cast<int>(token - b * a.S);
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+  asm volatile("griddepcontrol.wait;" ::: "memory");
+  if (blockIdx.x == 0 && a.len_out) {
+    const int64_t capacity = static_cast<int64_t>(a.max_pages) * a.page_size;
+    for (int b = threadIdx.x; b < a.B; b += kThreads) {
+      const int64_t n = a.new_len ? min(max(a.new_len[b], 0), a.S) : a.S;
+      a.len_out[b] = static_cast<int32_t>(min(static_cast<int64_t>(max(a.kv_len[b], 0)) + n, capacity));
+    }
+  }
+  if (!used) return;
   if (a.new_len) live = live && s < a.new_len[b];  // the others are padding
   if (!__any_sync(0xFFFFFFFFu, live)) return;
   const int half = a.rotary_dim >> 1;
@@ -149,7 +150,8 @@ __global__ void __launch_bounds__(kThreads, 4) append_kernel(const __grid_consta
     } else {
 #pragma unroll
       for (int e = 0; e < 8; ++e) {
-        const int i = LAYOUT == kInterleaved ? static_cast<int>((e < 4 ? g0 : g1) * 4) + (e & 3) : static_cast<int>(lr) + LPR * e;
+        const int i = LAYOUT == kInterleaved ? static_cast<int>((e < 4 ? g0 : g1) * 4) + (e & 3)
+                                             : static_cast<int>(lr) + LPR * e;
         if (i < half) {
           cv[e] = a.cos[at + i];
           sv[e] = a.sin[at + i];
@@ -221,7 +223,8 @@ __global__ void __launch_bounds__(kThreads, 4) append_kernel(const __grid_consta
               if (i < half) {
                 const float na = __uint_as_float(static_cast<uint32_t>(buf[i]) << 16);
                 const float nb = __uint_as_float(static_cast<uint32_t>(buf[i + half]) << 16);
-                const uint32_t y = pack_bf16(__fmaf_rn(na, cv[e], -__fmul_rn(nb, sv[e])), __fmaf_rn(nb, cv[e], __fmul_rn(na, sv[e])));
+                const uint32_t y = pack_bf16(__fmaf_rn(na, cv[e], -__fmul_rn(nb, sv[e])),
+                                             __fmaf_rn(nb, cv[e], __fmul_rn(na, sv[e])));
                 buf[i] = static_cast<uint16_t>(y);
                 buf[i + half] = static_cast<uint16_t>(y >> 16);
               }

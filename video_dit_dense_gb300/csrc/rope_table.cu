@@ -79,18 +79,22 @@ __device__ __forceinline__ void sincos2(const float (&x)[2], const uint32_t (&qu
 // that their phase steps stay in registers.
 template <int VEC>
 __global__ void __launch_bounds__(kThreads) rope_table_kernel(const __grid_constant__ RopeTableArgs a) {
-  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
-  asm volatile("griddepcontrol.wait;" ::: "memory");
+  // What the launch alone gives is read before the wait on the previous kernel.
   const int per_row = a.half / VEC;  // <= kMaxRotaryPairs < kThreads
   const int rows = kThreads / per_row;
   const int col = threadIdx.x % per_row, lane_row = threadIdx.x / per_row;
-  if (lane_row >= rows) return;
   uint64_t turn[VEC];
 #pragma unroll
   for (int e = 0; e < VEC; ++e) turn[e] = a.turn[col * VEC + e];
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+  asm volatile("griddepcontrol.wait;" ::: "memory");
+  if (lane_row >= rows) return;
   const int64_t step = static_cast<int64_t>(gridDim.x) * rows;
-  for (int64_t n = static_cast<int64_t>(blockIdx.x) * rows + lane_row; n < a.N; n += step) {
-    const int p = a.pos ? a.pos[n] : static_cast<int>(a.first + n);
+  int64_t n = static_cast<int64_t>(blockIdx.x) * rows + lane_row;
+  int p_next = a.pos && n < a.N ? a.pos[n] : 0;
+  for (; n < a.N; n += step) {
+    const int p = a.pos ? p_next : static_cast<int>(a.first + n);
+    if (a.pos && n + step < a.N) p_next = a.pos[n + step];
     constexpr int PAIRS = VEC == 1 ? 2 : VEC;  // the polynomials take two at a time
     float x[PAIRS], c[PAIRS], s[PAIRS];
     uint32_t q[PAIRS];
@@ -123,7 +127,7 @@ cudaError_t launch_rope_table(const RopeTableArgs& a, cudaStream_t stream) {
   const int vec = a.half % 4 == 0 ? 4 : 1;
   const int rows = kThreads / (a.half / vec);
   int64_t blocks = (static_cast<int64_t>(a.N) + rows - 1) / rows;
-  if (blocks > sms * 8) blocks = sms * 8;  // 2048 threads an SM
+  if (blocks > sms * 6) blocks = sms * 6;  // as many as 40 registers a thread let stay
   const dim3 grid(static_cast<unsigned>(blocks));
   return vec == 4 ? launch_dependent(rope_table_kernel<4>, grid, kThreads, 0, stream, a)
                   : launch_dependent(rope_table_kernel<1>, grid, kThreads, 0, stream, a);
