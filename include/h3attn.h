@@ -1,11 +1,12 @@
 /*
  * libh3attn -- the MiniMax-H3 / Wan video-DiT attention step on one GB300
  * (sm_103a): fused Q/K RMSNorm + bf16 boundary + partial RoPE, then dense
- * prefill attention.
+ * prefill attention; and generation after it, token by token over a paged
+ * key-value cache.
  *
  * Conventions shared by every entry point
  * ---------------------------------------
- * - Tensors are bf16, contiguous, in BSHD layout [batch, sequence, heads,
+ * - Tensors are bf16, contiguous (unless a call takes a stride), in BSHD layout [batch, sequence, heads,
  *   head_dim] (FastVideo PR #1832 "Add FlashInfer attention backend support
  *   for MiniMax H3", section "Summary": query/key/value are
  *   [batch, sequence, heads, head_dim]).  bf16 is passed as raw 16-bit words.

@@ -54,14 +54,15 @@ def gather(pages, table_row, n, page):
 
 def decode_f64(q, k, v, table, lens, page, scale, skip=None):
     """(o, bound): attention of q [B, Hq, D] over each sequence's first lens[b]
-    tokens in float64, and how far a float32 computation with bf16 weights may
-    be off.  skip[b]: tokens that are not attended.
+    tokens in float64, and how far a float32 computation whose weights are the
+    sum of two bf16 values may be off.  skip[b]: tokens that are not attended.
 
     With d = (D + 8) 2^-24 max_j scale sum|q k_j| + 2^-20 the error of a score
     in exp's argument (a float32 dot product of D terms, its scaling and the
     running maximum's subtraction) and of exp2, every weight is off by a factor
-    of at most e^(2 d) with the sum's; a weight is rounded to bf16 once more
-    and the output once: |error| <= 2^-8 |o| + (2^-8 + 4 d) sum_j p_j |v_j|."""
+    of at most e^(2 d) with the sum's; a weight loses 2^-8 of what its own
+    rounding by 2^-8 left, and the output is rounded once:
+    |error| <= 2^-8 |o| + (2^-16 + 4 d) sum_j p_j |v_j|."""
     B, Hq, D = q.shape
     Hkv = k.shape[2]
     o, bound = torch.zeros(B, Hq, D, dtype=torch.float64), torch.zeros(B, Hq, D, dtype=torch.float64)
@@ -79,7 +80,7 @@ def decode_f64(q, k, v, table, lens, page, scale, skip=None):
             p = torch.softmax(kh @ qh * scale, 0)
             o[b, h] = p @ vh
             d = (D + 8) * F32_HALF * float((kh.abs() @ qh.abs()).max()) * scale + 2.0 ** -20
-            bound[b, h] = BF16_HALF * o[b, h].abs() + (BF16_HALF + 4 * d) * (p @ vh.abs()) + 1e-30
+            bound[b, h] = BF16_HALF * o[b, h].abs() + (BF16_HALF ** 2 + 4 * d) * (p @ vh.abs()) + 1e-30
     return o, bound
 
 

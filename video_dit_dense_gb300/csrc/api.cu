@@ -13,7 +13,6 @@ using h3::check_device;
 using h3::head_dim_ok;
 using h3::kMaxDevices;
 using h3::overlap;
-using h3::wait_limit_ns;
 
 namespace {
 
@@ -47,6 +46,13 @@ bool make_bshd_map(CUtensorMap* m, const void* ptr, int B, int S, int H, int D) 
                   estr, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
                   CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
   return r == CUDA_SUCCESS;
+}
+
+uint64_t wait_limit_ns() {
+  const char* s = getenv("H3ATTN_WAIT_LIMIT_MS");
+  long ms = s ? strtol(s, nullptr, 10) : 0;
+  if (ms <= 0) ms = 2000;
+  return static_cast<uint64_t>(ms) * 1000000ull;
 }
 
 }  // namespace

@@ -2,7 +2,6 @@
 #pragma once
 
 #include <stdint.h>
-#include <stdlib.h>
 
 #include <atomic>
 
@@ -42,13 +41,5 @@ inline bool overlap(const void* a, int64_t na, const void* b, int64_t nb) {
 }
 
 inline bool head_dim_ok(int D) { return D == 64 || D == 128 || D == 256; }
-
-// Limit of one device-side wait.
-inline uint64_t wait_limit_ns() {
-  const char* s = getenv("H3ATTN_WAIT_LIMIT_MS");
-  long ms = s ? strtol(s, nullptr, 10) : 0;
-  if (ms <= 0) ms = 2000;
-  return static_cast<uint64_t>(ms) * 1000000ull;
-}
 
 }  // namespace h3

@@ -324,7 +324,6 @@ h3attn_status_t h3attn_paged_decode(const void* q, void* o, const h3attn_paged_k
   a.scale_log2 = scale * 1.4426950408889634f;
   a.status = h3::status_word_ptr();
   if (!a.status) return H3ATTN_ERR_LAUNCH;
-  a.wait_limit_ns = h3::wait_limit_ns();
   return h3::launch_decode(a, static_cast<cudaStream_t>(stream)) == cudaSuccess ? H3ATTN_OK : H3ATTN_ERR_LAUNCH;
 }
 

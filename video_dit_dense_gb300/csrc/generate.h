@@ -103,7 +103,6 @@ struct DecodeArgs {
   float scale_log2;  // scale * log2(e)
   float* ws;         // partials, or nullptr: each sequence is walked by one CTA
   int* status;
-  uint64_t wait_limit_ns;
 };
 // Workspace bytes of a call on the current device (0: the call does not split).
 cudaError_t decode_workspace(const DecodeArgs& a, size_t* bytes);
