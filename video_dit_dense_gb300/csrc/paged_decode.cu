@@ -21,7 +21,8 @@
 // stretch of the pages, and its other factor WT = warps / WH splits the
 // tokens.  All sequences' tiles of TILE tokens are numbered through and cut into
 // one range an SM (for each group of WH unit heads), so CTAs differ by one tile
-// however unlike the lengths are.  A range that holds all of a sequence
+// however unlike the lengths are; each sequence counts two tiles a warp more than it
+// has, which is what starting on one takes.  A range that holds all of a sequence
 // writes its output; of a sequence that ranges share, each range writes its
 // unnormalised O, its maximum and its sum to the workspace, and a second
 // kernel joins them in the order of the ranges (results do not depend on
@@ -40,6 +41,7 @@
 // copy reaches 6.8).  16 sequences of 4096 to 8192 tokens, 4 heads of 128: 36 us
 // of 30 at that rate: 4 us until the first tile has come through lengths, page
 // table and rows, 3 us between the first and the last CTA's end, 2 us for the join.
+// 64 sequences of up to 2048 tokens, 2 heads of 64: 11 us of 5.
 // One row of 256 bytes a bulk copy instead (any page size, no lane work) took
 // 236 us for the first case: about 14 cycles a copy and SM.  Joining in the decode kernel
 // by the CTA that arrives last took 41 us for the second: the arrival's fence and atomic,
@@ -130,6 +132,7 @@ struct DecodePlan {
   int groups;      // CTAs across the unit heads
   int ranges;      // ranges of tiles, 0: one range per sequence (no split)
   int min_tiles;   // tiles that a range has at least
+  int start;       // what starting on a sequence costs a CTA, in tiles
 };
 
 struct Kernelargs {
@@ -153,15 +156,18 @@ struct Ranges {
 // Ranges of at least min_tiles, but no fewer than there are sequences: a CTA
 // that walks several short ones joins its warps once for each.
 __device__ __forceinline__ Ranges cut(const DecodePlan& p, int T, int sequences) {
+  const int tiles = T - sequences * p.start;
   Ranges c;
-  c.count = max(1, min(p.ranges, max((T + p.min_tiles - 1) / p.min_tiles, sequences)));
+  c.count = max(1, min(p.ranges, max((tiles + p.min_tiles - 1) / p.min_tiles, sequences)));
   c.each = T / c.count;
   c.longer = T - c.each * c.count;
   return c;
 }
 
-// end[b] = tiles of sequences 0 .. b and len[b] (unless null) their tokens, for
-// all b < B, in shared memory.  Every thread of the block takes part; returns
+// end[b] = places of sequences 0 .. b on the line that ranges are cut from, and
+// len[b] (unless null) their tokens, for all b < B, in shared memory.  A sequence with a key
+// has p.start places without a tile, then one for each tile, so that a CTA
+// that starts on a sequence inside its range gets fewer tiles.  Every thread of the block takes part; returns
 // the ranges that the tiles are cut into.
 template <int THREADS>
 __device__ __forceinline__ Ranges scan_tiles(const DecodeArgs& a, const DecodePlan& p, int tile, int* end, int* len) {
@@ -171,7 +177,7 @@ __device__ __forceinline__ Ranges scan_tiles(const DecodeArgs& a, const DecodePl
   for (int b0 = 0; b0 < a.B; b0 += THREADS) {
     const int b = b0 + static_cast<int>(threadIdx.x);
     const int tokens = b < a.B ? len_of(a, b) : 0;
-    int n = (tokens + tile - 1) / tile;
+    int n = tokens > 0 ? (tokens + tile - 1) / tile + p.start : 0;
     const int there = __popc(__ballot_sync(0xFFFFFFFFu, n > 0));
 #pragma unroll
     for (int off = 1; off < 32; off <<= 1) {
@@ -267,6 +273,10 @@ __global__ void __launch_bounds__(DecodeCfg<D, NT>::kWarps * 32, 1) decode_kerne
   }
   auto seq_begin = [&](int b) { return p.ranges > 0 && b > 0 ? end[b - 1] : 0; };
   auto seq_end = [&](int b) { return p.ranges > 0 ? end[b] : t1; };
+  // the sequence's tiles that this range holds: [first_tile, stop_tile)
+  const int start = p.ranges > 0 ? p.start : 0;
+  auto first_tile = [&](int b) { return max(t0 - seq_begin(b) - start, 0); };
+  auto stop_tile = [&](int b) { return min(t1, seq_end(b)) - seq_begin(b) - start; };
   auto seq_len = [&](int b) { return lens[p.ranges > 0 ? b : 0]; };
 
   // The tiles that this warp loads, in the order it uses them, over sequence borders.
@@ -280,15 +290,15 @@ __global__ void __launch_bounds__(DecodeCfg<D, NT>::kWarps * 32, 1) decode_kerne
         return;
       }
       ++w.b;
-      w.stop = min(t1, seq_end(w.b)) - seq_begin(w.b);
+      w.stop = stop_tile(w.b);
       w.tile = wt;
       w.len = seq_len(w.b);
     }
   };
   Walk ld;
   ld.b = b0;
-  ld.tile = t0 - seq_begin(b0) + wt;
-  ld.stop = min(t1, seq_end(b0)) - seq_begin(b0);
+  ld.tile = first_tile(b0) + wt;
+  ld.stop = stop_tile(b0);
   ld.len = seq_len(b0);
   enter(ld);
 
@@ -346,24 +356,50 @@ __global__ void __launch_bounds__(DecodeCfg<D, NT>::kWarps * 32, 1) decode_kerne
 #pragma unroll
   for (int i = 0; i < STAGES - 1; ++i) load(i, mask_of[i]);
 
+  // The queries of a sequence as the second operand of the score product; where registers are left, those of the next
+  // sequence are loaded while the present one is walked.
+  const int g = lane >> 2, t = lane & 3;
+  auto load_q = [&](int b, uint32_t (&qf)[NT][D / 16][2]) {
+#pragma unroll
+    for (int n = 0; n < NT; ++n) {
+      const bool there = n * 8 + g < heads;
+      const uint16_t* qp = a.q + (static_cast<int64_t>(b) * a.Hq + head0 + (there ? n * 8 + g : 0)) * D + 2 * t;
+#pragma unroll
+      for (int ks = 0; ks < D / 16; ++ks) {
+        qf[n][ks][0] = there ? *reinterpret_cast<const uint32_t*>(qp + ks * 16) : 0u;
+        qf[n][ks][1] = there ? *reinterpret_cast<const uint32_t*>(qp + ks * 16 + 8) : 0u;
+      }
+    }
+  };
+  constexpr bool AHEAD = NT == 1 && D <= 128;
+  uint32_t q_next[AHEAD ? NT : 1][AHEAD ? D / 16 : 1][2];
+  if constexpr (AHEAD) {
+    int b1 = b0;
+    while (p.ranges > 0 && seq_end(b1) < t1 && first_tile(b1) >= stop_tile(b1)) ++b1;
+    load_q(b1, q_next);
+  }
+
   int turn = 0;  // tiles used by this warp
   int b = b0;
   bool first_segment = true;
-  const int g = lane >> 2, t = lane & 3;
   while (true) {
-    const int s0 = max(t0 - seq_begin(b), 0), s1 = min(t1, seq_end(b)) - seq_begin(b);
+    const int s0 = first_tile(b), s1 = stop_tile(b);
     if (s0 < s1 || p.ranges == 0) {
       // ---- one sequence's tiles [s0, s1) ----
       uint32_t qf[NT][D / 16][2];
+      if constexpr (AHEAD) {
 #pragma unroll
-      for (int n = 0; n < NT; ++n) {
-        const bool there = n * 8 + g < heads;
-        const uint16_t* qp = a.q + (static_cast<int64_t>(b) * a.Hq + head0 + (there ? n * 8 + g : 0)) * D + 2 * t;
+        for (int n = 0; n < NT; ++n)
 #pragma unroll
-        for (int ks = 0; ks < D / 16; ++ks) {
-          qf[n][ks][0] = there ? *reinterpret_cast<const uint32_t*>(qp + ks * 16) : 0u;
-          qf[n][ks][1] = there ? *reinterpret_cast<const uint32_t*>(qp + ks * 16 + 8) : 0u;
-        }
+          for (int ks = 0; ks < D / 16; ++ks) {
+            qf[n][ks][0] = q_next[n][ks][0];
+            qf[n][ks][1] = q_next[n][ks][1];
+          }
+        int next = b + 1;  // the range's next sequence with a key, if there is one
+        while (p.ranges > 0 && seq_end(next - 1) < t1 && first_tile(next) >= stop_tile(next)) ++next;
+        if (p.ranges > 0 && seq_end(next - 1) < t1) load_q(next, q_next);
+      } else {
+        load_q(b, qf);
       }
       float o[NT][D / 16][4];
       // m: what the exponents are taken against, within 8 of the running maximum; l: the lane's part of the sum
@@ -544,7 +580,7 @@ __global__ void __launch_bounds__(DecodeCfg<D, NT>::kWarps * 32, 1) decode_kerne
         }
       }
       if (wt == 0) {
-        const bool whole = s0 == 0 && s1 == seq_end(b) - seq_begin(b);
+        const bool whole = s0 == 0 && s1 == seq_end(b) - seq_begin(b) - start;
         if (whole) {
 #pragma unroll
           for (int n = 0; n < NT; ++n)
@@ -609,6 +645,7 @@ template <int D>
 __global__ void __launch_bounds__(kJoinThreads) __maxnreg__(D == 256 ? 96 : 56)
     decode_join_kernel(const __grid_constant__ Kernelargs k, int tile, int tile_heads) {
   constexpr int VEC = D / 32, WARPS = kJoinThreads / 32;
+  static_assert((WARPS & (WARPS - 1)) == 0, "warps are shared out to heads in powers of two");
   const DecodeArgs& a = k.a;
   const DecodePlan& p = k.p;
   __shared__ int end[kMaxSplitBatch];
@@ -617,16 +654,16 @@ __global__ void __launch_bounds__(kJoinThreads) __maxnreg__(D == 256 ? 96 : 56)
   __shared__ float part_o[WARPS][D];
   __shared__ float2 part_ml[WARPS];
   const Ranges ranges = scan_tiles<kJoinThreads>(a, p, tile, end, nullptr);
-  // The ranges cut a sequence in the middle where one begins inside it: the
+  // A sequence's tiles are in several ranges where one begins among them: the
   // first such range speaks for it.  The lists are in the order of the ranges,
   // so that every CTA has the same ones.
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   uint32_t mine = 0;
   int kind = -1;
   if (const int r = threadIdx.x; r > 0 && r < ranges.count) {
-    const int t = ranges.begin(r), b = sequence_at(end, a.B, t), begin = b > 0 ? end[b - 1] : 0;
-    if (begin < t && ranges.begin(r - 1) <= begin) {
-      const int last = ranges.of(end[b] - 1);
+    const int b = sequence_at(end, a.B, ranges.begin(r)), begin = b > 0 ? end[b - 1] : 0;
+    const int last = ranges.of(end[b] - 1);
+    if (r == ranges.of(begin + p.start) + 1 && r <= last) {
       kind = last - r + 2 > kFewParts ? 0 : 1;
       mine = static_cast<uint32_t>(b) << 16 | static_cast<uint32_t>(r - 1) << 8 | static_cast<uint32_t>(last);
     }
@@ -796,7 +833,11 @@ DecodePlan make_plan(const DecodeArgs& a, int sms, bool split) {
   // - tiles do not fit 32 bits.
   const int tile = a.D == 64 ? 32 : 16;
   const int64_t capacity = static_cast<int64_t>(a.max_pages) * a.page_size;
-  const bool whole = capacity <= 4 * p.WT * tile || a.B > kMaxSplitBatch || (capacity / 16 + 1) * a.B > INT32_MAX;
+  // Two tiles a warp, what joining its warps and asking for the next queries take (64 sequences of up to 2048 tokens, 2 key-value
+  // heads of 64: 13.1 us without them, 11.0 with them; 200 of up to 500, 8 and 1 head of 128: 27.9 and 24.1).
+  p.start = 2 * p.WT;
+  const bool whole =
+      capacity <= 4 * p.WT * tile || a.B > kMaxSplitBatch || (capacity / 16 + 1 + p.start) * a.B > INT32_MAX;
   p.ranges = split && !whole ? std::max(1, std::min(sms / p.groups, kMaxRanges)) : 0;
   p.min_tiles = p.WT;  // one a warp: two or more take longer than their partials (7.6 us against 7.0 at 1024 tokens)
   return p;
