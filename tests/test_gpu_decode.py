@@ -64,6 +64,32 @@ def test_heads_and_head_dims(h3, Hq, Hkv, D):
 
 
 @pytest.mark.gpu
+@pytest.mark.parametrize("D", [64, 128, 256])
+@pytest.mark.parametrize("Hq,Hkv", [(32, 1), (31, 1), (34, 2), (48, 1), (64, 1), (96, 3), (128, 4), (256, 8)])
+@pytest.mark.parametrize("capacity", [264, 3000])
+def test_more_heads_than_a_tile(h3, capacity, Hq, Hkv, D):
+    """Several tiles of query heads to a key-value head, in one launch and in two: odd and even numbers of token tiles,
+    and sequences that end at every place of a pair of them."""
+    check(h3, Case([1, 0, 15, 16, 17, 32, 33, 47, 49, 64, 65, 130, 263], Hq, Hkv, D, 8, capacity=capacity, seed=D + Hq))
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("D", [128, 256])
+def test_more_heads_than_a_tile_with_bad_pages(h3, D):
+    c = Case([100, 40, 1500], 32, 1, D, 16, capacity=1600, seed=D)
+    c.table[0, 1] = -1
+    c.table[1, 0] = c.table[1, 1] = c.table[1, 2] = c.k.shape[0]
+    c.table[2, 50] = 2 ** 31 - 1
+    ref, bound = c.reference([set(range(16, 32)), set(range(40)), set(range(800, 816))])
+    c.cuda(h3)
+    for split in (True, False):
+        o = c.run(h3, split)
+        assert h3.h3attn_check_device_status() == h3.H3ATTN_ERR_INVALID_ARG
+        close(o, ref, bound, f"split={split}")
+        assert bool((o[1] == 0).all())
+
+
+@pytest.mark.gpu
 @pytest.mark.parametrize("page", [1, 3, 16, 24, 64, 1000])
 @pytest.mark.parametrize("D", [64, 128, 256])
 def test_lengths_around_tiles_and_pages(h3, page, D):

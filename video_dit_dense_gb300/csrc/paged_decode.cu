@@ -12,8 +12,10 @@
 //   O^T[16 channels, 8 heads] += V^T[16, 16 tokens] P^T[16 tokens, 8 heads]
 // so that up to 8 heads cost one pass, and P^T is S^T's accumulator with each
 // 8x8 block transposed (movmatrix).  Groups of 9 to 16 heads take two column
-// tiles; larger groups are cut into tiles of 16 that read the cache again
-// (from L2, as they run side by side).
+// tiles; larger groups are cut into tiles of 16.  Where there is an even number
+// of those, the two warps of neighbouring ones load every second token tile
+// each and use both, a barrier of the pair a turn; an odd number reads the cache
+// again for each (from L2, as they run side by side).
 //
 // Work.  Lengths are known on the device only, and are unlike.  A "unit head"
 // is a key-value head (and a tile of 16 query heads of its group).  A CTA
@@ -93,6 +95,8 @@ __device__ __forceinline__ void ldmatrix4_trans(uint32_t (&r)[4], uint32_t addr)
                : "r"(addr)
                : "memory");
 }
+// Of the two warps that use barrier `id`.
+__device__ __forceinline__ void pair_sync(int id) { asm volatile("bar.sync %0, 64;" ::"r"(id) : "memory"); }
 __device__ __forceinline__ void prefetch_l2(const void* p) { asm volatile("prefetch.global.L2 [%0];" ::"l"(p)); }
 // The transpose of an 8x8 block of 16-bit values held as an accumulator fragment.
 __device__ __forceinline__ uint32_t transpose8x8(uint32_t v) {
@@ -129,6 +133,7 @@ struct DecodePlan {
   int unit_heads;  // Hkv * tiles of query heads
   int q_tiles;     // tiles of at most 16 query heads in a group
   int WH, WT;      // warps of a CTA: unit heads x token splits
+  int share;       // neighbouring tiles of query heads whose warps load for one another (1 or 2)
   int groups;      // CTAs across the unit heads
   int ranges;      // ranges of tiles, 0: one range per sequence (no split)
   int min_tiles;   // tiles that a range has at least
@@ -222,7 +227,7 @@ __host__ __device__ constexpr int64_t partial_floats(int heads, int D) {
   return partial_o(heads) + static_cast<int64_t>(heads) * D;
 }
 
-template <int D, int NT>
+template <int D, int NT, int SHARE>
 __global__ void __launch_bounds__(DecodeCfg<D, NT>::kWarps * 32, 1) decode_kernel(const __grid_constant__ Kernelargs k) {
   using C = DecodeCfg<D, NT>;
   constexpr int TILE = C::kTile, MT = TILE / 16, STAGES = C::kStages;
@@ -234,6 +239,7 @@ __global__ void __launch_bounds__(DecodeCfg<D, NT>::kWarps * 32, 1) decode_kerne
   float* stats = reinterpret_cast<float*>(smem + C::kRing + C::kJoin);
   int* end = reinterpret_cast<int*>(smem + C::kRing + C::kJoin + C::kStats);
   int* lens = end + kMaxSplitBatch;  // without a split: of the one sequence
+  __shared__ uint32_t shared_mask[SHARE > 1 ? C::kWarps : 1][STAGES];  // tokens of each warp's stages that are attended
   // The lengths and the page table are the first two links of the chain to the first K and V row, and the last
   // step's cache has pushed them out of L2: they are brought back while the kernel before this one drains.  (L2 is
   // where all SMs' writes meet, so what that kernel still writes is not missed.)
@@ -248,6 +254,8 @@ __global__ void __launch_bounds__(DecodeCfg<D, NT>::kWarps * 32, 1) decode_kerne
 
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int wh = warp % p.WH, wt = warp / p.WH;
+  // Warps that share their tiles: of the same tokens, neighbouring unit heads.
+  const int peer = warp % SHARE, peer0 = warp - peer;
   const int r = blockIdx.x / p.groups;
   const int unit = (blockIdx.x - r * p.groups) * p.WH + wh;
   const int kvh = unit / p.q_tiles, qt = unit - kvh * p.q_tiles;
@@ -279,7 +287,7 @@ __global__ void __launch_bounds__(DecodeCfg<D, NT>::kWarps * 32, 1) decode_kerne
   auto stop_tile = [&](int b) { return min(t1, seq_end(b)) - seq_begin(b) - start; };
   auto seq_len = [&](int b) { return lens[p.ranges > 0 ? b : 0]; };
 
-  // The tiles that this warp loads, in the order it uses them, over sequence borders.
+  // The tiles that this warp and its peers load, in the order they are used, over sequence borders: peer i takes tile + i.
   struct Walk {
     int b, tile, stop, len;  // sequence, tile of the sequence, the range's end in it
   };
@@ -291,13 +299,13 @@ __global__ void __launch_bounds__(DecodeCfg<D, NT>::kWarps * 32, 1) decode_kerne
       }
       ++w.b;
       w.stop = stop_tile(w.b);
-      w.tile = wt;
+      w.tile = wt * SHARE;
       w.len = seq_len(w.b);
     }
   };
   Walk ld;
   ld.b = b0;
-  ld.tile = first_tile(b0) + wt;
+  ld.tile = first_tile(b0) + wt * SHARE;
   ld.stop = stop_tile(b0);
   ld.len = seq_len(b0);
   enter(ld);
@@ -311,14 +319,14 @@ __global__ void __launch_bounds__(DecodeCfg<D, NT>::kWarps * 32, 1) decode_kerne
   auto look_ahead = [&](int i) {
     token_row[i] = -2;
     if (ld.b < 0) return;
-    const int token = ld.tile * TILE + lane % TILE;
+    const int token = (ld.tile + peer) * TILE + lane % TILE;
     token_row[i] = -1;
-    if (token < ld.len) {
+    if (token < ld.len && (SHARE == 1 || ld.tile + peer < ld.stop)) {
       const uint32_t pg = fdiv(static_cast<uint32_t>(token), a.div_page);
       page[i] = a.page_table[static_cast<int64_t>(ld.b) * a.max_pages + pg];
       token_row[i] = token - static_cast<int>(pg) * a.page_size;
     }
-    ld.tile += p.WT;
+    ld.tile += p.WT * SHARE;
     enter(ld);
   };
   look_ahead(0);
@@ -337,6 +345,7 @@ __global__ void __launch_bounds__(DecodeCfg<D, NT>::kWarps * 32, 1) decode_kerne
           atomicExch(a.status, static_cast<int>(H3ATTN_ERR_INVALID_ARG));  // its keys are not attended
       }
       mask = __ballot_sync(0xFFFFFFFFu, row >= 0);
+      if (SHARE > 1 && lane == 0) shared_mask[warp][at] = mask;
       const uint32_t ks = ring + at * (2 * C::kTileBytes), vs = ks + C::kTileBytes;
 #pragma unroll
       for (int i = 0; i < TILE * CH / 32; ++i) {
@@ -411,11 +420,14 @@ __global__ void __launch_bounds__(DecodeCfg<D, NT>::kWarps * 32, 1) decode_kerne
 #pragma unroll
         for (int dt = 0; dt < D / 16; ++dt) o[n][dt][0] = o[n][dt][1] = o[n][dt][2] = o[n][dt][3] = 0.0f;
       }
-      for (int tile = s0 + wt; tile < s1; tile += p.WT) {
+      for (int tile = s0 + wt * SHARE; tile < s1; tile += p.WT * SHARE) {
         const int st = turn % STAGES;
         cp_async_wait<STAGES - 2>();
-        __syncwarp();
-        const uint32_t mask = st == 0 ? mask_of[0] : st == 1 ? mask_of[1] : mask_of[2];
+        if constexpr (SHARE > 1)
+          pair_sync(1 + warp / SHARE);  // the peers' tiles are there, and what they read in the last turn is free
+        else
+          __syncwarp();
+        const uint32_t mine = st == 0 ? mask_of[0] : st == 1 ? mask_of[1] : mask_of[2];
         {
           const int at = (turn + STAGES - 1) % STAGES;
           uint32_t fresh = 0;
@@ -424,105 +436,111 @@ __global__ void __launch_bounds__(DecodeCfg<D, NT>::kWarps * 32, 1) decode_kerne
           for (int i = 0; i < STAGES; ++i) mask_of[i] = i == at ? fresh : mask_of[i];
         }
         ++turn;
-        const uint32_t ks_base = ring + st * 2 * C::kTileBytes, vs_base = ks_base + C::kTileBytes;
-        // two accumulators a product: a chain of tensor-core products waits for each of its links
-        float s[NT][MT][4], s2[NT][MT][4];
-#pragma unroll
-        for (int n = 0; n < NT; ++n)
-#pragma unroll
-          for (int mt = 0; mt < MT; ++mt)
-#pragma unroll
-            for (int e = 0; e < 4; ++e) s[n][mt][e] = s2[n][mt][e] = 0.0f;
-#pragma unroll
-        for (int ks = 0; ks < D / 16; ++ks) {
-#pragma unroll
-          for (int mt = 0; mt < MT; ++mt) {
-            uint32_t kf[4];
-            const int row = mt * 16 + (lane & 15), col = ks * 2 + (lane >> 4);
-            ldmatrix4(kf, ks_base + row * (D * 2) + ((col ^ (row & 7)) << 4));
-#pragma unroll
-            for (int n = 0; n < NT; ++n) mma16816(ks & 1 ? s2[n][mt] : s[n][mt], kf, qf[n][ks][0], qf[n][ks][1]);
-          }
-        }
-        // lane: tokens g and g + 8 of each 16, heads 2 t and 2 t + 1 of each 8
-#pragma unroll
-        for (int n = 0; n < NT; ++n)
-#pragma unroll
-          for (int mt = 0; mt < MT; ++mt)
-#pragma unroll
-            for (int e = 0; e < 4; ++e) s[n][mt][e] += s2[n][mt][e];
-        constexpr uint32_t kAll = TILE == 32 ? 0xFFFFFFFFu : 0xFFFFu;
-        if ((mask & kAll) != kAll) {
+#pragma unroll 1
+        for (int of = SHARE > 1 ? 0 : peer; of < SHARE; ++of) {
+          const uint32_t mask = SHARE > 1 ? shared_mask[peer0 + of][st] : mine;
+          if (SHARE > 1 && mask == 0) continue;  // no such tile, or none of its keys is there
+          const uint32_t ks_base = ring + ((of - peer) * STAGES + st) * (2 * C::kTileBytes);
+          const uint32_t vs_base = ks_base + C::kTileBytes;
+          // two accumulators a product: a chain of tensor-core products waits for each of its links
+          float s[NT][MT][4], s2[NT][MT][4];
 #pragma unroll
           for (int n = 0; n < NT; ++n)
 #pragma unroll
             for (int mt = 0; mt < MT; ++mt)
 #pragma unroll
-              for (int e = 0; e < 4; ++e)
-                if (!((mask >> (mt * 16 + g + (e < 2 ? 0 : 8))) & 1u)) s[n][mt][e] = -INFINITY;
-        }
-        uint32_t pf[NT][MT][2], pr[NT][MT][2];  // P and what its rounding left
+              for (int e = 0; e < 4; ++e) s[n][mt][e] = s2[n][mt][e] = 0.0f;
 #pragma unroll
-        for (int n = 0; n < NT; ++n) {
-          float top[2] = {-INFINITY, -INFINITY};
+          for (int ks = 0; ks < D / 16; ++ks) {
 #pragma unroll
-          for (int mt = 0; mt < MT; ++mt)
+            for (int mt = 0; mt < MT; ++mt) {
+              uint32_t kf[4];
+              const int row = mt * 16 + (lane & 15), col = ks * 2 + (lane >> 4);
+              ldmatrix4(kf, ks_base + row * (D * 2) + ((col ^ (row & 7)) << 4));
 #pragma unroll
-            for (int e = 0; e < 4; ++e) top[e & 1] = fmaxf(top[e & 1], s[n][mt][e]);
-          const bool over = top[0] * a.scale_log2 > m[n][0] + kSlack || top[1] * a.scale_log2 > m[n][1] + kSlack;
-          if (__any_sync(0xFFFFFFFFu, over)) {
+              for (int n = 0; n < NT; ++n) mma16816(ks & 1 ? s2[n][mt] : s[n][mt], kf, qf[n][ks][0], qf[n][ks][1]);
+            }
+          }
+          // lane: tokens g and g + 8 of each 16, heads 2 t and 2 t + 1 of each 8
 #pragma unroll
-            for (int c = 0; c < 2; ++c) {
-              top[c] = fmaxf(top[c], __shfl_xor_sync(0xFFFFFFFFu, top[c], 4));
-              top[c] = fmaxf(top[c], __shfl_xor_sync(0xFFFFFFFFu, top[c], 8));
-              top[c] = fmaxf(top[c], __shfl_xor_sync(0xFFFFFFFFu, top[c], 16));
-              const float to = fmaxf(m[n][c], top[c] * a.scale_log2);
-              const float fix = ex2(m[n][c] - to);
-              m[n][c] = to;
-              l[n][c] *= fix;
+          for (int n = 0; n < NT; ++n)
 #pragma unroll
-              for (int dt = 0; dt < D / 16; ++dt) {
-                o[n][dt][c] *= fix;
-                o[n][dt][c + 2] *= fix;
+            for (int mt = 0; mt < MT; ++mt)
+#pragma unroll
+              for (int e = 0; e < 4; ++e) s[n][mt][e] += s2[n][mt][e];
+          constexpr uint32_t kAll = TILE == 32 ? 0xFFFFFFFFu : 0xFFFFu;
+          if ((mask & kAll) != kAll) {
+#pragma unroll
+            for (int n = 0; n < NT; ++n)
+#pragma unroll
+              for (int mt = 0; mt < MT; ++mt)
+#pragma unroll
+                for (int e = 0; e < 4; ++e)
+                  if (!((mask >> (mt * 16 + g + (e < 2 ? 0 : 8))) & 1u)) s[n][mt][e] = -INFINITY;
+          }
+          uint32_t pf[NT][MT][2], pr[NT][MT][2];  // P and what its rounding left
+#pragma unroll
+          for (int n = 0; n < NT; ++n) {
+            float top[2] = {-INFINITY, -INFINITY};
+#pragma unroll
+            for (int mt = 0; mt < MT; ++mt)
+#pragma unroll
+              for (int e = 0; e < 4; ++e) top[e & 1] = fmaxf(top[e & 1], s[n][mt][e]);
+            const bool over = top[0] * a.scale_log2 > m[n][0] + kSlack || top[1] * a.scale_log2 > m[n][1] + kSlack;
+            if (__any_sync(0xFFFFFFFFu, over)) {
+#pragma unroll
+              for (int c = 0; c < 2; ++c) {
+                top[c] = fmaxf(top[c], __shfl_xor_sync(0xFFFFFFFFu, top[c], 4));
+                top[c] = fmaxf(top[c], __shfl_xor_sync(0xFFFFFFFFu, top[c], 8));
+                top[c] = fmaxf(top[c], __shfl_xor_sync(0xFFFFFFFFu, top[c], 16));
+                const float to = fmaxf(m[n][c], top[c] * a.scale_log2);
+                const float fix = ex2(m[n][c] - to);
+                m[n][c] = to;
+                l[n][c] *= fix;
+#pragma unroll
+                for (int dt = 0; dt < D / 16; ++dt) {
+                  o[n][dt][c] *= fix;
+                  o[n][dt][c + 2] *= fix;
+                }
+              }
+            }
+#pragma unroll
+            for (int mt = 0; mt < MT; ++mt) {
+#pragma unroll
+              for (int e = 0; e < 4; ++e) {
+                s[n][mt][e] = ex2(fmaf(s[n][mt][e], a.scale_log2, -m[n][e & 1]));
+                l[n][e & 1] += s[n][mt][e];
+              }
+#pragma unroll
+              for (int half = 0; half < 2; ++half) {
+                const float p0 = s[n][mt][2 * half], p1 = s[n][mt][2 * half + 1];
+                const uint32_t hi = pack_bf16(p0, p1);
+                pf[n][mt][half] = transpose8x8(hi);
+                pr[n][mt][half] =
+                    transpose8x8(pack_bf16(p0 - __uint_as_float(hi << 16), p1 - __uint_as_float(hi & 0xFFFF0000u)));
               }
             }
           }
+          constexpr int DB = 4;  // channel tiles whose products are interleaved
 #pragma unroll
           for (int mt = 0; mt < MT; ++mt) {
 #pragma unroll
-            for (int e = 0; e < 4; ++e) {
-              s[n][mt][e] = ex2(fmaf(s[n][mt][e], a.scale_log2, -m[n][e & 1]));
-              l[n][e & 1] += s[n][mt][e];
+            for (int d0 = 0; d0 < D / 16; d0 += DB) {
+              uint32_t vf[DB][4];
+#pragma unroll
+              for (int i = 0; i < DB; ++i) {
+                const int row = mt * 16 + (lane >> 4) * 8 + (lane & 7), col = (d0 + i) * 2 + ((lane >> 3) & 1);
+                ldmatrix4_trans(vf[i], vs_base + row * (D * 2) + ((col ^ (row & 7)) << 4));
+              }
+#pragma unroll
+              for (int n = 0; n < NT; ++n)
+#pragma unroll
+                for (int i = 0; i < DB; ++i) mma16816(o[n][d0 + i], vf[i], pf[n][mt][0], pf[n][mt][1]);
+#pragma unroll
+              for (int n = 0; n < NT; ++n)
+#pragma unroll
+                for (int i = 0; i < DB; ++i) mma16816(o[n][d0 + i], vf[i], pr[n][mt][0], pr[n][mt][1]);
             }
-#pragma unroll
-            for (int half = 0; half < 2; ++half) {
-              const float p0 = s[n][mt][2 * half], p1 = s[n][mt][2 * half + 1];
-              const uint32_t hi = pack_bf16(p0, p1);
-              pf[n][mt][half] = transpose8x8(hi);
-              pr[n][mt][half] =
-                  transpose8x8(pack_bf16(p0 - __uint_as_float(hi << 16), p1 - __uint_as_float(hi & 0xFFFF0000u)));
-            }
-          }
-        }
-        constexpr int DB = 4;  // channel tiles whose products are interleaved
-#pragma unroll
-        for (int mt = 0; mt < MT; ++mt) {
-#pragma unroll
-          for (int d0 = 0; d0 < D / 16; d0 += DB) {
-            uint32_t vf[DB][4];
-#pragma unroll
-            for (int i = 0; i < DB; ++i) {
-              const int row = mt * 16 + (lane >> 4) * 8 + (lane & 7), col = (d0 + i) * 2 + ((lane >> 3) & 1);
-              ldmatrix4_trans(vf[i], vs_base + row * (D * 2) + ((col ^ (row & 7)) << 4));
-            }
-#pragma unroll
-            for (int n = 0; n < NT; ++n)
-#pragma unroll
-              for (int i = 0; i < DB; ++i) mma16816(o[n][d0 + i], vf[i], pf[n][mt][0], pf[n][mt][1]);
-#pragma unroll
-            for (int n = 0; n < NT; ++n)
-#pragma unroll
-              for (int i = 0; i < DB; ++i) mma16816(o[n][d0 + i], vf[i], pr[n][mt][0], pr[n][mt][1]);
           }
         }
         __syncwarp();  // the stage is read; the next turn's load may fill it
@@ -824,6 +842,11 @@ DecodePlan make_plan(const DecodeArgs& a, int sms, bool split) {
   while (p.WH < warps && p.unit_heads % (2 * p.WH) == 0) p.WH *= 2;
   p.WT = warps / p.WH;
   p.groups = p.unit_heads / p.WH;
+  // 28 sequences of 0 to 52182 tokens, 32 heads to one of 128: 83 us without, 73 with; 64 of 0 to 6000, heads of 256: 86 and
+  // 75.  Then a tensor-core product is issued every 9 cycles, and 8 is their rate.  Heads of 64, 9 sequences of 20000 to
+  // 40000: 22.9 without, 23.6 with.
+  p.share = a.D > 64 && p.q_tiles % 2 == 0 ? 2 : 1;
+  const int loaders = p.WT * p.share;  // warps that load different tiles
   // Split into one range an SM, unless
   // - the cache has no room for sequences of more than four tiles a warp: one CTA walks them in less time than the
   //   second kernel takes (16 query and 4 key-value heads of 128, one sequence: 6.1 us against 6.9 at 128 tokens, 9.0
@@ -833,9 +856,9 @@ DecodePlan make_plan(const DecodeArgs& a, int sms, bool split) {
   // - tiles do not fit 32 bits.
   const int tile = a.D == 64 ? 32 : 16;
   const int64_t capacity = static_cast<int64_t>(a.max_pages) * a.page_size;
-  // Two tiles a warp, what joining its warps and asking for the next queries take (64 sequences of up to 2048 tokens, 2 key-value
-  // heads of 64: 13.1 us without them, 11.0 with them; 200 of up to 500, 8 and 1 head of 128: 27.9 and 24.1).
-  p.start = 2 * p.WT;
+  // Two tiles a warp, what joining its warps and asking for the next queries take (64 sequences of up to 2048 tokens, 2
+  // key-value heads of 64: 13.1 us without them, 11.0 with them; 200 of up to 2000, 8 and 1 head of 128: 27.9 and 24.1).
+  p.start = 2 * loaders;
   const bool whole =
       capacity <= 4 * p.WT * tile || a.B > kMaxSplitBatch || (capacity / 16 + 1 + p.start) * a.B > INT32_MAX;
   p.ranges = split && !whole ? std::max(1, std::min(sms / p.groups, kMaxRanges)) : 0;
@@ -843,7 +866,7 @@ DecodePlan make_plan(const DecodeArgs& a, int sms, bool split) {
   return p;
 }
 
-template <int D, int NT>
+template <int D, int NT, int SHARE>
 cudaError_t launch_d(const Kernelargs& k, cudaStream_t stream) {
   using C = DecodeCfg<D, NT>;
   static bool attr_set[64] = {};
@@ -852,17 +875,24 @@ cudaError_t launch_d(const Kernelargs& k, cudaStream_t stream) {
   if (e != cudaSuccess) return e;
   if (dev < 0 || dev >= 64) return cudaErrorInvalidDevice;
   if (!attr_set[dev]) {
-    e = cudaFuncSetAttribute(decode_kernel<D, NT>, cudaFuncAttributeMaxDynamicSharedMemorySize, C::kSmem);
+    e = cudaFuncSetAttribute(decode_kernel<D, NT, SHARE>, cudaFuncAttributeMaxDynamicSharedMemorySize, C::kSmem);
     if (e != cudaSuccess) return e;
     attr_set[dev] = true;
   }
   const int64_t ranges = k.p.ranges > 0 ? k.p.ranges : k.a.B;
-  e = launch_dependent(decode_kernel<D, NT>, dim3(static_cast<unsigned>(ranges * k.p.groups)), C::kWarps * 32, C::kSmem,
-                       stream, k);
+  e = launch_dependent(decode_kernel<D, NT, SHARE>, dim3(static_cast<unsigned>(ranges * k.p.groups)), C::kWarps * 32,
+                       C::kSmem, stream, k);
   if (e != cudaSuccess || k.p.ranges == 0) return e;
   const int G = k.a.Hq / k.a.Hkv;
   return launch_dependent(decode_join_kernel<D>, dim3(k.p.ranges * k.p.groups), kJoinThreads, 0, stream, k, C::kTile,
                           std::min(G, C::kHeads));
+}
+
+template <int D>
+cudaError_t launch_heads(const Kernelargs& k, cudaStream_t stream) {
+  if constexpr (D > 64)
+    if (k.p.share == 2) return launch_d<D, 2, 2>(k, stream);
+  return k.a.Hq / k.a.Hkv > 8 ? launch_d<D, 2, 1>(k, stream) : launch_d<D, 1, 1>(k, stream);
 }
 
 }  // namespace
@@ -882,11 +912,10 @@ cudaError_t launch_decode(const DecodeArgs& a, cudaStream_t stream) {
   cudaError_t e = sm_count(&sms);
   if (e != cudaSuccess) return e;
   Kernelargs k{a, make_plan(a, sms, a.ws != nullptr)};
-  const bool wide = a.Hq / a.Hkv > 8;
   switch (a.D) {
-    case 64: return wide ? launch_d<64, 2>(k, stream) : launch_d<64, 1>(k, stream);
-    case 128: return wide ? launch_d<128, 2>(k, stream) : launch_d<128, 1>(k, stream);
-    case 256: return wide ? launch_d<256, 2>(k, stream) : launch_d<256, 1>(k, stream);
+    case 64: return launch_heads<64>(k, stream);
+    case 128: return launch_heads<128>(k, stream);
+    case 256: return launch_heads<256>(k, stream);
     default: return cudaErrorInvalidValue;
   }
 }
