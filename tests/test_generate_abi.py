@@ -46,7 +46,7 @@ def table(lib, cos=M, sin=2 * M, pos=None, first=0, N=16, rot=96, theta=10000.0,
 @pytest.mark.parametrize("args,want", [
     (dict(N=-1), BAD), (dict(rot=0), BAD), (dict(rot=95), BAD), (dict(rot=258), BAD), (dict(rot=-2), BAD),
     (dict(theta=0.5), BAD), (dict(theta=INF), BAD), (dict(theta=NAN), BAD), (dict(first=-1), BAD),
-    (dict(first=2 ** 31 - 15), BAD), (dict(first=2 ** 62), BAD), (dict(first=1, pos=3 * M), BAD),
+    (dict(first=2 ** 31 - 15), BAD), (dict(first=2 ** 62), BAD), (dict(first=2 ** 63 - 1), BAD), (dict(first=1, pos=3 * M), BAD),
     (dict(cos=None), BAD), (dict(sin=None), BAD), (dict(cos=M + 4), ALIGN), (dict(pos=3 * M + 2), ALIGN),
     (dict(sin=M), BAD), (dict(pos=M), BAD), (dict(pos=2 * M + 64), BAD),
     # kind, original_len, factor, low, high, amplitude

@@ -135,7 +135,7 @@ h3attn_status_t h3attn_rope_table(float* cos, float* sin, const int32_t* pos, in
   if (N < 0 || rotary_dim < 2 || rotary_dim % 2 != 0 || rotary_dim > 2 * h3::kMaxRotaryPairs)
     return H3ATTN_ERR_INVALID_ARG;
   if (!(theta >= 1.0) || !isfinite(theta)) return H3ATTN_ERR_INVALID_ARG;
-  if (pos ? first != 0 : (first < 0 || first + N > (1LL << 31))) return H3ATTN_ERR_INVALID_ARG;
+  if (pos ? first != 0 : (first < 0 || first > (1LL << 31) - N)) return H3ATTN_ERR_INVALID_ARG;
   const int kind = scaling ? scaling->kind : static_cast<int>(H3ATTN_ROPE_NONE);
   if (kind < H3ATTN_ROPE_NONE || kind > H3ATTN_ROPE_BY_PARTS) return H3ATTN_ERR_INVALID_ARG;
   const double factor = kind == H3ATTN_ROPE_NONE ? 1.0 : scaling->factor;
