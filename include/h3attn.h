@@ -483,11 +483,12 @@ h3attn_status_t h3attn_qk_norm_rope_append(const void* q, const void* k, const v
  * key and value are in the cache already (appended before the call).  A
  * sequence without a key gets a zero row.  Rows of the last page past kv_len
  * may hold anything; a NaN or infinity in an attended row reaches its
- * sequence's heads only.  Keys of a page outside [0, num_pages) are not
+ * sequence's heads only, and may come out as a NaN.  A sequence whose scores
+ * are all -infinity gets a zero row.  Keys of a page outside [0, num_pages) are not
  * attended (and reported).
  *
  * q, o: [B, Hq, D] bf16 (a [B, 1, Hq, D] tensor), o overlapping nothing else;
- * scale finite and > 0; Hq a multiple of cache->Hkv; B, Hq <= 65535,
+ * scale > 0 and scale * log2(e) finite; Hq a multiple of cache->Hkv; B, Hq <= 65535,
  * B * Hkv * ceil(Hq / Hkv / 16) < 2^31; B == 0 is a no-op.
  * workspace: device memory of at least h3attn_paged_decode_workspace_size()
  *    bytes for the same cache geometry and Hq, 16-byte aligned, overlapping

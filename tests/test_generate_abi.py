@@ -103,7 +103,7 @@ def decode(lib, q=M, o=2 * M, Hq=4, scale=0.1, ws=None, nbytes=0, null=False, **
 
 @pytest.mark.parametrize("args,want", GEOMETRY + [
     (dict(null=True), BAD), (dict(Hq=0), BAD), (dict(Hq=5), BAD), (dict(Hq=65536), BAD), (dict(scale=0.0), BAD), (dict(scale=-1.0), BAD),
-    (dict(scale=NAN), BAD), (dict(scale=INF), BAD), (dict(q=None), BAD), (dict(o=None), BAD), (dict(k=None), BAD), (dict(v=None), BAD),
+    (dict(scale=NAN), BAD), (dict(scale=INF), BAD), (dict(scale=3e38), BAD), (dict(q=None), BAD), (dict(o=None), BAD), (dict(k=None), BAD), (dict(v=None), BAD),
     (dict(t=None), BAD), (dict(n=None), BAD), (dict(q=M + 8), ALIGN), (dict(o=2 * M + 2), ALIGN), (dict(k=100 * M + 8), ALIGN),
     (dict(t=140 * M + 2), ALIGN), (dict(ws=3 * M + 8, nbytes=1 << 20), ALIGN), (dict(o=M), BAD), (dict(o=100 * M + 256), BAD),
     (dict(o=141 * M), BAD), (dict(B=65535, Hkv=65535, Hq=65535), BAD), (dict(B=0), 0)])
@@ -148,3 +148,9 @@ def test_the_compiled_host_path_is_bound_to_the_library(lib):
         h3.h3attn_qk_norm_rope_append(x, x, x, x, object(), None, None, None, None)
     with pytest.raises(h3.H3AttnError, match="unknown scaling"):
         h3.RopeScaling("cubic")
+    for n in (2 ** 31, 2 ** 32 + 1, -2 ** 40):  # ctypes would keep the low 32 bits
+        with pytest.raises(h3.H3AttnError, match="original_len"):
+            h3.RopeScaling("by_parts", 2.0, n)
+    pages = torch.zeros(2 ** 32 + 3, 0, 2, 128, dtype=torch.bfloat16)
+    with pytest.raises(h3.H3AttnError, match="32 bits"):
+        h3.PagedKV(pages, pages, torch.zeros(1, 2, dtype=torch.int32), torch.zeros(1, dtype=torch.int32))

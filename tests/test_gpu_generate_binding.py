@@ -1,5 +1,9 @@
 """What the Python binding of the generation operators refuses on CUDA tensors,
 and the strides, streams and argument forms that it takes."""
+import os
+import subprocess
+import sys
+
 import pytest
 import torch
 
@@ -130,4 +134,84 @@ def test_two_streams_at_once(h3):
     torch.cuda.synchronize()
     for c, o in zip(cases, outs):
         close(o[0], *c.reference())
+        assert all(torch.equal(o[0], x) for x in o)
+
+
+FIRST_CALLS = """
+import torch
+import video_dit_dense_gb300 as h3
+d = dict(dtype=torch.bfloat16, device="cuda")
+g = torch.Generator("cuda").manual_seed(1)
+x, y, h = torch.randn(2, 512, generator=g, **d), torch.empty(2, 512, **d), torch.empty(2, 512, **d)
+q, k = torch.randn(2, 1, 8, 64, generator=g, **d), torch.randn(2, 1, 2, 64, generator=g, **d)
+pages, more = torch.randn(80, 16, 2, 64, generator=g, **d), torch.randn(80, 16, 2, 64, generator=g, **d)
+cos, sin = torch.empty(640, 32, device="cuda"), torch.empty(640, 32, device="cuda")
+lens = torch.tensor([600, 37], dtype=torch.int32, device="cuda")
+after, q1, o = torch.empty_like(lens), torch.empty_like(q), torch.empty_like(q)
+table = torch.arange(80, dtype=torch.int32, device="cuda").view(2, 40)
+cache = h3.PagedKV(pages, more, table, lens)
+grown = cache.with_lengths(after)
+ws = h3.paged_decode_workspace(q, grown)
+assert ws is not None
+outs = (h, y, cos, sin, q1, after, o)
+
+def step():
+    h3.h3attn_add_rmsnorm(x, x, h, y)
+    h3.h3attn_rope_table(cos, sin, 64)
+    h3.h3attn_qk_norm_rope_append(q, k, k, q1, cache, None, None, cos, sin, 64, len_out=after)
+    h3.h3attn_paged_decode(q1, o, grown, workspace=ws)
+
+torch.cuda.synchronize()
+graph = torch.cuda.CUDAGraph()
+with torch.cuda.graph(graph):
+    step()
+for t in outs:
+    t.zero_()
+graph.replay()
+torch.cuda.synchronize()
+got = [t.clone() for t in outs]
+step()
+torch.cuda.synchronize()
+assert all(torch.equal(a, b) for a, b in zip(got, outs)) and after.tolist() == [601, 38] and bool((o != 0).any())
+assert h3.h3attn_check_device_status() == 0
+print("replayed")
+"""
+
+
+@pytest.mark.gpu
+def test_the_first_calls_of_a_process_may_be_captured(h3):
+    root = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
+    r = subprocess.run([sys.executable, "-c", FIRST_CALLS], cwd=root, capture_output=True, text=True, timeout=300)
+    assert r.returncode == 0 and "replayed" in r.stdout, r.stderr[-2000:]
+
+
+@pytest.mark.gpu
+def test_threads_at_once(h3):
+    """Calls of several host threads, each on a stream and with a workspace of its own."""
+    import threading
+    from test_gpu_decode import Case, close
+    cases = [Case([3000, 40, 700], 32 if i % 2 else 8, 2 if i % 2 else 1, 128, 16, seed=70 + i).cuda(h3) for i in range(4)]
+    refs = [c.reference() for c in cases]
+    outs, errors = [None] * len(cases), []
+    torch.cuda.synchronize()
+
+    def work(i):
+        try:
+            s, c = torch.cuda.Stream(), cases[i]
+            with torch.cuda.stream(s):
+                ws = h3.paged_decode_workspace(c.dq, c.cache)
+                outs[i] = [torch.empty_like(c.dq) for _ in range(50)]
+                for o in outs[i]:
+                    h3.h3attn_paged_decode(c.dq, o, c.cache, workspace=ws)
+            s.synchronize()
+        except Exception as e:  # reported by the test's own thread
+            errors.append(e)
+    threads = [threading.Thread(target=work, args=(i,)) for i in range(len(cases))]
+    for t in threads:
+        t.start()
+    for t in threads:
+        t.join()
+    assert not errors, errors
+    for (ref, bound), o in zip(refs, outs):
+        close(o[0], ref, bound)
         assert all(torch.equal(o[0], x) for x in o)

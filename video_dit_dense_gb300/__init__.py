@@ -475,6 +475,8 @@ class RopeScaling:
     def __post_init__(self):
         if self.kind not in _ROPE_KINDS:
             raise H3AttnError(H3ATTN_ERR_INVALID_ARG, f"unknown scaling {self.kind!r}")
+        if not -2 ** 31 <= self.original_len < 2 ** 31:
+            raise H3AttnError(H3ATTN_ERR_INVALID_ARG, "original_len must fit 32 bits")
         object.__setattr__(self, "_struct", h3attn_rope_scaling_t(_ROPE_KINDS[self.kind], self.original_len, self.factor,
                                                                   self.low_turns, self.high_turns, self.amplitude))
 
@@ -518,6 +520,8 @@ class PagedKV:
             raise H3AttnError(H3ATTN_ERR_INVALID_ARG, "pages must be [num_pages, page_size, Hkv, D], page_table [B, max_pages]")
         num_pages, page_size, Hkv, D = k_pages.shape
         B, max_pages = page_table.shape
+        if max(num_pages, page_size, Hkv, D, B, max_pages) >= 2 ** 31:
+            raise H3AttnError(H3ATTN_ERR_INVALID_ARG, "the cache's sizes must fit 32 bits")
         self._device = k_pages.get_device()
         _check("k_pages", k_pages, torch.bfloat16, (num_pages, page_size, Hkv, D), self._device)
         _check("v_pages", v_pages, torch.bfloat16, (num_pages, page_size, Hkv, D), self._device)

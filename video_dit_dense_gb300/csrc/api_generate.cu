@@ -292,7 +292,8 @@ h3attn_status_t h3attn_paged_decode(const void* q, void* o, const h3attn_paged_k
   if (st != H3ATTN_OK) return st;
   st = check_decode_heads(cache, Hq);
   if (st != H3ATTN_OK) return st;
-  if (!(scale > 0.0f) || !isfinite(scale)) return H3ATTN_ERR_INVALID_ARG;
+  const float scale_log2 = scale * 1.4426950408889634f;
+  if (!(scale > 0.0f) || !isfinite(scale_log2)) return H3ATTN_ERR_INVALID_ARG;
   if (cache->B == 0) return H3ATTN_OK;
   if (!q || !o) return H3ATTN_ERR_INVALID_ARG;
   st = check_cache_pointers(cache);
@@ -321,7 +322,7 @@ h3attn_status_t h3attn_paged_decode(const void* q, void* o, const h3attn_paged_k
   }
   a.q = static_cast<const uint16_t*>(q);
   a.o = static_cast<uint16_t*>(o);
-  a.scale_log2 = scale * 1.4426950408889634f;
+  a.scale_log2 = scale_log2;
   a.status = h3::status_word_ptr();
   if (!a.status) return H3ATTN_ERR_LAUNCH;
   return h3::launch_decode(a, static_cast<cudaStream_t>(stream)) == cudaSuccess ? H3ATTN_OK : H3ATTN_ERR_LAUNCH;
