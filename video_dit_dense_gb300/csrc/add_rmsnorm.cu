@@ -25,8 +25,10 @@
 // vector cost as much as they leave idle: 256 threads for the 640 vectors of
 // 5120 channels took 195 us.  So does a register too many: 82 a thread instead of 80
 // took 318 us instead of 261 at 8192 channels, two CTAs an SM instead of three.
-// Without a residual an e4m3 output moves 3 bytes a channel instead of 7, and
-// the arithmetic is what bounds it (4096 channels: 82 us with row scales, floor 59).
+// Without a residual a row moves 3 or 4 bytes a channel instead of 6 to 8, and what is left is a
+// block's life: load, reduce, store, and 4 bytes of weights a channel from L1.  Two rows a
+// block share all of it.  32760 rows of 4096 channels with row scales: 68 us of 59 (a row a block
+// 82), of 5120: 94 (109), of 1288: 26 (35); bf16, 4096 channels: 78 of 79 (85), of 1288: 27 (35).
 // Products run on two channels at a time (packed float32 operations); the residual's addition
 // does not: packed, its operands were waited for together, 20.3 us instead of 18.2
 // at 4099 rows of 4096.
@@ -40,6 +42,7 @@ namespace h3 {
 namespace {
 
 constexpr int kShortRows = 8;  // short rows that a CTA takes, a warp each
+constexpr int kManyRows = 2048;  // from here on the memory is what counts, not a row's latencies
 
 __device__ __forceinline__ float lo16(uint32_t w) { return __uint_as_float(w << 16); }
 __device__ __forceinline__ float hi16(uint32_t w) { return __uint_as_float(w & 0xFFFF0000u); }
@@ -56,52 +59,63 @@ __device__ __forceinline__ uint32_t pack_e4m3x4(float a, float b, float c, float
 // Sum and maximum over the threads of a row: a warp (WARPS == 1), or the whole
 // block of at most WARPS warps.  A row's time is a chain of latencies, so the
 // warps' parts are read side by side and added as a tree.
-template <int WARPS>
-__device__ __forceinline__ void row_reduce(float& sum, float& top) {
+template <int WARPS, int ROWS>
+__device__ __forceinline__ void row_reduce(float (&sum)[ROWS], float (&top)[ROWS]) {
 #pragma unroll
   for (int off = 16; off >= 1; off >>= 1) {
-    sum += __shfl_xor_sync(0xFFFFFFFFu, sum, off);
-    top = fmaxf(top, __shfl_xor_sync(0xFFFFFFFFu, top, off));
+#pragma unroll
+    for (int j = 0; j < ROWS; ++j) {
+      sum[j] += __shfl_xor_sync(0xFFFFFFFFu, sum[j], off);
+      top[j] = fmaxf(top[j], __shfl_xor_sync(0xFFFFFFFFu, top[j], off));
+    }
   }
   if constexpr (WARPS > 1) {
-    __shared__ __align__(16) float2 part[WARPS];
-    if ((threadIdx.x & 31) == 0) part[threadIdx.x >> 5] = make_float2(sum, top);
-    if (threadIdx.x < WARPS && threadIdx.x >= (blockDim.x >> 5)) part[threadIdx.x] = make_float2(0.0f, 0.0f);
+    __shared__ __align__(16) float2 part[ROWS][WARPS];
+#pragma unroll
+    for (int j = 0; j < ROWS; ++j) {
+      if ((threadIdx.x & 31) == 0) part[j][threadIdx.x >> 5] = make_float2(sum[j], top[j]);
+      if (threadIdx.x < WARPS && threadIdx.x >= (blockDim.x >> 5)) part[j][threadIdx.x] = make_float2(0.0f, 0.0f);
+    }
     __syncthreads();
-    float s[WARPS / 2], m[WARPS / 2];
 #pragma unroll
-    for (int i = 0; i < WARPS / 2; ++i) {
-      const float4 two = *reinterpret_cast<const float4*>(&part[2 * i]);
-      s[i] = two.x + two.z;
-      m[i] = fmaxf(two.y, two.w);
-    }
+    for (int j = 0; j < ROWS; ++j) {
+      float s[WARPS / 2], m[WARPS / 2];
 #pragma unroll
-    for (int n = WARPS / 4; n >= 1; n >>= 1) {
-#pragma unroll
-      for (int i = 0; i < n; ++i) {
-        s[i] += s[i + n];
-        m[i] = fmaxf(m[i], m[i + n]);
+      for (int i = 0; i < WARPS / 2; ++i) {
+        const float4 two = *reinterpret_cast<const float4*>(&part[j][2 * i]);
+        s[i] = two.x + two.z;
+        m[i] = fmaxf(two.y, two.w);
       }
+#pragma unroll
+      for (int n = WARPS / 4; n >= 1; n >>= 1) {
+#pragma unroll
+        for (int i = 0; i < n; ++i) {
+          s[i] += s[i + n];
+          m[i] = fmaxf(m[i], m[i + n]);
+        }
+      }
+      sum[j] = s[0];
+      top[j] = m[0];
     }
-    sum = s[0];
-    top = m[0];
   }
 }
 
-// Vector k * threads + thread of the row is the thread's k-th.
-template <int WARPS, int VPT, int FORMAT, bool RESIDUAL>
+// Vector k * threads + thread of a row is the thread's k-th, of each of the block's ROWS rows.
+template <int WARPS, int VPT, int FORMAT, bool RESIDUAL, int ROWS = 1>
 __global__ void __launch_bounds__(WARPS == 1 ? kShortRows * 32 : WARPS * 32)
-    __maxnreg__(VPT == 2 ? 48 : WARPS == 1 ? 80 : 56)
+    __maxnreg__(ROWS == 2   ? (FORMAT == H3ATTN_Y_E4M3_ROW ? 48 : 64)
+                : VPT == 2   ? 48
+                : WARPS == 1 ? 80
+                : !RESIDUAL && FORMAT != H3ATTN_Y_E4M3_ROW ? 48
+                                                           : 56)
     add_rmsnorm_kernel(const __grid_constant__ AddNormArgs a) {
   constexpr bool SHORT = WARPS == 1;
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
   asm volatile("griddepcontrol.wait;" ::: "memory");
   const int TPR = SHORT ? 32 : blockDim.x;
   const int t = SHORT ? threadIdx.x & 31 : threadIdx.x, V = a.C >> 3;
-  const int64_t row = SHORT ? static_cast<int64_t>(blockIdx.x) * kShortRows + (threadIdx.x >> 5) : blockIdx.x;
-  const bool live = !SHORT || row < a.T;
-  const int64_t base = live ? row * a.C : 0;
-  uint4 xv[VPT], rv[VPT];
+  const int64_t row0 = SHORT ? static_cast<int64_t>(blockIdx.x) * kShortRows + (threadIdx.x >> 5)
+                             : static_cast<int64_t>(blockIdx.x) * ROWS;
   // The weights of a vector: kept from the first use to the second, or, where they would take registers that another
   // CTA needs, read again from L1.
   constexpr bool kKeepWeights = SHORT || VPT == 2;
@@ -111,90 +125,107 @@ __global__ void __launch_bounds__(WARPS == 1 ? kShortRows * 32 : WARPS * 32)
     *reinterpret_cast<float4*>(&to[0]) = v < V && a.w ? wp[0] : one;
     *reinterpret_cast<float4*>(&to[4]) = v < V && a.w ? wp[1] : one;
   };
+  auto inside = [&](int j, int v) { return v < V && (!(SHORT || ROWS > 1) || row0 + j < a.T); };
+  const int64_t base = row0 * a.C;
+  auto at = [&](int j, int v) { return base + j * a.C + 8 * v; };
+  uint4 xv[ROWS][VPT], rv[ROWS][VPT];
   float kept[kKeepWeights ? VPT : 1][8];
 #pragma unroll
   for (int k = 0; k < VPT; ++k) {
     const int v = k * TPR + t;
-    const bool in = live && v < V;
     if constexpr (kKeepWeights) weights(v, kept[k]);
-    xv[k] = in ? *reinterpret_cast<const uint4*>(a.x + base + 8 * v) : make_uint4(0u, 0u, 0u, 0u);
-    rv[k] = in && RESIDUAL ? *reinterpret_cast<const uint4*>(a.residual + base + 8 * v) : make_uint4(0u, 0u, 0u, 0u);
-  }
-  float even = 0.0f, odd = 0.0f, top = 0.0f;
 #pragma unroll
-  for (int k = 0; k < VPT; ++k) {
-    const int v = k * TPR + t;
-    if constexpr (RESIDUAL) {
-      uint32_t* x = &xv[k].x;
-      const uint32_t* r = &rv[k].x;
-#pragma unroll
-      for (int e = 0; e < 4; ++e) x[e] = pack2(lo16(x[e]) + lo16(r[e]), hi16(x[e]) + hi16(r[e]));
-      if (live && v < V) *reinterpret_cast<uint4*>(a.h + base + 8 * v) = xv[k];
+    for (int j = 0; j < ROWS; ++j) {
+      const bool in = inside(j, v);
+      xv[j][k] = in ? *reinterpret_cast<const uint4*>(a.x + at(j, v)) : make_uint4(0u, 0u, 0u, 0u);
+      rv[j][k] = in && RESIDUAL ? *reinterpret_cast<const uint4*>(a.residual + at(j, v)) : make_uint4(0u, 0u, 0u, 0u);
     }
-    const uint32_t x[4] = {xv[k].x, xv[k].y, xv[k].z, xv[k].w};
+  }
+  float sum[ROWS], top[ROWS];
 #pragma unroll
-    for (int e = 0; e < 4; ++e) ffma2(even, odd, lo16(x[e]), hi16(x[e]), lo16(x[e]), hi16(x[e]), even, odd);
+  for (int j = 0; j < ROWS; ++j) {
+    float even = 0.0f, odd = 0.0f;
+    top[j] = 0.0f;
+#pragma unroll
+    for (int k = 0; k < VPT; ++k) {
+      const int v = k * TPR + t;
+      if constexpr (RESIDUAL) {
+        uint32_t* x = &xv[j][k].x;
+        const uint32_t* r = &rv[j][k].x;
+#pragma unroll
+        for (int e = 0; e < 4; ++e) x[e] = pack2(lo16(x[e]) + lo16(r[e]), hi16(x[e]) + hi16(r[e]));
+        if (inside(j, v)) *reinterpret_cast<uint4*>(a.h + at(j, v)) = xv[j][k];
+      }
+      const uint32_t x[4] = {xv[j][k].x, xv[j][k].y, xv[j][k].z, xv[j][k].w};
+#pragma unroll
+      for (int e = 0; e < 4; ++e) ffma2(even, odd, lo16(x[e]), hi16(x[e]), lo16(x[e]), hi16(x[e]), even, odd);
+      if constexpr (FORMAT == H3ATTN_Y_E4M3_ROW) {
+        float w8[8];
+        if constexpr (!kKeepWeights) weights(v, w8);
+        const float(&wv)[8] = kKeepWeights ? kept[kKeepWeights ? k : 0] : w8;
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          float p0, p1;
+          fmul2(p0, p1, lo16(x[e]), hi16(x[e]), wv[2 * e], wv[2 * e + 1]);
+          top[j] = fmax3(top[j], fabsf(p0), fabsf(p1));
+        }
+      }
+    }
+    sum[j] = even + odd;
+  }
+  row_reduce<WARPS>(sum, top);
+#pragma unroll
+  for (int j = 0; j < ROWS; ++j) {
+    const int64_t row = row0 + j;
+    const float r = __frsqrt_rn(fmaf(sum[j], a.inv_C, a.eps));
+    float inv = 1.0f;
     if constexpr (FORMAT == H3ATTN_Y_E4M3_ROW) {
+      // not below 2^-126, so that 1 / s is finite: such a row is zero or next to it
+      const float m = top[j] * r;
+      const float s = m > 0.0f ? fmaxf(m * (1.0f / 448.0f), 1.17549435e-38f) : 1.0f;
+      inv = __frcp_rn(s);
+      if (inside(j, 0) && t == 0) static_cast<float*>(a.y_scale)[row] = s;
+    }
+#pragma unroll
+    for (int k = 0; k < VPT; ++k) {
+      const int v = k * TPR + t;
+      const bool in = inside(j, v);
+      const uint32_t x[4] = {xv[j][k].x, xv[j][k].y, xv[j][k].z, xv[j][k].w};
       float w8[8];
       if constexpr (!kKeepWeights) weights(v, w8);
       const float(&wv)[8] = kKeepWeights ? kept[kKeepWeights ? k : 0] : w8;
+      float y[8];
 #pragma unroll
-      for (int e = 0; e < 4; ++e) {
-        float p0, p1;
-        fmul2(p0, p1, lo16(x[e]), hi16(x[e]), wv[2 * e], wv[2 * e + 1]);
-        top = fmax3(top, fabsf(p0), fabsf(p1));
+      for (int e = 0; e < 8; e += 2) {
+        fmul2(y[e], y[e + 1], lo16(x[e >> 1]), hi16(x[e >> 1]), wv[e], wv[e + 1]);
+        fmul2(y[e], y[e + 1], y[e], y[e + 1], r, r);
       }
-    }
-  }
-  float sum = even + odd;
-  row_reduce<WARPS>(sum, top);
-  const float r = __frsqrt_rn(fmaf(sum, a.inv_C, a.eps));
-  float inv = 1.0f;
-  if constexpr (FORMAT == H3ATTN_Y_E4M3_ROW) {
-    // not below 2^-126, so that 1 / s is finite: such a row is zero or next to it
-    const float m = top * r;
-    const float s = m > 0.0f ? fmaxf(m * (1.0f / 448.0f), 1.17549435e-38f) : 1.0f;
-    inv = __frcp_rn(s);
-    if (live && t == 0) static_cast<float*>(a.y_scale)[row] = s;
-  }
+      if constexpr (FORMAT == H3ATTN_Y_BF16) {
+        if (in)
+          *reinterpret_cast<uint4*>(static_cast<uint16_t*>(a.y) + at(j, v)) =
+              make_uint4(pack2(y[0], y[1]), pack2(y[2], y[3]), pack2(y[4], y[5]), pack2(y[6], y[7]));
+      } else {
+        if constexpr (FORMAT == H3ATTN_Y_E4M3_MX32) {
+          // the four lanes of a 32-channel group hold neighbouring vectors
+          float m = 0.0f;
 #pragma unroll
-  for (int k = 0; k < VPT; ++k) {
-    const int v = k * TPR + t;
-    const bool in = live && v < V;
-    const uint32_t x[4] = {xv[k].x, xv[k].y, xv[k].z, xv[k].w};
-    float w8[8];
-    if constexpr (!kKeepWeights) weights(v, w8);
-    const float(&wv)[8] = kKeepWeights ? kept[kKeepWeights ? k : 0] : w8;
-    float y[8];
+          for (int e = 0; e < 8; e += 2) m = fmax3(m, fabsf(y[e]), fabsf(y[e + 1]));
+          m = fmaxf(m, __shfl_xor_sync(0xFFFFFFFFu, m, 1));
+          m = fmaxf(m, __shfl_xor_sync(0xFFFFFFFFu, m, 2));
+          // least e with 448 * 2^e >= m, 448 = 1.75 * 2^8: the exponent of m less 8, and one more above 1.75
+          const uint32_t bits = __float_as_uint(m);
+          int e8 = static_cast<int>(bits >> 23) - 8 + ((bits & 0x7FFFFFu) > 0x600000u ? 1 : 0);  // biased by 127
+          e8 = m > 0.0f ? max(e8, 1) : 127;  // 1 .. 247 (an infinite m): the inverse is a normal float too
+          inv = __uint_as_float(static_cast<uint32_t>(254 - e8) << 23);
+          if (in && (v & 3) == 0)
+            static_cast<uint8_t*>(a.y_scale)[row * (a.C >> 5) + (v >> 2)] = static_cast<uint8_t>(e8);
+        }
 #pragma unroll
-    for (int e = 0; e < 8; e += 2) {
-      fmul2(y[e], y[e + 1], lo16(x[e >> 1]), hi16(x[e >> 1]), wv[e], wv[e + 1]);
-      fmul2(y[e], y[e + 1], y[e], y[e + 1], r, r);
-    }
-    if constexpr (FORMAT == H3ATTN_Y_BF16) {
-      if (in)
-        *reinterpret_cast<uint4*>(static_cast<uint16_t*>(a.y) + base + 8 * v) =
-            make_uint4(pack2(y[0], y[1]), pack2(y[2], y[3]), pack2(y[4], y[5]), pack2(y[6], y[7]));
-    } else {
-      if constexpr (FORMAT == H3ATTN_Y_E4M3_MX32) {
-        // the four lanes of a 32-channel group hold neighbouring vectors
-        float m = 0.0f;
-#pragma unroll
-        for (int e = 0; e < 8; e += 2) m = fmax3(m, fabsf(y[e]), fabsf(y[e + 1]));
-        m = fmaxf(m, __shfl_xor_sync(0xFFFFFFFFu, m, 1));
-        m = fmaxf(m, __shfl_xor_sync(0xFFFFFFFFu, m, 2));
-        // least e with 448 * 2^e >= m, 448 = 1.75 * 2^8: the exponent of m less 8, and one more above 1.75
-        const uint32_t bits = __float_as_uint(m);
-        int e8 = static_cast<int>(bits >> 23) - 8 + ((bits & 0x7FFFFFu) > 0x600000u ? 1 : 0);  // biased by 127
-        e8 = m > 0.0f ? max(e8, 1) : 127;  // 1 .. 247 (an infinite m): the inverse is a normal float too
-        inv = __uint_as_float(static_cast<uint32_t>(254 - e8) << 23);
-        if (in && (v & 3) == 0) static_cast<uint8_t*>(a.y_scale)[row * (a.C >> 5) + (v >> 2)] = static_cast<uint8_t>(e8);
+        for (int e = 0; e < 8; e += 2) fmul2(y[e], y[e + 1], y[e], y[e + 1], inv, inv);
+        if (in)
+          *reinterpret_cast<uint2*>(static_cast<uint8_t*>(a.y) + at(j, v)) =
+              make_uint2(pack_e4m3x4(y[0], y[1], y[2], y[3]), pack_e4m3x4(y[4], y[5], y[6], y[7]));
       }
-#pragma unroll
-      for (int e = 0; e < 8; e += 2) fmul2(y[e], y[e + 1], y[e], y[e + 1], inv, inv);
-      if (in)
-        *reinterpret_cast<uint2*>(static_cast<uint8_t*>(a.y) + base + 8 * v) =
-            make_uint2(pack_e4m3x4(y[0], y[1], y[2], y[3]), pack_e4m3x4(y[4], y[5], y[6], y[7]));
     }
   }
 }
@@ -204,6 +235,12 @@ template <int WARPS, int VPT, int FORMAT>
 cudaError_t launch_format(const AddNormArgs& a, cudaStream_t stream) {
   const unsigned threads = WARPS == 1 ? kShortRows * 32 : ((a.C >> 3) + VPT * 32 - 1) / (VPT * 32) * 32;
   const dim3 grid(WARPS == 1 ? (static_cast<unsigned>(a.T) + kShortRows - 1) / kShortRows : a.T);
+  // Two rows a block (see above)
+  if constexpr (VPT == 2 && (WARPS == 8 || (WARPS == 16 && FORMAT == H3ATTN_Y_E4M3_ROW))) {
+    if (!a.residual && a.T >= kManyRows)
+      return launch_dependent(add_rmsnorm_kernel<WARPS, VPT, FORMAT, false, 2>, dim3((static_cast<unsigned>(a.T) + 1) / 2),
+                              threads, 0, stream, a);
+  }
   return a.residual ? launch_dependent(add_rmsnorm_kernel<WARPS, VPT, FORMAT, true>, grid, threads, 0, stream, a)
                     : launch_dependent(add_rmsnorm_kernel<WARPS, VPT, FORMAT, false>, grid, threads, 0, stream, a);
 }
@@ -227,11 +264,13 @@ cudaError_t launch_add_rmsnorm(const AddNormArgs& a, cudaStream_t stream) {
   // Two vectors a thread while the rows are short or few (one row of 5120 channels 1.7 us, with four 2.4; 1200 rows 8.5
   // and 11.1), four with weights read twice where the memory is what counts (32760 rows 168 us, with two 174; of 8192
   // channels 265 and 313).
-  // Without a residual the memory leaves less time for a thread's fixed part, and scales of 32 channels cost the most: four
-  // vectors from 257 on (32760 rows of 4096 channels 70 us, with two 89).
-  if (V > 256 && V <= 512 && !a.residual && a.format == H3ATTN_Y_E4M3_MX32) return launch_rows<8, 4>(a, stream);
+  // Many rows without a residual: scales of 32 channels cost the most instructions, and four vectors a thread share them
+  // from 257 on (32760 rows of 4096 channels 69 us; two rows of two 80).  Row scales keep to two rows of two up to 1024
+  // vectors (16000 rows of 8192 channels 85 us, one of four 91), bf16 does not (93 and 77).
+  const bool many = a.T >= kManyRows, alone = !a.residual && many;
+  if (alone && V > 256 && V <= 512 && a.format == H3ATTN_Y_E4M3_MX32) return launch_rows<8, 4>(a, stream);
   if (V <= 512) return launch_rows<8, 2>(a, stream);
-  if (V <= 1024 && a.T < 2048) return launch_rows<16, 2>(a, stream);
+  if (V <= 1024 && (!many || (alone && a.format == H3ATTN_Y_E4M3_ROW))) return launch_rows<16, 2>(a, stream);
   if (V <= 1024) return launch_rows<8, 4>(a, stream);
   return launch_rows<16, 4>(a, stream);
 }
