@@ -858,11 +858,17 @@ DecodePlan make_plan(const DecodeArgs& a, int sms, bool split) {
   const int64_t capacity = static_cast<int64_t>(a.max_pages) * a.page_size;
   // Two tiles a warp, what joining its warps and asking for the next queries take (64 sequences of up to 2048 tokens, 2
   // key-value heads of 64: 13.1 us without them, 11.0 with them; 200 of up to 2000, 8 and 1 head of 128: 27.9 and 24.1).
+  p.min_tiles = p.WT;  // one a warp: two or more take longer than their partials (7.6 us against 7.0 at 1024 tokens)
   p.start = 2 * loaders;
   const bool whole =
       capacity <= 4 * p.WT * tile || a.B > kMaxSplitBatch || (capacity / 16 + 1 + p.start) * a.B > INT32_MAX;
   p.ranges = split && !whole ? std::max(1, std::min(sms / p.groups, kMaxRanges)) : 0;
-  p.min_tiles = p.WT;  // one a warp: two or more take longer than their partials (7.6 us against 7.0 at 1024 tokens)
+  // Caches without room for a tile a warp, or two where one or two sequences are all, leave half of the SMs to the
+  // call's neighbours and have half the partials to join: one sequence of 8000 tokens, 16 query and 4 key-value heads of
+  // 128, 9.3 us (on all SMs 10.0), 32 and 1 head 9.3 (11.2); 4 of 2000 tokens, 8 and 1 head, 6.9 (7.6).  With two tiles
+  // a warp and many sequences all SMs are better: 48 of 342 tokens, 4 heads of 64, 7.5 (on half of them 8.5).
+  const int64_t tiles = (capacity + tile - 1) / tile * a.B, few = static_cast<int64_t>(p.ranges) * loaders;
+  if (tiles < (a.B <= 2 ? 2 * few : few)) p.ranges = (p.ranges + 1) / 2;
   return p;
 }
 
