@@ -204,3 +204,47 @@ def test_guards_around_the_outputs(h3):
     assert bool((buf[0] == 3).all()) and bool((buf[-1] == 3).all())
     h3.h3attn_add_rmsnorm(x[:0], None, None, buf[:0], None)
     assert np.isfinite(float(buf[1:-1].float().abs().sum()))
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("fmt", FORMATS)
+@pytest.mark.parametrize("T,C", [(2049, 520), (2048, 1016), (2051, 1032), (2049, 2048), (2050, 2080), (2049, 4096), (2049, 4104),
+                                 (2051, 8192), (2049, 8200)])
+def test_many_rows(h3, T, C, fmt):
+    """Enough rows for the layouts of large batches, an odd number of them: the first, the last and some between, a row
+    that is not finite beside others, and nothing behind the last one."""
+    if fmt.startswith("mx"):
+        C = -(-C // 32) * 32
+    x, res = randn(T, C, seed=T + C), randn(T, C, seed=T + C + 1, scale=4.0)
+    x[700, 3] = float("nan")
+    w = torch.rand(C, generator=torch.Generator().manual_seed(C)) + 0.5
+    rows = torch.cat((torch.arange(4), torch.tensor([699, 701]), torch.arange(900, T - 9, 37), torch.arange(T - 9, T)))
+    for residual in (None, res):
+        for weight in (w, None):
+            h, y, scale = call(h3, x.cuda(), None if residual is None else residual.cuda(),
+                               None if weight is None else weight.cuda(), fmt)
+            h_ref, y_ref = add_norm_f64(x[rows], None if residual is None else residual[rows], weight, 1e-6)
+            at = rows.cuda()
+            check(fmt, None if h is None else h[at], y[at] if fmt == "bf16" else y.view(torch.uint8)[at].view(y.dtype),
+                  None if scale is None else scale[at] if fmt == "row" else scale.view(torch.uint8)[at], h_ref, y_ref,
+                  f"T={T} C={C} {fmt} residual={residual is not None}")
+            assert bool(y[700, 3].float().isnan())
+    if fmt == "bf16":
+        buf = torch.full((T + 1, C), 3.0, dtype=torch.bfloat16, device="cuda")
+        h3.h3attn_add_rmsnorm(x.cuda(), None, None, buf[:T], None)
+        assert bool((buf[T] == 3).all())
+        own = x.cuda()
+        h3.h3attn_add_rmsnorm(own, None, None, own, None)  # in place
+        assert same_bits(own[rows.cuda()], buf[:T][rows.cuda()])
+
+
+@pytest.mark.gpu
+def test_guards_behind_scaled_rows(h3):
+    T, C = 2049, 1056
+    x = randn(T, C, seed=16).cuda()
+    y = torch.full((T + 1, C), 0x55, dtype=torch.uint8, device="cuda")
+    s, e = torch.full((T + 1,), 3.0, device="cuda"), torch.full((T + 1, C // 32), 9, dtype=torch.uint8, device="cuda")
+    for scale in (s, e):
+        h3.h3attn_add_rmsnorm(x, None, None, y[:T].view(torch.float8_e4m3fn), None, y_scale=scale[:T])
+        assert bool((y[T] == 0x55).all())
+    assert float(s[T]) == 3.0 and bool((e[T] == 9).all())

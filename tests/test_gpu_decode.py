@@ -284,3 +284,11 @@ def test_workspaces_that_hold_anything(h3):
         o.fill_(float("nan"))
         h3.h3attn_paged_decode(c.dq, o, c.cache, workspace=ws)
         assert torch.equal(o, want), fill
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("lens", [[2000], [8000], [5413, 5400], [2000, 1, 0, 1999], [333] * 12])
+@pytest.mark.parametrize("Hq,Hkv,D", [(16, 4, 128), (8, 1, 128), (32, 1, 128), (24, 8, 64), (4, 2, 256)])
+def test_few_tiles_a_warp(h3, lens, Hq, Hkv, D):
+    """Around the sizes from which on all SMs take part."""
+    check(h3, Case(lens, Hq, Hkv, D, 32, seed=len(lens) + D))
