@@ -22,8 +22,8 @@
 // takes WH neighbouring unit heads, so that its warps read one contiguous
 // stretch of the pages, and its other factor WT = warps / WH splits the
 // tokens.  All sequences' tiles of TILE tokens are numbered through and cut into
-// one range an SM (for each group of WH unit heads), so CTAs differ by one tile
-// however unlike the lengths are; each sequence counts two tiles a warp more than it
+// one range an SM, half of the SMs for small caches (for each group of WH unit
+// heads), so CTAs differ by one tile however unlike the lengths are; each sequence counts two tiles a warp more than it
 // has, which is what starting on one takes.  A range that holds all of a sequence
 // writes its output; of a sequence that ranges share, each range writes its
 // unnormalised O, its maximum and its sum to the workspace, and a second
@@ -227,6 +227,9 @@ __host__ __device__ constexpr int64_t partial_floats(int heads, int D) {
   return partial_o(heads) + static_cast<int64_t>(heads) * D;
 }
 
+// One column tile at D 128 takes 198 registers a thread, which with the joining kernel's 56 just fill an SM's; two take
+// 242, and the join's CTA waits for this one's end.  Held to 200 they spill in the loop: 28 sequences of 0 to 52182
+// tokens, 32 heads to one, 73 us and 94.
 template <int D, int NT, int SHARE>
 __global__ void __launch_bounds__(DecodeCfg<D, NT>::kWarps * 32, 1) decode_kernel(const __grid_constant__ Kernelargs k) {
   using C = DecodeCfg<D, NT>;
