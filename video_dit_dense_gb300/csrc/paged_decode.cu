@@ -52,6 +52,7 @@
 #include <float.h>
 
 #include <algorithm>
+#include <atomic>
 
 #include "generate.h"
 #include "ptx.cuh"
@@ -878,7 +879,7 @@ DecodePlan make_plan(const DecodeArgs& a, int sms, bool split) {
 template <int D, int NT, int SHARE>
 cudaError_t launch_d(const Kernelargs& k, cudaStream_t stream) {
   using C = DecodeCfg<D, NT>;
-  static bool attr_set[64] = {};
+  static std::atomic<bool> attr_set[64];  // calls of several host threads
   int dev = 0;
   cudaError_t e = cudaGetDevice(&dev);
   if (e != cudaSuccess) return e;
