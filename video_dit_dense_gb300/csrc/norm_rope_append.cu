@@ -18,10 +18,11 @@
 // registers.  The rows that a warp takes at a time (32 / (D/16)) are heads of one
 // token where there are many, so that it reads and writes one stretch, and fewer heads
 // of several tokens where there are few, so that no lanes idle.  The heads are
-// cut into parts for several warps as long as there are few tokens.
+// cut into parts for several warps by what fills the SMs in the end.
 // 32760 tokens of 24 + 24 + 24 heads of 128 with norm: 182 us, 6.7 TB/s (a row
 // at a time with its own lookups and table reads: 234 us).
 #include <cuda_bf16.h>
+#include <math.h>
 
 #include <algorithm>
 
@@ -33,7 +34,7 @@ namespace {
 
 constexpr int kThreads = 256;
 constexpr int kUnroll = 2;        // rows a lane works on at a time
-constexpr int kWarpsPerSm = 96;   // parts are made for so many: 32 are resident
+constexpr int kWarpsPerSm = 32;   // resident
 
 __device__ __forceinline__ float bf16lo(uint32_t w) { return __uint_as_float(w << 16); }
 __device__ __forceinline__ float bf16hi(uint32_t w) { return __uint_as_float(w & 0xFFFF0000u); }
@@ -290,8 +291,23 @@ cudaError_t launch_d(AppendArgs a, cudaStream_t stream) {
   a.heads_log2 = std::min(heads >= 48 ? 2 : heads >= 16 ? 1 : 0, RPW == 2 ? 1 : 2);
   const int batch = kUnroll << a.heads_log2, most = (heads + batch - 1) / batch;
   const int64_t warps = (static_cast<int64_t>(a.tokens) + (RPW >> a.heads_log2) - 1) / (RPW >> a.heads_log2);
-  const int64_t parts = std::min<int64_t>(most, std::max<int64_t>(1, static_cast<int64_t>(sms) * kWarpsPerSm / warps));
-  a.heads_per_part = static_cast<int>((most + parts - 1) / parts) * batch;
+  // Into how many parts, by the turns that a warp then takes.  A warp's lookups cost half a turn, and the last wave of
+  // warps fills the SMs half on average: the least of (waves + 1/2) (turns + 1/2), and of one wave where there is less
+  // (11680 tokens of 72 heads of 64: 9 turns in one part or 5 in two 42 us, 2 in five 37; 9769 of 34 heads of 128: 5 turns
+  // 34 us, 3 31; 22858 of 40: 10 turns 79 us, 5 76; one more part than that takes the lookups' time again: 8192 padded
+  // tokens of 24 heads, 2 turns 12.6 us, 1 13.7).
+  const double waves = static_cast<double>(warps) / (static_cast<double>(sms) * kWarpsPerSm);
+  int best = most;
+  double least = HUGE_VAL;
+  for (int turns = most; turns >= 1; turns = std::min(turns - 1, 32)) {
+    const int parts = (most + turns - 1) / turns;
+    const double cost = std::max(waves * parts + 0.5, 1.0) * (turns + 0.5);
+    if (cost < least) {
+      least = cost;
+      best = turns;
+    }
+  }
+  a.heads_per_part = best * batch;
   const int used = (heads + a.heads_per_part - 1) / a.heads_per_part;
   a.div_parts = make_fastdiv(static_cast<uint32_t>(used));
   a.items = static_cast<uint32_t>(warps * used);
