@@ -195,9 +195,9 @@ h3attn_status_t h3attn_qk_norm_rope_append(const void* q, const void* k, const v
   if (S < 0 || Hq < 0 || Hq > 65535) return H3ATTN_ERR_INVALID_ARG;
   if (rotary_dim < 0 || rotary_dim > D || rotary_dim % 2 != 0 || table_rows < 0) return H3ATTN_ERR_INVALID_ARG;
   if (!(eps >= 0.0f) || !isfinite(eps)) return H3ATTN_ERR_INVALID_ARG;
-  if ((q == nullptr) != (Hq == 0) || (q_out == nullptr) != (q == nullptr)) return H3ATTN_ERR_INVALID_ARG;
   const int64_t tokens = static_cast<int64_t>(B) * S;
-  if (tokens == 0) return H3ATTN_OK;
+  if (tokens == 0) return H3ATTN_OK;  // before the pointers: empty tensors have none
+  if ((q == nullptr) != (Hq == 0) || (q_out == nullptr) != (q == nullptr)) return H3ATTN_ERR_INVALID_ARG;
   if (tokens > INT32_MAX || tokens * (Hq + 2LL * Hkv) > INT32_MAX) return H3ATTN_ERR_INVALID_ARG;
   if (!k || !v || (wq && !q)) return H3ATTN_ERR_INVALID_ARG;
   if (rotary_dim > 0 && (!cos || !sin)) return H3ATTN_ERR_INVALID_ARG;
