@@ -462,7 +462,8 @@ typedef struct {
  * pos: [B, S] int32 or NULL.  new_len: [B] int32 or NULL; values are clamped
  *    to [0, S].  len_out: [B] int32 or NULL, not kv_len or new_len.
  * rotary_dim even, 0 <= rotary_dim <= D; eps >= 0 and finite;
- * B * S * (Hq + 2 Hkv) < 2^31; B * S == 0 is a no-op.  q, k, v, q_out, pages, weights and
+ * B * S * (Hq + 2 Hkv) < 2^31; with B * S == 0 there is no token, and nothing
+ * but len_out (B > 0) is written.  q, k, v, q_out, pages, weights and
  * tables 16-byte aligned, int32 arrays 4-byte aligned.  q_out and the pages
  * overlap nothing else.
  * Stream order as for h3attn_rmsnorm_modulate().

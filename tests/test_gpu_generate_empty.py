@@ -44,3 +44,29 @@ def test_the_others_of_no_rows(h3):
     h3.h3attn_add_rmsnorm(x, x.clone(), x.clone(), x.clone())
     cos = torch.empty(0, 32, device="cuda")
     h3.h3attn_rope_table(cos, cos.clone(), 64)
+
+
+@pytest.mark.gpu
+def test_a_step_without_tokens_leaves_the_lengths_in_len_out(h3):
+    """What decode takes next: the lengths as append counts them, not what the buffer held before."""
+    cache, args = step(h3, 2, 0)
+    cache.kv_len.copy_(torch.tensor([17, -4], dtype=torch.int32))
+    out, new = torch.full((3,), 1000, dtype=torch.int32, device="cuda"), torch.tensor([2, -1], dtype=torch.int32, device="cuda")
+    for new_len in (None, new):
+        out.fill_(1000)
+        h3.h3attn_qk_norm_rope_append(*args, new_len=new_len, len_out=out[:2])
+        assert out.tolist() == [17, 0, 1000]
+    cache.kv_len[0] = 40                                   # above the capacity of 32
+    h3.h3attn_qk_norm_rope_append(None, *args[1:3], None, cache, None, None, None, None, 0, len_out=out[:2])
+    assert out.tolist() == [32, 0, 1000]
+    assert bool((cache.k_pages == 3).all()) and h3.h3attn_check_device_status() == 0
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        h3.h3attn_qk_norm_rope_append(*args, len_out=out[:2])
+    cache.kv_len.copy_(torch.tensor([3, 9], dtype=torch.int32))
+    graph.replay()
+    torch.cuda.synchronize()
+    assert out.tolist() == [3, 9, 1000]
+    cache, args = step(h3, 0, 0)
+    h3.h3attn_qk_norm_rope_append(*args, len_out=out[:0])
+    assert h3.h3attn_check_device_status() == 0

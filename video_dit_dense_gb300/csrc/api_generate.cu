@@ -196,16 +196,24 @@ h3attn_status_t h3attn_qk_norm_rope_append(const void* q, const void* k, const v
   if (rotary_dim < 0 || rotary_dim > D || rotary_dim % 2 != 0 || table_rows < 0) return H3ATTN_ERR_INVALID_ARG;
   if (!(eps >= 0.0f) || !isfinite(eps)) return H3ATTN_ERR_INVALID_ARG;
   const int64_t tokens = static_cast<int64_t>(B) * S;
-  if (tokens == 0) return H3ATTN_OK;  // before the pointers: empty tensors have none
+  if (tokens == 0 && (!len_out || B == 0)) return H3ATTN_OK;  // before the pointers: empty tensors have none
+  if (tokens == 0) {
+    // no token, but the lengths are asked for: they stay, in len_out
+    q = k = v = q_out = nullptr;
+    wq = wk = cos = sin = nullptr;
+    pos = nullptr;
+    Hq = rotary_dim = 0;
+    q_stride = k_stride = v_stride = static_cast<int64_t>(Hkv) * D;
+  }
   if ((q == nullptr) != (Hq == 0) || (q_out == nullptr) != (q == nullptr)) return H3ATTN_ERR_INVALID_ARG;
   if (tokens > INT32_MAX || tokens * (Hq + 2LL * Hkv) > INT32_MAX) return H3ATTN_ERR_INVALID_ARG;
-  if (!k || !v || (wq && !q)) return H3ATTN_ERR_INVALID_ARG;
+  if ((tokens > 0 && (!k || !v)) || (wq && !q)) return H3ATTN_ERR_INVALID_ARG;
   if (rotary_dim > 0 && (!cos || !sin)) return H3ATTN_ERR_INVALID_ARG;
   if (k_stride < static_cast<int64_t>(Hkv) * D || v_stride < static_cast<int64_t>(Hkv) * D ||
       (q && q_stride < static_cast<int64_t>(Hq) * D))
     return H3ATTN_ERR_INVALID_ARG;
-  if (k_stride > INT64_MAX / 4 / tokens || v_stride > INT64_MAX / 4 / tokens || (q && q_stride > INT64_MAX / 4 / tokens))
-    return H3ATTN_ERR_INVALID_ARG;
+  const int64_t most = INT64_MAX / 4 / (tokens > 0 ? tokens : 1);
+  if (k_stride > most || v_stride > most || (q && q_stride > most)) return H3ATTN_ERR_INVALID_ARG;
   st = check_cache_pointers(cache);
   if (st != H3ATTN_OK) return st;
   if (!aligned16(k) || !aligned16(v) || (q && (!aligned16(q) || !aligned16(q_out))) || (wq && !aligned16(wq)) ||
@@ -252,7 +260,7 @@ h3attn_status_t h3attn_qk_norm_rope_append(const void* q, const void* k, const v
   a.k_stride = k_stride;
   a.v_stride = v_stride;
   a.tokens = static_cast<uint32_t>(tokens);
-  a.div_s = h3::make_fastdiv(static_cast<uint32_t>(S));
+  a.div_s = h3::make_fastdiv(static_cast<uint32_t>(S > 0 ? S : 1));
   a.div_page = h3::make_fastdiv(static_cast<uint32_t>(cache->page_size));
   a.B = B;
   a.S = S;

@@ -311,7 +311,8 @@ cudaError_t launch_d(AppendArgs a, cudaStream_t stream) {
   const int used = (heads + a.heads_per_part - 1) / a.heads_per_part;
   a.div_parts = make_fastdiv(static_cast<uint32_t>(used));
   a.items = static_cast<uint32_t>(warps * used);
-  const dim3 grid((a.items + kThreads / 32 - 1) / (kThreads / 32));
+  // a block without warps of its own, where there is no token: len_out is written all the same
+  const dim3 grid(std::max((a.items + kThreads / 32 - 1) / (kThreads / 32), 1u));
   if (a.interleaved) return launch_dependent(append_kernel<D, kInterleaved>, grid, kThreads, 0, stream, a);
   if (a.rotary_dim % 16 == 0) return launch_dependent(append_kernel<D, kHalf>, grid, kThreads, 0, stream, a);
   return launch_dependent(append_kernel<D, kStraddling>, grid, kThreads, 0, stream, a);
