@@ -1,5 +1,6 @@
 """Build libh3attn.so in-tree with nvcc for sm_103a, and _step.so, the Python
-binding's host path of the generation operators, with g++ against torch.
+binding's host path of the generation operators, with g++ against torch (where
+there is one: the C library needs the CUDA toolkit alone).
 
 Translation units compile in parallel; the CUDA runtime is linked
 statically so the library loads without a CUDA toolkit on the library path.
@@ -49,21 +50,32 @@ def _stamp() -> str:
     return h.hexdigest()[:20]
 
 
-def _step_command(out: str) -> list[str]:
-    import torch
+def _torch():
+    """The torch that the Python binding's host path is built against: None where there is none with CUDA.  The C library
+    needs neither torch nor Python."""
+    try:
+        import torch
+    except ImportError:
+        return None
+    return torch if torch.version.cuda is not None else None
+
+
+def _step_flags(torch) -> list[str]:
+    return ["-O2", "-std=c++17", "-fPIC", "-shared", f"-D_GLIBCXX_USE_CXX11_ABI={int(torch._C._GLIBCXX_USE_CXX11_ABI)}"]
+
+
+def _step_command(torch, out: str) -> list[str]:
     root = os.path.dirname(torch.__file__)
     cuda = os.path.dirname(os.path.dirname(os.path.realpath(_nvcc())))
     includes = [os.path.join(root, "include"), os.path.join(root, "include", "torch", "csrc", "api", "include"),
                 sysconfig.get_paths()["include"], os.path.join(cuda, "include")]
-    return ["g++", "-O2", "-std=c++17", "-fPIC", "-shared",
-            f"-D_GLIBCXX_USE_CXX11_ABI={int(torch._C._GLIBCXX_USE_CXX11_ABI)}", *(f"-isystem{i}" for i in includes),
-            os.path.join(CSRC, STEP_SOURCE), "-o", out, "-L" + os.path.join(root, "lib"), "-lc10", "-lc10_cuda", "-ltorch_cpu",
-            "-ltorch_python"]
+    return ["g++", *_step_flags(torch), *(f"-isystem{i}" for i in includes), os.path.join(CSRC, STEP_SOURCE), "-o", out,
+            "-L" + os.path.join(root, "lib"), "-lc10", "-lc10_cuda", "-ltorch_cpu", "-ltorch_python"]
 
 
-def _step_stamp() -> str:
-    import torch
-    h = hashlib.sha256(" ".join(_step_command("") + [torch.__version__, sys.version]).encode())
+def _step_stamp(torch) -> str:
+    """Of the sources, the flags and the versions, not of the toolkit: what is current needs no nvcc."""
+    h = hashlib.sha256(" ".join(_step_flags(torch) + [torch.__version__, sys.version]).encode())
     for path in (os.path.join(CSRC, STEP_SOURCE), os.path.join(INCLUDE, "h3attn.h")):
         with open(path, "rb") as f:
             h.update(f.read())
@@ -77,9 +89,9 @@ def _current(lib: str, stamp: str) -> bool:
         return f.read().strip() == stamp
 
 
-def _build_step(stamp: str) -> None:
+def _build_step(torch, stamp: str) -> None:
     tmp = STEP_LIB + f".tmp{os.getpid()}"
-    r = subprocess.run(_step_command(tmp), capture_output=True, text=True)
+    r = subprocess.run(_step_command(torch, tmp), capture_output=True, text=True)
     if r.returncode != 0:
         raise RuntimeError(f"g++ failed on {STEP_SOURCE}:\n{r.stderr}")
     os.replace(tmp, STEP_LIB)
@@ -88,13 +100,21 @@ def _build_step(stamp: str) -> None:
 
 
 def build(force: bool = False, verbose: bool = False) -> str:
-    stamp_path = LIB + ".stamp"
-    st, step_stamp = _stamp(), _step_stamp()
-    lib_current, step_current = not force and _current(LIB, st), not force and _current(STEP_LIB, step_stamp)
-    if lib_current:
-        if not step_current:
-            _build_step(step_stamp)
-        return LIB
+    """Builds what is not current, and returns the C library's path.  Without a torch the binding's host path is left out
+    (its functions say so when they are called); where it does not compile, the C library is built before that is raised."""
+    torch = _torch()
+    st, step_stamp = _stamp(), _step_stamp(torch) if torch else None
+    step_needed = torch is not None and (force or not _current(STEP_LIB, step_stamp))
+    with cf.ThreadPoolExecutor(max_workers=1) as ex:
+        step = ex.submit(_build_step, torch, step_stamp) if step_needed else None
+        if force or not _current(LIB, st):
+            _build_lib(st, verbose)
+        if step is not None:
+            step.result()
+    return LIB
+
+
+def _build_lib(stamp: str, verbose: bool) -> None:
     nvcc = _nvcc()
     os.makedirs(BUILD_DIR, exist_ok=True)
 
@@ -109,20 +129,16 @@ def build(force: bool = False, verbose: bool = False) -> str:
             print(r.stderr)
         return obj
 
-    with cf.ThreadPoolExecutor(max_workers=len(SOURCES) + 1) as ex:
-        step = None if step_current else ex.submit(_build_step, step_stamp)
+    with cf.ThreadPoolExecutor(max_workers=len(SOURCES)) as ex:
         objs = list(ex.map(compile_one, SOURCES))
-        if step is not None:
-            step.result()
     tmp = LIB + f".tmp{os.getpid()}"
     cmd = [nvcc] + ARCH + ["-shared", "-cudart", "static", "-o", tmp] + objs
     r = subprocess.run(cmd, capture_output=True, text=True)
     if r.returncode != 0:
         raise RuntimeError(f"link failed:\n{r.stderr}")
     os.replace(tmp, LIB)
-    with open(stamp_path, "w") as f:
-        f.write(st)
-    return LIB
+    with open(LIB + ".stamp", "w") as f:
+        f.write(stamp)
 
 
 if __name__ == "__main__":
