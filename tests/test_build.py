@@ -73,3 +73,29 @@ def test_each_part_is_rebuilt_by_itself(sandbox):
     del sandbox.ran[:]
     _build.build()
     assert sandbox.ran and all("nvcc" in c[0] for c in sandbox.ran)
+
+
+def test_the_host_path_is_loaded_with_the_versions_it_was_built_for(sandbox, monkeypatch):
+    """Checked before the file is opened: it would read another torch's objects by this one's layouts."""
+    import torch
+    import video_dit_dense_gb300 as h3
+    _build.build()
+    monkeypatch.setattr(h3, "_bound", None)
+    monkeypatch.setattr(h3, "load", lambda: None)
+    opened = []
+
+    def open_module(*_):
+        opened.append(1)
+        raise ImportError("opened")
+    monkeypatch.setattr(h3.importlib, "import_module", open_module)
+    with pytest.raises(ImportError, match="opened"):
+        h3._get_step()
+    for change in (lambda: monkeypatch.setattr(torch, "__version__", "2.0.0"),
+                   lambda: (sandbox.path / "_step.so.stamp").write_text("0123456789abcdef0123")):
+        change()
+        with pytest.raises(RuntimeError, match="was built for"):
+            h3._get_step()
+    assert len(opened) == 1
+    (sandbox.path / "_step.so").unlink()
+    with pytest.raises(RuntimeError, match="missing"):
+        h3._get_step()

@@ -435,9 +435,14 @@ def _get_step():
     global _bound
     if _bound is None:
         lib = load()
-        import torch  # noqa: F401  (the module is linked against torch's libraries)
-        if not os.path.exists(os.path.join(HERE, "_step.so")):
+        import torch  # the module is linked against torch's libraries
+        from . import _build
+        if not os.path.exists(_build.STEP_LIB):
             raise RuntimeError("_step.so is missing: build it with video_dit_dense_gb300.build()")
+        built_for, running = _build.step_built_for(), _build.step_versions(torch)
+        if built_for != running:  # before it is loaded: another version's layouts would be read
+            raise RuntimeError(f"_step.so was built for {built_for or 'versions that are not known'}, this is {running}: "
+                               "build it with video_dit_dense_gb300.build()")
         module = importlib.import_module("._step", __name__)
         module.bind(H3AttnError, PagedKV, *(ctypes.cast(f, ctypes.c_void_p).value for f in (
             lib.h3attn_add_rmsnorm, lib.h3attn_rope_table, lib.h3attn_qk_norm_rope_append, lib.h3attn_paged_decode)))

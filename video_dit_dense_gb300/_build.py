@@ -73,13 +73,26 @@ def _step_command(torch, out: str) -> list[str]:
             "-L" + os.path.join(root, "lib"), "-lc10", "-lc10_cuda", "-ltorch_cpu", "-ltorch_python"]
 
 
+def step_versions(torch) -> str:
+    """What the host path is compiled for and loads with, no other: neither has a stable binary interface."""
+    return f"torch {torch.__version__}, Python {sys.version_info.major}.{sys.version_info.minor}"
+
+
+def step_built_for() -> str:
+    """step_versions() of the host path that is there ("" where that is not known)."""
+    if not os.path.exists(STEP_LIB + ".stamp"):
+        return ""
+    with open(STEP_LIB + ".stamp") as f:
+        return f.read().strip().partition(" ")[2]
+
+
 def _step_stamp(torch) -> str:
     """Of the sources, the flags and the versions, not of the toolkit: what is current needs no nvcc."""
-    h = hashlib.sha256(" ".join(_step_flags(torch) + [torch.__version__, sys.version]).encode())
+    h = hashlib.sha256(" ".join(_step_flags(torch)).encode())
     for path in (os.path.join(CSRC, STEP_SOURCE), os.path.join(INCLUDE, "h3attn.h")):
         with open(path, "rb") as f:
             h.update(f.read())
-    return h.hexdigest()[:20]
+    return f"{h.hexdigest()[:20]} {step_versions(torch)}"
 
 
 def _current(lib: str, stamp: str) -> bool:
