@@ -327,6 +327,7 @@ h3attn_status_t h3attn_prefill_window(const void* q, const void* k, const void* 
  *                        least max |y| / 448 (and at least 2^-126), of each 32
  *                        neighbouring channels, as an 8-bit exponent biased by
  *                        127 (e8m0)
+ * A row's y / s is taken as (h w) (448 / max |h w|), from which r falls out.
  * 448 is the largest e4m3 value, so nothing saturates.  An all-zero row or
  * group has s = 1.  NaN stays NaN, and an infinite h, or squares whose sum
  * passes float32's range, make their row zeros (and NaN where 0 * infinity).
