@@ -385,8 +385,11 @@ typedef struct {
  * The cos / sin tables that h3attn_qk_norm_rope(), its _out form and
  * h3attn_qk_norm_rope_append() take: row n is position p_n, with
  *   cos[n, i] = amplitude * cos(p_n f_i),  sin[n, i] = amplitude * sin(p_n f_i).
- * Angles are kept in 64-bit fractions of a turn, so a row is as exact at
- * position 2^31 as at position 1 (two float32 roundings).
+ * Frequencies are worked out in double precision (a power, and the scaling).
+ * From there on angles are 64-bit fractions of a turn, so a row is as near to
+ * amplitude * cos(p_n f_i) of those frequencies at position 2^31 as at position
+ * 1: within 4 * 2^-24 * amplitude.  A frequency's own rounding moves the angle
+ * by up to |p_n| f_i (2 + ln theta) 2^-53 besides.
  *
  * cos, sin: [N, rotary_dim / 2] float32 outputs (device, 16-byte aligned, no overlap).
  * pos: [N] int32 positions (device, 4-byte aligned; negative ones turn
