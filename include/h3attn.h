@@ -503,6 +503,11 @@ h3attn_status_t h3attn_qk_norm_rope_append(const void* q, const void* k, const v
  *    kernel.  NULL, or a geometry whose size is 0: one CTA walks each sequence
  *    and group of key-value heads (no second kernel).  Calls that share a
  *    workspace must be ordered: one stream, events, or graphs replayed in turn.
+ *    The size is 0 where the page tables have room (max_pages * page_size) for
+ *    a few tiles of tokens only, and for more than 512 sequences: with
+ *    lengths that are unlike, parts of up to 512 in calls of their own are
+ *    faster then.  Lengths are not known on the host, so the launch goes by the
+ *    tables' room: wide tables take short sequences in two kernels, not in one.
  * Products on the tensor cores with float32 accumulation, softmax in float32
  * with exp2, weights kept to 16 bits in the second product, the output rounded
  * once to bf16.  Results do not depend on timing.

@@ -856,7 +856,9 @@ DecodePlan make_plan(const DecodeArgs& a, int sms, bool split) {
   //   second kernel takes (16 query and 4 key-value heads of 128, one sequence: 6.1 us against 6.9 at 128 tokens, 9.0
   //   against 7.2 at 256; 24 heads of each: 5.6 against 6.6 at 64, 8.5 against 6.8 at 128; 8 and 1: 6.8 against 7.7 at
   //   512, 9.7 against 7.8 at 1024);
-  // - the batch is too long for the tables in shared memory: it has sequences enough to fill the GPU;
+  // - the batch is too long for the tables in shared memory.  It has sequences enough to fill the GPU then, which is as
+  //   good where they are alike and is not where one outlasts the others (16 query and 2 key-value heads of 64; 500 to
+  //   1500 tokens: 512 sequences 47 us, 513 46; 0 to 4000 and one of 50000: 512 sequences 91 us, 513 395);
   // - tiles do not fit 32 bits.
   const int tile = a.D == 64 ? 32 : 16;
   const int64_t capacity = static_cast<int64_t>(a.max_pages) * a.page_size;
