@@ -336,7 +336,9 @@ h3attn_status_t h3attn_prefill_window(const void* q, const void* k, const void* 
  *    present exactly when residual is, may be x or residual itself.
  * y: [T, C] bf16 or e4m3 output; in bf16 it may be x or residual itself (then
  *    not h).  w: [C] float32 or NULL.
- * y_scale: [T] float32 (ROW), [T, C / 32] bytes (MX32), NULL (BF16).
+ * y_scale: [T] float32 (ROW), [T, C / 32] bytes (MX32), NULL (BF16).  Row by
+ *    row: a product that takes its block scales in tiles of another order
+ *    needs them rearranged first.
  * C a multiple of 8 (MX32: of 32), 8 <= C <= 16384; eps >= 0 and finite;
  * T == 0 is a no-op.  x, residual, h, y, w 16-byte aligned, a float32 y_scale
  * 4-byte aligned; no other overlap of an output with an input or output.
@@ -503,6 +505,8 @@ h3attn_status_t h3attn_qk_norm_rope_append(const void* q, const void* k, const v
  *    kernel.  NULL, or a geometry whose size is 0: one CTA walks each sequence
  *    and group of key-value heads (no second kernel).  Calls that share a
  *    workspace must be ordered: one stream, events, or graphs replayed in turn.
+ *    Both kernels read the lengths: where several host threads use one stream,
+ *    a call that changes them must not fall between the two.
  *    The size is 0 where the page tables have room (max_pages * page_size) for
  *    a few tiles of tokens only, and for more than 512 sequences: with
  *    lengths that are unlike, parts of up to 512 in calls of their own are

@@ -457,7 +457,7 @@ def h3attn_add_rmsnorm(x, residual, h, y, w=None, eps=1e-6, y_scale=None, stream
     the norm is then of x; h may be x or residual); w: [C] float32 or None.
     y: [T, C], bfloat16, or float8_e4m3fn with y_scale [T] float32 (one scale a
     row) or [T, C / 32] float8_e8m0fnu or uint8 (a power of two for each 32
-    channels).  Returns y.
+    channels, row by row).  Returns y.
     """
     return (_bound or _get_step()).add_rmsnorm(x, residual, h, y, w, eps, y_scale, stream)
 
@@ -568,8 +568,8 @@ def h3attn_paged_decode(q, o, cache: PagedKV, scale=None, workspace=None, stream
 
     q, o: [B, 1, Hq, D] or [B, Hq, D] bf16 (o preallocated); the token's own key
     and value are in the cache.  workspace: None (one CTA walks a sequence), or
-    a CUDA tensor from paged_decode_workspace(): the sequences are then split
-    over the GPU.  Returns o.
+    a CUDA tensor from paged_decode_workspace(): the sequences, up to 512, are
+    then split over the GPU.  Returns o.
     """
     return (_bound or _get_step()).decode(q, o, cache, scale, workspace, stream)
 

@@ -24,7 +24,9 @@
 // (registers) and 186 us and more (shared memory) at 5120.  Threads without a
 // vector cost as much as they leave idle: 256 threads for the 640 vectors of
 // 5120 channels took 195 us.  So does a register too many: 82 a thread instead of 80
-// took 318 us instead of 261 at 8192 channels, two CTAs an SM instead of three.
+// took 318 us instead of 261 at 8192 channels, two CTAs an SM instead of three.  Row scales
+// of up to 16 warps and two vectors a thread do not fit their 48 registers: 4 bytes a thread are
+// stored to local memory without a residual, 16 with one, 12 with two rows a block.
 // Without a residual a row moves 3 or 4 bytes a channel instead of 6 to 8, and what is left is a
 // block's life: load, reduce, store, and 4 bytes of weights a channel from L1.  Two rows a
 // block share all of it.  32760 rows of 4096 channels with row scales: 68 us of 59 (a row a block

@@ -12,9 +12,14 @@
 namespace h3 {
 
 // Launch with programmatic stream serialization: the kernel's CTAs may be
-// placed while the kernel before it in the stream drains; every kernel
-// launched this way executes griddepcontrol.wait before it touches global
-// memory.  What the kernels before may have written (lengths, page tables,
+// placed while the kernel before it in the stream drains.  Every thread of a kernel
+// launched this way executes griddepcontrol.wait, before it writes anything and
+// before it reads what the kernel before it may have written.  One reads global
+// memory earlier: the decode attention's join takes the lengths before its wait,
+// because the kernel before it only reads them and lets it start
+// (griddepcontrol.launch_dependents) after its own wait, when they are final.  A kernel
+// that writes lengths or that lets others start before it has waited must not stand
+// there.  What the kernels before may have written (lengths, page tables,
 // rotary tables) is read with ordinary loads, not through the read-only path,
 // which is for data that stays as it is for the whole life of a kernel.
 template <class... P, class... A>

@@ -15,7 +15,8 @@
 // tiles; larger groups are cut into tiles of 16.  Where there is an even number
 // of those, the two warps of neighbouring ones load every second token tile
 // each and use both, a barrier of the pair a turn; an odd number reads the cache
-// again for each (from L2, as they run side by side).
+// again for each (from L2, as they run side by side: 28 sequences of 754 thousand tokens,
+// 48 heads to one of 128 122 us, 32 to one 74, 16 to one 67).
 //
 // Work.  Lengths are known on the device only, and are unlike.  A "unit head"
 // is a key-value head (and a tile of 16 query heads of its group).  A CTA
@@ -230,7 +231,8 @@ __host__ __device__ constexpr int64_t partial_floats(int heads, int D) {
 
 // One column tile at D 128 takes 198 registers a thread, which with the joining kernel's 56 just fill an SM's; two take
 // 242, and the join's CTA waits for this one's end.  Held to 200 they spill in the loop: 28 sequences of 0 to 52182
-// tokens, 32 heads to one, 73 us and 94.
+// tokens, 32 heads to one, 73 us and 94.  At D 256 two column tiles take all 255 registers and spill (16 bytes stored and
+// 24 loaded a thread; 40 and 72 where warps share their tiles), one takes 244 and does not.
 template <int D, int NT, int SHARE>
 __global__ void __launch_bounds__(DecodeCfg<D, NT>::kWarps * 32, 1) decode_kernel(const __grid_constant__ Kernelargs k) {
   using C = DecodeCfg<D, NT>;
@@ -847,8 +849,9 @@ DecodePlan make_plan(const DecodeArgs& a, int sms, bool split) {
   p.WT = warps / p.WH;
   p.groups = p.unit_heads / p.WH;
   // 28 sequences of 0 to 52182 tokens, 32 heads to one of 128: 83 us without, 73 with; 64 of 0 to 6000, heads of 256: 86 and
-  // 75.  Then a tensor-core product is issued every 9 cycles, and 8 is their rate.  Heads of 64, 9 sequences of 20000 to
-  // 40000: 22.9 without, 23.6 with.
+  // 75.  Neither the memory nor the tensor cores are full then (DRAM 68 %, tensor pipe 46 % busy; heads of 256 36 and 23 %):
+  // a sub-core has two warps, with heads of 256 one, and each is one chain of loads, products, softmax and products.
+  // Heads of 64, 9 sequences of 20000 to 40000: 22.9 without, 23.6 with (DRAM 40 %, tensor pipe 29 %).
   p.share = a.D > 64 && p.q_tiles % 2 == 0 ? 2 : 1;
   const int loaders = p.WT * p.share;  // warps that load different tiles
   // Split into one range an SM, unless
@@ -858,7 +861,7 @@ DecodePlan make_plan(const DecodeArgs& a, int sms, bool split) {
   //   512, 9.7 against 7.8 at 1024);
   // - the batch is too long for the tables in shared memory.  It has sequences enough to fill the GPU then, which is as
   //   good where they are alike and is not where one outlasts the others (16 query and 2 key-value heads of 64; 500 to
-  //   1500 tokens: 512 sequences 47 us, 513 46; 0 to 4000 and one of 50000: 512 sequences 91 us, 513 395);
+  //   1500 tokens: 512 sequences 48 us, 513 48; 0 to 4000 and one of 50000: 512 sequences 91 us, 513 392, 513 in two calls 98);
   // - tiles do not fit 32 bits.
   const int tile = a.D == 64 ? 32 : 16;
   const int64_t capacity = static_cast<int64_t>(a.max_pages) * a.page_size;

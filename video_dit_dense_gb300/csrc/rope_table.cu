@@ -16,8 +16,12 @@
 // Bound by the stores, 8 bytes for each sine and cosine, as long as the
 // arithmetic takes less than 40 instructions a pair: the phase is two 32-bit
 // multiplications, and the polynomials run on two pairs at a time (packed
-// float32 operations).  524291 rows of 64 pairs: 40 us, 6.7 TB/s (66 us
-// with the library's sincospif).
+// float32 operations).  524291 rows of 64 pairs: 39 us, 6.9 TB/s (66 us
+// with the library's sincospif); the values are 3.6e-8 off, where rounding
+// alone leaves 2.7e-8.  A row whose pairs are no multiple of 4 is not 16-byte
+// aligned: then a thread keeps one pair, stores 4 bytes at a time and evaluates it twice,
+// 524291 rows of 23 pairs 24 us (14 at the copy rate), of 65, where a
+// quarter of the threads has no pair, 120 us (40).
 #include "generate.h"
 #include "ptx.cuh"
 
