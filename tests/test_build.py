@@ -99,3 +99,15 @@ def test_the_host_path_is_loaded_with_the_versions_it_was_built_for(sandbox, mon
     (sandbox.path / "_step.so").unlink()
     with pytest.raises(RuntimeError, match="missing"):
         h3._get_step()
+
+
+def test_a_torch_that_does_not_load_is_none(sandbox, monkeypatch):
+    class Broken:
+        @staticmethod
+        def find_spec(name, *_):
+            if name == "torch":
+                raise OSError("libcudart.so: cannot open shared object file")
+    monkeypatch.delitem(sys.modules, "torch", raising=False)
+    monkeypatch.setattr(sys, "meta_path", [Broken] + sys.meta_path)
+    assert _build.build() == _build.LIB
+    assert all("nvcc" in c[0] for c in sandbox.ran)

@@ -55,7 +55,7 @@ def _torch():
     needs neither torch nor Python."""
     try:
         import torch
-    except ImportError:
+    except (ImportError, OSError):  # none, or one whose libraries do not load
         return None
     return torch if torch.version.cuda is not None else None
 
