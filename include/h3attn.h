@@ -529,6 +529,137 @@ h3attn_status_t h3attn_paged_decode(const void* q, void* o, const h3attn_paged_k
  */
 h3attn_status_t h3attn_paged_decode_workspace_size(const h3attn_paged_kv_t* cache, int Hq, size_t* bytes);
 
+/*
+ * A paged key-value cache in 4 bits: pages and page table as in
+ * h3attn_paged_kv_t, a row of D channels held as D / 2 bytes of codes and D / 16
+ * scales.  Channel d of a row stands for (c - 8) s, where
+ *   c = the lower (d even) or upper (d odd) half of byte d / 2,
+ *   s = the binary16 whose bits are byte d / 16 of the row's scales, moved up by 7
+ *       (an unsigned float of 5 exponent and 3 mantissa bits: 0, 2^-17 to 3840 in
+ *       steps of at most 1/8); bytes above 0xD7 (3840) stand for NaN.
+ * A row x is stored with, for each 16 neighbouring channels,
+ *   s = max |x| / 7 rounded to the nearest scale (ties to the even byte), at most 3840,
+ *   c = 8 + min(max(k, -8), 7), k = x / s rounded to the nearest integer, ties away from 0;
+ *   c = 8 where s is 0.  An infinity or a NaN among the 16 makes all of them NaN (s = 0xFF).
+ * Values are exact in bf16.  Errors are at most s / 2, and at most s where k was
+ * cut at -8 or 7, which happens for normal scales (from 2^-14 on) only to x beyond 7.5 s; groups whose
+ * maximum lies past 26880 are cut at 7 * 3840.
+ * 4.5 bits a channel.
+ */
+typedef struct {
+  void* k_codes;             /* [num_pages, page_size, Hkv, D / 2] bytes, 16-byte aligned */
+  void* v_codes;             /* the same */
+  void* k_scales;            /* [num_pages, page_size, Hkv, D / 16] bytes, 16-byte aligned */
+  void* v_scales;            /* the same */
+  const int32_t* page_table; /* [B, max_pages], 4-byte aligned */
+  const int32_t* kv_len;     /* [B], 4-byte aligned */
+  int B;                     /* these as in h3attn_paged_kv_t */
+  int num_pages;
+  int page_size;
+  int max_pages;
+  int Hkv;
+  int D;
+} h3attn_paged_kv4_t;
+
+/*
+ * h3attn_qk_norm_rope_append() into a cache in 4 bits: q_out, len_out and the
+ * bf16 rows that K and V are stored from are bit-identical to that call's.
+ * Arguments and errors as there; the codes and scales are outputs like its pages.
+ */
+h3attn_status_t h3attn_qk_norm_rope_append_q4(const void* q, const void* k, const void* v, void* q_out,
+                                              const h3attn_paged_kv4_t* cache, const float* wq, const float* wk,
+                                              const float* cos, const float* sin, const int32_t* pos,
+                                              const int32_t* new_len, int32_t* len_out, int S, int Hq,
+                                              int64_t q_stride, int64_t k_stride, int64_t v_stride, int table_rows,
+                                              int rotary_dim, int interleaved, float eps, h3attn_stream_t stream);
+
+/*
+ * Tokens of a paged cache as contiguous rows, the K and V of a prefill that
+ * goes on from what the cache holds:
+ *   k[b, s] = token first[b] + s of sequence b (first NULL: s),  0 <= s < S,
+ * where that token is there (first[b] + s < kv_len[b]); the other rows are left
+ * as they are.  Rows of a page outside [0, num_pages) are left too (and
+ * reported), and those of a negative first[b] + s.
+ *
+ * k, v: [B, S, Hkv, D] bf16 outputs, contiguous; either may be NULL.  first: [B] int32 or NULL.
+ * S >= 0, B * S * Hkv < 2^31; B * S == 0 is a no-op.  k, v 16-byte aligned, first 4-byte
+ * aligned; k and v overlap nothing else.  Stream order as for h3attn_rmsnorm_modulate().
+ * Errors: INVALID_ARG, MISALIGNED, UNSUPPORTED_HEAD_DIM, UNSUPPORTED_DEVICE, LAUNCH.
+ */
+h3attn_status_t h3attn_paged_read(const h3attn_paged_kv_t* cache, void* k, void* v, const int32_t* first, int S,
+                                  h3attn_stream_t stream);
+h3attn_status_t h3attn_paged_read_q4(const h3attn_paged_kv4_t* cache, void* k, void* v, const int32_t* first, int S,
+                                     h3attn_stream_t stream);
+
+/*
+ * h3attn_paged_decode() over a cache in 4 bits: o[b, h] = sum_j softmax_j(scale *
+ * q[b, h] . k_j) v_j of the values that codes and scales stand for.
+ * Arguments, errors, workspace rules and rows without a key as there.
+ * The queries are taken in binary16 after scaling each head's row by a power of
+ * two, exact but for channels below 2^-20 of the row's largest, and a weight is
+ * kept to 11 bits in the second product; sums are float32, the output is
+ * rounded once to bf16.  Results do not depend on timing.
+ */
+h3attn_status_t h3attn_paged_decode_q4(const void* q, void* o, const h3attn_paged_kv4_t* cache, int Hq, float scale,
+                                       void* workspace, size_t workspace_bytes, h3attn_stream_t stream);
+h3attn_status_t h3attn_paged_decode_q4_workspace_size(const h3attn_paged_kv4_t* cache, int Hq, size_t* bytes);
+
+/*
+ * The decode attention, with what each token of the cache was attended to by
+ * all query heads added up:
+ *   weights[b, j] += sum_h softmax_j(scale * q[b, h] . k_j),   j < kv_len[b],
+ * o as in h3attn_paged_decode() and h3attn_paged_decode_q4().  The sum over h is
+ * in the order of the heads, float32.  Tokens of a page outside [0, num_pages)
+ * and sequences whose scores are all -infinity add 0.
+ *
+ * weights: [B, max_pages * page_size] float32, 4-byte aligned, overlapping nothing else.
+ * workspace: of at least h3attn_paged_decode_weights_workspace_size() bytes, which
+ *    is never 0 but for B == 0, so it is required: the scores lie in it between the
+ *    kernels, 4 bytes for each query head and token that the page tables have room for.
+ * Other arguments, rules and errors as for h3attn_paged_decode().
+ */
+h3attn_status_t h3attn_paged_decode_weights(const void* q, void* o, const h3attn_paged_kv_t* cache, int Hq,
+                                            float scale, float* weights, void* workspace, size_t workspace_bytes,
+                                            h3attn_stream_t stream);
+h3attn_status_t h3attn_paged_decode_weights_workspace_size(const h3attn_paged_kv_t* cache, int Hq, size_t* bytes);
+h3attn_status_t h3attn_paged_decode_weights_q4(const void* q, void* o, const h3attn_paged_kv4_t* cache, int Hq,
+                                               float scale, float* weights, void* workspace, size_t workspace_bytes,
+                                               h3attn_stream_t stream);
+h3attn_status_t h3attn_paged_decode_weights_q4_workspace_size(const h3attn_paged_kv4_t* cache, int Hq, size_t* bytes);
+
+/*
+ * Eviction from a paged cache by the weights that h3attn_paged_decode_weights()
+ * adds up.  A sequence of n = kv_len[b] > keep tokens is brought back to keep:
+ * its last `recent` tokens stay, and of the n - recent older ones the keep -
+ * recent of greatest weight (of equal weights the lower place; a NaN counts as the
+ * greatest).  Kept tokens move into places [0, keep):
+ *   - an older one in a place below keep - recent stays there; the i-th one, by
+ *     place, of those beyond moves to the i-th place below that is given up;
+ *   - the recent ones take places keep - recent to keep - 1 in their order.
+ * A decode step does not depend on the order of a cache (a key's position is in
+ * its rotation), so few rows move: appends go on at len_out, with their own pos.
+ * weights move with their tokens, those of the places from keep to n - 1 become 0,
+ * and so does what is appended there; rows and weights of the other places stay as they were.  Sequences of at most keep tokens
+ * are left as they are.
+ * Pages of the places that change must be the sequence's own.  Rows that lie in a
+ * page outside [0, num_pages), or are to go to one, are not moved (and reported).
+ *
+ * weights: [B, max_pages * page_size] float32, 4-byte aligned.
+ * keep >= 1, 0 <= recent <= keep.  len_out: [B] int32, receives min(kv_len, keep)
+ *    (at least 0; kv_len is not changed); may not be kv_len.
+ * workspace: h3attn_paged_evict_workspace_size() bytes for the same sizes, 16-byte
+ *    aligned (NULL where that is 0: B == 0); its contents on entry do not matter.  Calls that share one must be ordered.
+ * Outputs (pages, weights, len_out, workspace) overlap nothing else.  Stream order as for
+ * h3attn_rmsnorm_modulate().
+ * Errors: INVALID_ARG, MISALIGNED, UNSUPPORTED_HEAD_DIM, UNSUPPORTED_DEVICE, LAUNCH.
+ */
+h3attn_status_t h3attn_paged_evict(const h3attn_paged_kv_t* cache, float* weights, int keep, int recent,
+                                   int32_t* len_out, void* workspace, size_t workspace_bytes, h3attn_stream_t stream);
+h3attn_status_t h3attn_paged_evict_q4(const h3attn_paged_kv4_t* cache, float* weights, int keep, int recent,
+                                      int32_t* len_out, void* workspace, size_t workspace_bytes, h3attn_stream_t stream);
+h3attn_status_t h3attn_paged_evict_workspace_size(int B, int page_size, int max_pages, int keep, int recent,
+                                                  size_t* bytes);
+
 /* Static English description of a status code (never NULL). */
 const char* h3attn_status_string(h3attn_status_t status);
 

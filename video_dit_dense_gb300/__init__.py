@@ -37,6 +37,20 @@ Generation over a paged key-value cache (``PagedKV``), one step of a block:
   of one new token per sequence over the cache.
 * ``h3attn_rope_table(cos, sin, rotary_dim, theta, scaling, pos, first,
   stream)`` -- rotary tables, also scaled for long contexts.
+
+and what keeps the cache small:
+
+* ``h3attn_qk_norm_rope_append_q4(q, k, v, q_out, cache, ...)`` -- the append
+  into a cache in 4 bits (``PagedKV4``).
+* ``h3attn_paged_decode_q4(q, o, cache, scale, workspace, stream)`` -- the
+  decode attention over it.
+* ``h3attn_paged_read(cache, k, v, first, stream)`` -- tokens of either cache
+  as contiguous rows, for a prefill that goes on from them.
+* ``h3attn_paged_decode_weights(q, o, cache, weights, workspace, scale,
+  stream)`` -- the decode attention of either cache, with what each token was
+  attended to added up.
+* ``h3attn_paged_evict(cache, weights, keep, recent, len_out, workspace,
+  stream)`` -- eviction of the tokens that were attended to least.
 """
 from __future__ import annotations
 
@@ -63,6 +77,11 @@ EXPORTED = ("h3attn_qk_norm_rope", "h3attn_qk_norm_rope_out", "h3attn_prefill", 
             "h3attn_prefill_workspace_size", "h3attn_prefill_noalloc", "h3attn_prefill_window",
             "h3attn_rmsnorm_modulate", "h3attn_add_rmsnorm", "h3attn_rope_table", "h3attn_qk_norm_rope_append",
             "h3attn_paged_decode", "h3attn_paged_decode_workspace_size",
+            "h3attn_qk_norm_rope_append_q4", "h3attn_paged_read", "h3attn_paged_read_q4", "h3attn_paged_decode_q4",
+            "h3attn_paged_decode_q4_workspace_size", "h3attn_paged_decode_weights",
+            "h3attn_paged_decode_weights_workspace_size", "h3attn_paged_decode_weights_q4",
+            "h3attn_paged_decode_weights_q4_workspace_size", "h3attn_paged_evict", "h3attn_paged_evict_q4",
+            "h3attn_paged_evict_workspace_size",
             "h3attn_status_string", "h3attn_check_device_status", "h3attn_version")
 
 
@@ -87,6 +106,13 @@ class h3attn_paged_kv_t(ctypes.Structure):
     _fields_ = [("k_pages", ctypes.c_void_p), ("v_pages", ctypes.c_void_p), ("page_table", ctypes.c_void_p),
                 ("kv_len", ctypes.c_void_p), ("B", ctypes.c_int), ("num_pages", ctypes.c_int),
                 ("page_size", ctypes.c_int), ("max_pages", ctypes.c_int), ("Hkv", ctypes.c_int), ("D", ctypes.c_int)]
+
+
+class h3attn_paged_kv4_t(ctypes.Structure):
+    _fields_ = [("k_codes", ctypes.c_void_p), ("v_codes", ctypes.c_void_p), ("k_scales", ctypes.c_void_p),
+                ("v_scales", ctypes.c_void_p), ("page_table", ctypes.c_void_p), ("kv_len", ctypes.c_void_p),
+                ("B", ctypes.c_int), ("num_pages", ctypes.c_int), ("page_size", ctypes.c_int), ("max_pages", ctypes.c_int),
+                ("Hkv", ctypes.c_int), ("D", ctypes.c_int)]
 
 
 class h3attn_rope_scaling_t(ctypes.Structure):
@@ -151,6 +177,19 @@ def load(path: str = LIB_PATH):
             lib.h3attn_paged_decode.restype = I
             lib.h3attn_paged_decode_workspace_size.argtypes = [cache, I, ctypes.POINTER(ctypes.c_size_t)]
             lib.h3attn_paged_decode_workspace_size.restype = I
+            cache4, sized = ctypes.POINTER(h3attn_paged_kv4_t), ctypes.POINTER(ctypes.c_size_t)
+            lib.h3attn_qk_norm_rope_append_q4.argtypes = [cache4 if t is cache else t
+                                                          for t in lib.h3attn_qk_norm_rope_append.argtypes]
+            lib.h3attn_paged_decode_q4.argtypes = [P, P, cache4, I, F, P, ctypes.c_size_t, P]
+            lib.h3attn_paged_decode_q4_workspace_size.argtypes = [cache4, I, sized]
+            for c, suffix in ((cache, ""), (cache4, "_q4")):
+                getattr(lib, "h3attn_paged_read" + suffix).argtypes = [c, P, P, P, I, P]
+                getattr(lib, "h3attn_paged_decode_weights" + suffix).argtypes = [P, P, c, I, F, P, P, ctypes.c_size_t, P]
+                getattr(lib, f"h3attn_paged_decode_weights{suffix}_workspace_size").argtypes = [c, I, sized]
+                getattr(lib, "h3attn_paged_evict" + suffix).argtypes = [c, P, I, I, P, P, ctypes.c_size_t, P]
+            lib.h3attn_paged_evict_workspace_size.argtypes = [I, I, I, I, I, sized]
+            for name in EXPORTED:
+                getattr(lib, name).restype = I
             lib.h3attn_status_string.argtypes = [I]
             lib.h3attn_status_string.restype = ctypes.c_char_p
             lib.h3attn_check_device_status.argtypes = [P]
@@ -444,8 +483,11 @@ def _get_step():
             raise RuntimeError(f"_step.so was built for {built_for or 'versions that are not known'}, this is {running}: "
                                "build it with video_dit_dense_gb300.build()")
         module = importlib.import_module("._step", __name__)
-        module.bind(H3AttnError, PagedKV, *(ctypes.cast(f, ctypes.c_void_p).value for f in (
-            lib.h3attn_add_rmsnorm, lib.h3attn_rope_table, lib.h3attn_qk_norm_rope_append, lib.h3attn_paged_decode)))
+        module.bind(H3AttnError, PagedKV, PagedKV4, *(ctypes.cast(f, ctypes.c_void_p).value for f in (
+            lib.h3attn_add_rmsnorm, lib.h3attn_rope_table, lib.h3attn_qk_norm_rope_append, lib.h3attn_paged_decode,
+            lib.h3attn_qk_norm_rope_append_q4, lib.h3attn_paged_decode_q4, lib.h3attn_paged_decode_weights,
+            lib.h3attn_paged_decode_weights_q4, lib.h3attn_paged_read, lib.h3attn_paged_read_q4, lib.h3attn_paged_evict,
+            lib.h3attn_paged_evict_q4)))
         _bound = module
     return _bound
 
@@ -547,6 +589,46 @@ class PagedKV:
         return PagedKV(self.k_pages, self.v_pages, self.page_table, kv_len)
 
 
+class PagedKV4:
+    """A paged key-value cache in 4 bits: see h3attn_paged_kv4_t.
+
+    k_codes, v_codes: [num_pages, page_size, Hkv, D / 2] uint8; k_scales,
+    v_scales: [num_pages, page_size, Hkv, D / 16] uint8; page_table and kv_len as
+    in PagedKV.  Kept by reference like there.
+    """
+    __slots__ = ("_tensors", "_struct", "_address", "_device")
+
+    def __init__(self, k_codes, v_codes, k_scales, v_scales, page_table, kv_len):
+        import torch
+        if k_codes.dim() != 4 or page_table.dim() != 2:
+            raise H3AttnError(H3ATTN_ERR_INVALID_ARG,
+                              "codes must be [num_pages, page_size, Hkv, D / 2], page_table [B, max_pages]")
+        num_pages, page_size, Hkv, half = k_codes.shape
+        B, max_pages = page_table.shape
+        D = 2 * half
+        if max(num_pages, page_size, Hkv, D, B, max_pages) >= 2 ** 31:
+            raise H3AttnError(H3ATTN_ERR_INVALID_ARG, "the cache's sizes must fit 32 bits")
+        self._device = k_codes.get_device()
+        for name, t, n in (("k_codes", k_codes, 2), ("v_codes", v_codes, 2), ("k_scales", k_scales, 16), ("v_scales", v_scales, 16)):
+            _check(name, t, torch.uint8, (num_pages, page_size, Hkv, D // n), self._device)
+        _check("page_table", page_table, torch.int32, (B, max_pages), self._device)
+        _check("kv_len", kv_len, torch.int32, (B,), self._device)
+        self._tensors = (k_codes, v_codes, k_scales, v_scales, page_table, kv_len)
+        self._struct = h3attn_paged_kv4_t(*(t.data_ptr() for t in self._tensors), B, num_pages, page_size, max_pages, Hkv, D)
+        self._address = ctypes.addressof(self._struct)
+
+    k_codes = property(lambda self: self._tensors[0])
+    v_codes = property(lambda self: self._tensors[1])
+    k_scales = property(lambda self: self._tensors[2])
+    v_scales = property(lambda self: self._tensors[3])
+    page_table = property(lambda self: self._tensors[4])
+    kv_len = property(lambda self: self._tensors[5])
+
+    def with_lengths(self, kv_len):
+        """The same cache with another lengths tensor (len_out of an append or an eviction)."""
+        return PagedKV4(*self._tensors[:5], kv_len)
+
+
 def h3attn_qk_norm_rope_append(q, k, v, q_out, cache: PagedKV, wq, wk, cos, sin, rotary_dim=96, eps=1e-6,
                                interleaved=False, pos=None, new_len=None, len_out=None, stream=None):
     """Q/K RMSNorm + bf16 boundary + partial RoPE of new tokens; K and V go to
@@ -589,6 +671,98 @@ def paged_decode_workspace(q, cache: PagedKV):
     n = h3attn_paged_decode_workspace_size(cache, q.shape[-2])
     import torch
     return torch.empty(n, dtype=torch.uint8, device=q.device) if n else None
+
+
+def h3attn_qk_norm_rope_append_q4(q, k, v, q_out, cache: PagedKV4, wq, wk, cos, sin, rotary_dim=96, eps=1e-6,
+                                  interleaved=False, pos=None, new_len=None, len_out=None, stream=None):
+    """h3attn_qk_norm_rope_append into a cache in 4 bits: the same arguments, the
+    same q_out and len_out; K and V rows are stored as codes and scales."""
+    return (_bound or _get_step()).append_q4(q, k, v, q_out, cache, wq, wk, cos, sin, rotary_dim, eps, interleaved, pos, new_len,
+                                            len_out, stream)
+
+
+def h3attn_paged_read(cache, k, v, first=None, stream=None):
+    """k, v <- the tokens first[b], first[b] + 1, ... of each sequence.
+
+    cache: a PagedKV or a PagedKV4; k, v: contiguous [B, S, Hkv, D] bf16 (either
+    may be None); first: [B] int32 or None (from token 0).  Rows of tokens that
+    the cache does not hold are left as they are.  Returns (k, v).
+    """
+    (_bound or _get_step()).read(cache, k, v, first, stream)
+    return k, v
+
+
+def h3attn_paged_decode_q4(q, o, cache: PagedKV4, scale=None, workspace=None, stream=None):
+    """h3attn_paged_decode over a cache in 4 bits; workspace: None, or a CUDA
+    tensor from paged_decode_q4_workspace().  Returns o."""
+    return (_bound or _get_step()).decode_q4(q, o, cache, scale, workspace, stream)
+
+
+def h3attn_paged_decode_weights(q, o, cache, weights, workspace, scale=None, stream=None):
+    """The decode attention of a PagedKV or a PagedKV4, with each token's
+    attention weights, summed over the query heads, added to weights: [B,
+    max_pages * page_size] float32.  workspace: a CUDA tensor from
+    paged_decode_weights_workspace().  Returns o.
+    """
+    return (_bound or _get_step()).decode_weights(q, o, cache, scale, weights, workspace, stream)
+
+
+def h3attn_paged_evict(cache, weights, keep, recent, len_out, workspace, stream=None):
+    """Brings each sequence of more than keep tokens back to keep: its recent
+    last ones, and of the others the heaviest by weights.
+
+    cache: a PagedKV or a PagedKV4, whose rows move; weights: [B, max_pages *
+    page_size] float32, moved with them; len_out: [B] int32, the lengths after it
+    (for cache.with_lengths); workspace: a CUDA tensor from
+    paged_evict_workspace().  Returns len_out.
+    """
+    return (_bound or _get_step()).evict(cache, weights, keep, recent, len_out, workspace, stream)
+
+
+def _sized(entry, *args) -> int:
+    out = ctypes.c_size_t(0)
+    _raise_if(getattr(load(), entry)(*args, ctypes.byref(out)), entry)
+    return int(out.value)
+
+
+def _workspace(n, device):
+    import torch
+    return torch.empty(n, dtype=torch.uint8, device=device) if n else None
+
+
+def h3attn_paged_decode_q4_workspace_size(cache: PagedKV4, Hq) -> int:
+    """Bytes of workspace h3attn_paged_decode_q4 takes for this cache and Hq query heads (0: no split)."""
+    return _sized("h3attn_paged_decode_q4_workspace_size", ctypes.byref(cache._struct), int(Hq))
+
+
+def paged_decode_q4_workspace(q, cache: PagedKV4):
+    """A workspace tensor for h3attn_paged_decode_q4(q, ..., cache) on the current
+    device, or None when the call does not split (allocated by torch)."""
+    return _workspace(h3attn_paged_decode_q4_workspace_size(cache, q.shape[-2]), q.device)
+
+
+def h3attn_paged_decode_weights_workspace_size(cache, Hq) -> int:
+    """Bytes of workspace h3attn_paged_decode_weights takes for this cache (of either kind) and Hq query heads."""
+    kind = "_q4" if isinstance(cache, PagedKV4) else ""
+    return _sized(f"h3attn_paged_decode_weights{kind}_workspace_size", ctypes.byref(cache._struct), int(Hq))
+
+
+def paged_decode_weights_workspace(q, cache):
+    """A workspace tensor for h3attn_paged_decode_weights(q, ..., cache) on the
+    current device (allocated by torch; None for an empty batch)."""
+    return _workspace(h3attn_paged_decode_weights_workspace_size(cache, q.shape[-2]), q.device)
+
+
+def h3attn_paged_evict_workspace_size(cache, keep, recent) -> int:
+    """Bytes of workspace h3attn_paged_evict takes for this cache (of either kind), keep and recent."""
+    s = cache._struct
+    return _sized("h3attn_paged_evict_workspace_size", s.B, s.page_size, s.max_pages, int(keep), int(recent))
+
+
+def paged_evict_workspace(cache, keep, recent):
+    """A workspace tensor for h3attn_paged_evict(cache, ..., keep, recent)
+    (allocated by torch on the cache's device; None for an empty batch)."""
+    return _workspace(h3attn_paged_evict_workspace_size(cache, keep, recent), cache.page_table.device)
 
 
 def h3attn_check_device_status(stream=None) -> int:

@@ -25,8 +25,9 @@ STEP_LIB = os.path.join(HERE, "_step.so")
 STEP_SOURCE = "step.cpp"
 BUILD_DIR = os.path.join(HERE, "_build")
 SOURCES = ["api.cu", "api_generate.cu", "qk_norm_rope.cu", "attn_fwd.cu", "rmsnorm_modulate.cu", "add_rmsnorm.cu",
-           "rope_table.cu", "norm_rope_append.cu", "paged_decode.cu"]
-HEADERS = ["ptx.cuh", "internal.h", "api_common.h", "generate.h", "attn_pipe.cuh", "attn_persist.cuh", "attn_wide.cuh", "attn_chain.cuh"]
+           "rope_table.cu", "norm_rope_append.cu", "paged_decode.cu", "paged_decode_q4.cu", "decode_weights.cu", "paged_read.cu",
+           "paged_evict.cu"]
+HEADERS = ["ptx.cuh", "internal.h", "api_common.h", "generate.h", "cache4.cuh", "decode_common.cuh", "attn_pipe.cuh", "attn_persist.cuh", "attn_wide.cuh", "attn_chain.cuh"]
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 NVCC_FLAGS = ARCH + ["-O3", "-lineinfo", "-std=c++17", "-Xcompiler", "-fPIC", "-Xcompiler", "-O2",
                      "--expt-relaxed-constexpr", f"-I{INCLUDE}"]

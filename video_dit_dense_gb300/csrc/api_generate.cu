@@ -1,5 +1,6 @@
 // C-ABI entry points of the generation operators: residual add + RMSNorm,
-// rotary tables, append to a paged cache, decode attention.  Argument
+// rotary tables, append to a paged cache in bf16 or in 4 bits, reading it,
+// decode attention with and without the tokens' weights, eviction.  Argument
 // validation and error mapping; nothing is allocated, and all work is
 // enqueued on the caller's stream.
 #include <math.h>
@@ -43,46 +44,354 @@ uint64_t turn_fraction(double f) {
   return static_cast<uint64_t>(whole) + static_cast<uint64_t>(static_cast<int64_t>(llrint((p - whole) + err)));
 }
 
+// A paged cache in bf16 or in 4 bits.
+struct Cache {
+  const void *k, *v, *k_scales, *v_scales;
+  const int32_t *page_table, *kv_len;
+  int B, num_pages, page_size, max_pages, Hkv, D;
+  bool there, q4;
+  int64_t tokens() const { return static_cast<int64_t>(num_pages) * page_size; }
+  int64_t capacity() const { return static_cast<int64_t>(max_pages) * page_size; }
+  int64_t row_bytes() const { return static_cast<int64_t>(Hkv) * (q4 ? D / 2 : 2 * D); }
+  int64_t scale_bytes() const { return q4 ? static_cast<int64_t>(Hkv) * (D / 16) : 0; }
+  Span k_span() const { return {k, tokens() * row_bytes()}; }
+  Span v_span() const { return {v, tokens() * row_bytes()}; }
+  Span ks_span() const { return {k_scales, tokens() * scale_bytes()}; }
+  Span vs_span() const { return {v_scales, tokens() * scale_bytes()}; }
+  Span table_span() const { return {page_table, 4LL * B * max_pages}; }
+  Span len_span() const { return {kv_len, 4LL * B}; }
+};
+Cache of(const h3attn_paged_kv_t* c) {
+  if (!c) return Cache{};
+  return {c->k_pages, c->v_pages, nullptr,      nullptr,      c->page_table, c->kv_len, c->B,
+          c->num_pages, c->page_size, c->max_pages, c->Hkv, c->D, true, false};
+}
+Cache of(const h3attn_paged_kv4_t* c) {
+  if (!c) return Cache{};
+  return {c->k_codes, c->v_codes, c->k_scales,  c->v_scales,  c->page_table, c->kv_len, c->B,
+          c->num_pages, c->page_size, c->max_pages, c->Hkv, c->D, true, true};
+}
+
 // Geometry of a paged cache (its pointers apart).
-h3attn_status_t check_cache(const h3attn_paged_kv_t* c) {
-  if (!c || c->B < 0 || c->B > 65535 || c->Hkv < 1 || c->Hkv > 65535) return H3ATTN_ERR_INVALID_ARG;
-  if (!head_dim_ok(c->D)) return H3ATTN_ERR_UNSUPPORTED_HEAD_DIM;
-  if (c->num_pages < 1 || c->page_size < 1 || c->max_pages < 1) return H3ATTN_ERR_INVALID_ARG;
-  if (static_cast<int64_t>(c->num_pages) * c->page_size > INT32_MAX ||
-      static_cast<int64_t>(c->max_pages) * c->page_size > INT32_MAX - 63)
+h3attn_status_t check_geometry(int B, int num_pages, int page_size, int max_pages) {
+  if (B < 0 || B > 65535 || num_pages < 1 || page_size < 1 || max_pages < 1) return H3ATTN_ERR_INVALID_ARG;
+  if (static_cast<int64_t>(num_pages) * page_size > INT32_MAX || static_cast<int64_t>(max_pages) * page_size > INT32_MAX - 63)
     return H3ATTN_ERR_INVALID_ARG;
   return H3ATTN_OK;
 }
-h3attn_status_t check_cache_pointers(const h3attn_paged_kv_t* c) {
-  if (!c->k_pages || !c->v_pages || !c->page_table || !c->kv_len) return H3ATTN_ERR_INVALID_ARG;
-  if (!aligned16(c->k_pages) || !aligned16(c->v_pages) || !aligned4(c->page_table) || !aligned4(c->kv_len))
+h3attn_status_t check_cache(const Cache& c) {
+  if (!c.there || c.B < 0 || c.B > 65535 || c.Hkv < 1 || c.Hkv > 65535) return H3ATTN_ERR_INVALID_ARG;
+  if (!head_dim_ok(c.D)) return H3ATTN_ERR_UNSUPPORTED_HEAD_DIM;
+  return check_geometry(c.B, c.num_pages, c.page_size, c.max_pages);
+}
+h3attn_status_t check_cache_pointers(const Cache& c) {
+  if (!c.k || !c.v || !c.page_table || !c.kv_len || (c.q4 && (!c.k_scales || !c.v_scales))) return H3ATTN_ERR_INVALID_ARG;
+  if (!aligned16(c.k) || !aligned16(c.v) || !aligned16(c.k_scales) || !aligned16(c.v_scales) || !aligned4(c.page_table) ||
+      !aligned4(c.kv_len))
     return H3ATTN_ERR_MISALIGNED;
   return H3ATTN_OK;
 }
-int64_t page_bytes(const h3attn_paged_kv_t* c) {
-  return static_cast<int64_t>(c->num_pages) * c->page_size * c->Hkv * c->D * 2;
-}
 
-void decode_fields(h3::DecodeArgs* a, const h3attn_paged_kv_t* c, int Hq) {
-  a->k_pages = static_cast<const uint16_t*>(c->k_pages);
-  a->v_pages = static_cast<const uint16_t*>(c->v_pages);
-  a->page_table = c->page_table;
-  a->kv_len = c->kv_len;
-  a->B = c->B;
+void decode_fields(h3::DecodeArgs* a, const Cache& c, int Hq) {
+  *a = {};
+  a->k_pages = static_cast<const uint16_t*>(c.k);
+  a->v_pages = static_cast<const uint16_t*>(c.v);
+  a->k_scales = static_cast<const uint8_t*>(c.k_scales);
+  a->v_scales = static_cast<const uint8_t*>(c.v_scales);
+  a->page_table = c.page_table;
+  a->kv_len = c.kv_len;
+  a->B = c.B;
   a->Hq = Hq;
-  a->Hkv = c->Hkv;
-  a->D = c->D;
-  a->page_size = c->page_size;
-  a->max_pages = c->max_pages;
-  a->num_pages = c->num_pages;
-  a->div_page = h3::make_fastdiv(static_cast<uint32_t>(c->page_size));
+  a->Hkv = c.Hkv;
+  a->D = c.D;
+  a->page_size = c.page_size;
+  a->max_pages = c.max_pages;
+  a->num_pages = c.num_pages;
+  a->div_page = h3::make_fastdiv(static_cast<uint32_t>(c.page_size));
 }
 
 // Head counts of a decode call: whole groups, and work units in 32 bits.
-h3attn_status_t check_decode_heads(const h3attn_paged_kv_t* c, int Hq) {
-  if (Hq < 1 || Hq > 65535 || Hq % c->Hkv != 0) return H3ATTN_ERR_INVALID_ARG;
-  if (static_cast<int64_t>(c->B) * c->Hkv * ((Hq / c->Hkv + 15) / 16) > INT32_MAX) return H3ATTN_ERR_INVALID_ARG;
+h3attn_status_t check_decode_heads(const Cache& c, int Hq) {
+  if (Hq < 1 || Hq > 65535 || Hq % c.Hkv != 0) return H3ATTN_ERR_INVALID_ARG;
+  if (static_cast<int64_t>(c.B) * c.Hkv * ((Hq / c.Hkv + 15) / 16) > INT32_MAX) return H3ATTN_ERR_INVALID_ARG;
   return H3ATTN_OK;
+}
+
+h3attn_status_t append_to(const void* q, const void* k, const void* v, void* q_out,
+                          const Cache& cache, const float* wq, const float* wk, const float* cos, const float* sin,
+                          const int32_t* pos, const int32_t* new_len, int32_t* len_out, int S, int Hq, int64_t q_stride,
+                          int64_t k_stride, int64_t v_stride, int table_rows, int rotary_dim, int interleaved, float eps,
+                          h3attn_stream_t stream) {
+  h3attn_status_t st = check_cache(cache);
+  if (st != H3ATTN_OK) return st;
+  const int B = cache.B, Hkv = cache.Hkv, D = cache.D;
+  if (S < 0 || Hq < 0 || Hq > 65535) return H3ATTN_ERR_INVALID_ARG;
+  if (rotary_dim < 0 || rotary_dim > D || rotary_dim % 2 != 0 || table_rows < 0) return H3ATTN_ERR_INVALID_ARG;
+  if (!(eps >= 0.0f) || !isfinite(eps)) return H3ATTN_ERR_INVALID_ARG;
+  const int64_t tokens = static_cast<int64_t>(B) * S;
+  if (tokens == 0 && (!len_out || B == 0)) return H3ATTN_OK;  // before the pointers: empty tensors have none
+  if (tokens == 0) {
+    // no token, but the lengths are asked for: they stay, in len_out
+    q = k = v = q_out = nullptr;
+    wq = wk = cos = sin = nullptr;
+    pos = nullptr;
+    Hq = rotary_dim = 0;
+    q_stride = k_stride = v_stride = static_cast<int64_t>(Hkv) * D;
+  }
+  if ((q == nullptr) != (Hq == 0) || (q_out == nullptr) != (q == nullptr)) return H3ATTN_ERR_INVALID_ARG;
+  if (tokens > INT32_MAX || tokens * (Hq + 2LL * Hkv) > INT32_MAX) return H3ATTN_ERR_INVALID_ARG;
+  if ((tokens > 0 && (!k || !v)) || (wq && !q)) return H3ATTN_ERR_INVALID_ARG;
+  if (rotary_dim > 0 && (!cos || !sin)) return H3ATTN_ERR_INVALID_ARG;
+  if (k_stride < static_cast<int64_t>(Hkv) * D || v_stride < static_cast<int64_t>(Hkv) * D ||
+      (q && q_stride < static_cast<int64_t>(Hq) * D))
+    return H3ATTN_ERR_INVALID_ARG;
+  const int64_t most = INT64_MAX / 4 / (tokens > 0 ? tokens : 1);
+  if (k_stride > most || v_stride > most || (q && q_stride > most)) return H3ATTN_ERR_INVALID_ARG;
+  st = check_cache_pointers(cache);
+  if (st != H3ATTN_OK) return st;
+  if (!aligned16(k) || !aligned16(v) || (q && (!aligned16(q) || !aligned16(q_out))) || (wq && !aligned16(wq)) ||
+      (wk && !aligned16(wk)) || (cos && !aligned16(cos)) || (sin && !aligned16(sin)) || (pos && !aligned4(pos)) ||
+      (new_len && !aligned4(new_len)) || (len_out && !aligned4(len_out)))
+    return H3ATTN_ERR_MISALIGNED;
+  if (k_stride % 8 != 0 || v_stride % 8 != 0 || (q && q_stride % 8 != 0)) return H3ATTN_ERR_MISALIGNED;
+  // spans of the inputs, and of the outputs, none of which may meet another
+  const Span sq{q, ((tokens - 1) * q_stride + static_cast<int64_t>(Hq) * D) * 2};
+  const Span sk{k, ((tokens - 1) * k_stride + static_cast<int64_t>(Hkv) * D) * 2};
+  const Span sv{v, ((tokens - 1) * v_stride + static_cast<int64_t>(Hkv) * D) * 2};
+  const Span so{q_out, tokens * Hq * D * 2}, kp = cache.k_span(), vp = cache.v_span(), kss = cache.ks_span(), vss = cache.vs_span();
+  const Span sl{len_out, 4LL * B}, kl = cache.len_span(), nl{new_len, 4LL * B}, sp{pos, 4 * tokens};
+  const Span pt = cache.table_span();
+  const int64_t tb = 2LL * rotary_dim * table_rows;
+  const Span sc{cos, tb}, ss{sin, tb}, swq{wq, 4LL * D}, swk{wk, 4LL * D}, none{nullptr, 0};
+  const bool in_place = q_out == q && q_stride == static_cast<int64_t>(Hq) * D;
+  const Span of_o[] = {in_place ? none : sq, sk, sv, kp, vp, kss, vss, sl, kl, nl, sp, pt, sc, ss, swq, swk};
+  const Span of_k[] = {vp, kss, vss, sq, sk, sv, sl, kl, nl, sp, pt, sc, ss, swq, swk};  // each array's are those behind it
+  const Span of_l[] = {kl, nl, sp, pt, sq, sk, sv, sc, ss, swq, swk};
+  if (overlaps_any(so, of_o, 16) || overlaps_any(kp, of_k, 15) || overlaps_any(vp, of_k + 1, 14) ||
+      overlaps_any(kss, of_k + 2, 13) || overlaps_any(vss, of_k + 3, 12) || overlaps_any(sl, of_l, 11))
+    return H3ATTN_ERR_INVALID_ARG;
+  st = check_device();
+  if (st != H3ATTN_OK) return st;
+  h3::AppendArgs a;
+  a.q = static_cast<const uint16_t*>(q);
+  a.k = static_cast<const uint16_t*>(k);
+  a.v = static_cast<const uint16_t*>(v);
+  a.q_out = static_cast<uint16_t*>(q_out);
+  a.k_pages = static_cast<uint16_t*>(const_cast<void*>(cache.k));
+  a.v_pages = static_cast<uint16_t*>(const_cast<void*>(cache.v));
+  a.k_scales = static_cast<uint8_t*>(const_cast<void*>(cache.k_scales));
+  a.v_scales = static_cast<uint8_t*>(const_cast<void*>(cache.v_scales));
+  a.page_table = cache.page_table;
+  a.kv_len = cache.kv_len;
+  a.wq = wq;
+  a.wk = wk;
+  a.cos = cos;
+  a.sin = sin;
+  a.pos = pos;
+  a.new_len = new_len;
+  a.len_out = len_out;
+  a.q_stride = q_stride;
+  a.k_stride = k_stride;
+  a.v_stride = v_stride;
+  a.tokens = static_cast<uint32_t>(tokens);
+  a.div_s = h3::make_fastdiv(static_cast<uint32_t>(S > 0 ? S : 1));
+  a.div_page = h3::make_fastdiv(static_cast<uint32_t>(cache.page_size));
+  a.B = B;
+  a.S = S;
+  a.Hq = Hq;
+  a.Hkv = Hkv;
+  a.D = D;
+  a.page_size = cache.page_size;
+  a.max_pages = cache.max_pages;
+  a.num_pages = cache.num_pages;
+  a.table_rows = table_rows;
+  a.rotary_dim = rotary_dim;
+  a.interleaved = interleaved ? 1 : 0;
+  a.eps = eps;
+  a.status = h3::status_word_ptr();
+  if (!a.status) return H3ATTN_ERR_LAUNCH;
+  return h3::launch_append(a, static_cast<cudaStream_t>(stream)) == cudaSuccess ? H3ATTN_OK : H3ATTN_ERR_LAUNCH;
+}
+
+cudaError_t decode_bytes(const h3::DecodeArgs& a, size_t* bytes) {
+  return a.k_scales ? h3::decode_q4_workspace(a, bytes) : h3::decode_workspace(a, bytes);
+}
+size_t up(size_t bytes) { return (bytes + 127) / 128 * 128; }
+
+// A workspace: the ranges' partials, and for the tokens' weights each head's
+// maximum and sum and the scores.
+struct DecodeSpace {
+  size_t partials, stats, bytes;  // of the first two, and of all
+  int64_t score_stride;
+};
+h3attn_status_t decode_space(const Cache& c, int Hq, bool weights, DecodeSpace* space) {
+  *space = {};
+  h3attn_status_t st = check_cache(c);
+  if (st != H3ATTN_OK) return st;
+  st = check_decode_heads(c, Hq);
+  if (st != H3ATTN_OK) return st;
+  if (c.B == 0) return H3ATTN_OK;
+  st = check_device();
+  if (st != H3ATTN_OK) return st;
+  h3::DecodeArgs a;
+  decode_fields(&a, c, Hq);
+  static const uint8_t kThere = 0;
+  if (c.q4) a.k_scales = &kThere;  // asked for by geometry alone: its pointers may be null
+  if (decode_bytes(a, &space->partials) != cudaSuccess) return H3ATTN_ERR_LAUNCH;
+  space->bytes = space->partials;
+  if (weights) {
+    const size_t rows = static_cast<size_t>(c.B) * Hq;
+    space->score_stride = (c.capacity() + 31) / 32 * 32;
+    space->stats = up(rows * sizeof(float2));
+    // at most 2^16 * 2^16 * 2^31 * 4 bytes: refused where they are not an address
+    if (static_cast<double>(rows) * static_cast<double>(space->score_stride) > 0x1p58) return H3ATTN_ERR_INVALID_ARG;
+    space->bytes = up(space->partials) + space->stats + rows * static_cast<size_t>(space->score_stride) * sizeof(float);
+  }
+  return H3ATTN_OK;
+}
+h3attn_status_t decode_size(const Cache& c, int Hq, bool weights, size_t* bytes) {
+  if (!bytes) return H3ATTN_ERR_INVALID_ARG;
+  DecodeSpace space;
+  const h3attn_status_t st = decode_space(c, Hq, weights, &space);
+  *bytes = st == H3ATTN_OK ? space.bytes : 0;
+  return st;
+}
+
+h3attn_status_t decode(const void* q, void* o, const Cache& cache, int Hq, float scale, bool weighted, float* weights,
+                       void* workspace, size_t workspace_bytes, h3attn_stream_t stream) {
+  h3attn_status_t st = check_cache(cache);
+  if (st != H3ATTN_OK) return st;
+  st = check_decode_heads(cache, Hq);
+  if (st != H3ATTN_OK) return st;
+  const float scale_log2 = scale * 1.4426950408889634f;
+  if (!(scale > 0.0f) || !isfinite(scale_log2)) return H3ATTN_ERR_INVALID_ARG;
+  if (cache.B == 0) return H3ATTN_OK;
+  if (!q || !o || (weighted && (!weights || !workspace))) return H3ATTN_ERR_INVALID_ARG;
+  st = check_cache_pointers(cache);
+  if (st != H3ATTN_OK) return st;
+  if (!aligned16(q) || !aligned16(o) || !aligned16(workspace) || !aligned4(weights)) return H3ATTN_ERR_MISALIGNED;
+  const int64_t nq = static_cast<int64_t>(cache.B) * Hq * cache.D * 2;
+  const Span so{o, nq}, sw{weights, weighted ? 4 * cache.B * cache.capacity() : 0};
+  const Span inputs[] = {{q, nq},           cache.k_span(),   cache.v_span(), cache.ks_span(),
+                         cache.vs_span(),   cache.len_span(), cache.table_span(), so, sw};
+  if (overlaps_any(so, inputs, 7) || overlaps_any(sw, inputs, 8)) return H3ATTN_ERR_INVALID_ARG;
+  st = check_device();
+  if (st != H3ATTN_OK) return st;
+  h3::DecodeArgs a;
+  decode_fields(&a, cache, Hq);
+  if (workspace) {
+    DecodeSpace space;
+    st = decode_space(cache, Hq, weighted, &space);
+    if (st != H3ATTN_OK) return st;
+    if (workspace_bytes < space.bytes || overlaps_any({workspace, static_cast<int64_t>(space.bytes)}, inputs, 9))
+      return H3ATTN_ERR_INVALID_ARG;
+    uint8_t* const at = static_cast<uint8_t*>(workspace);
+    if (space.partials > 0) a.ws = reinterpret_cast<float*>(at);
+    if (weighted) {
+      a.stats = reinterpret_cast<float2*>(at + up(space.partials));
+      a.scores = reinterpret_cast<float*>(at + up(space.partials) + space.stats);
+      a.score_stride = space.score_stride;
+    }
+  }
+  a.q = static_cast<const uint16_t*>(q);
+  a.o = static_cast<uint16_t*>(o);
+  a.scale_log2 = scale_log2;
+  a.status = h3::status_word_ptr();
+  if (!a.status) return H3ATTN_ERR_LAUNCH;
+  const cudaStream_t s = static_cast<cudaStream_t>(stream);
+  cudaError_t e = cache.q4 ? h3::launch_decode_q4(a, s) : h3::launch_decode(a, s);
+  if (e == cudaSuccess && weighted) e = h3::launch_add_weights(a, weights, s);
+  return e == cudaSuccess ? H3ATTN_OK : H3ATTN_ERR_LAUNCH;
+}
+
+h3attn_status_t read(const Cache& cache, void* k, void* v, const int32_t* first, int S, h3attn_stream_t stream) {
+  h3attn_status_t st = check_cache(cache);
+  if (st != H3ATTN_OK) return st;
+  if (S < 0) return H3ATTN_ERR_INVALID_ARG;
+  const int64_t tokens = static_cast<int64_t>(cache.B) * S;
+  if (tokens == 0) return H3ATTN_OK;
+  if (tokens > INT32_MAX || tokens * cache.Hkv > INT32_MAX) return H3ATTN_ERR_INVALID_ARG;
+  if (!k && !v) return H3ATTN_ERR_INVALID_ARG;
+  st = check_cache_pointers(cache);
+  if (st != H3ATTN_OK) return st;
+  if (!aligned16(k) || !aligned16(v) || !aligned4(first)) return H3ATTN_ERR_MISALIGNED;
+  const int64_t bytes = tokens * cache.Hkv * cache.D * 2;
+  const Span sk{k, bytes}, sv{v, bytes};
+  const Span of_k[] = {sv, cache.k_span(), cache.v_span(), cache.ks_span(), cache.vs_span(), cache.table_span(), cache.len_span(),
+                       {first, 4LL * cache.B}};
+  if (overlaps_any(sk, of_k, 8) || overlaps_any(sv, of_k + 1, 7)) return H3ATTN_ERR_INVALID_ARG;
+  st = check_device();
+  if (st != H3ATTN_OK) return st;
+  h3::ReadArgs a = {};
+  a.k_pages = cache.k;
+  a.v_pages = cache.v;
+  a.k_scales = static_cast<const uint8_t*>(cache.k_scales);
+  a.v_scales = static_cast<const uint8_t*>(cache.v_scales);
+  a.page_table = cache.page_table;
+  a.kv_len = cache.kv_len;
+  a.first = first;
+  a.k = static_cast<uint16_t*>(k);
+  a.v = static_cast<uint16_t*>(v);
+  a.div_page = h3::make_fastdiv(static_cast<uint32_t>(cache.page_size));
+  a.div_s = h3::make_fastdiv(static_cast<uint32_t>(S));
+  a.B = cache.B;
+  a.S = S;
+  a.Hkv = cache.Hkv;
+  a.D = cache.D;
+  a.page_size = cache.page_size;
+  a.max_pages = cache.max_pages;
+  a.num_pages = cache.num_pages;
+  a.status = h3::status_word_ptr();
+  if (!a.status) return H3ATTN_ERR_LAUNCH;
+  return h3::launch_read(a, static_cast<cudaStream_t>(stream)) == cudaSuccess ? H3ATTN_OK : H3ATTN_ERR_LAUNCH;
+}
+
+h3attn_status_t evict_size(int B, int64_t capacity, int keep, int recent, size_t* bytes) {
+  if (keep < 1 || recent < 0 || recent > keep) return H3ATTN_ERR_INVALID_ARG;
+  *bytes = static_cast<size_t>(B) * h3::evict_ints(h3::evict_most(capacity, keep, recent)) * sizeof(int);
+  return H3ATTN_OK;
+}
+
+h3attn_status_t evict(const Cache& cache, float* weights, int keep, int recent, int32_t* len_out, void* workspace,
+                      size_t workspace_bytes, h3attn_stream_t stream) {
+  h3attn_status_t st = check_cache(cache);
+  if (st != H3ATTN_OK) return st;
+  size_t need = 0;
+  st = evict_size(cache.B, cache.capacity(), keep, recent, &need);
+  if (st != H3ATTN_OK) return st;
+  if (cache.B == 0) return H3ATTN_OK;
+  if (!weights || !len_out || !workspace || workspace_bytes < need) return H3ATTN_ERR_INVALID_ARG;
+  st = check_cache_pointers(cache);
+  if (st != H3ATTN_OK) return st;
+  if (!aligned4(weights) || !aligned4(len_out) || !aligned16(workspace)) return H3ATTN_ERR_MISALIGNED;
+  const Span spans[] = {cache.k_span(), cache.v_span(), cache.ks_span(), cache.vs_span(), {weights, 4 * cache.B * cache.capacity()},
+                        {len_out, 4LL * cache.B}, {workspace, static_cast<int64_t>(need)}, cache.table_span(), cache.len_span()};
+  for (int i = 0; i < 7; ++i)
+    if (overlaps_any(spans[i], spans + i + 1, 8 - i)) return H3ATTN_ERR_INVALID_ARG;
+  st = check_device();
+  if (st != H3ATTN_OK) return st;
+  h3::EvictArgs a = {};
+  const void* rows[4] = {cache.k, cache.v, cache.k_scales, cache.v_scales};
+  for (int i = 0; i < 4; ++i) a.row[i] = static_cast<uint8_t*>(const_cast<void*>(rows[i]));
+  a.row_bytes[0] = static_cast<int>(cache.row_bytes());
+  a.row_bytes[1] = static_cast<int>(cache.scale_bytes());
+  a.page_table = cache.page_table;
+  a.kv_len = cache.kv_len;
+  a.weights = weights;
+  a.len_out = len_out;
+  a.ws = static_cast<int*>(workspace);
+  a.div_page = h3::make_fastdiv(static_cast<uint32_t>(cache.page_size));
+  a.capacity = cache.capacity();
+  a.B = cache.B;
+  a.page_size = cache.page_size;
+  a.max_pages = cache.max_pages;
+  a.num_pages = cache.num_pages;
+  a.keep = keep;
+  a.recent = recent;
+  a.most = h3::evict_most(a.capacity, keep, recent);
+  a.status = h3::status_word_ptr();
+  if (!a.status) return H3ATTN_ERR_LAUNCH;
+  return h3::launch_evict(a, static_cast<cudaStream_t>(stream)) == cudaSuccess ? H3ATTN_OK : H3ATTN_ERR_LAUNCH;
 }
 
 }  // namespace
@@ -184,156 +493,77 @@ h3attn_status_t h3attn_rope_table(float* cos, float* sin, const int32_t* pos, in
 }
 
 h3attn_status_t h3attn_qk_norm_rope_append(const void* q, const void* k, const void* v, void* q_out,
-                                           const h3attn_paged_kv_t* cache, const float* wq, const float* wk,
-                                           const float* cos, const float* sin, const int32_t* pos,
-                                           const int32_t* new_len, int32_t* len_out, int S, int Hq, int64_t q_stride,
-                                           int64_t k_stride, int64_t v_stride, int table_rows, int rotary_dim,
-                                           int interleaved, float eps, h3attn_stream_t stream) {
-  h3attn_status_t st = check_cache(cache);
-  if (st != H3ATTN_OK) return st;
-  const int B = cache->B, Hkv = cache->Hkv, D = cache->D;
-  if (S < 0 || Hq < 0 || Hq > 65535) return H3ATTN_ERR_INVALID_ARG;
-  if (rotary_dim < 0 || rotary_dim > D || rotary_dim % 2 != 0 || table_rows < 0) return H3ATTN_ERR_INVALID_ARG;
-  if (!(eps >= 0.0f) || !isfinite(eps)) return H3ATTN_ERR_INVALID_ARG;
-  const int64_t tokens = static_cast<int64_t>(B) * S;
-  if (tokens == 0 && (!len_out || B == 0)) return H3ATTN_OK;  // before the pointers: empty tensors have none
-  if (tokens == 0) {
-    // no token, but the lengths are asked for: they stay, in len_out
-    q = k = v = q_out = nullptr;
-    wq = wk = cos = sin = nullptr;
-    pos = nullptr;
-    Hq = rotary_dim = 0;
-    q_stride = k_stride = v_stride = static_cast<int64_t>(Hkv) * D;
-  }
-  if ((q == nullptr) != (Hq == 0) || (q_out == nullptr) != (q == nullptr)) return H3ATTN_ERR_INVALID_ARG;
-  if (tokens > INT32_MAX || tokens * (Hq + 2LL * Hkv) > INT32_MAX) return H3ATTN_ERR_INVALID_ARG;
-  if ((tokens > 0 && (!k || !v)) || (wq && !q)) return H3ATTN_ERR_INVALID_ARG;
-  if (rotary_dim > 0 && (!cos || !sin)) return H3ATTN_ERR_INVALID_ARG;
-  if (k_stride < static_cast<int64_t>(Hkv) * D || v_stride < static_cast<int64_t>(Hkv) * D ||
-      (q && q_stride < static_cast<int64_t>(Hq) * D))
-    return H3ATTN_ERR_INVALID_ARG;
-  const int64_t most = INT64_MAX / 4 / (tokens > 0 ? tokens : 1);
-  if (k_stride > most || v_stride > most || (q && q_stride > most)) return H3ATTN_ERR_INVALID_ARG;
-  st = check_cache_pointers(cache);
-  if (st != H3ATTN_OK) return st;
-  if (!aligned16(k) || !aligned16(v) || (q && (!aligned16(q) || !aligned16(q_out))) || (wq && !aligned16(wq)) ||
-      (wk && !aligned16(wk)) || (cos && !aligned16(cos)) || (sin && !aligned16(sin)) || (pos && !aligned4(pos)) ||
-      (new_len && !aligned4(new_len)) || (len_out && !aligned4(len_out)))
-    return H3ATTN_ERR_MISALIGNED;
-  if (k_stride % 8 != 0 || v_stride % 8 != 0 || (q && q_stride % 8 != 0)) return H3ATTN_ERR_MISALIGNED;
-  // spans of the inputs, and of the outputs, none of which may meet another
-  const int64_t np = page_bytes(cache);
-  const Span sq{q, ((tokens - 1) * q_stride + static_cast<int64_t>(Hq) * D) * 2};
-  const Span sk{k, ((tokens - 1) * k_stride + static_cast<int64_t>(Hkv) * D) * 2};
-  const Span sv{v, ((tokens - 1) * v_stride + static_cast<int64_t>(Hkv) * D) * 2};
-  const Span so{q_out, tokens * Hq * D * 2}, kp{cache->k_pages, np}, vp{cache->v_pages, np};
-  const Span sl{len_out, 4LL * B}, kl{cache->kv_len, 4LL * B}, nl{new_len, 4LL * B}, sp{pos, 4 * tokens};
-  const Span pt{cache->page_table, 4LL * B * cache->max_pages};
-  const int64_t tb = 2LL * rotary_dim * table_rows;
-  const Span sc{cos, tb}, ss{sin, tb}, swq{wq, 4LL * D}, swk{wk, 4LL * D}, none{nullptr, 0};
-  const bool in_place = q_out == q && q_stride == static_cast<int64_t>(Hq) * D;
-  const Span of_o[] = {in_place ? none : sq, sk, sv, kp, vp, sl, kl, nl, sp, pt, sc, ss, swq, swk};
-  const Span of_k[] = {vp, sq, sk, sv, sl, kl, nl, sp, pt, sc, ss, swq, swk};
-  const Span of_l[] = {kl, nl, sp, pt, sq, sk, sv, sc, ss, swq, swk};
-  if (overlaps_any(so, of_o, 14) || overlaps_any(kp, of_k, 13) || overlaps_any(vp, of_k + 1, 12) ||
-      overlaps_any(sl, of_l, 11))
-    return H3ATTN_ERR_INVALID_ARG;
-  st = check_device();
-  if (st != H3ATTN_OK) return st;
-  h3::AppendArgs a;
-  a.q = static_cast<const uint16_t*>(q);
-  a.k = static_cast<const uint16_t*>(k);
-  a.v = static_cast<const uint16_t*>(v);
-  a.q_out = static_cast<uint16_t*>(q_out);
-  a.k_pages = static_cast<uint16_t*>(cache->k_pages);
-  a.v_pages = static_cast<uint16_t*>(cache->v_pages);
-  a.page_table = cache->page_table;
-  a.kv_len = cache->kv_len;
-  a.wq = wq;
-  a.wk = wk;
-  a.cos = cos;
-  a.sin = sin;
-  a.pos = pos;
-  a.new_len = new_len;
-  a.len_out = len_out;
-  a.q_stride = q_stride;
-  a.k_stride = k_stride;
-  a.v_stride = v_stride;
-  a.tokens = static_cast<uint32_t>(tokens);
-  a.div_s = h3::make_fastdiv(static_cast<uint32_t>(S > 0 ? S : 1));
-  a.div_page = h3::make_fastdiv(static_cast<uint32_t>(cache->page_size));
-  a.B = B;
-  a.S = S;
-  a.Hq = Hq;
-  a.Hkv = Hkv;
-  a.D = D;
-  a.page_size = cache->page_size;
-  a.max_pages = cache->max_pages;
-  a.num_pages = cache->num_pages;
-  a.table_rows = table_rows;
-  a.rotary_dim = rotary_dim;
-  a.interleaved = interleaved ? 1 : 0;
-  a.eps = eps;
-  a.status = h3::status_word_ptr();
-  if (!a.status) return H3ATTN_ERR_LAUNCH;
-  return h3::launch_append(a, static_cast<cudaStream_t>(stream)) == cudaSuccess ? H3ATTN_OK : H3ATTN_ERR_LAUNCH;
+                           const h3attn_paged_kv_t* cache, const float* wq, const float* wk,
+                           const float* cos, const float* sin, const int32_t* pos,
+                           const int32_t* new_len, int32_t* len_out, int S, int Hq, int64_t q_stride,
+                           int64_t k_stride, int64_t v_stride, int table_rows, int rotary_dim,
+                           int interleaved, float eps, h3attn_stream_t stream) {
+  return append_to(q, k, v, q_out, of(cache), wq, wk, cos, sin, pos, new_len, len_out, S, Hq, q_stride, k_stride, v_stride,
+                   table_rows, rotary_dim, interleaved, eps, stream);
+}
+h3attn_status_t h3attn_qk_norm_rope_append_q4(const void* q, const void* k, const void* v, void* q_out,
+                           const h3attn_paged_kv4_t* cache, const float* wq, const float* wk,
+                           const float* cos, const float* sin, const int32_t* pos,
+                           const int32_t* new_len, int32_t* len_out, int S, int Hq, int64_t q_stride,
+                           int64_t k_stride, int64_t v_stride, int table_rows, int rotary_dim,
+                           int interleaved, float eps, h3attn_stream_t stream) {
+  return append_to(q, k, v, q_out, of(cache), wq, wk, cos, sin, pos, new_len, len_out, S, Hq, q_stride, k_stride, v_stride,
+                   table_rows, rotary_dim, interleaved, eps, stream);
+}
+
+h3attn_status_t h3attn_paged_read(const h3attn_paged_kv_t* cache, void* k, void* v, const int32_t* first, int S,
+                                  h3attn_stream_t stream) {
+  return read(of(cache), k, v, first, S, stream);
+}
+h3attn_status_t h3attn_paged_read_q4(const h3attn_paged_kv4_t* cache, void* k, void* v, const int32_t* first, int S,
+                                     h3attn_stream_t stream) {
+  return read(of(cache), k, v, first, S, stream);
 }
 
 h3attn_status_t h3attn_paged_decode_workspace_size(const h3attn_paged_kv_t* cache, int Hq, size_t* bytes) {
-  if (!bytes) return H3ATTN_ERR_INVALID_ARG;
-  *bytes = 0;
-  h3attn_status_t st = check_cache(cache);
-  if (st != H3ATTN_OK) return st;
-  st = check_decode_heads(cache, Hq);
-  if (st != H3ATTN_OK) return st;
-  if (cache->B == 0) return H3ATTN_OK;
-  st = check_device();
-  if (st != H3ATTN_OK) return st;
-  h3::DecodeArgs a;
-  decode_fields(&a, cache, Hq);
-  return h3::decode_workspace(a, bytes) == cudaSuccess ? H3ATTN_OK : H3ATTN_ERR_LAUNCH;
+  return decode_size(of(cache), Hq, false, bytes);
 }
-
 h3attn_status_t h3attn_paged_decode(const void* q, void* o, const h3attn_paged_kv_t* cache, int Hq, float scale,
                                     void* workspace, size_t workspace_bytes, h3attn_stream_t stream) {
-  h3attn_status_t st = check_cache(cache);
-  if (st != H3ATTN_OK) return st;
-  st = check_decode_heads(cache, Hq);
-  if (st != H3ATTN_OK) return st;
-  const float scale_log2 = scale * 1.4426950408889634f;
-  if (!(scale > 0.0f) || !isfinite(scale_log2)) return H3ATTN_ERR_INVALID_ARG;
-  if (cache->B == 0) return H3ATTN_OK;
-  if (!q || !o) return H3ATTN_ERR_INVALID_ARG;
-  st = check_cache_pointers(cache);
-  if (st != H3ATTN_OK) return st;
-  if (!aligned16(q) || !aligned16(o) || (workspace && !aligned16(workspace))) return H3ATTN_ERR_MISALIGNED;
-  const int64_t nq = static_cast<int64_t>(cache->B) * Hq * cache->D * 2, np = page_bytes(cache);
-  const Span so{o, nq};
-  const Span inputs[] = {{q, nq},
-                         {cache->k_pages, np},
-                         {cache->v_pages, np},
-                         {cache->kv_len, 4LL * cache->B},
-                         {cache->page_table, 4LL * cache->B * cache->max_pages},
-                         {o, nq}};
-  if (overlaps_any(so, inputs, 5)) return H3ATTN_ERR_INVALID_ARG;
-  st = check_device();
-  if (st != H3ATTN_OK) return st;
-  h3::DecodeArgs a;
-  decode_fields(&a, cache, Hq);
-  a.ws = nullptr;
-  if (workspace) {
-    size_t need = 0;
-    if (h3::decode_workspace(a, &need) != cudaSuccess) return H3ATTN_ERR_LAUNCH;
-    if (workspace_bytes < need || overlaps_any({workspace, static_cast<int64_t>(need)}, inputs, 6))
-      return H3ATTN_ERR_INVALID_ARG;
-    if (need > 0) a.ws = static_cast<float*>(workspace);
-  }
-  a.q = static_cast<const uint16_t*>(q);
-  a.o = static_cast<uint16_t*>(o);
-  a.scale_log2 = scale_log2;
-  a.status = h3::status_word_ptr();
-  if (!a.status) return H3ATTN_ERR_LAUNCH;
-  return h3::launch_decode(a, static_cast<cudaStream_t>(stream)) == cudaSuccess ? H3ATTN_OK : H3ATTN_ERR_LAUNCH;
+  return decode(q, o, of(cache), Hq, scale, false, nullptr, workspace, workspace_bytes, stream);
+}
+h3attn_status_t h3attn_paged_decode_q4_workspace_size(const h3attn_paged_kv4_t* cache, int Hq, size_t* bytes) {
+  return decode_size(of(cache), Hq, false, bytes);
+}
+h3attn_status_t h3attn_paged_decode_q4(const void* q, void* o, const h3attn_paged_kv4_t* cache, int Hq, float scale,
+                                       void* workspace, size_t workspace_bytes, h3attn_stream_t stream) {
+  return decode(q, o, of(cache), Hq, scale, false, nullptr, workspace, workspace_bytes, stream);
+}
+h3attn_status_t h3attn_paged_decode_weights_workspace_size(const h3attn_paged_kv_t* cache, int Hq, size_t* bytes) {
+  return decode_size(of(cache), Hq, true, bytes);
+}
+h3attn_status_t h3attn_paged_decode_weights(const void* q, void* o, const h3attn_paged_kv_t* cache, int Hq,
+                                            float scale, float* weights, void* workspace, size_t workspace_bytes,
+                                            h3attn_stream_t stream) {
+  return decode(q, o, of(cache), Hq, scale, true, weights, workspace, workspace_bytes, stream);
+}
+h3attn_status_t h3attn_paged_decode_weights_q4_workspace_size(const h3attn_paged_kv4_t* cache, int Hq, size_t* bytes) {
+  return decode_size(of(cache), Hq, true, bytes);
+}
+h3attn_status_t h3attn_paged_decode_weights_q4(const void* q, void* o, const h3attn_paged_kv4_t* cache, int Hq,
+                                               float scale, float* weights, void* workspace, size_t workspace_bytes,
+                                               h3attn_stream_t stream) {
+  return decode(q, o, of(cache), Hq, scale, true, weights, workspace, workspace_bytes, stream);
+}
+
+h3attn_status_t h3attn_paged_evict_workspace_size(int B, int page_size, int max_pages, int keep, int recent, size_t* bytes) {
+  if (!bytes) return H3ATTN_ERR_INVALID_ARG;
+  *bytes = 0;
+  const h3attn_status_t st = check_geometry(B, 1, page_size, max_pages);
+  return st != H3ATTN_OK ? st : evict_size(B, static_cast<int64_t>(page_size) * max_pages, keep, recent, bytes);
+}
+h3attn_status_t h3attn_paged_evict(const h3attn_paged_kv_t* cache, float* weights, int keep, int recent,
+                                   int32_t* len_out, void* workspace, size_t workspace_bytes, h3attn_stream_t stream) {
+  return evict(of(cache), weights, keep, recent, len_out, workspace, workspace_bytes, stream);
+}
+h3attn_status_t h3attn_paged_evict_q4(const h3attn_paged_kv4_t* cache, float* weights, int keep, int recent,
+                                      int32_t* len_out, void* workspace, size_t workspace_bytes, h3attn_stream_t stream) {
+  return evict(of(cache), weights, keep, recent, len_out, workspace, workspace_bytes, stream);
 }
 
 }  // extern "C"

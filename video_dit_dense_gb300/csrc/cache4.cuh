@@ -1,0 +1,50 @@
+// The numbers of a cache in 4 bits: 16 neighbouring channels of a row share a
+// scale s, a byte whose bits moved up by 7 are a binary16, and each stands for
+// (code - 8) s.
+#pragma once
+
+#include <cuda_bf16.h>
+#include <cuda_fp16.h>
+#include <stdint.h>
+
+namespace h3 {
+namespace {
+
+constexpr uint32_t kScaleMax = 0xD7;  // 3840; bytes above it stand for NaN
+
+__device__ __forceinline__ float scale_value(uint32_t byte) {
+  return byte > kScaleMax ? __int_as_float(0x7FFFFFFF) : __half2float(__ushort_as_half(static_cast<unsigned short>(byte << 7)));
+}
+
+// The largest of 8 bf16 values without their signs, as bits (a NaN is larger than an infinity).
+__device__ __forceinline__ uint32_t abs_max8(const uint32_t* n) {
+  constexpr uint32_t kAbs = 0x7FFF7FFFu;
+  const uint32_t m = __vmaxu2(__vmaxu2(n[0] & kAbs, n[1] & kAbs), __vmaxu2(n[2] & kAbs, n[3] & kAbs));
+  return max(m & 0xFFFFu, m >> 16);
+}
+// The scale of a group whose largest value has these bits: max / 7 rounded to 5 exponent and 3 mantissa bits.
+__device__ __forceinline__ uint32_t scale_of(uint32_t top) {
+  if (top >= 0x7F80u) return 0xFFu;
+  const float t = fminf(__fdiv_rn(__uint_as_float(top << 16), 7.0f), 3840.0f);
+  if (t < 0x1p-14f) return static_cast<uint32_t>(__float2int_rn(t * 0x1p17f));
+  const uint32_t u = __float_as_uint(t);
+  return ((u + 0x7FFFFu + ((u >> 20) & 1u)) >> 20) - (112u << 3);
+}
+// The codes of 8 values.  |x| / s is a quotient of an 8-bit and a 4-bit significand, so it either lies half way between
+// two integers or is at least 2^-9 of itself away from there: taken 2^-13 too large, which is more than its float32 error,
+// halves are rounded away from zero and nothing else is.
+__device__ __forceinline__ uint32_t codes_of(const uint32_t* n, uint32_t scale) {
+  if (scale == 0u || scale == 0xFFu) return 0x88888888u;
+  const float inv = __fdiv_rn(1.0f + 0x1p-13f, scale_value(scale));
+  uint32_t codes = 0;
+#pragma unroll
+  for (int e = 0; e < 8; ++e) {
+    const float x = __uint_as_float(e & 1 ? n[e >> 1] & 0xFFFF0000u : n[e >> 1] << 16);
+    const int k = static_cast<int>(fminf(fmaf(fabsf(x), inv, 0.5f), 8.5f));
+    codes |= static_cast<uint32_t>(x < 0.0f ? 8 - k : min(8 + k, 15)) << (4 * e);
+  }
+  return codes;
+}
+
+}  // namespace
+}  // namespace h3

@@ -1,5 +1,5 @@
 // Launcher interface of the generation operators (rotary tables, append to
-// a paged cache, decode attention, residual add + RMSNorm) between the C-ABI
+// a paged cache, reading it, decode attention, eviction, residual add + RMSNorm) between the C-ABI
 // layer (api_generate.cu) and the kernels.  Arguments arriving here are
 // already validated.
 #pragma once
@@ -75,6 +75,8 @@ struct AppendArgs {
   uint16_t* v_pages;
   const int32_t* page_table;  // [B, max_pages]
   const int32_t* kv_len;      // [B] tokens in the cache before the call
+  uint8_t* k_scales;          // a cache in 4 bits: codes in k_pages and v_pages, and their scales; nullptr: bf16
+  uint8_t* v_scales;
   const float* wq;            // [D] or nullptr (no norm)
   const float* wk;
   const float* cos;           // [table_rows, rotary_dim / 2]
@@ -108,9 +110,62 @@ struct DecodeArgs {
   float scale_log2;  // scale * log2(e)
   float* ws;         // partials, or nullptr: each sequence is walked by one CTA
   int* status;
+  // a cache in 4 bits: codes in k_pages and v_pages, and their scales
+  const uint8_t* k_scales;
+  const uint8_t* v_scales;
+  // for the tokens' weights: scale * log2(e) * score of each query head and token, score_stride tokens a head, and for each
+  // query head what exponents were taken against and 1 / their sum; nullptr: not asked for
+  float* scores;
+  float2* stats;
+  int64_t score_stride;
 };
 // Workspace bytes of a call on the current device (0: the call does not split).
 cudaError_t decode_workspace(const DecodeArgs& a, size_t* bytes);
 cudaError_t launch_decode(const DecodeArgs& a, cudaStream_t stream);
+cudaError_t decode_q4_workspace(const DecodeArgs& a, size_t* bytes);
+cudaError_t launch_decode_q4(const DecodeArgs& a, cudaStream_t stream);
+// weights[b, j] += sum over the heads of 2^(score - stats.x) * stats.y
+cudaError_t launch_add_weights(const DecodeArgs& a, float* weights, cudaStream_t stream);
+
+// ---- cached tokens as contiguous rows ----
+struct ReadArgs {
+  const void* k_pages;        // bf16, or codes where k_scales is there
+  const void* v_pages;
+  const uint8_t* k_scales;    // nullptr: a cache in bf16
+  const uint8_t* v_scales;
+  const int32_t* page_table;
+  const int32_t* kv_len;
+  const int32_t* first;       // [B] or nullptr: from token 0 on
+  uint16_t* k;                // [B, S, Hkv, D] or nullptr
+  uint16_t* v;
+  FastDiv div_page, div_s;
+  int B, S, Hkv, D, page_size, max_pages, num_pages;
+  int* status;
+};
+cudaError_t launch_read(const ReadArgs& a, cudaStream_t stream);
+
+// ---- eviction from a paged cache ----
+struct EvictArgs {
+  uint8_t* row[4];       // K, V, and their scales (nullptr: a cache in bf16)
+  int row_bytes[2];      // of a token in K and V, and in the scales
+  const int32_t* page_table;
+  const int32_t* kv_len;
+  float* weights;        // [B, capacity]
+  int32_t* len_out;
+  int* ws;               // [B, 4 + 2 * most]: counts, rows that move, rows they move to
+  FastDiv div_page;
+  int64_t capacity;
+  int B, page_size, max_pages, num_pages, keep, recent, most;
+  int* status;
+};
+// Rows of one sequence that move into gaps, at most.
+inline int evict_most(int64_t capacity, int keep, int recent) {
+  const int64_t n = capacity - keep < keep - recent ? capacity - keep : keep - recent;
+  return n > 0 ? static_cast<int>(n) : 0;
+}
+// Ints of a sequence's part of the workspace.
+constexpr int kEvictHeader = 4;  // rows that move into gaps, and those of them from below keep
+inline size_t evict_ints(int most) { return kEvictHeader + 2 * static_cast<size_t>(most); }
+cudaError_t launch_evict(const EvictArgs& a, cudaStream_t stream);
 
 }  // namespace h3

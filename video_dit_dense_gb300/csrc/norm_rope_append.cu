@@ -8,7 +8,8 @@
 // correctly rounded; n = bf16((x * r) * w); y_a = fma(a, c, -(b s)),
 // y_b = fma(b, c, a s); so a cached K row is bit-identical to what the
 // contiguous call writes.  Interleaved pairs (2i, 2i + 1) take the same
-// operations on other pairs; without weights n = x.
+// operations on other pairs; without weights n = x.  For a cache in 4 bits the
+// K and V rows are rounded to bf16 as for the other, and then to codes and scales.
 //
 // Memory-bound: every row is read once and written once.  A row is one
 // (token, head) vector; D/16 lanes own a row and hold two 16-byte groups of it.
@@ -26,6 +27,7 @@
 
 #include <algorithm>
 
+#include "cache4.cuh"
 #include "generate.h"
 #include "ptx.cuh"
 
@@ -57,7 +59,8 @@ __device__ __forceinline__ uint32_t fdiv(uint32_t n, const FastDiv& f) {
 //     stored to local memory and 24 loaded.
 enum : int { kHalf = 0, kInterleaved = 1, kStraddling = 2 };
 
-template <int D, int LAYOUT>
+// Q4: a cache in 4 bits.
+template <int D, int LAYOUT, bool Q4>
 __global__ void __launch_bounds__(kThreads, 4) append_kernel(const __grid_constant__ AppendArgs a) {
   constexpr int LPR = D / 16, RPW = 32 / LPR, U = kUnroll;
   constexpr float kInvD = 1.0f / static_cast<float>(D);
@@ -167,6 +170,13 @@ __global__ void __launch_bounds__(kThreads, 4) append_kernel(const __grid_consta
   uint16_t* const q_dst = a.q_out + static_cast<int64_t>(token) * a.Hq * D;
   uint16_t* const k_dst = a.k_pages + (cache_row * a.Hkv - a.Hq) * D;
   uint16_t* const v_dst = a.v_pages + (cache_row * a.Hkv - a.Hq - a.Hkv) * D;
+  // in 4 bits: the lanes of the row that hold the neighbours of this one's groups, the two that share a scale
+  auto holder = [&](uint32_t group) {  // lane, and 16 where it is that lane's second group
+    if (LAYOUT == kInterleaved) return group < LPR ? group : (group - LPR) | 16u;
+    if (group < h8 || group >= LPR + h8) return group < h8 ? group : group - LPR;
+    return (group - h8) | 16u;
+  };
+  const uint32_t other0 = Q4 ? holder(g0 ^ 1u) : 0u, other1 = Q4 ? holder(g1 ^ 1u) : 0u;
 
   while (true) {
     // acc: sum of squares, channels in order, then the butterfly over the row's lanes
@@ -270,7 +280,25 @@ __global__ void __launch_bounds__(kThreads, 4) append_kernel(const __grid_consta
           for (int e = 0; e < 8; ++e) n[e] = 0u;
         }
       }
-      if (live && head < last && (is_q || cache_row >= 0)) {
+      if constexpr (Q4) {
+        if (first + (u + 1) * static_cast<int>(hw) > a.Hq) {  // not query rows alone; the same in all lanes
+          const uint32_t top0 = abs_max8(n), top1 = abs_max8(n + 4), mine = top0 | top1 << 16;
+          const uint32_t of0 = __shfl_sync(0xFFFFFFFFu, mine, lane - lr + (other0 & 15u));
+          const uint32_t of1 = __shfl_sync(0xFFFFFFFFu, mine, lane - lr + (other1 & 15u));
+          const uint32_t scale0 = scale_of(max(top0, other0 & 16u ? of0 >> 16 : of0 & 0xFFFFu));
+          const uint32_t scale1 = scale_of(max(top1, other1 & 16u ? of1 >> 16 : of1 & 0xFFFFu));
+          if (live && head >= a.Hq && head < last && cache_row >= 0) {
+            const int64_t row = cache_row * a.Hkv + head - a.Hq - (is_v ? a.Hkv : 0);
+            uint32_t* codes = reinterpret_cast<uint32_t*>(is_v ? a.v_pages : a.k_pages) + row * (D / 8);
+            uint8_t* scales = (is_v ? a.v_scales : a.k_scales) + row * (D / 16);
+            codes[g0] = codes_of(n, scale0);
+            codes[g1] = codes_of(n + 4, scale1);
+            if (!(g0 & 1u)) scales[g0 >> 1] = static_cast<uint8_t>(scale0);
+            if (!(g1 & 1u)) scales[g1 >> 1] = static_cast<uint8_t>(scale1);
+          }
+        }
+      }
+      if (live && head < last && (is_q || (!Q4 && cache_row >= 0))) {
         uint16_t* dst = (is_q ? q_dst : is_v ? v_dst : k_dst) + head * D;
         *reinterpret_cast<uint4*>(dst + g0 * 8) = make_uint4(n[0], n[1], n[2], n[3]);
         *reinterpret_cast<uint4*>(dst + g1 * 8) = make_uint4(n[4], n[5], n[6], n[7]);
@@ -282,7 +310,7 @@ __global__ void __launch_bounds__(kThreads, 4) append_kernel(const __grid_consta
   }
 }
 
-template <int D>
+template <int D, bool Q4>
 cudaError_t launch_d(AppendArgs a, cudaStream_t stream) {
   constexpr int RPW = 32 / (D / 16);
   int dev = 0, sms = 0;
@@ -317,18 +345,18 @@ cudaError_t launch_d(AppendArgs a, cudaStream_t stream) {
   a.items = static_cast<uint32_t>(warps * used);
   // a block without warps of its own, where there is no token: len_out is written all the same
   const dim3 grid(std::max((a.items + kThreads / 32 - 1) / (kThreads / 32), 1u));
-  if (a.interleaved) return launch_dependent(append_kernel<D, kInterleaved>, grid, kThreads, 0, stream, a);
-  if (a.rotary_dim % 16 == 0) return launch_dependent(append_kernel<D, kHalf>, grid, kThreads, 0, stream, a);
-  return launch_dependent(append_kernel<D, kStraddling>, grid, kThreads, 0, stream, a);
+  if (a.interleaved) return launch_dependent(append_kernel<D, kInterleaved, Q4>, grid, kThreads, 0, stream, a);
+  if (a.rotary_dim % 16 == 0) return launch_dependent(append_kernel<D, kHalf, Q4>, grid, kThreads, 0, stream, a);
+  return launch_dependent(append_kernel<D, kStraddling, Q4>, grid, kThreads, 0, stream, a);
 }
 
 }  // namespace
 
 cudaError_t launch_append(const AppendArgs& a, cudaStream_t stream) {
   switch (a.D) {
-    case 64: return launch_d<64>(a, stream);
-    case 128: return launch_d<128>(a, stream);
-    case 256: return launch_d<256>(a, stream);
+    case 64: return a.k_scales ? launch_d<64, true>(a, stream) : launch_d<64, false>(a, stream);
+    case 128: return a.k_scales ? launch_d<128, true>(a, stream) : launch_d<128, false>(a, stream);
+    case 256: return a.k_scales ? launch_d<256, true>(a, stream) : launch_d<256, false>(a, stream);
     default: return cudaErrorInvalidValue;
   }
 }

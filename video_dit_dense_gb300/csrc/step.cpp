@@ -19,6 +19,7 @@ namespace {
 
 PyObject* g_error = nullptr;     // H3AttnError(status, where)
 PyObject* g_paged_kv = nullptr;  // PagedKV
+PyObject* g_paged_kv4 = nullptr;  // PagedKV4
 PyObject *s_address, *s_device, *s_cuda_stream;
 
 struct Entry {
@@ -26,6 +27,14 @@ struct Entry {
   decltype(&h3attn_rope_table) rope_table;
   decltype(&h3attn_qk_norm_rope_append) append;
   decltype(&h3attn_paged_decode) decode;
+  decltype(&h3attn_qk_norm_rope_append_q4) append_q4;
+  decltype(&h3attn_paged_decode_q4) decode_q4;
+  decltype(&h3attn_paged_decode_weights) decode_weights;
+  decltype(&h3attn_paged_decode_weights_q4) decode_weights_q4;
+  decltype(&h3attn_paged_read) read;
+  decltype(&h3attn_paged_read_q4) read_q4;
+  decltype(&h3attn_paged_evict) evict;
+  decltype(&h3attn_paged_evict_q4) evict_q4;
 } g_entry;
 
 // An argument that is refused; status 0: a Python error is set already.
@@ -128,13 +137,46 @@ h3attn_stream_t stream_of(PyObject* o, int dev) {
   if (PyLong_Check(o)) return reinterpret_cast<h3attn_stream_t>(static_cast<intptr_t>(integer(o)));
   return reinterpret_cast<h3attn_stream_t>(static_cast<intptr_t>(attribute(o, s_cuda_stream)));
 }
-// The descriptor that a PagedKV keeps.
-const h3attn_paged_kv_t& cache_of(PyObject* o, int dev) {
-  const int is = PyObject_IsInstance(o, g_paged_kv);
+bool is_a(PyObject* o, PyObject* type) {
+  const int is = PyObject_IsInstance(o, type);
   if (is < 0) python_error();
-  if (!is) refuse("cache must be a PagedKV");
+  return is != 0;
+}
+// The descriptor that a PagedKV keeps, or a PagedKV4.
+const void* descriptor(PyObject* o, int dev) {
   if (attribute(o, s_device) != dev) refuse("the cache must be on the current device");
-  return *reinterpret_cast<const h3attn_paged_kv_t*>(static_cast<intptr_t>(attribute(o, s_address)));
+  return reinterpret_cast<const void*>(static_cast<intptr_t>(attribute(o, s_address)));
+}
+// One of the two, and the fields that both have.
+struct CacheOf {
+  const h3attn_paged_kv_t* kv = nullptr;
+  const h3attn_paged_kv4_t* kv4 = nullptr;
+  int B, Hkv, D;
+  int64_t capacity;
+  explicit CacheOf(const h3attn_paged_kv_t* c)
+      : kv(c), B(c->B), Hkv(c->Hkv), D(c->D), capacity(static_cast<int64_t>(c->max_pages) * c->page_size) {}
+  explicit CacheOf(const h3attn_paged_kv4_t* c)
+      : kv4(c), B(c->B), Hkv(c->Hkv), D(c->D), capacity(static_cast<int64_t>(c->max_pages) * c->page_size) {}
+};
+CacheOf kv_of(PyObject* o, int dev) {
+  if (!is_a(o, g_paged_kv)) refuse("cache must be a PagedKV");
+  return CacheOf(static_cast<const h3attn_paged_kv_t*>(descriptor(o, dev)));
+}
+CacheOf kv4_of(PyObject* o, int dev) {
+  if (!is_a(o, g_paged_kv4)) refuse("cache must be a PagedKV4");
+  return CacheOf(static_cast<const h3attn_paged_kv4_t*>(descriptor(o, dev)));
+}
+CacheOf any_of(PyObject* o, int dev) {
+  if (is_a(o, g_paged_kv)) return kv_of(o, dev);
+  if (!is_a(o, g_paged_kv4)) refuse("cache must be a PagedKV or a PagedKV4");
+  return kv4_of(o, dev);
+}
+// A workspace's bytes.
+size_t bytes_of(const at::Tensor* workspace, int dev) {
+  if (!workspace) return 0;
+  if (!workspace->is_cuda() || workspace->get_device() != dev || !workspace->is_contiguous())
+    refuse("workspace must be a contiguous CUDA tensor on the current device");
+  return workspace->nbytes();
 }
 
 void raise(int status, const char* where) {
@@ -240,15 +282,16 @@ PyObject* rope_table(PyObject*, PyObject* const* a, Py_ssize_t n) {
 }
 
 // q, k, v, q_out, cache, wq, wk, cos, sin, rotary_dim, eps, interleaved, pos, new_len, len_out, stream
-PyObject* append(PyObject*, PyObject* const* a, Py_ssize_t n) {
+template <bool Q4>
+PyObject* append_to(PyObject* const* a, Py_ssize_t n) {
   if (!count(n, 16)) return nullptr;
-  return guarded("h3attn_qk_norm_rope_append", a[3], [&] {
+  return guarded(Q4 ? "h3attn_qk_norm_rope_append_q4" : "h3attn_qk_norm_rope_append", a[3], [&] {
     const at::Tensor *q = maybe("q", a[0]), *q_out = maybe("q_out", a[3]), *wq = maybe("wq", a[5]), *wk = maybe("wk", a[6]),
                      *cos = maybe("cos", a[7]), *sin = maybe("sin", a[8]), *pos = maybe("pos", a[12]),
                      *new_len = maybe("new_len", a[13]), *len_out = maybe("len_out", a[14]);
     const at::Tensor &k = tensor("k", a[1]), &v = tensor("v", a[2]);
     const int dev = current_device("k", k);
-    const h3attn_paged_kv_t& cache = cache_of(a[4], dev);
+    const CacheOf cache = Q4 ? kv4_of(a[4], dev) : kv_of(a[4], dev);
     const int64_t B = cache.B, Hkv = cache.Hkv, D = cache.D;
     if (k.dim() != 4) refuse("k must be a [B, S, Hkv, D] bf16 CUDA tensor");
     const int S = int32("S", k.size(1));
@@ -280,20 +323,29 @@ PyObject* append(PyObject*, PyObject* const* a, Py_ssize_t n) {
     const int interleaved = truth(a[11]) ? 1 : 0;
     const h3attn_stream_t s = stream_of(a[15], dev);
     return without_gil([&] {
-      return g_entry.append(data<void>(q), data<void>(&k), data<void>(&v), const_cast<void*>(data<void>(q_out)), &cache, wqp, wkp,
-                            cp, sp, pp, np, const_cast<int32_t*>(lp), S, Hq, qs, ks, vs, rows, rotary_dim, interleaved, eps, s);
+      void* const qo = const_cast<void*>(data<void>(q_out));
+      int32_t* const lo = const_cast<int32_t*>(lp);
+      return Q4 ? g_entry.append_q4(data<void>(q), data<void>(&k), data<void>(&v), qo, cache.kv4, wqp, wkp, cp, sp, pp, np, lo, S, Hq,
+                                    qs, ks, vs, rows, rotary_dim, interleaved, eps, s)
+                : g_entry.append(data<void>(q), data<void>(&k), data<void>(&v), qo, cache.kv, wqp, wkp, cp, sp, pp, np, lo, S, Hq,
+                                 qs, ks, vs, rows, rotary_dim, interleaved, eps, s);
     });
   });
 }
+PyObject* append(PyObject*, PyObject* const* a, Py_ssize_t n) { return append_to<false>(a, n); }
+PyObject* append_q4(PyObject*, PyObject* const* a, Py_ssize_t n) { return append_to<true>(a, n); }
 
-// q, o, cache, scale or None, workspace, stream
-PyObject* decode(PyObject*, PyObject* const* a, Py_ssize_t n) {
-  if (!count(n, 6)) return nullptr;
-  return guarded("h3attn_paged_decode", a[1], [&] {
+// q, o, cache, scale or None, weights (where they are asked for), workspace, stream
+enum class Decode { kPlain, kQ4, kWeights };
+template <Decode KIND>
+PyObject* decode_of(const char* where, PyObject* const* a, Py_ssize_t n) {
+  constexpr bool W = KIND == Decode::kWeights;
+  if (!count(n, W ? 7 : 6)) return nullptr;
+  return guarded(where, a[1], [&] {
     const at::Tensor &q = tensor("q", a[0]), &o = tensor("o", a[1]);
-    const at::Tensor* workspace = maybe("workspace", a[4]);
+    const at::Tensor* workspace = maybe("workspace", a[W ? 5 : 4]);
     const int dev = current_device("q", q);
-    const h3attn_paged_kv_t& cache = cache_of(a[2], dev);
+    const CacheOf cache = W ? any_of(a[2], dev) : KIND == Decode::kQ4 ? kv4_of(a[2], dev) : kv_of(a[2], dev);
     const at::IntArrayRef shape = q.sizes();
     if (!(shape.size() == 3 || (shape.size() == 4 && shape[1] == 1)))
       refuse("q must be [B, 1, Hq, D] or [B, Hq, D]: one new token per sequence");
@@ -301,37 +353,107 @@ PyObject* decode(PyObject*, PyObject* const* a, Py_ssize_t n) {
     if (shape[0] != cache.B || shape.back() != cache.D) refuse("shape mismatch between q and the cache");
     check("q", q, at::kBFloat16, shape, dev);
     check("o", o, at::kBFloat16, shape, dev);
-    size_t bytes = 0;
-    if (workspace) {
-      if (!workspace->is_cuda() || workspace->get_device() != dev || !workspace->is_contiguous())
-        refuse("workspace must be a contiguous CUDA tensor on the current device");
-      bytes = workspace->nbytes();
+    float* weights = nullptr;
+    if (W) {
+      const at::Tensor& w = tensor("weights", a[4]);
+      check("weights", w, at::kFloat, {cache.B, cache.capacity}, dev);
+      weights = const_cast<float*>(data<float>(&w));
     }
+    const size_t bytes = bytes_of(workspace, dev);
     const float scale = a[3] == Py_None ? static_cast<float>(1.0 / std::sqrt(static_cast<double>(cache.D)))
                                         : static_cast<float>(number(a[3]));
-    const h3attn_stream_t s = stream_of(a[5], dev);
+    const h3attn_stream_t s = stream_of(a[W ? 6 : 5], dev);
     return without_gil([&] {
-      return g_entry.decode(data<void>(&q), const_cast<void*>(data<void>(&o)), &cache, Hq, scale,
-                            const_cast<void*>(data<void>(workspace)), bytes, s);
+      const void* const qp = data<void>(&q);
+      void *const op = const_cast<void*>(data<void>(&o)), *const wp = const_cast<void*>(data<void>(workspace));
+      if (W)
+        return cache.kv ? g_entry.decode_weights(qp, op, cache.kv, Hq, scale, weights, wp, bytes, s)
+                        : g_entry.decode_weights_q4(qp, op, cache.kv4, Hq, scale, weights, wp, bytes, s);
+      return cache.kv ? g_entry.decode(qp, op, cache.kv, Hq, scale, wp, bytes, s)
+                      : g_entry.decode_q4(qp, op, cache.kv4, Hq, scale, wp, bytes, s);
+    });
+  });
+}
+PyObject* decode(PyObject*, PyObject* const* a, Py_ssize_t n) { return decode_of<Decode::kPlain>("h3attn_paged_decode", a, n); }
+PyObject* decode_q4(PyObject*, PyObject* const* a, Py_ssize_t n) { return decode_of<Decode::kQ4>("h3attn_paged_decode_q4", a, n); }
+PyObject* decode_weights(PyObject*, PyObject* const* a, Py_ssize_t n) {
+  return decode_of<Decode::kWeights>("h3attn_paged_decode_weights", a, n);
+}
+
+// cache, k or None, v or None, first or None, stream
+PyObject* read(PyObject*, PyObject* const* a, Py_ssize_t n) {
+  if (!count(n, 5)) return nullptr;
+  return guarded("h3attn_paged_read", Py_None, [&] {
+    const at::Tensor *k = maybe("k", a[1]), *v = maybe("v", a[2]), *first = maybe("first", a[3]);
+    if (!k && !v) refuse("at least one of k and v must be given");
+    const at::Tensor& one = k ? *k : *v;
+    const int dev = current_device(k ? "k" : "v", one);
+    const CacheOf cache = any_of(a[0], dev);
+    if (one.dim() != 4) refuse("k and v must be [B, S, Hkv, D] bf16 CUDA tensors");
+    const int S = int32("S", one.size(1));
+    const int64_t shape[] = {cache.B, S, cache.Hkv, cache.D};
+    const void* kp = checked<void>("k", k, at::kBFloat16, {shape, 4}, dev);
+    const void* vp = checked<void>("v", v, at::kBFloat16, {shape, 4}, dev);
+    const int32_t* fp = checked<int32_t>("first", first, at::kInt, {cache.B}, dev);
+    const h3attn_stream_t s = stream_of(a[4], dev);
+    return without_gil([&] {
+      return cache.kv ? g_entry.read(cache.kv, const_cast<void*>(kp), const_cast<void*>(vp), fp, S, s)
+                      : g_entry.read_q4(cache.kv4, const_cast<void*>(kp), const_cast<void*>(vp), fp, S, s);
     });
   });
 }
 
-// H3AttnError, PagedKV, and the addresses of the four entry points of the loaded library
+// cache, weights, keep, recent, len_out, workspace or None, stream
+PyObject* evict(PyObject*, PyObject* const* a, Py_ssize_t n) {
+  if (!count(n, 7)) return nullptr;
+  return guarded("h3attn_paged_evict", a[4], [&] {
+    const at::Tensor &weights = tensor("weights", a[1]), &len_out = tensor("len_out", a[4]);
+    const at::Tensor* workspace = maybe("workspace", a[5]);
+    const int dev = current_device("weights", weights);
+    const CacheOf cache = any_of(a[0], dev);
+    check("weights", weights, at::kFloat, {cache.B, cache.capacity}, dev);
+    check("len_out", len_out, at::kInt, {cache.B}, dev);
+    const int keep = int32("keep", a[2]), recent = int32("recent", a[3]);
+    const size_t bytes = bytes_of(workspace, dev);
+    const h3attn_stream_t s = stream_of(a[6], dev);
+    return without_gil([&] {
+      float* const w = const_cast<float*>(data<float>(&weights));
+      int32_t* const lo = const_cast<int32_t*>(data<int32_t>(&len_out));
+      void* const wp = const_cast<void*>(data<void>(workspace));
+      return cache.kv ? g_entry.evict(cache.kv, w, keep, recent, lo, wp, bytes, s)
+                      : g_entry.evict_q4(cache.kv4, w, keep, recent, lo, wp, bytes, s);
+    });
+  });
+}
+
+// H3AttnError, PagedKV, PagedKV4, and the addresses of the loaded library's entry points in the order of Entry
 PyObject* bind(PyObject*, PyObject* args) {
-  PyObject *error, *paged_kv;
-  unsigned long long at[4];
-  if (!PyArg_ParseTuple(args, "OOKKKK", &error, &paged_kv, &at[0], &at[1], &at[2], &at[3])) return nullptr;
-  Py_INCREF(error);
-  Py_INCREF(paged_kv);
-  Py_XDECREF(g_error);
-  Py_XDECREF(g_paged_kv);
-  g_error = error;
-  g_paged_kv = paged_kv;
-  g_entry.add_rmsnorm = reinterpret_cast<decltype(g_entry.add_rmsnorm)>(at[0]);
-  g_entry.rope_table = reinterpret_cast<decltype(g_entry.rope_table)>(at[1]);
-  g_entry.append = reinterpret_cast<decltype(g_entry.append)>(at[2]);
-  g_entry.decode = reinterpret_cast<decltype(g_entry.decode)>(at[3]);
+  PyObject *error, *paged_kv, *paged_kv4;
+  unsigned long long at[12];
+  if (!PyArg_ParseTuple(args, "OOOKKKKKKKKKKKK", &error, &paged_kv, &paged_kv4, &at[0], &at[1], &at[2], &at[3], &at[4], &at[5], &at[6],
+                        &at[7], &at[8], &at[9], &at[10], &at[11]))
+    return nullptr;
+  PyObject** const kept[] = {&g_error, &g_paged_kv, &g_paged_kv4};
+  PyObject* const given[] = {error, paged_kv, paged_kv4};
+  for (int i = 0; i < 3; ++i) {
+    Py_INCREF(given[i]);
+    Py_XDECREF(*kept[i]);
+    *kept[i] = given[i];
+  }
+  int i = 0;
+  auto entry = [&](auto& f) { f = reinterpret_cast<std::decay_t<decltype(f)>>(at[i++]); };
+  entry(g_entry.add_rmsnorm);
+  entry(g_entry.rope_table);
+  entry(g_entry.append);
+  entry(g_entry.decode);
+  entry(g_entry.append_q4);
+  entry(g_entry.decode_q4);
+  entry(g_entry.decode_weights);
+  entry(g_entry.decode_weights_q4);
+  entry(g_entry.read);
+  entry(g_entry.read_q4);
+  entry(g_entry.evict);
+  entry(g_entry.evict_q4);
   Py_RETURN_NONE;
 }
 
@@ -340,7 +462,8 @@ PyMethodDef method(const char* name) {
   return {name, reinterpret_cast<PyCFunction>(reinterpret_cast<void (*)()>(F)), METH_FASTCALL, nullptr};
 }
 PyMethodDef g_methods[] = {method<add_rmsnorm>("add_rmsnorm"), method<rope_table>("rope_table"), method<append>("append"),
-                           method<decode>("decode"), {"bind", bind, METH_VARARGS, nullptr}, {nullptr, nullptr, 0, nullptr}};
+                           method<decode>("decode"), method<append_q4>("append_q4"), method<decode_q4>("decode_q4"),
+                           method<decode_weights>("decode_weights"), method<read>("read"), method<evict>("evict"), {"bind", bind, METH_VARARGS, nullptr}, {nullptr, nullptr, 0, nullptr}};
 PyModuleDef g_module = {PyModuleDef_HEAD_INIT, "_step", nullptr, -1, g_methods, nullptr, nullptr, nullptr, nullptr};
 
 }  // namespace
