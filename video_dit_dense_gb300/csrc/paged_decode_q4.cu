@@ -1,97 +1,647 @@
 // Attention of one new token per sequence over a paged cache in 4 bits.
 //
 //   o_h = sum_j softmax_j(scale q_h . k_j) v_j,   j < kv_len[b],
-// with k = (code - 8) s of 16 channels a scale.  One CTA takes a query head of a sequence, its warps every
-// kWarps-th token each, the lanes the channels of a row; running maximum and sum in
-// float32, the warps joined through shared memory.
+// k and v standing for (code - 8) s, 16 channels a scale.  The split of the
+// sequences over the SMs, the walk of a range and the join are those of the decode
+// attention over a bf16 cache (paged_decode.cu), and so are the two products: the
+// cache side is the 16-row operand of mma.sync m16n8k16, query heads the 8 columns.
+// What differs is how the cache side gets into registers.
+//
+// A token and key-value head is D + D / 8 bytes instead of 4 D, so at the memory's
+// rate an SM takes 41 channels a cycle: what bounds the kernel is instructions, and
+// codes must become operands in few of them.
+//   - 1024 + c is the binary16 with bits 0x6400 | c, so (c - 8) s is one fused
+//     multiply-add, (1024 + c) s' - 1032 s', of two channels at a time.  It is exact:
+//     s' = s / 128 is a binary16 of 4 bits (at least 2^-24, at most 30), 1032 s' = 129 s' 2^3
+//     takes 11.  The 128 is undone in the scores' scale and in the output's.
+//   - A nibble that lies 4 bits higher is 1024 + 16 c, giving 16 (c - 8) s' with 1152 s';
+//     the 16 is undone in the queries (/ 16) and in the output's channels.  So of the four nibbles
+//     of a 16-bit half two take a mask, two a shift by 8 and a mask.
+//   - Which channel is which row or column of a product is free: the sum over channels
+//     is in any order if the queries' are in the same, and the output's rows go where their
+//     channels are.  So a lane takes D / 4 neighbouring channels of a K row and D / 8 of a V row, in one
+//     load each, with one or few scales.
+// Both products are exact in their operands but for P, which is rounded to 11 bits
+// (binary16: half a step is 2^-12 of a weight, an eighth of the output's own rounding): P is taken
+// 2^7 times larger than its sum's reference so that weights down to 2^-31 of the largest are normal.
+// Queries are taken in binary16 after a scaling by a power of two for each row.
 #include "cache4.cuh"
 #include "decode_common.cuh"
+#include "ptx.cuh"
 
 namespace h3 {
 namespace {
 
-constexpr int kWarps = 8;
+constexpr float kLift = 7.0f;  // exponents of two by which P is raised: 2^(kSlack + kLift) is below binary16's largest
 
+template <int BYTES>
+__device__ __forceinline__ void cp_async(uint32_t dst, const void* src, bool valid) {
+  if constexpr (BYTES == 16)
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(valid ? 16 : 0) : "memory");
+  else
+    asm volatile("cp.async.ca.shared.global [%0], [%1], %3, %2;" ::"r"(dst), "l"(src), "r"(valid ? BYTES : 0), "n"(BYTES) : "memory");
+}
+template <int BYTES>
+struct Words {
+  uint32_t w[BYTES / 4];
+};
+template <int BYTES>
+__device__ __forceinline__ void lds(uint32_t (&w)[BYTES / 4], uint32_t addr) {
+  if constexpr (BYTES == 4) asm volatile("ld.shared.b32 %0, [%1];" : "=r"(w[0]) : "r"(addr) : "memory");
+  if constexpr (BYTES == 8) asm volatile("ld.shared.v2.b32 {%0, %1}, [%2];" : "=r"(w[0]), "=r"(w[1]) : "r"(addr) : "memory");
+  if constexpr (BYTES == 16)
+    asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];" : "=r"(w[0]), "=r"(w[1]), "=r"(w[2]), "=r"(w[3]) : "r"(addr) : "memory");
+}
+__device__ __forceinline__ uint32_t lds8(uint32_t addr) {
+  uint16_t v;
+  asm volatile("ld.shared.u8 %0, [%1];" : "=h"(v) : "r"(addr) : "memory");
+  return v;
+}
+__device__ __forceinline__ uint32_t lds16(uint32_t addr) {
+  uint16_t v;
+  asm volatile("ld.shared.u16 %0, [%1];" : "=h"(v) : "r"(addr) : "memory");
+  return v;
+}
+__device__ __forceinline__ uint32_t hmul2(uint32_t a, uint32_t b) {
+  uint32_t d;
+  asm("mul.rn.f16x2 %0, %1, %2;" : "=r"(d) : "r"(a), "r"(b));
+  return d;
+}
+__device__ __forceinline__ uint32_t hfma2(uint32_t a, uint32_t b, uint32_t c) {
+  uint32_t d;
+  asm("fma.rn.f16x2 %0, %1, %2, %3;" : "=r"(d) : "r"(a), "r"(b), "r"(c));
+  return d;
+}
+__device__ __forceinline__ uint32_t pack_f16(float lo, float hi) {
+  __half2 v = __floats2half2_rn(lo, hi);
+  return *reinterpret_cast<uint32_t*>(&v);
+}
+__device__ __forceinline__ void mma_f16(float (&c)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
+  asm volatile(
+      "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, "
+      "{%0, %1, %2, %3};"
+      : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
+      : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+}
+// Two scales, one in each half: s' = s / 128 and what it takes from 1024 + c and from 1024 + 16 c.
+struct Scale2 {
+  uint32_t m, c0, c1;
+};
+__device__ __forceinline__ Scale2 scale2(uint32_t shifted) {  // bytes moved up by 7
+  Scale2 s;
+  s.m = hmul2(shifted, 0x20002000u);     // 2^-7
+  s.c0 = hmul2(s.m, 0xE408E408u);        // -1032
+  s.c1 = hmul2(s.m, 0xE480E480u);        // -1152
+  return s;
+}
+// Nibbles 0 and 4 of x (counted in 4 bits), and nibbles 1 and 5 sixteen times larger.
+__device__ __forceinline__ uint32_t low2(uint32_t x, const Scale2& s) { return hfma2((x & 0x000F000Fu) | 0x64006400u, s.m, s.c0); }
+__device__ __forceinline__ uint32_t high2(uint32_t x, const Scale2& s) { return hfma2((x & 0x00F000F0u) | 0x64006400u, s.m, s.c1); }
+
+// NT: tiles of 8 query heads (1 or 2).
+template <int D, int NT>
+struct Q4Cfg {
+  static constexpr int kTile = 32;  // tokens a warp takes at a time, one a lane where pages are looked up
+  static constexpr int kWarps = D * NT <= 128 ? 16 : 8;
+  static constexpr int kStages = 2;
+  static constexpr int kCodes = kTile * D / 2, kScales = kTile * D / 16;  // bytes of K, and the same of V
+  static constexpr int kStage = 2 * (kCodes + kScales);
+  static constexpr int kRing = kWarps * kStages * kStage;
+  // joining the warps of a unit head: accumulators, max and sum of every second warp, 8 heads at a time
+  static constexpr int kJoin = kWarps / 2 * 8 * D * 4;
+  static constexpr int kStats = kWarps / 2 * 8 * 2 * 4;
+  static constexpr int kSmem = kRing + kJoin + kStats + 2 * kMaxSplitBatch * 4;
+  static constexpr int kHeads = NT * 8;
+  static_assert(kSmem <= 232448, "shared memory of one CTA");
+};
+
+// Where the 16-byte pieces of token tr's row lie in a stage: moved so that the lanes' loads of K rows (two tokens a
+// quarter-warp) and of V rows (tokens 0 2 5 7 or 1 3 4 6 of eight) use all banks.
 template <int D>
-__global__ void __launch_bounds__(kWarps * 32) decode_q4_kernel(const __grid_constant__ DecodeArgs a) {
-  constexpr int VEC = D / 32;
-  __shared__ float part_o[kWarps][D];
-  __shared__ float2 part_ml[kWarps];
+__device__ __forceinline__ uint32_t swizzle(int tr) {
+  if constexpr (D == 64) return 0;
+  if constexpr (D == 128) return (tr & 2);
+  return (tr & 1) * 5 ^ (tr & 2);
+}
+// The token of a product's row r among 8: neighbouring rows differ in parity, and rows 0 2 4 6 in their place modulo 4.
+__device__ __forceinline__ int token_of(int r) { return r ^ (r >> 2 & 1); }
+
+// W: the scores are kept for the tokens' weights.
+template <int D, int NT, bool W>
+__global__ void __launch_bounds__(Q4Cfg<D, NT>::kWarps * 32, 1) decode_q4_kernel(const __grid_constant__ Kernelargs k) {
+  using C = Q4Cfg<D, NT>;
+  constexpr int TILE = C::kTile, MT = TILE / 16, STAGES = C::kStages;
+  constexpr int CH = D / 32;          // 16-byte pieces of a row's codes
+  constexpr int KW = D / 32;          // words of a K row that a lane takes (8 channels each)
+  constexpr int VB = D / 16;          // bytes of a V row that a lane takes, and of a row's scales
+  constexpr int VW = VB / 4;
+  const DecodeArgs& a = k.a;
+  const DecodePlan& p = k.p;
+  extern __shared__ __align__(128) uint8_t smem[];
+  float* join = reinterpret_cast<float*>(smem + C::kRing);
+  float* stats = reinterpret_cast<float*>(smem + C::kRing + C::kJoin);
+  int* end = reinterpret_cast<int*>(smem + C::kRing + C::kJoin + C::kStats);
+  int* lens = end + kMaxSplitBatch;  // without a split: of the one sequence
+  // lengths and page table: brought back to L2 while the kernel before this one drains
+  if (threadIdx.x * 32 < static_cast<unsigned>(a.B)) prefetch_l2(a.kv_len + threadIdx.x * 32);
+  {
+    const int64_t line = (static_cast<int64_t>(blockIdx.x) * (C::kWarps * 32) + threadIdx.x) * 32;
+    if (line < static_cast<int64_t>(a.B) * a.max_pages) prefetch_l2(a.page_table + line);
+  }
   asm volatile("griddepcontrol.wait;" ::: "memory");
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const int b = blockIdx.x / a.Hq, h = blockIdx.x - b * a.Hq, kvh = h / (a.Hq / a.Hkv);
-  const int n = len_of(a, b);
-  float q[VEC], o[VEC] = {}, m = -FLT_MAX, l = 0.0f;
-#pragma unroll
-  for (int e = 0; e < VEC; ++e)
-    q[e] = __bfloat162float(reinterpret_cast<const __nv_bfloat16*>(a.q)[(static_cast<int64_t>(b) * a.Hq + h) * D + lane * VEC + e]);
-  auto row_values = [&](const uint16_t* pages, const uint8_t* scales, int64_t row, float (&x)[VEC]) {
-    const uint8_t* c = reinterpret_cast<const uint8_t*>(pages) + row * (D / 2) + lane * (VEC / 2);
-    const float s = scale_value(scales[row * (D / 16) + lane * VEC / 16]);
-#pragma unroll
-    for (int e = 0; e < VEC; ++e) x[e] = static_cast<float>((c[e / 2] >> (4 * (e & 1)) & 15) - 8) * s;
+  const int wh = warp % p.WH, wt = warp / p.WH;
+  const int r = blockIdx.x / p.groups;
+  const int unit = (blockIdx.x - r * p.groups) * p.WH + wh;
+  const int kvh = unit / p.q_tiles, qt = unit - kvh * p.q_tiles;
+  const int G = a.Hq / a.Hkv;
+  const int head0 = kvh * G + qt * 16;            // first query head of the unit
+  const int heads = min(G - qt * 16, C::kHeads);  // its query heads
+
+  // This CTA's tiles [t0, t1) of all sequences' tiles.  Without a split the range is sequence r.
+  int t0, t1, b0;
+  if (p.ranges > 0) {
+    const Ranges ranges = scan_tiles<C::kWarps * 32>(a, p, TILE, end, lens);
+    if (r >= ranges.count) return;
+    t0 = ranges.begin(r);
+    t1 = ranges.begin(r + 1);
+    if (t0 >= t1) return;
+    b0 = sequence_at(end, a.B, t0);
+  } else {
+    t0 = 0;
+    b0 = r;
+    if (threadIdx.x == 0) lens[0] = len_of(a, r);
+    __syncthreads();
+    t1 = (lens[0] + TILE - 1) / TILE;
+  }
+  auto seq_begin = [&](int b) { return p.ranges > 0 && b > 0 ? end[b - 1] : 0; };
+  auto seq_end = [&](int b) { return p.ranges > 0 ? end[b] : t1; };
+  // the sequence's tiles that this range holds: [first_tile, stop_tile)
+  const int start = p.ranges > 0 ? p.start : 0;
+  auto first_tile = [&](int b) { return max(t0 - seq_begin(b) - start, 0); };
+  auto stop_tile = [&](int b) { return min(t1, seq_end(b)) - seq_begin(b) - start; };
+  auto seq_len = [&](int b) { return lens[p.ranges > 0 ? b : 0]; };
+
+  // The tiles that this warp loads, in the order they are used, over sequence borders.
+  struct Walk {
+    int b, tile, stop, len;  // sequence, tile of the sequence, the range's end in it
   };
-  for (int j = warp; j < n; j += kWarps) {
-    const uint32_t p = fdiv(static_cast<uint32_t>(j), a.div_page);
-    const int page = a.page_table[static_cast<int64_t>(b) * a.max_pages + p];
-    float* score = a.scores ? a.scores + (static_cast<int64_t>(b) * a.Hq + h) * a.score_stride + j : nullptr;
-    if (page < 0 || page >= a.num_pages) {
-      atomicExch(a.status, static_cast<int>(H3ATTN_ERR_INVALID_ARG));  // not attended
-      if (score && lane == 0) *score = -INFINITY;
-      continue;
+  auto enter = [&](Walk& w) {  // to the first tile at or after the present one that is there
+    while (w.tile >= w.stop) {
+      if (p.ranges == 0 || seq_end(w.b) >= t1) {
+        w.b = -1;
+        return;
+      }
+      ++w.b;
+      w.stop = stop_tile(w.b);
+      w.tile = wt;
+      w.len = seq_len(w.b);
     }
-    const int64_t row = (static_cast<int64_t>(page) * a.page_size + (j - static_cast<int>(p) * a.page_size)) * a.Hkv + kvh;
-    float k[VEC], v[VEC], s = 0.0f;
-    row_values(a.k_pages, a.k_scales, row, k);
-    row_values(a.v_pages, a.v_scales, row, v);
+  };
+  Walk ld;
+  ld.b = b0;
+  ld.tile = first_tile(b0) + wt;
+  ld.stop = stop_tile(b0);
+  ld.len = seq_len(b0);
+  enter(ld);
+
+  const uint32_t ring = smem_u32(smem) + warp * (STAGES * C::kStage);
+
+  // The lane's token of the next two tiles to be loaded: its page, asked for two turns ahead and looked at only when
+  // the rows are loaded, and its row in the page.  token_row < 0: no such token.  -2: no such tile.
+  int page[2], token_row[2];
+  auto look_ahead = [&](int i) {
+    token_row[i] = -2;
+    if (ld.b < 0) return;
+    const int token = ld.tile * TILE + lane;
+    token_row[i] = -1;
+    if (token < ld.len) {
+      const uint32_t pg = fdiv(static_cast<uint32_t>(token), a.div_page);
+      page[i] = a.page_table[static_cast<int64_t>(ld.b) * a.max_pages + pg];
+      token_row[i] = token - static_cast<int>(pg) * a.page_size;
+    }
+    ld.tile += p.WT;
+    enter(ld);
+  };
+  look_ahead(0);
+  look_ahead(1);
+  uint32_t mask_of[STAGES] = {};  // tokens of the stages' tiles that are attended, the next to be used first
+  const uint8_t* const kcodes = reinterpret_cast<const uint8_t*>(a.k_pages) + kvh * (D / 2) + (lane % CH) * 16;
+  const uint8_t* const vcodes = reinterpret_cast<const uint8_t*>(a.v_pages) + kvh * (D / 2) + (lane % CH) * 16;
+  const uint8_t* const kscales = a.k_scales + kvh * VB;
+  const uint8_t* const vscales = a.v_scales + kvh * VB;
+  // Fills stage `at` with the next tile; rows that are not attended are zeros.
+  auto load = [&](int at, uint32_t& mask) {
+    if (token_row[0] != -2) {  // the same in all lanes
+      int row = -1;  // of the whole cache
+      if (token_row[0] >= 0) {
+        if (page[0] >= 0 && page[0] < a.num_pages)
+          row = page[0] * a.page_size + token_row[0];
+        else
+          atomicExch(a.status, static_cast<int>(H3ATTN_ERR_INVALID_ARG));  // its keys are not attended
+      }
+      mask = __ballot_sync(0xFFFFFFFFu, row >= 0);
+      const uint32_t ks = ring + at * C::kStage, vs = ks + C::kCodes, kss = vs + C::kCodes, vss = kss + C::kScales;
 #pragma unroll
-    for (int e = 0; e < VEC; ++e) s = fmaf(q[e], k[e], s);
+      for (int i = 0; i < CH; ++i) {
+        const int tr = (i * 32 + lane) / CH, col = lane % CH;
+        const int src_row = __shfl_sync(0xFFFFFFFFu, row, tr);
+        const int64_t off = static_cast<int64_t>(max(src_row, 0)) * (a.Hkv * (D / 2));
+        const uint32_t dst = tr * (D / 2) + ((col ^ swizzle<D>(tr)) << 4);
+        cp_async<16>(ks + dst, kcodes + off, src_row >= 0);
+        cp_async<16>(vs + dst, vcodes + off, src_row >= 0);
+      }
+      const int64_t off = static_cast<int64_t>(max(row, 0)) * (a.Hkv * VB);
+      cp_async<VB>(kss + lane * VB, kscales + off, row >= 0);
+      cp_async<VB>(vss + lane * VB, vscales + off, row >= 0);
+      page[0] = page[1];
+      token_row[0] = token_row[1];
+      look_ahead(1);
+    }
+    cp_async_commit();
+  };
 #pragma unroll
-    for (int off = 16; off >= 1; off >>= 1) s += __shfl_xor_sync(0xFFFFFFFFu, s, off);
-    s *= a.scale_log2;
-    if (score && lane == 0) *score = s;
-    const float to = fmaxf(m, s), fix = ex2(m - to), w = ex2(s - to);
-    l = fmaf(l, fix, w);
+  for (int i = 0; i < STAGES - 1; ++i) load(i, mask_of[i]);
+
+  // The queries of a sequence as the second operand of the score product, each row scaled so that its largest channel
+  // lies in [2^9, 2^10), and for the lane's columns what makes exponents of two of their scores.
+  const int g = lane >> 2, t = lane & 3;
+  auto load_q = [&](int b, uint32_t (&qf)[NT][D / 16][2], float (&to_log2)[NT][2]) {
 #pragma unroll
-    for (int e = 0; e < VEC; ++e) o[e] = fmaf(o[e], fix, w * v[e]);
-    m = to;
+    for (int n = 0; n < NT; ++n) {
+      const bool there = n * 8 + g < heads;
+      const uint4* qp = reinterpret_cast<const uint4*>(a.q + (static_cast<int64_t>(b) * a.Hq + head0 + (there ? n * 8 + g : 0)) * D +
+                                                       t * (D / 4));
+      uint4 x[KW];
+      uint32_t top = 0;
+#pragma unroll
+      for (int i = 0; i < KW; ++i) {
+        x[i] = there ? qp[i] : make_uint4(0u, 0u, 0u, 0u);
+        const uint32_t w[4] = {x[i].x, x[i].y, x[i].z, x[i].w};
+        top = max(top, abs_max8(w));
+      }
+      top = max(top, __shfl_xor_sync(0xFFFFFFFFu, top, 1));
+      top = max(top, __shfl_xor_sync(0xFFFFFFFFu, top, 2));
+      const int up = min(263 - static_cast<int>(top >> 7), 254);  // the factor's exponent, biased by 127
+      const float f = __uint_as_float(static_cast<uint32_t>(up) << 23), f16th = f * 0.0625f;
+#pragma unroll
+      for (int i = 0; i < KW; ++i) {  // channels 0 and 4, 2 and 6; 1 and 5, 3 and 7
+        qf[n][2 * i][0] = pack_f16(__uint_as_float(x[i].x << 16) * f, __uint_as_float(x[i].z << 16) * f);
+        qf[n][2 * i][1] = pack_f16(__uint_as_float(x[i].y << 16) * f, __uint_as_float(x[i].w << 16) * f);
+        qf[n][2 * i + 1][0] = pack_f16(__uint_as_float(x[i].x & 0xFFFF0000u) * f16th, __uint_as_float(x[i].z & 0xFFFF0000u) * f16th);
+        qf[n][2 * i + 1][1] = pack_f16(__uint_as_float(x[i].y & 0xFFFF0000u) * f16th, __uint_as_float(x[i].w & 0xFFFF0000u) * f16th);
+      }
+      const float back = a.scale_log2 * __uint_as_float(static_cast<uint32_t>(261 - up) << 23);  // 128 / f
+#pragma unroll
+      for (int c = 0; c < 2; ++c) to_log2[n][c] = __shfl_sync(0xFFFFFFFFu, back, (2 * t + c) * 4);
+    }
+  };
+
+  int turn = 0;  // tiles used by this warp
+  int b = b0;
+  bool first_segment = true;
+  while (true) {
+    const int s0 = first_tile(b), s1 = stop_tile(b);
+    if (s0 < s1 || p.ranges == 0) {
+      // ---- one sequence's tiles [s0, s1) ----
+      uint32_t qf[NT][D / 16][2];
+      float to_log2[NT][2];
+      load_q(b, qf, to_log2);
+      float o[NT][D / 16][4];
+      // m: what the exponents are taken against, within 8 of the running maximum; l: the lane's part of the sum
+      float m[NT][2], l[NT][2];
+#pragma unroll
+      for (int n = 0; n < NT; ++n) {
+        m[n][0] = m[n][1] = -FLT_MAX;
+        l[n][0] = l[n][1] = 0.0f;
+#pragma unroll
+        for (int dt = 0; dt < D / 16; ++dt) o[n][dt][0] = o[n][dt][1] = o[n][dt][2] = o[n][dt][3] = 0.0f;
+      }
+      for (int tile = s0 + wt; tile < s1; tile += p.WT) {
+        const int st = turn % STAGES;
+        cp_async_wait<STAGES - 2>();
+        __syncwarp();
+        const uint32_t mask = mask_of[0];
+        load((turn + STAGES - 1) % STAGES, mask_of[STAGES - 1]);
+#pragma unroll
+        for (int i = 0; i + 1 < STAGES; ++i) mask_of[i] = mask_of[i + 1];
+        ++turn;
+        const uint32_t ks = ring + st * C::kStage, vs = ks + C::kCodes, kss = vs + C::kCodes, vss = kss + C::kScales;
+        float s[NT][MT][4];
+#pragma unroll
+        for (int mt = 0; mt < MT; ++mt) {
+          const int tok = mt * 16 + token_of(g);  // row g of the product; row g + 8 is 8 tokens on
+          uint32_t w[2][KW];
+          Scale2 sc[2][KW / 2 > 0 ? (KW + 1) / 2 : 1];
+#pragma unroll
+          for (int half = 0; half < 2; ++half) {
+            const int tr = tok + 8 * half;
+            const uint32_t row = ks + tr * (D / 2), sw = swizzle<D>(tr);
+            if constexpr (D == 64) {
+              lds<8>(w[half], row + t * 8);
+              sc[half][0] = scale2(lds8(kss + tr * VB + t) * 0x00800080u);
+            } else if constexpr (D == 128) {
+              lds<16>(w[half], row + ((t ^ sw) << 4));
+              const uint32_t two = lds16(kss + tr * VB + t * 2);
+              sc[half][0] = scale2((two & 0xFFu) * 0x00800080u);
+              sc[half][1] = scale2((two >> 8) * 0x00800080u);
+            } else {
+              uint32_t part[4];
+              lds<16>(part, row + (((2 * t) ^ sw) << 4));
+#pragma unroll
+              for (int i = 0; i < 4; ++i) w[half][i] = part[i];
+              lds<16>(part, row + (((2 * t + 1) ^ sw) << 4));
+#pragma unroll
+              for (int i = 0; i < 4; ++i) w[half][KW - 4 + i] = part[i];
+              uint32_t four[1];
+              lds<4>(four, kss + tr * VB + t * 4);
+#pragma unroll
+              for (int i = 0; i < 4; ++i) sc[half][i < (KW + 1) / 2 ? i : 0] = scale2((four[0] >> (8 * i) & 0xFFu) * 0x00800080u);
+            }
+          }
+          float x[NT][2][4];  // two accumulators: a chain of products waits for each of its links
+#pragma unroll
+          for (int n = 0; n < NT; ++n)
+#pragma unroll
+            for (int e = 0; e < 4; ++e) x[n][0][e] = x[n][1][e] = 0.0f;
+#pragma unroll
+          for (int i = 0; i < KW; ++i) {
+            const Scale2 &a0 = sc[0][i / 2], &a1 = sc[1][i / 2];
+            const uint32_t u0 = w[0][i] >> 8, u1 = w[1][i] >> 8;
+            const uint32_t even[4] = {low2(w[0][i], a0), low2(w[1][i], a1), low2(u0, a0), low2(u1, a1)};
+            const uint32_t odd[4] = {high2(w[0][i], a0), high2(w[1][i], a1), high2(u0, a0), high2(u1, a1)};
+#pragma unroll
+            for (int n = 0; n < NT; ++n) {
+              mma_f16(x[n][0], even, qf[n][2 * i][0], qf[n][2 * i][1]);
+              mma_f16(x[n][1], odd, qf[n][2 * i + 1][0], qf[n][2 * i + 1][1]);
+            }
+          }
+#pragma unroll
+          for (int n = 0; n < NT; ++n)
+#pragma unroll
+            for (int e = 0; e < 4; ++e) s[n][mt][e] = (x[n][0][e] + x[n][1][e]) * to_log2[n][e & 1];
+        }
+        // lane: tokens token_of(g) and 8 more of each 16, heads 2 t and 2 t + 1 of each 8
+        if (mask != 0xFFFFFFFFu) {
+#pragma unroll
+          for (int n = 0; n < NT; ++n)
+#pragma unroll
+            for (int mt = 0; mt < MT; ++mt)
+#pragma unroll
+              for (int e = 0; e < 4; ++e)
+                if (!((mask >> (mt * 16 + token_of(g) + (e < 2 ? 0 : 8))) & 1u)) s[n][mt][e] = -INFINITY;
+        }
+        if constexpr (W) {
+#pragma unroll
+          for (int n = 0; n < NT; ++n)
+#pragma unroll
+            for (int c = 0; c < 2; ++c) {
+              const int h = n * 8 + 2 * t + c;
+              float* row = a.scores + (static_cast<int64_t>(b) * a.Hq + head0 + h) * a.score_stride + tile * TILE + token_of(g);
+#pragma unroll
+              for (int mt = 0; mt < MT; ++mt)
+                if (h < heads) {
+                  row[mt * 16] = s[n][mt][c];
+                  row[mt * 16 + 8] = s[n][mt][c + 2];
+                }
+            }
+        }
+        uint32_t pf[NT][MT][2];
+#pragma unroll
+        for (int n = 0; n < NT; ++n) {
+          float top[2] = {-INFINITY, -INFINITY};
+#pragma unroll
+          for (int mt = 0; mt < MT; ++mt)
+#pragma unroll
+            for (int e = 0; e < 4; ++e) top[e & 1] = fmaxf(top[e & 1], s[n][mt][e]);
+          const bool over = top[0] > m[n][0] + kSlack || top[1] > m[n][1] + kSlack;
+          if (__any_sync(0xFFFFFFFFu, over)) {
+#pragma unroll
+            for (int c = 0; c < 2; ++c) {
+              top[c] = fmaxf(top[c], __shfl_xor_sync(0xFFFFFFFFu, top[c], 4));
+              top[c] = fmaxf(top[c], __shfl_xor_sync(0xFFFFFFFFu, top[c], 8));
+              top[c] = fmaxf(top[c], __shfl_xor_sync(0xFFFFFFFFu, top[c], 16));
+              const float to = fmaxf(m[n][c], top[c]);
+              const float fix = ex2(m[n][c] - to);
+              m[n][c] = to;
+              l[n][c] *= fix;
+#pragma unroll
+              for (int dt = 0; dt < D / 16; ++dt) {
+                o[n][dt][c] *= fix;
+                o[n][dt][c + 2] *= fix;
+              }
+            }
+          }
+#pragma unroll
+          for (int mt = 0; mt < MT; ++mt) {
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+              s[n][mt][e] = ex2(s[n][mt][e] - (m[n][e & 1] - kLift));
+              l[n][e & 1] += s[n][mt][e];
+            }
+            pf[n][mt][0] = transpose8x8(pack_f16(s[n][mt][0], s[n][mt][1]));
+            pf[n][mt][1] = transpose8x8(pack_f16(s[n][mt][2], s[n][mt][3]));
+          }
+        }
+#pragma unroll
+        for (int mt = 0; mt < MT; ++mt) {
+          // tokens 2 t and 2 t + 1 of the product's 8, and 8 on
+          uint32_t w[4][VW];
+          Scale2 sc[2][D == 256 ? 2 : 1];
+          const int tok = mt * 16 + token_of(2 * t), tok1 = mt * 16 + token_of(2 * t + 1);
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            const int tr = (i & 1 ? tok1 : tok) + (i >> 1) * 8;
+            const uint32_t row = vs + tr * (D / 2);
+            if constexpr (D == 64) lds<4>(w[i], row + g * 4);
+            if constexpr (D == 128) lds<8>(w[i], row + (((g >> 1) ^ swizzle<D>(tr)) << 4) + (g & 1) * 8);
+            if constexpr (D == 256) lds<16>(w[i], row + ((g ^ swizzle<D>(tr)) << 4));
+          }
+#pragma unroll
+          for (int half = 0; half < 2; ++half) {
+            const uint32_t s0 = vss + (tok + 8 * half) * VB, s1 = vss + (tok1 + 8 * half) * VB;
+            if constexpr (D == 256) {
+              const uint32_t x0 = lds16(s0 + 2 * g), x1 = lds16(s1 + 2 * g);
+              sc[half][0] = scale2((x0 & 0xFFu) << 7 | (x1 & 0xFFu) << 23);
+              sc[half][D == 256 ? 1 : 0] = scale2((x0 >> 8) << 7 | (x1 >> 8) << 23);
+            } else {
+              const int at = D == 64 ? g >> 1 : g;
+              sc[half][0] = scale2(lds8(s0 + at) << 7 | lds8(s1 + at) << 23);
+            }
+          }
+#pragma unroll
+          for (int i = 0; i < VW; ++i) {
+            const Scale2 &a0 = sc[0][D == 256 ? i / 2 : 0], &a1 = sc[1][D == 256 ? i / 2 : 0];
+#pragma unroll
+            for (int hw = 0; hw < 2; ++hw) {  // channels 0 to 3, 4 to 7 of the word
+              const uint32_t x0 = __byte_perm(w[0][i], w[1][i], hw ? 0x7632 : 0x5410);
+              const uint32_t x1 = __byte_perm(w[2][i], w[3][i], hw ? 0x7632 : 0x5410);
+              const uint32_t u0 = x0 >> 8, u1 = x1 >> 8;
+              const uint32_t even[4] = {low2(x0, a0), low2(u0, a0), low2(x1, a1), low2(u1, a1)};
+              const uint32_t odd[4] = {high2(x0, a0), high2(u0, a0), high2(x1, a1), high2(u1, a1)};
+#pragma unroll
+              for (int n = 0; n < NT; ++n) {
+                mma_f16(o[n][4 * i + 2 * hw], even, pf[n][mt][0], pf[n][mt][1]);
+                mma_f16(o[n][4 * i + 2 * hw + 1], odd, pf[n][mt][0], pf[n][mt][1]);
+              }
+            }
+          }
+        }
+        __syncwarp();  // the stage is read; the next turn's load may fill it
+      }
+#pragma unroll
+      for (int n = 0; n < NT; ++n)
+#pragma unroll
+        for (int c = 0; c < 2; ++c) {
+          l[n][c] += __shfl_xor_sync(0xFFFFFFFFu, l[n][c], 4);
+          l[n][c] += __shfl_xor_sync(0xFFFFFFFFu, l[n][c], 8);
+          l[n][c] += __shfl_xor_sync(0xFFFFFFFFu, l[n][c], 16);
+        }
+      // ---- the warps of a unit head are joined, halving their number ----
+      for (int step = p.WT >> 1; step >= 1; step >>= 1) {
+#pragma unroll
+        for (int n = 0; n < NT; ++n) {
+          __syncthreads();  // the buffers are free
+          if (wt >= step && wt < 2 * step) {
+            const int at = (wt - step) * p.WH + wh;
+            float4* dst = reinterpret_cast<float4*>(join + at * (8 * D));
+#pragma unroll
+            for (int dt = 0; dt < D / 16; ++dt)
+              dst[dt * 32 + lane] = make_float4(o[n][dt][0], o[n][dt][1], o[n][dt][2], o[n][dt][3]);
+            if (lane < 4) {
+#pragma unroll
+              for (int c = 0; c < 2; ++c) {
+                stats[(at * 8 + 2 * t + c) * 2] = m[n][c];
+                stats[(at * 8 + 2 * t + c) * 2 + 1] = l[n][c];
+              }
+            }
+          }
+          __syncthreads();
+          if (wt < step) {
+            const int at = wt * p.WH + wh;
+            const float4* src = reinterpret_cast<const float4*>(join + at * (8 * D));
+            float mine[2], theirs[2];
+#pragma unroll
+            for (int c = 0; c < 2; ++c) {
+              const float mo = stats[(at * 8 + 2 * t + c) * 2], lo = stats[(at * 8 + 2 * t + c) * 2 + 1];
+              const float to = fmaxf(m[n][c], mo);
+              mine[c] = ex2(m[n][c] - to);
+              theirs[c] = ex2(mo - to);
+              m[n][c] = to;
+              l[n][c] = l[n][c] * mine[c] + lo * theirs[c];
+            }
+#pragma unroll
+            for (int dt = 0; dt < D / 16; ++dt) {
+              const float4 v = src[dt * 32 + lane];
+              o[n][dt][0] = o[n][dt][0] * mine[0] + v.x * theirs[0];
+              o[n][dt][1] = o[n][dt][1] * mine[1] + v.y * theirs[1];
+              o[n][dt][2] = o[n][dt][2] * mine[0] + v.z * theirs[0];
+              o[n][dt][3] = o[n][dt][3] * mine[1] + v.w * theirs[1];
+            }
+          }
+        }
+      }
+      if (wt == 0) {
+        const bool whole = s0 == 0 && s1 == seq_end(b) - seq_begin(b) - start;
+        // slot 0: the range's first sequence, slot 1: its last
+        float* const part = a.ws + ((static_cast<int64_t>(r) * 2 + (first_segment ? 0 : 1)) * p.unit_heads + unit) *
+                                       partial_floats(min(G, C::kHeads), D);
+#pragma unroll
+        for (int n = 0; n < NT; ++n)
+#pragma unroll
+          for (int c = 0; c < 2; ++c) {
+            const int h = n * 8 + 2 * t + c;
+            if (h >= heads) continue;
+            // P was raised by 2^kLift, and so are l and o: the weight of a score is 2^(score - (m - kLift)) / l
+            const float inv = whole ? (l[n][c] == 0.0f ? 0.0f : 1.0f / l[n][c]) : 1.0f;  // no key: zeros
+            float y[D / 8];  // the lane's channels in order
+#pragma unroll
+            for (int dt = 0; dt < D / 16; ++dt) {
+              const int at = (dt >> 1) * 4 + (dt & 1);
+              const float undo = (dt & 1 ? 8.0f : 128.0f) * inv;
+              y[at] = o[n][dt][c] * undo;
+              y[at + 2] = o[n][dt][c + 2] * undo;
+            }
+            if (whole) {
+              if (W && g == 0) a.stats[static_cast<int64_t>(b) * a.Hq + head0 + h] = make_float2(m[n][c] - kLift, inv);
+              uint4* op = reinterpret_cast<uint4*>(a.o + (static_cast<int64_t>(b) * a.Hq + head0 + h) * D + g * (D / 8));
+#pragma unroll
+              for (int i = 0; i < D / 64; ++i)
+                op[i] = make_uint4(pack_bf16(y[8 * i], y[8 * i + 1]), pack_bf16(y[8 * i + 2], y[8 * i + 3]),
+                                   pack_bf16(y[8 * i + 4], y[8 * i + 5]), pack_bf16(y[8 * i + 6], y[8 * i + 7]));
+            } else {
+              if (g == 0) {
+                part[2 * h] = m[n][c] - kLift;
+                part[2 * h + 1] = l[n][c];
+              }
+              float4* op = reinterpret_cast<float4*>(part + partial_o(min(G, C::kHeads)) + h * D + g * (D / 8));
+#pragma unroll
+              for (int i = 0; i < D / 32; ++i) op[i] = make_float4(y[4 * i], y[4 * i + 1], y[4 * i + 2], y[4 * i + 3]);
+            }
+          }
+      }
+      first_segment = false;
+    }
+    if (p.ranges == 0 || seq_end(b) >= t1) break;
+    ++b;
   }
-#pragma unroll
-  for (int e = 0; e < VEC; ++e) part_o[warp][lane * VEC + e] = o[e];
-  if (lane == 0) part_ml[warp] = make_float2(m, l);
-  __syncthreads();
-  if (warp > 0) return;
-  for (int w = 1; w < kWarps; ++w) m = fmaxf(m, part_ml[w].x);
-  l = 0.0f;
-#pragma unroll
-  for (int e = 0; e < VEC; ++e) o[e] = 0.0f;
-  for (int w = 0; w < kWarps; ++w) {
-    const float weight = ex2(part_ml[w].x - m);
-    l = fmaf(part_ml[w].y, weight, l);
-#pragma unroll
-    for (int e = 0; e < VEC; ++e) o[e] = fmaf(part_o[w][lane * VEC + e], weight, o[e]);
+  cp_async_wait<0>();
+}
+
+int warps_of(const DecodeArgs& a) { return a.D * (a.Hq / a.Hkv > 8 ? 2 : 1) <= 128 ? 16 : 8; }
+DecodePlan plan_of(const DecodeArgs& a, int sms, bool split) { return make_plan(a, sms, split, warps_of(a), 32, 1); }
+
+template <int D, int NT, bool W>
+cudaError_t launch_d(const Kernelargs& k, cudaStream_t stream) {
+  using C = Q4Cfg<D, NT>;
+  static std::atomic<bool> attr_set[64];  // calls of several host threads
+  int dev = 0;
+  cudaError_t e = cudaGetDevice(&dev);
+  if (e != cudaSuccess) return e;
+  if (dev < 0 || dev >= 64) return cudaErrorInvalidDevice;
+  if (!attr_set[dev]) {
+    e = cudaFuncSetAttribute(decode_q4_kernel<D, NT, W>, cudaFuncAttributeMaxDynamicSharedMemorySize, C::kSmem);
+    if (e != cudaSuccess) return e;
+    attr_set[dev] = true;
   }
-  const float inv = l == 0.0f ? 0.0f : 1.0f / l;  // no key: zeros
-  if (a.stats && lane == 0) a.stats[blockIdx.x] = make_float2(m, inv);
-  __nv_bfloat16* out = reinterpret_cast<__nv_bfloat16*>(a.o) + (static_cast<int64_t>(b) * a.Hq + h) * D + lane * VEC;
-#pragma unroll
-  for (int e = 0; e < VEC; ++e) out[e] = __float2bfloat16_rn(o[e] * inv);
+  const int64_t ranges = k.p.ranges > 0 ? k.p.ranges : k.a.B;
+  e = launch_dependent(decode_q4_kernel<D, NT, W>, dim3(static_cast<unsigned>(ranges * k.p.groups)), C::kWarps * 32, C::kSmem,
+                       stream, k);
+  if (e != cudaSuccess || k.p.ranges == 0) return e;
+  const int G = k.a.Hq / k.a.Hkv;
+  return launch_dependent(decode_join_kernel<D, W>, dim3(k.p.ranges * k.p.groups), kJoinThreads, 0, stream, k, C::kTile,
+                          std::min(G, C::kHeads));
+}
+
+template <int D>
+cudaError_t launch_heads(const Kernelargs& k, cudaStream_t stream) {
+  if (k.a.Hq / k.a.Hkv > 8) return k.a.scores ? launch_d<D, 2, true>(k, stream) : launch_d<D, 2, false>(k, stream);
+  return k.a.scores ? launch_d<D, 1, true>(k, stream) : launch_d<D, 1, false>(k, stream);
 }
 
 }  // namespace
 
-cudaError_t decode_q4_workspace(const DecodeArgs&, size_t* bytes) {
-  *bytes = 0;
+cudaError_t decode_q4_workspace(const DecodeArgs& a, size_t* bytes) {
+  int sms = 0;
+  cudaError_t e = sm_count(&sms);
+  if (e != cudaSuccess) return e;
+  const DecodePlan p = plan_of(a, sms, true);
+  const int heads = std::min(a.Hq / a.Hkv, 16);
+  *bytes = static_cast<size_t>(p.ranges) * 2 * p.unit_heads * partial_floats(heads, a.D) * sizeof(float);
   return cudaSuccess;
 }
 
 cudaError_t launch_decode_q4(const DecodeArgs& a, cudaStream_t stream) {
-  const dim3 grid(static_cast<unsigned>(a.B) * a.Hq);
+  int sms = 0;
+  cudaError_t e = sm_count(&sms);
+  if (e != cudaSuccess) return e;
+  Kernelargs k{a, plan_of(a, sms, a.ws != nullptr)};
   switch (a.D) {
-    case 64: return launch_dependent(decode_q4_kernel<64>, grid, kWarps * 32, 0, stream, a);
-    case 128: return launch_dependent(decode_q4_kernel<128>, grid, kWarps * 32, 0, stream, a);
-    case 256: return launch_dependent(decode_q4_kernel<256>, grid, kWarps * 32, 0, stream, a);
+    case 64: return launch_heads<64>(k, stream);
+    case 128: return launch_heads<128>(k, stream);
+    case 256: return launch_heads<256>(k, stream);
     default: return cudaErrorInvalidValue;
   }
 }
