@@ -25,6 +25,8 @@
 // (binary16: half a step is 2^-12 of a weight, an eighth of the output's own rounding): P is taken
 // 2^7 times larger than its sum's reference so that weights down to 2^-31 of the largest are normal.
 // Queries are taken in binary16 after a scaling by a power of two for each row.
+#include <type_traits>
+
 #include "cache4.cuh"
 #include "decode_common.cuh"
 #include "ptx.cuh"
@@ -42,10 +44,6 @@ __device__ __forceinline__ void cp_async(uint32_t dst, const void* src, bool val
     asm volatile("cp.async.ca.shared.global [%0], [%1], %3, %2;" ::"r"(dst), "l"(src), "r"(valid ? BYTES : 0), "n"(BYTES) : "memory");
 }
 template <int BYTES>
-struct Words {
-  uint32_t w[BYTES / 4];
-};
-template <int BYTES>
 __device__ __forceinline__ void lds(uint32_t (&w)[BYTES / 4], uint32_t addr) {
   if constexpr (BYTES == 4) asm volatile("ld.shared.b32 %0, [%1];" : "=r"(w[0]) : "r"(addr) : "memory");
   if constexpr (BYTES == 8) asm volatile("ld.shared.v2.b32 {%0, %1}, [%2];" : "=r"(w[0]), "=r"(w[1]) : "r"(addr) : "memory");
@@ -53,13 +51,8 @@ __device__ __forceinline__ void lds(uint32_t (&w)[BYTES / 4], uint32_t addr) {
     asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];" : "=r"(w[0]), "=r"(w[1]), "=r"(w[2]), "=r"(w[3]) : "r"(addr) : "memory");
 }
 __device__ __forceinline__ uint32_t lds8(uint32_t addr) {
-  uint16_t v;
-  asm volatile("ld.shared.u8 %0, [%1];" : "=h"(v) : "r"(addr) : "memory");
-  return v;
-}
-__device__ __forceinline__ uint32_t lds16(uint32_t addr) {
-  uint16_t v;
-  asm volatile("ld.shared.u16 %0, [%1];" : "=h"(v) : "r"(addr) : "memory");
+  uint32_t v;
+  asm volatile("ld.shared.u8 %0, [%1];" : "=r"(v) : "r"(addr) : "memory");
   return v;
 }
 __device__ __forceinline__ uint32_t hmul2(uint32_t a, uint32_t b) {
@@ -88,11 +81,7 @@ struct Scale2 {
   uint32_t m, c0, c1;
 };
 __device__ __forceinline__ Scale2 scale2(uint32_t shifted) {  // bytes moved up by 7
-  Scale2 s;
-  s.m = hmul2(shifted, 0x20002000u);     // 2^-7
-  s.c0 = hmul2(s.m, 0xE408E408u);        // -1032
-  s.c1 = hmul2(s.m, 0xE480E480u);        // -1152
-  return s;
+  return {hmul2(shifted, 0x20002000u), hmul2(shifted, 0xC808C808u), hmul2(shifted, 0xC880C880u)};  // 2^-7, -1032 2^-7, -1152 2^-7
 }
 // Nibbles 0 and 4 of x (counted in 4 bits), and nibbles 1 and 5 sixteen times larger.
 __device__ __forceinline__ uint32_t low2(uint32_t x, const Scale2& s) { return hfma2((x & 0x000F000Fu) | 0x64006400u, s.m, s.c0); }
@@ -186,7 +175,8 @@ __global__ void __launch_bounds__(Q4Cfg<D, NT>::kWarps * 32, 1) decode_q4_kernel
 
   // The tiles that this warp loads, in the order they are used, over sequence borders.
   struct Walk {
-    int b, tile, stop, len;  // sequence, tile of the sequence, the range's end in it
+    int b, tile, stop, len;  // sequence, tile of the sequence, the range's end in it, the sequence's tokens
+    const int32_t* table;    // its pages
   };
   auto enter = [&](Walk& w) {  // to the first tile at or after the present one that is there
     while (w.tile >= w.stop) {
@@ -198,6 +188,7 @@ __global__ void __launch_bounds__(Q4Cfg<D, NT>::kWarps * 32, 1) decode_q4_kernel
       w.stop = stop_tile(w.b);
       w.tile = wt;
       w.len = seq_len(w.b);
+      w.table += a.max_pages;
     }
   };
   Walk ld;
@@ -205,6 +196,7 @@ __global__ void __launch_bounds__(Q4Cfg<D, NT>::kWarps * 32, 1) decode_q4_kernel
   ld.tile = first_tile(b0) + wt;
   ld.stop = stop_tile(b0);
   ld.len = seq_len(b0);
+  ld.table = a.page_table + static_cast<int64_t>(b0) * a.max_pages;
   enter(ld);
 
   const uint32_t ring = smem_u32(smem) + warp * (STAGES * C::kStage);
@@ -219,7 +211,7 @@ __global__ void __launch_bounds__(Q4Cfg<D, NT>::kWarps * 32, 1) decode_q4_kernel
     token_row[i] = -1;
     if (token < ld.len) {
       const uint32_t pg = fdiv(static_cast<uint32_t>(token), a.div_page);
-      page[i] = a.page_table[static_cast<int64_t>(ld.b) * a.max_pages + pg];
+      page[i] = ld.table[pg];
       token_row[i] = token - static_cast<int>(pg) * a.page_size;
     }
     ld.tile += p.WT;
@@ -232,30 +224,39 @@ __global__ void __launch_bounds__(Q4Cfg<D, NT>::kWarps * 32, 1) decode_q4_kernel
   const uint8_t* const vcodes = reinterpret_cast<const uint8_t*>(a.v_pages) + kvh * (D / 2) + (lane % CH) * 16;
   const uint8_t* const kscales = a.k_scales + kvh * VB;
   const uint8_t* const vscales = a.v_scales + kvh * VB;
+  const uint32_t row_codes = a.Hkv * (D / 2), row_scales = a.Hkv * VB;  // bytes from token to token
   // Fills stage `at` with the next tile; rows that are not attended are zeros.
   auto load = [&](int at, uint32_t& mask) {
     if (token_row[0] != -2) {  // the same in all lanes
-      int row = -1;  // of the whole cache
-      if (token_row[0] >= 0) {
-        if (page[0] >= 0 && page[0] < a.num_pages)
+      uint32_t row = 0;  // of the whole cache
+      bool there = token_row[0] >= 0;
+      if (there) {
+        if (static_cast<uint32_t>(page[0]) < static_cast<uint32_t>(a.num_pages)) {
           row = page[0] * a.page_size + token_row[0];
-        else
+        } else {
           atomicExch(a.status, static_cast<int>(H3ATTN_ERR_INVALID_ARG));  // its keys are not attended
+          there = false;
+        }
       }
-      mask = __ballot_sync(0xFFFFFFFFu, row >= 0);
-      const uint32_t ks = ring + at * C::kStage, vs = ks + C::kCodes, kss = vs + C::kCodes, vss = kss + C::kScales;
+      mask = __ballot_sync(0xFFFFFFFFu, there);
+      const uint32_t ks = ring + at * C::kStage, vs = ks + C::kCodes, kss = vs + C::kCodes + lane * VB, vss = kss + C::kScales;
+      auto rows = [&](auto whole) {  // whole: all tokens are there
 #pragma unroll
-      for (int i = 0; i < CH; ++i) {
-        const int tr = (i * 32 + lane) / CH, col = lane % CH;
-        const int src_row = __shfl_sync(0xFFFFFFFFu, row, tr);
-        const int64_t off = static_cast<int64_t>(max(src_row, 0)) * (a.Hkv * (D / 2));
-        const uint32_t dst = tr * (D / 2) + ((col ^ swizzle<D>(tr)) << 4);
-        cp_async<16>(ks + dst, kcodes + off, src_row >= 0);
-        cp_async<16>(vs + dst, vcodes + off, src_row >= 0);
-      }
-      const int64_t off = static_cast<int64_t>(max(row, 0)) * (a.Hkv * VB);
-      cp_async<VB>(kss + lane * VB, kscales + off, row >= 0);
-      cp_async<VB>(vss + lane * VB, vscales + off, row >= 0);
+        for (int i = 0; i < CH; ++i) {
+          const int tr = (i * 32 + lane) / CH, col = lane % CH;
+          const uint32_t src = __shfl_sync(0xFFFFFFFFu, row, tr);
+          const bool valid = whole || (mask >> tr & 1u);
+          const uint32_t dst = tr * (D / 2) + ((col ^ swizzle<D>(tr)) << 4);
+          cp_async<16>(ks + dst, kcodes + static_cast<uint64_t>(src) * row_codes, valid);
+          cp_async<16>(vs + dst, vcodes + static_cast<uint64_t>(src) * row_codes, valid);
+        }
+        cp_async<VB>(kss, kscales + static_cast<uint64_t>(row) * row_scales, whole || there);
+        cp_async<VB>(vss, vscales + static_cast<uint64_t>(row) * row_scales, whole || there);
+      };
+      if (mask == 0xFFFFFFFFu)
+        rows(std::true_type{});
+      else
+        rows(std::false_type{});
       page[0] = page[1];
       token_row[0] = token_row[1];
       look_ahead(1);
@@ -293,7 +294,8 @@ __global__ void __launch_bounds__(Q4Cfg<D, NT>::kWarps * 32, 1) decode_q4_kernel
         qf[n][2 * i + 1][0] = pack_f16(__uint_as_float(x[i].x & 0xFFFF0000u) * f16th, __uint_as_float(x[i].z & 0xFFFF0000u) * f16th);
         qf[n][2 * i + 1][1] = pack_f16(__uint_as_float(x[i].y & 0xFFFF0000u) * f16th, __uint_as_float(x[i].w & 0xFFFF0000u) * f16th);
       }
-      const float back = a.scale_log2 * __uint_as_float(static_cast<uint32_t>(261 - up) << 23);  // 128 / f
+      // 128 / f; normal, so that -infinity times it is not a NaN, nor 0 times it
+      const float back = fminf(fmaxf(a.scale_log2 * __uint_as_float(static_cast<uint32_t>(261 - up) << 23), FLT_MIN), FLT_MAX);
 #pragma unroll
       for (int c = 0; c < 2; ++c) to_log2[n][c] = __shfl_sync(0xFFFFFFFFu, back, (2 * t + c) * 4);
     }
@@ -344,9 +346,8 @@ __global__ void __launch_bounds__(Q4Cfg<D, NT>::kWarps * 32, 1) decode_q4_kernel
               sc[half][0] = scale2(lds8(kss + tr * VB + t) * 0x00800080u);
             } else if constexpr (D == 128) {
               lds<16>(w[half], row + ((t ^ sw) << 4));
-              const uint32_t two = lds16(kss + tr * VB + t * 2);
-              sc[half][0] = scale2((two & 0xFFu) * 0x00800080u);
-              sc[half][1] = scale2((two >> 8) * 0x00800080u);
+              sc[half][0] = scale2(lds8(kss + tr * VB + t * 2) * 0x00800080u);
+              sc[half][1] = scale2(lds8(kss + tr * VB + t * 2 + 1) * 0x00800080u);
             } else {
               uint32_t part[4];
               lds<16>(part, row + (((2 * t) ^ sw) << 4));
@@ -355,17 +356,14 @@ __global__ void __launch_bounds__(Q4Cfg<D, NT>::kWarps * 32, 1) decode_q4_kernel
               lds<16>(part, row + (((2 * t + 1) ^ sw) << 4));
 #pragma unroll
               for (int i = 0; i < 4; ++i) w[half][KW - 4 + i] = part[i];
-              uint32_t four[1];
-              lds<4>(four, kss + tr * VB + t * 4);
 #pragma unroll
-              for (int i = 0; i < 4; ++i) sc[half][i < (KW + 1) / 2 ? i : 0] = scale2((four[0] >> (8 * i) & 0xFFu) * 0x00800080u);
+              for (int i = 0; i < 4; ++i) sc[half][i < (KW + 1) / 2 ? i : 0] = scale2(lds8(kss + tr * VB + t * 4 + i) * 0x00800080u);
             }
           }
-          float x[NT][2][4];  // two accumulators: a chain of products waits for each of its links
 #pragma unroll
           for (int n = 0; n < NT; ++n)
 #pragma unroll
-            for (int e = 0; e < 4; ++e) x[n][0][e] = x[n][1][e] = 0.0f;
+            for (int e = 0; e < 4; ++e) s[n][mt][e] = 0.0f;
 #pragma unroll
           for (int i = 0; i < KW; ++i) {
             const Scale2 &a0 = sc[0][i / 2], &a1 = sc[1][i / 2];
@@ -374,14 +372,10 @@ __global__ void __launch_bounds__(Q4Cfg<D, NT>::kWarps * 32, 1) decode_q4_kernel
             const uint32_t odd[4] = {high2(w[0][i], a0), high2(w[1][i], a1), high2(u0, a0), high2(u1, a1)};
 #pragma unroll
             for (int n = 0; n < NT; ++n) {
-              mma_f16(x[n][0], even, qf[n][2 * i][0], qf[n][2 * i][1]);
-              mma_f16(x[n][1], odd, qf[n][2 * i + 1][0], qf[n][2 * i + 1][1]);
+              mma_f16(s[n][mt], even, qf[n][2 * i][0], qf[n][2 * i][1]);
+              mma_f16(s[n][mt], odd, qf[n][2 * i + 1][0], qf[n][2 * i + 1][1]);
             }
           }
-#pragma unroll
-          for (int n = 0; n < NT; ++n)
-#pragma unroll
-            for (int e = 0; e < 4; ++e) s[n][mt][e] = (x[n][0][e] + x[n][1][e]) * to_log2[n][e & 1];
         }
         // lane: tokens token_of(g) and 8 more of each 16, heads 2 t and 2 t + 1 of each 8
         if (mask != 0xFFFFFFFFu) {
@@ -403,8 +397,8 @@ __global__ void __launch_bounds__(Q4Cfg<D, NT>::kWarps * 32, 1) decode_q4_kernel
 #pragma unroll
               for (int mt = 0; mt < MT; ++mt)
                 if (h < heads) {
-                  row[mt * 16] = s[n][mt][c];
-                  row[mt * 16 + 8] = s[n][mt][c + 2];
+                  row[mt * 16] = s[n][mt][c] * to_log2[n][c];
+                  row[mt * 16 + 8] = s[n][mt][c + 2] * to_log2[n][c];
                 }
             }
         }
@@ -416,14 +410,14 @@ __global__ void __launch_bounds__(Q4Cfg<D, NT>::kWarps * 32, 1) decode_q4_kernel
           for (int mt = 0; mt < MT; ++mt)
 #pragma unroll
             for (int e = 0; e < 4; ++e) top[e & 1] = fmaxf(top[e & 1], s[n][mt][e]);
-          const bool over = top[0] > m[n][0] + kSlack || top[1] > m[n][1] + kSlack;
+          const bool over = top[0] * to_log2[n][0] > m[n][0] + kSlack || top[1] * to_log2[n][1] > m[n][1] + kSlack;
           if (__any_sync(0xFFFFFFFFu, over)) {
 #pragma unroll
             for (int c = 0; c < 2; ++c) {
               top[c] = fmaxf(top[c], __shfl_xor_sync(0xFFFFFFFFu, top[c], 4));
               top[c] = fmaxf(top[c], __shfl_xor_sync(0xFFFFFFFFu, top[c], 8));
               top[c] = fmaxf(top[c], __shfl_xor_sync(0xFFFFFFFFu, top[c], 16));
-              const float to = fmaxf(m[n][c], top[c]);
+              const float to = fmaxf(m[n][c], top[c] * to_log2[n][c]);
               const float fix = ex2(m[n][c] - to);
               m[n][c] = to;
               l[n][c] *= fix;
@@ -438,7 +432,7 @@ __global__ void __launch_bounds__(Q4Cfg<D, NT>::kWarps * 32, 1) decode_q4_kernel
           for (int mt = 0; mt < MT; ++mt) {
 #pragma unroll
             for (int e = 0; e < 4; ++e) {
-              s[n][mt][e] = ex2(s[n][mt][e] - (m[n][e & 1] - kLift));
+              s[n][mt][e] = ex2(fmaf(s[n][mt][e], to_log2[n][e & 1], kLift - m[n][e & 1]));
               l[n][e & 1] += s[n][mt][e];
             }
             pf[n][mt][0] = transpose8x8(pack_f16(s[n][mt][0], s[n][mt][1]));
@@ -463,12 +457,11 @@ __global__ void __launch_bounds__(Q4Cfg<D, NT>::kWarps * 32, 1) decode_q4_kernel
           for (int half = 0; half < 2; ++half) {
             const uint32_t s0 = vss + (tok + 8 * half) * VB, s1 = vss + (tok1 + 8 * half) * VB;
             if constexpr (D == 256) {
-              const uint32_t x0 = lds16(s0 + 2 * g), x1 = lds16(s1 + 2 * g);
-              sc[half][0] = scale2((x0 & 0xFFu) << 7 | (x1 & 0xFFu) << 23);
-              sc[half][D == 256 ? 1 : 0] = scale2((x0 >> 8) << 7 | (x1 >> 8) << 23);
+              sc[half][0] = scale2((lds8(s0 + 2 * g) + lds8(s1 + 2 * g) * 0x10000u) * 0x80u);
+              sc[half][D == 256 ? 1 : 0] = scale2((lds8(s0 + 2 * g + 1) + lds8(s1 + 2 * g + 1) * 0x10000u) * 0x80u);
             } else {
               const int at = D == 64 ? g >> 1 : g;
-              sc[half][0] = scale2(lds8(s0 + at) << 7 | lds8(s1 + at) << 23);
+              sc[half][0] = scale2((lds8(s0 + at) + lds8(s1 + at) * 0x10000u) * 0x80u);
             }
           }
 #pragma unroll
