@@ -43,16 +43,21 @@ __device__ __forceinline__ void cp_async(uint32_t dst, const void* src, bool val
   else
     asm volatile("cp.async.ca.shared.global [%0], [%1], %3, %2;" ::"r"(dst), "l"(src), "r"(valid ? BYTES : 0), "n"(BYTES) : "memory");
 }
+// BYTES of shared memory at addr + off (a constant that becomes the instruction's own).
 template <int BYTES>
-__device__ __forceinline__ void lds(uint32_t (&w)[BYTES / 4], uint32_t addr) {
-  if constexpr (BYTES == 4) asm volatile("ld.shared.b32 %0, [%1];" : "=r"(w[0]) : "r"(addr) : "memory");
-  if constexpr (BYTES == 8) asm volatile("ld.shared.v2.b32 {%0, %1}, [%2];" : "=r"(w[0]), "=r"(w[1]) : "r"(addr) : "memory");
+__device__ __forceinline__ void lds(uint32_t (&w)[BYTES / 4], uint32_t addr, int off) {
+  if constexpr (BYTES == 4) asm volatile("ld.shared.b32 %0, [%1];" : "=r"(w[0]) : "r"(addr + off) : "memory");
+  if constexpr (BYTES == 8)
+    asm volatile("ld.shared.v2.b32 {%0, %1}, [%2];" : "=r"(w[0]), "=r"(w[1]) : "r"(addr + off) : "memory");
   if constexpr (BYTES == 16)
-    asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];" : "=r"(w[0]), "=r"(w[1]), "=r"(w[2]), "=r"(w[3]) : "r"(addr) : "memory");
+    asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];"
+                 : "=r"(w[0]), "=r"(w[1]), "=r"(w[2]), "=r"(w[3])
+                 : "r"(addr + off)
+                 : "memory");
 }
-__device__ __forceinline__ uint32_t lds8(uint32_t addr) {
+__device__ __forceinline__ uint32_t lds8(uint32_t addr, int off) {
   uint32_t v;
-  asm volatile("ld.shared.u8 %0, [%1];" : "=r"(v) : "r"(addr) : "memory");
+  asm volatile("ld.shared.u8 %0, [%1];" : "=r"(v) : "r"(addr + off) : "memory");
   return v;
 }
 __device__ __forceinline__ uint32_t hmul2(uint32_t a, uint32_t b) {
@@ -84,8 +89,15 @@ __device__ __forceinline__ Scale2 scale2(uint32_t shifted) {  // bytes moved up 
   return {hmul2(shifted, 0x20002000u), hmul2(shifted, 0xC808C808u), hmul2(shifted, 0xC880C880u)};  // 2^-7, -1032 2^-7, -1152 2^-7
 }
 // Nibbles 0 and 4 of x (counted in 4 bits), and nibbles 1 and 5 sixteen times larger.
-__device__ __forceinline__ uint32_t low2(uint32_t x, const Scale2& s) { return hfma2((x & 0x000F000Fu) | 0x64006400u, s.m, s.c0); }
-__device__ __forceinline__ uint32_t high2(uint32_t x, const Scale2& s) { return hfma2((x & 0x00F000F0u) | 0x64006400u, s.m, s.c1); }
+// k1024 is 0x64006400 in a register that the compiler neither sees through nor takes for the same in all lanes: mask and
+// or are one instruction then, where two constants, or a constant and a uniform register, make two (240 instead of 128 of a
+// tile's 780 instructions).
+__device__ __forceinline__ uint32_t low2(uint32_t x, uint32_t k1024, const Scale2& s) {
+  return hfma2((x & 0x000F000Fu) | k1024, s.m, s.c0);
+}
+__device__ __forceinline__ uint32_t high2(uint32_t x, uint32_t k1024, const Scale2& s) {
+  return hfma2((x & 0x00F000F0u) | k1024, s.m, s.c1);
+}
 
 // NT: tiles of 8 query heads (1 or 2).
 template <int D, int NT>
@@ -301,6 +313,23 @@ __global__ void __launch_bounds__(Q4Cfg<D, NT>::kWarps * 32, 1) decode_q4_kernel
     }
   };
 
+  // Where in a stage the lane's K row and its scales begin (row g of the first product; the others are a constant
+  // further), and its V rows and their scales (tokens 2 t and 2 t + 1): two 16-bit offsets each, kept from being worked out anew every tile.
+  uint32_t of_k, of_v[2];
+  {
+    const int tr = token_of(g), kt = D == 256 ? 2 * t : D == 128 ? t : t >> 1;
+    of_k = tr * (D / 2) + ((kt ^ swizzle<D>(tr)) << 4) + (D == 64 ? (t & 1) * 8 : 0);
+    of_k |= static_cast<uint32_t>(2 * C::kCodes + tr * VB + t * (VB / 4)) << 16;
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+      const int vr = token_of(2 * t + i), vt = D == 256 ? g : D == 128 ? g >> 1 : g >> 2;
+      of_v[i] = C::kCodes + vr * (D / 2) + ((vt ^ swizzle<D>(vr)) << 4) + (D == 128 ? (g & 1) * 8 : D == 64 ? (g & 3) * 4 : 0);
+      of_v[i] |= static_cast<uint32_t>(2 * C::kCodes + C::kScales + vr * VB + (D == 256 ? 2 * g : D == 128 ? g : g >> 1)) << 16;
+    }
+    asm volatile("" : "+r"(of_k), "+r"(of_v[0]), "+r"(of_v[1]));
+  }
+  uint32_t k1024;
+  asm volatile("shfl.sync.idx.b32 %0, %1, %2, 31, 0xFFFFFFFF;" : "=r"(k1024) : "r"(0x64006400u), "r"(lane));
   int turn = 0;  // tiles used by this warp
   int b = b0;
   bool first_segment = true;
@@ -330,35 +359,31 @@ __global__ void __launch_bounds__(Q4Cfg<D, NT>::kWarps * 32, 1) decode_q4_kernel
 #pragma unroll
         for (int i = 0; i + 1 < STAGES; ++i) mask_of[i] = mask_of[i + 1];
         ++turn;
-        const uint32_t ks = ring + st * C::kStage, vs = ks + C::kCodes, kss = vs + C::kCodes, vss = kss + C::kScales;
+        const uint32_t stage = ring + st * C::kStage;
+        const uint32_t k_at = stage + (of_k & 0xFFFFu), ks_at = stage + (of_k >> 16);
+        const uint32_t v_at[2] = {stage + (of_v[0] & 0xFFFFu), stage + (of_v[1] & 0xFFFFu)};
+        const uint32_t vs_at[2] = {stage + (of_v[0] >> 16), stage + (of_v[1] >> 16)};
         float s[NT][MT][4];
 #pragma unroll
         for (int mt = 0; mt < MT; ++mt) {
-          const int tok = mt * 16 + token_of(g);  // row g of the product; row g + 8 is 8 tokens on
           uint32_t w[2][KW];
-          Scale2 sc[2][KW / 2 > 0 ? (KW + 1) / 2 : 1];
+          Scale2 sc[2][(KW + 1) / 2];
 #pragma unroll
-          for (int half = 0; half < 2; ++half) {
-            const int tr = tok + 8 * half;
-            const uint32_t row = ks + tr * (D / 2), sw = swizzle<D>(tr);
-            if constexpr (D == 64) {
-              lds<8>(w[half], row + t * 8);
-              sc[half][0] = scale2(lds8(kss + tr * VB + t) * 0x00800080u);
-            } else if constexpr (D == 128) {
-              lds<16>(w[half], row + ((t ^ sw) << 4));
-              sc[half][0] = scale2(lds8(kss + tr * VB + t * 2) * 0x00800080u);
-              sc[half][1] = scale2(lds8(kss + tr * VB + t * 2 + 1) * 0x00800080u);
-            } else {
+          for (int half = 0; half < 2; ++half) {  // rows g and g + 8 of the product, tokens 8 apart
+            const int tr = mt * 16 + half * 8;
+            if constexpr (D == 256) {
               uint32_t part[4];
-              lds<16>(part, row + (((2 * t) ^ sw) << 4));
+              lds<16>(part, k_at, tr * (D / 2));
 #pragma unroll
               for (int i = 0; i < 4; ++i) w[half][i] = part[i];
-              lds<16>(part, row + (((2 * t + 1) ^ sw) << 4));
+              lds<16>(part, k_at ^ 16u, tr * (D / 2));  // the other piece of the pair
 #pragma unroll
               for (int i = 0; i < 4; ++i) w[half][KW - 4 + i] = part[i];
-#pragma unroll
-              for (int i = 0; i < 4; ++i) sc[half][i < (KW + 1) / 2 ? i : 0] = scale2(lds8(kss + tr * VB + t * 4 + i) * 0x00800080u);
+            } else {
+              lds<D / 8>(w[half], k_at, tr * (D / 2));
             }
+#pragma unroll
+            for (int i = 0; i < (KW + 1) / 2; ++i) sc[half][i] = scale2(lds8(ks_at, tr * VB + i) * 0x00800080u);
           }
 #pragma unroll
           for (int n = 0; n < NT; ++n)
@@ -368,8 +393,8 @@ __global__ void __launch_bounds__(Q4Cfg<D, NT>::kWarps * 32, 1) decode_q4_kernel
           for (int i = 0; i < KW; ++i) {
             const Scale2 &a0 = sc[0][i / 2], &a1 = sc[1][i / 2];
             const uint32_t u0 = w[0][i] >> 8, u1 = w[1][i] >> 8;
-            const uint32_t even[4] = {low2(w[0][i], a0), low2(w[1][i], a1), low2(u0, a0), low2(u1, a1)};
-            const uint32_t odd[4] = {high2(w[0][i], a0), high2(w[1][i], a1), high2(u0, a0), high2(u1, a1)};
+            const uint32_t even[4] = {low2(w[0][i], k1024, a0), low2(w[1][i], k1024, a1), low2(u0, k1024, a0), low2(u1, k1024, a1)};
+            const uint32_t odd[4] = {high2(w[0][i], k1024, a0), high2(w[1][i], k1024, a1), high2(u0, k1024, a0), high2(u1, k1024, a1)};
 #pragma unroll
             for (int n = 0; n < NT; ++n) {
               mma_f16(s[n][mt], even, qf[n][2 * i][0], qf[n][2 * i][1]);
@@ -379,6 +404,7 @@ __global__ void __launch_bounds__(Q4Cfg<D, NT>::kWarps * 32, 1) decode_q4_kernel
         }
         // lane: tokens token_of(g) and 8 more of each 16, heads 2 t and 2 t + 1 of each 8
         if (mask != 0xFFFFFFFFu) {
+          asm volatile("" ::: "memory");  // a branch, not selects
 #pragma unroll
           for (int n = 0; n < NT; ++n)
 #pragma unroll
@@ -443,37 +469,26 @@ __global__ void __launch_bounds__(Q4Cfg<D, NT>::kWarps * 32, 1) decode_q4_kernel
         for (int mt = 0; mt < MT; ++mt) {
           // tokens 2 t and 2 t + 1 of the product's 8, and 8 on
           uint32_t w[4][VW];
-          Scale2 sc[2][D == 256 ? 2 : 1];
-          const int tok = mt * 16 + token_of(2 * t), tok1 = mt * 16 + token_of(2 * t + 1);
-#pragma unroll
-          for (int i = 0; i < 4; ++i) {
-            const int tr = (i & 1 ? tok1 : tok) + (i >> 1) * 8;
-            const uint32_t row = vs + tr * (D / 2);
-            if constexpr (D == 64) lds<4>(w[i], row + g * 4);
-            if constexpr (D == 128) lds<8>(w[i], row + (((g >> 1) ^ swizzle<D>(tr)) << 4) + (g & 1) * 8);
-            if constexpr (D == 256) lds<16>(w[i], row + ((g ^ swizzle<D>(tr)) << 4));
-          }
+          Scale2 sc[2][(VW + 1) / 2];
 #pragma unroll
           for (int half = 0; half < 2; ++half) {
-            const uint32_t s0 = vss + (tok + 8 * half) * VB, s1 = vss + (tok1 + 8 * half) * VB;
-            if constexpr (D == 256) {
-              sc[half][0] = scale2((lds8(s0 + 2 * g) + lds8(s1 + 2 * g) * 0x10000u) * 0x80u);
-              sc[half][D == 256 ? 1 : 0] = scale2((lds8(s0 + 2 * g + 1) + lds8(s1 + 2 * g + 1) * 0x10000u) * 0x80u);
-            } else {
-              const int at = D == 64 ? g >> 1 : g;
-              sc[half][0] = scale2((lds8(s0 + at) + lds8(s1 + at) * 0x10000u) * 0x80u);
-            }
+            const int tr = mt * 16 + half * 8;
+            lds<VB>(w[2 * half], v_at[0], tr * (D / 2));
+            lds<VB>(w[2 * half + 1], v_at[1], tr * (D / 2));
+#pragma unroll
+            for (int i = 0; i < (VW + 1) / 2; ++i)
+              sc[half][i] = scale2((lds8(vs_at[0], tr * VB + i) + lds8(vs_at[1], tr * VB + i) * 0x10000u) * 0x80u);
           }
 #pragma unroll
           for (int i = 0; i < VW; ++i) {
-            const Scale2 &a0 = sc[0][D == 256 ? i / 2 : 0], &a1 = sc[1][D == 256 ? i / 2 : 0];
+            const Scale2 &a0 = sc[0][i / 2], &a1 = sc[1][i / 2];
 #pragma unroll
             for (int hw = 0; hw < 2; ++hw) {  // channels 0 to 3, 4 to 7 of the word
               const uint32_t x0 = __byte_perm(w[0][i], w[1][i], hw ? 0x7632 : 0x5410);
               const uint32_t x1 = __byte_perm(w[2][i], w[3][i], hw ? 0x7632 : 0x5410);
               const uint32_t u0 = x0 >> 8, u1 = x1 >> 8;
-              const uint32_t even[4] = {low2(x0, a0), low2(u0, a0), low2(x1, a1), low2(u1, a1)};
-              const uint32_t odd[4] = {high2(x0, a0), high2(u0, a0), high2(x1, a1), high2(u1, a1)};
+              const uint32_t even[4] = {low2(x0, k1024, a0), low2(u0, k1024, a0), low2(x1, k1024, a1), low2(u1, k1024, a1)};
+              const uint32_t odd[4] = {high2(x0, k1024, a0), high2(u0, k1024, a0), high2(x1, k1024, a1), high2(u1, k1024, a1)};
 #pragma unroll
               for (int n = 0; n < NT; ++n) {
                 mma_f16(o[n][4 * i + 2 * hw], even, pf[n][mt][0], pf[n][mt][1]);
