@@ -55,6 +55,11 @@ __device__ __forceinline__ void lds(uint32_t (&w)[BYTES / 4], uint32_t addr, int
                  : "r"(addr + off)
                  : "memory");
 }
+__device__ __forceinline__ uint32_t lds16(uint32_t addr, int off) {
+  uint32_t v;
+  asm volatile("ld.shared.u16 %0, [%1];" : "=r"(v) : "r"(addr + off) : "memory");
+  return v;
+}
 __device__ __forceinline__ uint32_t lds8(uint32_t addr, int off) {
   uint32_t v;
   asm volatile("ld.shared.u8 %0, [%1];" : "=r"(v) : "r"(addr + off) : "memory");
@@ -81,6 +86,14 @@ __device__ __forceinline__ void mma_f16(float (&c)[4], const uint32_t (&a)[4], u
       : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
       : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
 }
+// The same with zero for c.
+__device__ __forceinline__ void mma_f16_first(float (&c)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
+  asm volatile(
+      "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, "
+      "{%10, %10, %10, %10};"
+      : "=f"(c[0]), "=f"(c[1]), "=f"(c[2]), "=f"(c[3])
+      : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1), "f"(0.0f));
+}
 // Two scales, one in each half: s' = s / 128 and what it takes from 1024 + c and from 1024 + 16 c.
 struct Scale2 {
   uint32_t m, c0, c1;
@@ -88,6 +101,16 @@ struct Scale2 {
 __device__ __forceinline__ Scale2 scale2(uint32_t shifted) {  // bytes moved up by 7
   return {hmul2(shifted, 0x20002000u), hmul2(shifted, 0xC808C808u), hmul2(shifted, 0xC880C880u)};  // 2^-7, -1032 2^-7, -1152 2^-7
 }
+// One of the two scales for both halves (an operand modifier, no instruction).
+__device__ __forceinline__ uint32_t both(uint32_t x, int which) {
+  uint32_t d;
+  if (which == 0)
+    asm("{.reg .b16 l, h; mov.b32 {l, h}, %1; mov.b32 %0, {l, l};}" : "=r"(d) : "r"(x));
+  else
+    asm("{.reg .b16 l, h; mov.b32 {l, h}, %1; mov.b32 %0, {h, h};}" : "=r"(d) : "r"(x));
+  return d;
+}
+__device__ __forceinline__ Scale2 both(const Scale2& s, int which) { return {both(s.m, which), both(s.c0, which), both(s.c1, which)}; }
 // Nibbles 0 and 4 of x (counted in 4 bits), and nibbles 1 and 5 sixteen times larger.
 // k1024 is 0x64006400 in a register that the compiler neither sees through nor takes for the same in all lanes: mask and
 // or are one instruction then, where two constants, or a constant and a uniform register, make two (240 instead of 128 of a
@@ -367,7 +390,7 @@ __global__ void __launch_bounds__(Q4Cfg<D, NT>::kWarps * 32, 1) decode_q4_kernel
 #pragma unroll
         for (int mt = 0; mt < MT; ++mt) {
           uint32_t w[2][KW];
-          Scale2 sc[2][(KW + 1) / 2];
+          Scale2 sc[2][(KW + 3) / 4];  // of two blocks each, but for D 64 with one
 #pragma unroll
           for (int half = 0; half < 2; ++half) {  // rows g and g + 8 of the product, tokens 8 apart
             const int tr = mt * 16 + half * 8;
@@ -382,22 +405,26 @@ __global__ void __launch_bounds__(Q4Cfg<D, NT>::kWarps * 32, 1) decode_q4_kernel
             } else {
               lds<D / 8>(w[half], k_at, tr * (D / 2));
             }
+            if constexpr (D == 64) {
+              sc[half][0] = scale2(lds8(ks_at, tr * VB) * 0x00800080u);
+            } else {
 #pragma unroll
-            for (int i = 0; i < (KW + 1) / 2; ++i) sc[half][i] = scale2(lds8(ks_at, tr * VB + i) * 0x00800080u);
+              for (int i = 0; i < KW / 4; ++i)
+                sc[half][i] = scale2(__byte_perm(lds16(ks_at, tr * VB + 2 * i), 0u, 0x4140) * 0x80u);
+            }
           }
 #pragma unroll
-          for (int n = 0; n < NT; ++n)
-#pragma unroll
-            for (int e = 0; e < 4; ++e) s[n][mt][e] = 0.0f;
-#pragma unroll
           for (int i = 0; i < KW; ++i) {
-            const Scale2 &a0 = sc[0][i / 2], &a1 = sc[1][i / 2];
+            const Scale2 a0 = D == 64 ? sc[0][0] : both(sc[0][i / 4], i / 2 % 2), a1 = D == 64 ? sc[1][0] : both(sc[1][i / 4], i / 2 % 2);
             const uint32_t u0 = w[0][i] >> 8, u1 = w[1][i] >> 8;
             const uint32_t even[4] = {low2(w[0][i], k1024, a0), low2(w[1][i], k1024, a1), low2(u0, k1024, a0), low2(u1, k1024, a1)};
             const uint32_t odd[4] = {high2(w[0][i], k1024, a0), high2(w[1][i], k1024, a1), high2(u0, k1024, a0), high2(u1, k1024, a1)};
 #pragma unroll
             for (int n = 0; n < NT; ++n) {
-              mma_f16(s[n][mt], even, qf[n][2 * i][0], qf[n][2 * i][1]);
+              if (i == 0)
+                mma_f16_first(s[n][mt], even, qf[n][0][0], qf[n][0][1]);
+              else
+                mma_f16(s[n][mt], even, qf[n][2 * i][0], qf[n][2 * i][1]);
               mma_f16(s[n][mt], odd, qf[n][2 * i + 1][0], qf[n][2 * i + 1][1]);
             }
           }
