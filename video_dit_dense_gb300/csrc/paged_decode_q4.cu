@@ -55,6 +55,9 @@ __device__ __forceinline__ void lds(uint32_t (&w)[BYTES / 4], uint32_t addr, int
                  : "r"(addr + off)
                  : "memory");
 }
+__device__ __forceinline__ void sts16(uint32_t addr, const uint32_t (&w)[4]) {
+  asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(addr), "r"(w[0]), "r"(w[1]), "r"(w[2]), "r"(w[3]) : "memory");
+}
 __device__ __forceinline__ uint32_t lds16(uint32_t addr, int off) {
   uint32_t v;
   asm volatile("ld.shared.u16 %0, [%1];" : "=r"(v) : "r"(addr + off) : "memory");
@@ -131,10 +134,13 @@ struct Q4Cfg {
   static constexpr int kCodes = kTile * D / 2, kScales = kTile * D / 16;  // bytes of K, and the same of V
   static constexpr int kStage = 2 * (kCodes + kScales);
   static constexpr int kRing = kWarps * kStages * kStage;
-  // joining the warps of a unit head: accumulators, max and sum of every second warp, 8 heads at a time
+  // the queries of each warp's sequence, in registers' order; once its tiles are walked, in the same place the joining of
+  // the warps of a unit head: accumulators, max and sum of every second warp, 8 heads at a time
+  static constexpr int kQueries = NT * D * 16;  // of a warp
   static constexpr int kJoin = kWarps / 2 * 8 * D * 4;
   static constexpr int kStats = kWarps / 2 * 8 * 2 * 4;
-  static constexpr int kSmem = kRing + kJoin + kStats + 2 * kMaxSplitBatch * 4;
+  static constexpr int kShared = kWarps * kQueries > kJoin + kStats ? kWarps * kQueries : kJoin + kStats;
+  static constexpr int kSmem = kRing + kShared + 2 * kMaxSplitBatch * 4;
   static constexpr int kHeads = NT * 8;
   static_assert(kSmem <= 232448, "shared memory of one CTA");
 };
@@ -164,7 +170,7 @@ __global__ void __launch_bounds__(Q4Cfg<D, NT>::kWarps * 32, 1) decode_q4_kernel
   extern __shared__ __align__(128) uint8_t smem[];
   float* join = reinterpret_cast<float*>(smem + C::kRing);
   float* stats = reinterpret_cast<float*>(smem + C::kRing + C::kJoin);
-  int* end = reinterpret_cast<int*>(smem + C::kRing + C::kJoin + C::kStats);
+  int* end = reinterpret_cast<int*>(smem + C::kRing + C::kShared);
   int* lens = end + kMaxSplitBatch;  // without a split: of the one sequence
   // lengths and page table: brought back to L2 while the kernel before this one drains
   if (threadIdx.x * 32 < static_cast<unsigned>(a.B)) prefetch_l2(a.kv_len + threadIdx.x * 32);
@@ -301,10 +307,11 @@ __global__ void __launch_bounds__(Q4Cfg<D, NT>::kWarps * 32, 1) decode_q4_kernel
 #pragma unroll
   for (int i = 0; i < STAGES - 1; ++i) load(i, mask_of[i]);
 
-  // The queries of a sequence as the second operand of the score product, each row scaled so that its largest channel
+  // The queries of a sequence as the second operand of the score product, in shared memory, each row scaled so that its largest channel
   // lies in [2^9, 2^10), and for the lane's columns what makes exponents of two of their scores.
   const int g = lane >> 2, t = lane & 3;
-  auto load_q = [&](int b, uint32_t (&qf)[NT][D / 16][2], float (&to_log2)[NT][2]) {
+  const uint32_t q_at = smem_u32(smem) + C::kRing + warp * C::kQueries + lane * 16;
+  auto load_q = [&](int b, float (&to_log2)[NT][2]) {
 #pragma unroll
     for (int n = 0; n < NT; ++n) {
       const bool there = n * 8 + g < heads;
@@ -324,10 +331,11 @@ __global__ void __launch_bounds__(Q4Cfg<D, NT>::kWarps * 32, 1) decode_q4_kernel
       const float f = __uint_as_float(static_cast<uint32_t>(up) << 23), f16th = f * 0.0625f;
 #pragma unroll
       for (int i = 0; i < KW; ++i) {  // channels 0 and 4, 2 and 6; 1 and 5, 3 and 7
-        qf[n][2 * i][0] = pack_f16(__uint_as_float(x[i].x << 16) * f, __uint_as_float(x[i].z << 16) * f);
-        qf[n][2 * i][1] = pack_f16(__uint_as_float(x[i].y << 16) * f, __uint_as_float(x[i].w << 16) * f);
-        qf[n][2 * i + 1][0] = pack_f16(__uint_as_float(x[i].x & 0xFFFF0000u) * f16th, __uint_as_float(x[i].z & 0xFFFF0000u) * f16th);
-        qf[n][2 * i + 1][1] = pack_f16(__uint_as_float(x[i].y & 0xFFFF0000u) * f16th, __uint_as_float(x[i].w & 0xFFFF0000u) * f16th);
+        const uint32_t w[4] = {pack_f16(__uint_as_float(x[i].x << 16) * f, __uint_as_float(x[i].z << 16) * f),
+                               pack_f16(__uint_as_float(x[i].y << 16) * f, __uint_as_float(x[i].w << 16) * f),
+                               pack_f16(__uint_as_float(x[i].x & 0xFFFF0000u) * f16th, __uint_as_float(x[i].z & 0xFFFF0000u) * f16th),
+                               pack_f16(__uint_as_float(x[i].y & 0xFFFF0000u) * f16th, __uint_as_float(x[i].w & 0xFFFF0000u) * f16th)};
+        sts16(q_at + (n * KW + i) * 512, w);
       }
       // 128 / f; normal, so that -infinity times it is not a NaN, nor 0 times it
       const float back = fminf(fmaxf(a.scale_log2 * __uint_as_float(static_cast<uint32_t>(261 - up) << 23), FLT_MIN), FLT_MAX);
@@ -360,9 +368,9 @@ __global__ void __launch_bounds__(Q4Cfg<D, NT>::kWarps * 32, 1) decode_q4_kernel
     const int s0 = first_tile(b), s1 = stop_tile(b);
     if (s0 < s1 || p.ranges == 0) {
       // ---- one sequence's tiles [s0, s1) ----
-      uint32_t qf[NT][D / 16][2];
       float to_log2[NT][2];
-      load_q(b, qf, to_log2);
+      load_q(b, to_log2);
+      __syncwarp();
       float o[NT][D / 16][4];
       // m: what the exponents are taken against, within 8 of the running maximum; l: the lane's part of the sum
       float m[NT][2], l[NT][2];
@@ -421,11 +429,13 @@ __global__ void __launch_bounds__(Q4Cfg<D, NT>::kWarps * 32, 1) decode_q4_kernel
             const uint32_t odd[4] = {high2(w[0][i], k1024, a0), high2(w[1][i], k1024, a1), high2(u0, k1024, a0), high2(u1, k1024, a1)};
 #pragma unroll
             for (int n = 0; n < NT; ++n) {
+              uint32_t q[4];
+              lds<16>(q, q_at, (n * KW + i) * 512);
               if (i == 0)
-                mma_f16_first(s[n][mt], even, qf[n][0][0], qf[n][0][1]);
+                mma_f16_first(s[n][mt], even, q[0], q[1]);
               else
-                mma_f16(s[n][mt], even, qf[n][2 * i][0], qf[n][2 * i][1]);
-              mma_f16(s[n][mt], odd, qf[n][2 * i + 1][0], qf[n][2 * i + 1][1]);
+                mma_f16(s[n][mt], even, q[0], q[1]);
+              mma_f16(s[n][mt], odd, q[2], q[3]);
             }
           }
         }
@@ -618,6 +628,7 @@ __global__ void __launch_bounds__(Q4Cfg<D, NT>::kWarps * 32, 1) decode_q4_kernel
           }
       }
       first_segment = false;
+      if (p.WT > 1) __syncthreads();  // the joins' buffers are read; the next sequence's queries go there
     }
     if (p.ranges == 0 || seq_end(b) >= t1) break;
     ++b;
