@@ -91,6 +91,22 @@ template <int THREADS>
 __device__ __forceinline__ Ranges scan_tiles(const DecodeArgs& a, const DecodePlan& p, int tile, int* end, int* len) {
   __shared__ int2 warp_sum[THREADS / 32];  // tiles, sequences with a tile
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  if (a.B <= 32) {  // every warp for itself, without a barrier: all write the same
+    const int tokens = lane < a.B ? len_of(a, lane) : 0;
+    int n = tokens > 0 ? (tokens + tile - 1) / tile + p.start : 0;
+    const int sequences = __popc(__ballot_sync(0xFFFFFFFFu, n > 0));
+#pragma unroll
+    for (int off = 1; off < 32; off <<= 1) {
+      const int m = __shfl_up_sync(0xFFFFFFFFu, n, off);
+      if (lane >= off) n += m;
+    }
+    if (lane < a.B) {
+      end[lane] = n;
+      if (len) len[lane] = tokens;
+    }
+    __syncwarp();
+    return cut(p, __shfl_sync(0xFFFFFFFFu, n, 31), sequences);
+  }
   int carry = 0, sequences = 0;
   for (int b0 = 0; b0 < a.B; b0 += THREADS) {
     const int b = b0 + static_cast<int>(threadIdx.x);

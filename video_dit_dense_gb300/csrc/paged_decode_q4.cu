@@ -126,11 +126,11 @@ __device__ __forceinline__ uint32_t high2(uint32_t x, uint32_t k1024, const Scal
 }
 
 // NT: tiles of 8 query heads (1 or 2).
-template <int D, int NT>
+template <int D, int NT, int WARPS>
 struct Q4Cfg {
   static constexpr int kTile = 32;  // tokens a warp takes at a time, one a lane where pages are looked up
-  static constexpr int kWarps = D * NT <= 128 ? 16 : 8;
-  static constexpr int kStages = 2;
+  static constexpr int kWarps = WARPS;
+  static constexpr int kStages = WARPS == 8 && D * NT <= 128 ? 4 : 2;
   static constexpr int kCodes = kTile * D / 2, kScales = kTile * D / 16;  // bytes of K, and the same of V
   static constexpr int kStage = 2 * (kCodes + kScales);
   static constexpr int kRing = kWarps * kStages * kStage;
@@ -157,9 +157,9 @@ __device__ __forceinline__ uint32_t swizzle(int tr) {
 __device__ __forceinline__ int token_of(int r) { return r ^ (r >> 2 & 1); }
 
 // W: the scores are kept for the tokens' weights.
-template <int D, int NT, bool W>
-__global__ void __launch_bounds__(Q4Cfg<D, NT>::kWarps * 32, 1) decode_q4_kernel(const __grid_constant__ Kernelargs k) {
-  using C = Q4Cfg<D, NT>;
+template <int D, int NT, int WARPS, bool W>
+__global__ void __launch_bounds__(WARPS * 32, 1) decode_q4_kernel(const __grid_constant__ Kernelargs k) {
+  using C = Q4Cfg<D, NT, WARPS>;
   constexpr int TILE = C::kTile, MT = TILE / 16, STAGES = C::kStages;
   constexpr int CH = D / 32;          // 16-byte pieces of a row's codes
   constexpr int KW = D / 32;          // words of a K row that a lane takes (8 channels each)
@@ -636,24 +636,32 @@ __global__ void __launch_bounds__(Q4Cfg<D, NT>::kWarps * 32, 1) decode_q4_kernel
   cp_async_wait<0>();
 }
 
-int warps_of(const DecodeArgs& a) { return a.D * (a.Hq / a.Hkv > 8 ? 2 : 1) <= 128 ? 16 : 8; }
-DecodePlan plan_of(const DecodeArgs& a, int sms, bool split) { return make_plan(a, sms, split, warps_of(a), 32, 1); }
+// Warps of a CTA.  Heads of 128 and two column tiles, or of 256, leave registers for 8.  Otherwise 16 where each has many
+// tiles (one sequence of 104448 tokens, 24 heads of 128: 75 us, with 8 warps 83), and 8 where they have few, whose registers leave room
+// for the joining kernel beside them (16 sequences of up to 8192, 16 and 4 heads: 23 and 21).
+int warps_of(const DecodeArgs& a, int sms) {
+  if (a.D * (a.Hq / a.Hkv > 8 ? 2 : 1) > 128) return 8;
+  const int64_t capacity = static_cast<int64_t>(a.max_pages) * a.page_size;
+  const int64_t units = static_cast<int64_t>(a.Hkv) * ((a.Hq / a.Hkv + 15) / 16);
+  return (capacity + 31) / 32 * a.B * units >= 160LL * sms ? 16 : 8;
+}
+DecodePlan plan_of(const DecodeArgs& a, int sms, bool split) { return make_plan(a, sms, split, warps_of(a, sms), 32, 1); }
 
-template <int D, int NT, bool W>
+template <int D, int NT, int WARPS, bool W>
 cudaError_t launch_d(const Kernelargs& k, cudaStream_t stream) {
-  using C = Q4Cfg<D, NT>;
+  using C = Q4Cfg<D, NT, WARPS>;
   static std::atomic<bool> attr_set[64];  // calls of several host threads
   int dev = 0;
   cudaError_t e = cudaGetDevice(&dev);
   if (e != cudaSuccess) return e;
   if (dev < 0 || dev >= 64) return cudaErrorInvalidDevice;
   if (!attr_set[dev]) {
-    e = cudaFuncSetAttribute(decode_q4_kernel<D, NT, W>, cudaFuncAttributeMaxDynamicSharedMemorySize, C::kSmem);
+    e = cudaFuncSetAttribute(decode_q4_kernel<D, NT, WARPS, W>, cudaFuncAttributeMaxDynamicSharedMemorySize, C::kSmem);
     if (e != cudaSuccess) return e;
     attr_set[dev] = true;
   }
   const int64_t ranges = k.p.ranges > 0 ? k.p.ranges : k.a.B;
-  e = launch_dependent(decode_q4_kernel<D, NT, W>, dim3(static_cast<unsigned>(ranges * k.p.groups)), C::kWarps * 32, C::kSmem,
+  e = launch_dependent(decode_q4_kernel<D, NT, WARPS, W>, dim3(static_cast<unsigned>(ranges * k.p.groups)), WARPS * 32, C::kSmem,
                        stream, k);
   if (e != cudaSuccess || k.p.ranges == 0) return e;
   const int G = k.a.Hq / k.a.Hkv;
@@ -661,10 +669,16 @@ cudaError_t launch_d(const Kernelargs& k, cudaStream_t stream) {
                           std::min(G, C::kHeads));
 }
 
+template <int D, int NT>
+cudaError_t launch_warps(const Kernelargs& k, cudaStream_t stream) {
+  if constexpr (D * NT <= 128)
+    if (k.p.WH * k.p.WT == 16) return k.a.scores ? launch_d<D, NT, 16, true>(k, stream) : launch_d<D, NT, 16, false>(k, stream);
+  return k.a.scores ? launch_d<D, NT, 8, true>(k, stream) : launch_d<D, NT, 8, false>(k, stream);
+}
+
 template <int D>
 cudaError_t launch_heads(const Kernelargs& k, cudaStream_t stream) {
-  if (k.a.Hq / k.a.Hkv > 8) return k.a.scores ? launch_d<D, 2, true>(k, stream) : launch_d<D, 2, false>(k, stream);
-  return k.a.scores ? launch_d<D, 1, true>(k, stream) : launch_d<D, 1, false>(k, stream);
+  return k.a.Hq / k.a.Hkv > 8 ? launch_warps<D, 2>(k, stream) : launch_warps<D, 1>(k, stream);
 }
 
 }  // namespace
