@@ -22,26 +22,34 @@ __device__ __forceinline__ uint32_t abs_max8(const uint32_t* n) {
   const uint32_t m = __vmaxu2(__vmaxu2(n[0] & kAbs, n[1] & kAbs), __vmaxu2(n[2] & kAbs, n[3] & kAbs));
   return max(m & 0xFFFFu, m >> 16);
 }
-// The scale of a group whose largest value has these bits: max / 7 rounded to 5 exponent and 3 mantissa bits.
+// The scale of a group whose largest value has these bits: max / 7 rounded to 5 exponent and 3 mantissa bits.  A quotient
+// of an 8-bit significand and 7 lies half way between two such numbers or at least 2^-8 of itself away, so the product with
+// 1 / 7, a few steps of float32 off, is put back on the halves by rounding it to 8 steps.
 __device__ __forceinline__ uint32_t scale_of(uint32_t top) {
   if (top >= 0x7F80u) return 0xFFu;
-  const float t = fminf(__fdiv_rn(__uint_as_float(top << 16), 7.0f), 3840.0f);
-  if (t < 0x1p-14f) return static_cast<uint32_t>(__float2int_rn(t * 0x1p17f));
-  const uint32_t u = __float_as_uint(t);
+  const float t = fminf(__uint_as_float(top << 16) * (1.0f / 7.0f), 3840.0f);
+  const uint32_t u = (__float_as_uint(t) + 4u) & ~7u;
+  if (u < 0x38800000u) return static_cast<uint32_t>(__float2int_rn(__uint_as_float(u) * 0x1p17f));  // below 2^-14
   return ((u + 0x7FFFFu + ((u >> 20) & 1u)) >> 20) - (112u << 3);
 }
 // The codes of 8 values.  |x| / s is a quotient of an 8-bit and a 4-bit significand, so it either lies half way between
 // two integers or is at least 2^-9 of itself away from there: taken 2^-13 too large, which is more than its float32 error,
-// halves are rounded away from zero and nothing else is.
+// halves are rounded away from zero and nothing else is.  The rounding is the addition of 1.5 * 2^23, whose bits are taken
+// off the packed codes at the end.  Between the least normal and the largest scale |x| / s is below 7.5.
 __device__ __forceinline__ uint32_t codes_of(const uint32_t* n, uint32_t scale) {
   if (scale == 0u || scale == 0xFFu) return 0x88888888u;
-  const float inv = __fdiv_rn(1.0f + 0x1p-13f, scale_value(scale));
+  const float s = scale < 8u ? static_cast<float>(scale) * 0x1p-17f : __uint_as_float((scale + (112u << 3)) << 20);
+  const float inv = __fdividef(1.0f + 0x1p-13f, s);
+  constexpr float kRound = 12582912.0f + 8.0f;  // and the codes' 8
+  constexpr uint32_t kBits = 0x4B400000u;       // of 12582912
+  const bool cut = scale < 8u || scale == kScaleMax;
   uint32_t codes = 0;
 #pragma unroll
-  for (int e = 0; e < 8; ++e) {
+  for (int e = 7; e >= 0; --e) {
     const float x = __uint_as_float(e & 1 ? n[e >> 1] & 0xFFFF0000u : n[e >> 1] << 16);
-    const int k = static_cast<int>(fminf(fmaf(fabsf(x), inv, 0.5f), 8.5f));
-    codes |= static_cast<uint32_t>(x < 0.0f ? 8 - k : min(8 + k, 15)) << (4 * e);
+    float t = fmaf(x, inv, kRound);
+    if (cut) t = fminf(fmaxf(x * inv, -8.0f), 7.0f) + kRound;
+    codes = codes * 16u + (__float_as_uint(t) - kBits);
   }
   return codes;
 }

@@ -12,7 +12,7 @@
 namespace h3 {
 namespace {
 
-constexpr int kThreads = 128, kTokens = 4;  // a thread's
+constexpr int kThreads = 256, kTokens = 1;  // a thread's
 
 __global__ void __launch_bounds__(kThreads) add_weights_kernel(const __grid_constant__ DecodeArgs a, float* weights) {
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
@@ -25,7 +25,7 @@ __global__ void __launch_bounds__(kThreads) add_weights_kernel(const __grid_cons
     const float* score = a.scores + static_cast<int64_t>(b) * a.Hq * a.score_stride + j0;
     const float2* stats = a.stats + static_cast<int64_t>(b) * a.Hq;
     float sum[kTokens] = {};
-#pragma unroll 4
+#pragma unroll 8
     for (int h = 0; h < a.Hq; ++h) {
       const float2 ml = stats[h];
 #pragma unroll

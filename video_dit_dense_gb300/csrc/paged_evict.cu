@@ -5,18 +5,21 @@
 //   the recent ones to front, front + 1, ... in their order.
 // Few rows move where few tokens are evicted: movers and gaps are at most n - keep.
 //
-// First kernel, a cluster of 1 to 8 CTAs a sequence by the cache's room: the
-// weight T of the front-th heaviest old token by three counting passes over 11, 11
-// and 10 bits of the weights' order (each CTA counts its part of the tokens, the counts
-// are added up across the cluster), then kept = above T, or equal to it and among
-// the first ones; each warp owns a contiguous part of the tokens, so that a
-// ballot numbers movers and gaps.  It writes their lists, and moves the weights.
+// First kernel, a cluster of 1 to 8 CTAs a sequence by the cache's room: each CTA
+// holds its part of the weights in shared memory, as integers in their order.  The
+// weight T of the front-th heaviest old token comes from three counting passes over
+// 11, 11 and 10 bits of that order (the CTAs' counts are added up across the cluster), then
+// kept = above T, or equal to it and among the first ones.  Each warp owns a
+// contiguous part of the tokens, so that a ballot numbers movers and gaps.  It writes
+// their lists, moves the weights, and looks up the rows that the places are.
+// Weights read again from memory in each pass, a load at a time, took 64 us of one
+// sequence of 104448 tokens.
 //
-// Second kernel: moves the rows.  A CTA owns a column of pieces of all rows of one
-// sequence, so that the order in which rows are read and written is its own: movers
-// from below `keep`, then the recent rows in tiles from the first on (a row moves
-// down, so what a tile overwrites has been read).  Movers from beyond `keep` are not in the way
-// of anything and are dealt to further CTAs.
+// Second kernel: moves the rows.  Movers from beyond `keep` are not in the way of
+// anything: a warp takes a row.  What else moves into [front, keep) or out of it is in order:
+// a CTA owns a column of pieces of all rows of one sequence, and moves first the movers from
+// below `keep`, then the recent rows in tiles from the first on (a row moves
+// down, so what a tile overwrites has been read).
 #include <algorithm>
 
 #include "decode_common.cuh"
@@ -24,8 +27,9 @@
 namespace h3 {
 namespace {
 
-constexpr int kSelectThreads = 512, kSelectWarps = kSelectThreads / 32;
+constexpr int kSelectThreads = 1024, kSelectWarps = kSelectThreads / 32;
 constexpr int kBins = 2048, kPasses = 3;
+constexpr int kMostHeld = 200 * 1024 / 4;  // weights in a CTA's shared memory
 
 __device__ __forceinline__ uint32_t cluster_rank() {
   uint32_t r;
@@ -48,40 +52,67 @@ __device__ __forceinline__ uint32_t order_of(float w) {
   return w != w ? 0xFFFFFFFFu : u & 0x80000000u ? ~u : u | 0x80000000u;
 }
 
-// Sum of `mine` over the threads before this one in the cluster (CTAs in their order), and over all of them.
+// Sums of the warps' x, y and z (the same in a warp's lanes): of x and y over the warps before this one in the cluster
+// (CTAs in their order), and of all three over all.
 struct Scan {
-  uint32_t before, all;
+  uint32_t x, y, all_x, all_z;
 };
-__device__ __forceinline__ Scan cluster_scan(uint32_t mine, uint32_t ctas, uint32_t rank, uint32_t (&warp_sum)[kSelectWarps + 1]) {
+__device__ __forceinline__ Scan cluster_scan(uint32_t x, uint32_t y, uint32_t z, uint32_t ctas, uint32_t rank,
+                                             uint32_t (&sums)[3][kSelectWarps + 1]) {
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  uint32_t n = mine;
-#pragma unroll
-  for (int off = 1; off < 32; off <<= 1) {
-    const uint32_t m = __shfl_up_sync(0xFFFFFFFFu, n, off);
-    if (lane >= off) n += m;
-  }
-  if (lane == 31) warp_sum[warp] = n;
+  static_assert(kSelectWarps == 32, "a lane for each warp");
+  if (lane < 3) sums[lane][warp] = lane == 0 ? x : lane == 1 ? y : z;
   __syncthreads();
-  if (threadIdx.x == 0) {
-    uint32_t sum = 0;
-    for (int w = 0; w < kSelectWarps; ++w) sum += warp_sum[w];
-    warp_sum[kSelectWarps] = sum;
+  // every warp adds up all of them
+  uint32_t before[3], all[3];
+#pragma unroll
+  for (int i = 0; i < 3; ++i) {
+    const uint32_t of = sums[i][lane];
+    before[i] = __reduce_add_sync(0xFFFFFFFFu, lane < warp ? of : 0u);
+    all[i] = __reduce_add_sync(0xFFFFFFFFu, of);
+    if (threadIdx.x == 0) sums[i][kSelectWarps] = all[i];
   }
-  cluster_sync();
-  Scan s{n - mine, 0};
-  for (int w = 0; w < warp; ++w) s.before += warp_sum[w];
-  for (uint32_t r = 0; r < ctas; ++r) {
-    const uint32_t of = peer_load(&warp_sum[kSelectWarps], r);
-    if (r < rank) s.before += of;
-    s.all += of;
+  Scan s{before[0], before[1], all[0], all[2]};
+  if (ctas > 1) {
+    cluster_sync();
+    uint32_t theirs[3] = {0, 0, 0};
+    if (lane < static_cast<int>(ctas)) {
+#pragma unroll
+      for (int i = 0; i < 3; ++i) theirs[i] = peer_load(&sums[i][kSelectWarps], lane);
+    }
+    const bool earlier = lane < static_cast<int>(rank);
+    s.x += __reduce_add_sync(0xFFFFFFFFu, earlier ? theirs[0] : 0u);
+    s.y += __reduce_add_sync(0xFFFFFFFFu, earlier ? theirs[1] : 0u);
+    s.all_x = __reduce_add_sync(0xFFFFFFFFu, theirs[0]);
+    s.all_z = __reduce_add_sync(0xFFFFFFFFu, theirs[2]);
   }
   return s;
 }
 
+// Tokens of a warp where a sequence has `old` to choose from: whole turns of 32.
+__host__ __device__ inline int64_t tokens_per_warp(int64_t old, uint32_t ctas) {
+  const int64_t warps = static_cast<int64_t>(ctas) * kSelectWarps;
+  return ((old + warps - 1) / warps + 31) / 32 * 32;
+}
+
+// The row of the cache that place j of a sequence is, or -1 (reported).
+__device__ __forceinline__ int row_of(const EvictArgs& a, const int32_t* table, int j) {
+  const uint32_t p = fdiv(static_cast<uint32_t>(j), a.div_page);
+  const int page = table[p];
+  if (page < 0 || page >= a.num_pages) {
+    atomicExch(a.status, static_cast<int>(H3ATTN_ERR_INVALID_ARG));
+    return -1;
+  }
+  return page * a.page_size + (j - static_cast<int>(p) * a.page_size);
+}
+
+// HELD: the weights' order is kept in shared memory; otherwise (more tokens than fit) it is read anew in each pass.
+template <bool HELD>
 __global__ void __launch_bounds__(kSelectThreads) evict_select_kernel(const __grid_constant__ EvictArgs a, uint32_t ctas) {
+  extern __shared__ uint32_t held[];
   __shared__ uint32_t hist[kPasses][kBins];
-  __shared__ uint32_t scan[3][kSelectWarps + 1];
-  __shared__ uint32_t found[kPasses][2];  // bin, and how many of its tokens are still wanted
+  __shared__ uint32_t sums[2][3][kSelectWarps + 1];
+  __shared__ uint32_t found[kPasses][3];  // bin, how many of its tokens are still wanted, how many it has
   __shared__ uint32_t above_of[kSelectWarps];
   const int b = blockIdx.x / ctas, warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const uint32_t rank = ctas > 1 ? cluster_rank() : 0;
@@ -90,39 +121,66 @@ __global__ void __launch_bounds__(kSelectThreads) evict_select_kernel(const __gr
   asm volatile("griddepcontrol.wait;" ::: "memory");
   const int n = static_cast<int>(min(static_cast<int64_t>(max(a.kv_len[b], 0)), a.capacity));
   int* const list = a.ws + static_cast<int64_t>(b) * (kEvictHeader + 2 * static_cast<int64_t>(a.most));
-  if (rank == 0 && threadIdx.x == 0) {
-    a.len_out[b] = min(n, a.keep);
-    list[0] = list[1] = 0;
-  }
+  if (rank == 0 && threadIdx.x == 0) a.len_out[b] = min(n, a.keep);
   if (n <= a.keep) return;  // the whole cluster
   float* const weights = a.weights + b * a.capacity;
+  const int32_t* const table = a.page_table + static_cast<int64_t>(b) * a.max_pages;
   const int old = n - a.recent, front = a.keep - a.recent;  // front < old
-  // this thread's tokens: a warp's are neighbours, 32 at a time
-  const int64_t warps = static_cast<int64_t>(ctas) * kSelectWarps, per_warp = ((old + warps - 1) / warps + 31) / 32 * 32;
-  const int64_t w0 = (rank * kSelectWarps + warp) * per_warp;
+  // this warp's tokens are neighbours, 32 a turn
+  const int64_t per_warp = tokens_per_warp(old, ctas), w0 = (rank * kSelectWarps + warp) * per_warp;
   const int begin = static_cast<int>(min(w0, static_cast<int64_t>(old)));
   const int end = static_cast<int>(min(w0 + per_warp, static_cast<int64_t>(old)));
+  uint32_t* const mine = held + warp * per_warp - begin;  // of token j: mine[j]
+  if constexpr (HELD) {
+    constexpr int U = 8;
+    for (int j0 = begin + lane; j0 < end; j0 += 32 * U) {
+      float w[U];
+#pragma unroll
+      for (int u = 0; u < U; ++u) w[u] = j0 + 32 * u < end ? weights[j0 + 32 * u] : 0.0f;
+#pragma unroll
+      for (int u = 0; u < U; ++u)
+        if (j0 + 32 * u < end) mine[j0 + 32 * u] = order_of(w[u]);
+    }
+    __syncwarp();
+  }
+  auto order = [&](int j) { return HELD ? mine[j] : order_of(weights[j]); };
   __syncthreads();
   // ---- the weight of the front-th heaviest ----
   uint32_t prefix = 0, want = static_cast<uint32_t>(front);  // of tokens whose order begins with prefix, so many are kept
+  bool all_ties = false;
   if (front > 0) {
 #pragma unroll 1
     for (int pass = 0; pass < kPasses; ++pass) {
       const int shift = pass == 0 ? 21 : pass == 1 ? 10 : 0, bits = pass == 2 ? 10 : 11;
       const uint32_t mask = pass == 0 ? 0u : pass == 1 ? 0xFFE00000u : 0xFFFFFC00u;
-      for (int j = begin + lane; j < end; j += 32) {
-        const uint32_t o = order_of(weights[j]);
-        if ((o & mask) == prefix) atomicAdd(&hist[pass][o >> shift & ((1u << bits) - 1u)], 1u);
+#pragma unroll 4
+      for (int j0 = begin; j0 < end; j0 += 32) {
+        const uint32_t o = j0 + lane < end ? order(j0 + lane) : 0u;
+        const bool counts = j0 + lane < end && (o & mask) == prefix;
+        if (!__any_sync(0xFFFFFFFFu, counts)) continue;
+        // lanes with the same bin add to it once
+        const uint32_t bin = counts ? o >> shift & ((1u << bits) - 1u) : 0xFFFFFFFFu;
+        const uint32_t same = __match_any_sync(0xFFFFFFFFu, bin);
+        if (counts && (same & ((1u << lane) - 1u)) == 0) atomicAdd(&hist[pass][bin], static_cast<uint32_t>(__popc(same)));
       }
-      cluster_sync();
-      // each thread adds up four bins over the cluster, from the last bin on
-      uint32_t mine[kBins / kSelectThreads], sum = 0;
+      if (ctas > 1)
+        cluster_sync();
+      else
+        __syncthreads();
+      // each thread adds up its bins over the cluster, from the last bin on
+      constexpr int kMine = kBins / kSelectThreads;
+      uint32_t of_bin[kMine], sum = 0;
 #pragma unroll
-      for (int i = 0; i < kBins / kSelectThreads; ++i) {
-        const int bin = kBins - 1 - (static_cast<int>(threadIdx.x) * (kBins / kSelectThreads) + i);
-        mine[i] = 0;
-        for (uint32_t r = 0; r < ctas; ++r) mine[i] += peer_load(&hist[pass][bin], r);
-        sum += mine[i];
+      for (int i = 0; i < kMine; ++i) {
+        const int bin = kBins - 1 - (static_cast<int>(threadIdx.x) * kMine + i);
+        of_bin[i] = hist[pass][bin];
+        if (ctas > 1) {
+          of_bin[i] = 0;
+#pragma unroll
+          for (uint32_t r = 0; r < 8; ++r)
+            if (r < ctas) of_bin[i] += peer_load(&hist[pass][bin], r);
+        }
+        sum += of_bin[i];
       }
       uint32_t above = sum;
 #pragma unroll
@@ -133,66 +191,78 @@ __global__ void __launch_bounds__(kSelectThreads) evict_select_kernel(const __gr
       if (lane == 31) above_of[warp] = above;
       __syncthreads();
       above -= sum;
-      for (int w = 0; w < warp; ++w) above += above_of[w];
+      above += __reduce_add_sync(0xFFFFFFFFu, lane < warp ? above_of[lane] : 0u);
 #pragma unroll
-      for (int i = 0; i < kBins / kSelectThreads; ++i) {
-        if (above < want && want <= above + mine[i]) {
-          found[pass][0] = kBins - 1 - (threadIdx.x * (kBins / kSelectThreads) + i);
+      for (int i = 0; i < kMine; ++i) {
+        if (above < want && want <= above + of_bin[i]) {
+          found[pass][0] = kBins - 1 - (threadIdx.x * kMine + i);
           found[pass][1] = want - above;
+          found[pass][2] = of_bin[i];
         }
-        above += mine[i];
+        above += of_bin[i];
       }
       __syncthreads();
       prefix |= found[pass][0] << shift;
       want = found[pass][1];
+      all_ties = want == found[pass][2];
     }
   } else {
     prefix = 0xFFFFFFFFu;  // none is kept
     want = 0;
   }
   // ---- which are kept: above the prefix, or equal and among the first `want` ----
-  uint32_t ties = 0;
-  for (int j = begin + lane; j < end; j += 32) ties += order_of(weights[j]) == prefix;
-  ties = __reduce_add_sync(0xFFFFFFFFu, ties);
-  const uint32_t ties_before = __shfl_sync(0xFFFFFFFFu, cluster_scan(lane == 0 ? ties : 0u, ctas, rank, scan[0]).before, 0);
+  uint32_t ties_before = 0;
+  if (front > 0 && !all_ties) {
+    uint32_t ties = 0;
+    for (int j = begin + lane; j < end; j += 32) ties += order(j) == prefix;
+    ties_before = cluster_scan(__reduce_add_sync(0xFFFFFFFFu, ties), 0, 0, ctas, rank, sums[0]).x;
+  }
   auto walk = [&](auto&& each) {
     uint32_t seen = ties_before;
+#pragma unroll 2
     for (int j0 = begin; j0 < end; j0 += 32) {
       const int j = j0 + lane;
-      const uint32_t o = j < end ? order_of(weights[j]) : 0u;
+      const uint32_t o = j < end ? order(j) : 0u;
       const bool tie = j < end && o == prefix;
-      const uint32_t tied = __ballot_sync(0xFFFFFFFFu, tie);
-      const bool kept = j < end && front > 0 && (o > prefix || (tie && seen + __popc(tied & ((1u << lane) - 1u)) < want));
+      const uint32_t tied = all_ties ? 0u : __ballot_sync(0xFFFFFFFFu, tie);
+      const bool kept =
+          j < end && front > 0 && (o > prefix || (tie && (all_ties || seen + __popc(tied & ((1u << lane) - 1u)) < want)));
       seen += __popc(tied);
       const uint32_t movers = __ballot_sync(0xFFFFFFFFu, kept && j >= front);
       const uint32_t gaps = __ballot_sync(0xFFFFFFFFu, j < end && !kept && j < front);
-      each(j, movers, gaps);
+      each(j0, movers, gaps);
     }
   };
-  uint32_t n_movers = 0, n_gaps = 0, n_below = 0;
-  walk([&](int j, uint32_t movers, uint32_t gaps) {
+  uint32_t n_movers = 0, n_gaps = 0, n_below = 0;  // below: from places below keep
+  walk([&](int j0, uint32_t movers, uint32_t gaps) {
     n_movers += __popc(movers);
     n_gaps += __popc(gaps);
-    n_below += __popc(__ballot_sync(0xFFFFFFFFu, (movers >> lane & 1u) && j < a.keep));
+    const int64_t left = static_cast<int64_t>(a.keep) - j0;  // this turn's tokens below keep
+    n_below += left >= 32 ? __popc(movers) : left > 0 ? __popc(movers & ((1u << left) - 1u)) : 0;
   });
-  const Scan at_mover = cluster_scan(lane == 0 ? n_movers : 0u, ctas, rank, scan[1]);
-  const Scan at_gap = cluster_scan(lane == 0 ? n_gaps : 0u, ctas, rank, scan[2]);
-  uint32_t to_mover = __shfl_sync(0xFFFFFFFFu, at_mover.before, 0), to_gap = __shfl_sync(0xFFFFFFFFu, at_gap.before, 0);
+  const Scan at = cluster_scan(n_movers, n_gaps, n_below, ctas, rank, sums[1]);
+  uint32_t to_mover = at.x, to_gap = at.y;
   int *const from = list + kEvictHeader, *const to = from + a.most;
-  walk([&](int j, uint32_t movers, uint32_t gaps) {
+  walk([&](int j0, uint32_t movers, uint32_t gaps) {
     const uint32_t before = (1u << lane) - 1u;
-    if (movers >> lane & 1u) from[to_mover + __popc(movers & before)] = j;
-    if (gaps >> lane & 1u) to[to_gap + __popc(gaps & before)] = j;
+    if (movers >> lane & 1u) from[to_mover + __popc(movers & before)] = j0 + lane;
+    if (gaps >> lane & 1u) to[to_gap + __popc(gaps & before)] = j0 + lane;
     to_mover += __popc(movers);
     to_gap += __popc(gaps);
   });
-  if (rank == 0 && threadIdx.x == 0) list[0] = static_cast<int>(at_mover.all);
-  if (lane == 0 && n_below > 0) atomicAdd(&list[1], static_cast<int>(n_below));
+  const int moves = static_cast<int>(at.all_x);
+  if (rank == 0 && threadIdx.x == 0) {
+    list[0] = moves;
+    list[1] = static_cast<int>(at.all_z);
+  }
   cluster_sync();
   // ---- the weights move: gaps are below all movers and recent ones, which are read before they are overwritten ----
-  const int moves = static_cast<int>(at_mover.all);
-  for (int i = static_cast<int>(rank) * kSelectThreads + threadIdx.x; i < moves; i += ctas * kSelectThreads)
-    weights[to[i]] = weights[from[i]];
+  for (int64_t i = static_cast<int64_t>(rank) * kSelectThreads + threadIdx.x; i < moves; i += ctas * kSelectThreads) {
+    const int f = from[i], t = to[i];
+    weights[t] = weights[f];
+    from[i] = row_of(a, table, f);
+    to[i] = row_of(a, table, t);
+  }
   cluster_sync();
   if (rank == 0) {
     constexpr int U = 4;
@@ -213,100 +283,140 @@ __global__ void __launch_bounds__(kSelectThreads) evict_select_kernel(const __gr
     }
   }
   cluster_sync();
-  for (int64_t j = a.keep + rank * kSelectThreads + static_cast<int>(threadIdx.x); j < n; j += ctas * kSelectThreads) weights[j] = 0.0f;
+  for (int64_t j = a.keep + static_cast<int64_t>(rank) * kSelectThreads + threadIdx.x; j < n; j += ctas * kSelectThreads)
+    weights[j] = 0.0f;
 }
 
 constexpr int kMoveThreads = 256;
-constexpr int kLanes = 8;                       // pieces of a row that a CTA owns
-constexpr int kAtOnce = kMoveThreads / kLanes;  // rows that it takes a turn
+constexpr int kLanes = 8;                       // pieces of a row that a CTA of the ordered moves owns
+constexpr int kAtOnce = kMoveThreads / kLanes;  // rows that it takes at a time
 constexpr int kMoveUnroll = 8;
 
 struct MovePlan {
-  int columns[4];  // groups of kLanes pieces of each array
+  int columns[4];  // CTAs that own kLanes pieces of each array
   int piece[2];    // bytes of a piece of K and V, and of the scales: 16, 8 or 4
-  int parts;       // CTAs a column: one for what is ordered, the others for movers from beyond keep
+  int ordered;     // all columns; the CTAs from there on take movers from beyond keep
 };
 
+// The moves that are in order: `below` movers, then the recent rows, of the pieces from piece0 on.
 template <class T>
-__device__ __forceinline__ void move_rows(const EvictArgs& a, uint8_t* base, int bytes, int piece0, int b, int part, int parts) {
-  const int n = static_cast<int>(min(static_cast<int64_t>(max(a.kv_len[b], 0)), a.capacity));
-  if (n <= a.keep) return;
-  const int* list = a.ws + static_cast<int64_t>(b) * (kEvictHeader + 2 * static_cast<int64_t>(a.most));
+__device__ __forceinline__ void move_column(const EvictArgs& a, uint8_t* base, int bytes, int piece0, int b, int n, const int* list) {
+  const int below = list[1], old = n - a.recent, front = a.keep - a.recent;
   const int *from = list + kEvictHeader, *to = from + a.most;
   const int col = threadIdx.x % kLanes, slot = threadIdx.x / kLanes;
   const bool mine = (piece0 + col) * static_cast<int>(sizeof(T)) < bytes;
-  const int64_t off = static_cast<int64_t>(piece0 + col) * sizeof(T);
-  const int* table = a.page_table + static_cast<int64_t>(b) * a.max_pages;
-  auto place = [&](int j) -> uint8_t* {
-    const uint32_t p = fdiv(static_cast<uint32_t>(j), a.div_page);
-    const int page = table[p];
-    if (page < 0 || page >= a.num_pages) {
-      atomicExch(a.status, static_cast<int>(H3ATTN_ERR_INVALID_ARG));
-      return nullptr;
-    }
-    return base + (static_cast<int64_t>(page) * a.page_size + (j - static_cast<int>(p) * a.page_size)) * bytes + off;
-  };
+  uint8_t* const column = base + static_cast<int64_t>(piece0 + col) * sizeof(T);
+  const int32_t* const table = a.page_table + static_cast<int64_t>(b) * a.max_pages;
   T x[kMoveUnroll];
-  uint8_t* dst[kMoveUnroll];
-  // `count` rows: the i-th from src_of(i) to dst_of(i), `ordered` turns after one another
-  auto move = [&](int first, int count, int step, bool ordered, auto&& src_of, auto&& dst_of) {
-    for (int64_t i0 = first; i0 < count; i0 += step) {
+  int dst[kMoveUnroll];
+  auto move = [&](int count, auto&& src_of, auto&& dst_of) {
+    for (int64_t i0 = 0; i0 < count; i0 += kAtOnce * kMoveUnroll) {
+      int src[kMoveUnroll];
 #pragma unroll
       for (int u = 0; u < kMoveUnroll; ++u) {
-        const int i = static_cast<int>(min(i0 + u * kAtOnce + slot, static_cast<int64_t>(count)));
-        dst[u] = nullptr;
+        const int64_t i = i0 + u * kAtOnce + slot;
+        src[u] = dst[u] = -1;
         if (mine && i < count) {
-          const uint8_t* src = place(src_of(i));
-          dst[u] = place(dst_of(i));
-          if (src && dst[u])
-            x[u] = *reinterpret_cast<const T*>(src);
-          else
-            dst[u] = nullptr;
+          src[u] = src_of(static_cast<int>(i));
+          dst[u] = dst_of(static_cast<int>(i));
         }
       }
-      if (ordered) __syncthreads();
+#pragma unroll
+      for (int u = 0; u < kMoveUnroll; ++u) {
+        if (src[u] < 0 || dst[u] < 0)
+          dst[u] = -1;
+        else
+          x[u] = *reinterpret_cast<const T*>(column + static_cast<int64_t>(src[u]) * bytes);
+      }
+      __syncthreads();  // what the stores overwrite has been read
 #pragma unroll
       for (int u = 0; u < kMoveUnroll; ++u)
-        if (dst[u]) *reinterpret_cast<T*>(dst[u]) = x[u];
-      if (ordered) __syncthreads();
+        if (dst[u] >= 0) *reinterpret_cast<T*>(column + static_cast<int64_t>(dst[u]) * bytes) = x[u];
+      __syncthreads();
     }
   };
-  const int movers = list[0], below = list[1], turn = kAtOnce * kMoveUnroll;
-  auto mover = [&](int i) { return from[i]; };
-  auto gap = [&](int i) { return to[i]; };
-  if (part == 0) {
-    move(0, below, turn, false, mover, gap);
-    __syncthreads();
-    const int old = n - a.recent, front = a.keep - a.recent;
-    move(0, a.recent, turn, true, [&](int i) { return old + i; }, [&](int i) { return front + i; });
+  move(below, [&](int i) { return from[i]; }, [&](int i) { return to[i]; });
+  move(a.recent, [&](int i) { return row_of(a, table, old + i); }, [&](int i) { return row_of(a, table, front + i); });
+}
+
+// `pieces` pieces of each of two arrays, from row src to row dst, by the lanes of a warp.
+template <class T>
+__device__ __forceinline__ void move_row(uint8_t* first, uint8_t* second, int pieces, int64_t src, int64_t dst) {
+  const int lane = threadIdx.x & 31;
+  for (int i0 = lane; i0 < 2 * pieces; i0 += 32 * kMoveUnroll) {
+    T x[kMoveUnroll];
+#pragma unroll
+    for (int u = 0; u < kMoveUnroll; ++u) {
+      const int i = i0 + 32 * u;
+      if (i < 2 * pieces) x[u] = reinterpret_cast<const T*>(i < pieces ? first : second)[src * pieces + (i < pieces ? i : i - pieces)];
+    }
+#pragma unroll
+    for (int u = 0; u < kMoveUnroll; ++u) {
+      const int i = i0 + 32 * u;
+      if (i < 2 * pieces) reinterpret_cast<T*>(i < pieces ? first : second)[dst * pieces + (i < pieces ? i : i - pieces)] = x[u];
+    }
   }
-  if (part > 0 || parts == 1)
-    move(below + (parts == 1 ? 0 : part - 1) * turn, movers, (parts == 1 ? 1 : parts - 1) * turn, false, mover, gap);
 }
 
 __global__ void __launch_bounds__(kMoveThreads) evict_move_kernel(const __grid_constant__ EvictArgs a, const __grid_constant__ MovePlan p) {
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
   asm volatile("griddepcontrol.wait;" ::: "memory");
+  const int b = blockIdx.y;
+  const int n = static_cast<int>(min(static_cast<int64_t>(max(a.kv_len[b], 0)), a.capacity));
+  if (n <= a.keep) return;
+  const int* const list = a.ws + static_cast<int64_t>(b) * (kEvictHeader + 2 * static_cast<int64_t>(a.most));
+  if (static_cast<int>(blockIdx.x) >= p.ordered) {  // movers from beyond keep, a warp each
+    const int moves = list[0], below = list[1], step = (gridDim.x - p.ordered) * (kMoveThreads / 32);
+    const int *from = list + kEvictHeader, *to = from + a.most;
+    for (int64_t i = below + static_cast<int64_t>(blockIdx.x - p.ordered) * (kMoveThreads / 32) + (threadIdx.x >> 5); i < moves; i += step) {
+      const int src = from[i], dst = to[i];
+      if (src < 0 || dst < 0) continue;
+      move_row<uint4>(a.row[0], a.row[1], a.row_bytes[0] / 16, src, dst);
+      if (!a.row[2]) continue;
+      if (p.piece[1] == 16)
+        move_row<uint4>(a.row[2], a.row[3], a.row_bytes[1] / 16, src, dst);
+      else
+        move_row<uint32_t>(a.row[2], a.row[3], a.row_bytes[1] / 4, src, dst);
+    }
+    return;
+  }
   int column = blockIdx.x, of = 0;
   while (column >= p.columns[of]) column -= p.columns[of++];
-  const int piece = p.piece[of >> 1], bytes = a.row_bytes[of >> 1];
+  const int bytes = a.row_bytes[of >> 1], piece = p.piece[of >> 1];
   if (piece == 16)
-    move_rows<uint4>(a, a.row[of], bytes, column * kLanes, blockIdx.z, blockIdx.y, p.parts);
+    move_column<uint4>(a, a.row[of], bytes, column * kLanes, b, n, list);
   else if (piece == 8)
-    move_rows<uint2>(a, a.row[of], bytes, column * kLanes, blockIdx.z, blockIdx.y, p.parts);
+    move_column<uint2>(a, a.row[of], bytes, column * kLanes, b, n, list);
   else
-    move_rows<uint32_t>(a, a.row[of], bytes, column * kLanes, blockIdx.z, blockIdx.y, p.parts);
+    move_column<uint32_t>(a, a.row[of], bytes, column * kLanes, b, n, list);
 }
 
 }  // namespace
 
 cudaError_t launch_evict(const EvictArgs& a, cudaStream_t stream) {
-  // a CTA's part of the tokens is passed over six times: 4096 of them a CTA, up to the 8 CTAs that any cluster may have
+  // One CTA for up to 8192 tokens, which has no cluster to wait for; then as many as leave 4096 each, up to the 8 that
+  // any cluster may have.
   uint32_t ctas = 1;
-  while (ctas < 8 && a.capacity > 4096 * static_cast<int64_t>(ctas)) ctas *= 2;
+  while (ctas < 8 && a.capacity > 8192 && a.capacity > 4096 * static_cast<int64_t>(ctas)) ctas *= 2;
+  const int64_t each = tokens_per_warp(a.capacity - a.recent > 0 ? a.capacity - a.recent : 0, ctas) * kSelectWarps;
+  const bool fits = each <= kMostHeld;
+  auto* const select = fits ? evict_select_kernel<true> : evict_select_kernel<false>;
+  if (fits) {
+    static std::atomic<bool> attr_set[64];  // calls of several host threads
+    int dev = 0;
+    cudaError_t e = cudaGetDevice(&dev);
+    if (e != cudaSuccess) return e;
+    if (dev < 0 || dev >= 64) return cudaErrorInvalidDevice;
+    if (!attr_set[dev]) {
+      e = cudaFuncSetAttribute(evict_select_kernel<true>, cudaFuncAttributeMaxDynamicSharedMemorySize, kMostHeld * 4);
+      if (e != cudaSuccess) return e;
+      attr_set[dev] = true;
+    }
+  }
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(static_cast<unsigned>(a.B) * ctas);
   cfg.blockDim = dim3(kSelectThreads);
+  cfg.dynamicSmemBytes = fits ? static_cast<size_t>(each) * 4 : 0;
   cfg.stream = stream;
   cudaLaunchAttribute attr[2];
   attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
@@ -316,22 +426,24 @@ cudaError_t launch_evict(const EvictArgs& a, cudaStream_t stream) {
   attr[1].val.clusterDim.y = attr[1].val.clusterDim.z = 1;
   cfg.attrs = attr;
   cfg.numAttrs = 2;
-  cudaError_t e = cudaLaunchKernelEx(&cfg, evict_select_kernel, a, ctas);
+  cudaError_t e = cudaLaunchKernelEx(&cfg, select, a, ctas);
   if (e != cudaSuccess) return e;
   MovePlan p = {};
-  int columns = 0;
   for (int i = 0; i < 4; ++i) {
     const int bytes = a.row_bytes[i >> 1];
     if (!a.row[i]) continue;
     p.piece[i >> 1] = bytes % 16 == 0 ? 16 : bytes % 8 == 0 ? 8 : 4;
     p.columns[i] = (bytes / p.piece[i >> 1] + kLanes - 1) / kLanes;
-    columns += p.columns[i];
+    p.ordered += p.columns[i];
   }
-  // movers from beyond keep: one more CTA for each two turns of them that there may be, up to 32
-  const int64_t free_movers = std::max<int64_t>(std::min<int64_t>(a.most, a.capacity - a.keep - a.recent), 0);
-  p.parts = 1 + static_cast<int>(std::min<int64_t>((free_movers + 511) / 512, 32));
-  return launch_dependent(evict_move_kernel, dim3(static_cast<unsigned>(columns), static_cast<unsigned>(p.parts), static_cast<unsigned>(a.B)),
-                          kMoveThreads, 0, stream, a, p);
+  // movers from beyond keep: a CTA for each 16 that there may be (two a warp), up to 8 an SM over all sequences
+  const int64_t beyond = std::max<int64_t>(std::min<int64_t>(a.most, a.capacity - a.keep - a.recent), 0);
+  int sms = 0;
+  e = sm_count(&sms);
+  if (e != cudaSuccess) return e;
+  const int64_t dealt = std::min<int64_t>((beyond + 15) / 16, std::max(8 * sms / a.B, 1));
+  return launch_dependent(evict_move_kernel, dim3(static_cast<unsigned>(p.ordered + dealt), static_cast<unsigned>(a.B)), kMoveThreads,
+                          0, stream, a, p);
 }
 
 }  // namespace h3

@@ -2,8 +2,8 @@
 // bits.
 //
 // Memory-bound: each row is read once and written once.  A warp takes a token (two
-// where a token's K and V rows are short), looks up its page once, and its lanes
-// walk over the pieces of 8 channels of its K and V rows, kUnroll at a time: a
+// where a token's K and V rows are short, a part of one where there are few tokens), looks up
+// its page once, and its lanes walk over the pieces of 8 channels of its K and V rows, kUnroll at a time: a
 // piece is 16 bytes of a bf16 row, or 4 bytes of codes and a scale that two
 // neighbouring lanes share, and 16 bytes of the output.
 #include "cache4.cuh"
@@ -15,10 +15,12 @@ namespace {
 constexpr int kThreads = 256, kUnroll = 4;
 
 template <bool Q4>
-__global__ void __launch_bounds__(kThreads) read_kernel(const __grid_constant__ ReadArgs a, int lanes_log2) {
+__global__ void __launch_bounds__(kThreads) read_kernel(const __grid_constant__ ReadArgs a, int lanes_log2,
+                                                        const __grid_constant__ FastDiv parts) {
   const int lane = threadIdx.x & 31, per = 1 << lanes_log2;  // lanes of a token
-  const int64_t token = (static_cast<int64_t>(blockIdx.x) * (kThreads / 32) + (threadIdx.x >> 5)) * (32 >> lanes_log2) +
-                        (lane >> lanes_log2);
+  const uint32_t item = blockIdx.x * (kThreads / 32) + (threadIdx.x >> 5), tokens_at = fdiv(item, parts);
+  const uint32_t part = item - tokens_at * parts.d;
+  const int64_t token = static_cast<int64_t>(tokens_at) * (32 >> lanes_log2) + (lane >> lanes_log2);
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
   asm volatile("griddepcontrol.wait;" ::: "memory");
   if (token >= static_cast<int64_t>(a.B) * a.S) return;
@@ -36,7 +38,8 @@ __global__ void __launch_bounds__(kThreads) read_kernel(const __grid_constant__ 
   const int64_t row = static_cast<int64_t>(page) * a.page_size + static_cast<int>(at - static_cast<int64_t>(p) * a.page_size);
   const int pieces = a.Hkv * (a.D / 8);  // of K, and the same of V
   const int begin = a.k ? 0 : pieces, end = a.v ? 2 * pieces : pieces;
-  for (int i0 = begin + (lane & (per - 1)); i0 < end; i0 += per * kUnroll) {
+  for (int i0 = begin + (lane & (per - 1)) + static_cast<int>(part) * per * kUnroll; i0 < end;
+       i0 += per * kUnroll * static_cast<int>(parts.d)) {
     uint4 x[kUnroll];
     uint32_t codes[kUnroll], scale[kUnroll];
 #pragma unroll
@@ -73,10 +76,17 @@ __global__ void __launch_bounds__(kThreads) read_kernel(const __grid_constant__ 
 cudaError_t launch_read(const ReadArgs& a, cudaStream_t stream) {
   const int pieces = a.Hkv * (a.D / 8) * 2;
   const int lanes_log2 = pieces <= 16 ? 4 : 5;
-  const int64_t per_block = static_cast<int64_t>(kThreads) >> lanes_log2, tokens = static_cast<int64_t>(a.B) * a.S;
-  const dim3 grid(static_cast<unsigned>((tokens + per_block - 1) / per_block));
-  return a.k_scales ? launch_dependent(read_kernel<true>, grid, kThreads, 0, stream, a, lanes_log2)
-                    : launch_dependent(read_kernel<false>, grid, kThreads, 0, stream, a, lanes_log2);
+  const int64_t tokens = static_cast<int64_t>(a.B) * a.S, per_warp = 32 >> lanes_log2, warps = (tokens + per_warp - 1) / per_warp;
+  int sms = 0;
+  cudaError_t e = sm_count(&sms);
+  if (e != cudaSuccess) return e;
+  // a token in as many parts as it has turns, where the warps are then all resident
+  const int64_t turns = (pieces + (kUnroll << lanes_log2) - 1) / (kUnroll << lanes_log2);
+  const int64_t parts = std::max<int64_t>(1, std::min<int64_t>(turns, sms * 32LL / warps));
+  const FastDiv div = make_fastdiv(static_cast<uint32_t>(parts));
+  const dim3 grid(static_cast<unsigned>((warps * parts + kThreads / 32 - 1) / (kThreads / 32)));
+  return a.k_scales ? launch_dependent(read_kernel<true>, grid, kThreads, 0, stream, a, lanes_log2, div)
+                    : launch_dependent(read_kernel<false>, grid, kThreads, 0, stream, a, lanes_log2, div);
 }
 
 }  // namespace h3
