@@ -41,17 +41,23 @@ __device__ __forceinline__ uint32_t codes_of(const uint32_t* n, uint32_t scale) 
   const float s = scale < 8u ? static_cast<float>(scale) * 0x1p-17f : __uint_as_float((scale + (112u << 3)) << 20);
   const float inv = __fdividef(1.0f + 0x1p-13f, s);
   constexpr float kRound = 12582912.0f + 8.0f;  // and the codes' 8
-  constexpr uint32_t kBits = 0x4B400000u;       // of 12582912
-  const bool cut = scale < 8u || scale == kScaleMax;
+  constexpr uint32_t kBits = 0x4B400000u * 0x11111111u;  // of 12582912, in all eight places
   uint32_t codes = 0;
+  if (scale >= 8u && scale < kScaleMax) {
 #pragma unroll
-  for (int e = 7; e >= 0; --e) {
-    const float x = __uint_as_float(e & 1 ? n[e >> 1] & 0xFFFF0000u : n[e >> 1] << 16);
-    float t = fmaf(x, inv, kRound);
-    if (cut) t = fminf(fmaxf(x * inv, -8.0f), 7.0f) + kRound;
-    codes = codes * 16u + (__float_as_uint(t) - kBits);
+    for (int e = 7; e >= 0; --e) {
+      const float x = __uint_as_float(e & 1 ? n[e >> 1] & 0xFFFF0000u : n[e >> 1] << 16);
+      codes = codes * 16u + __float_as_uint(fmaf(x, inv, kRound));
+    }
+  } else {
+#pragma unroll 1
+    for (int e = 7; e >= 0; --e) {
+      const uint32_t w = e < 2 ? n[0] : e < 4 ? n[1] : e < 6 ? n[2] : n[3];
+      const float x = __uint_as_float(e & 1 ? w & 0xFFFF0000u : w << 16);
+      codes = codes * 16u + __float_as_uint(fminf(fmaxf(x * inv, -8.0f), 7.0f) + kRound);
+    }
   }
-  return codes;
+  return codes - kBits;
 }
 
 }  // namespace
