@@ -177,6 +177,7 @@ __global__ void __launch_bounds__(kThreads, 4) append_kernel(const __grid_consta
     return (group - h8) | 16u;
   };
   const uint32_t other0 = Q4 ? holder(g0 ^ 1u) : 0u, other1 = Q4 ? holder(g1 ^ 1u) : 0u;
+  const uint32_t pair_of = (other0 & 16u ? 0x32u : 0x10u) | (other1 & 16u ? 0x7600u : 0x5400u);
 
   while (true) {
     // acc: sum of squares, channels in order, then the butterfly over the row's lanes
@@ -282,17 +283,27 @@ __global__ void __launch_bounds__(kThreads, 4) append_kernel(const __grid_consta
       }
       if constexpr (Q4) {
         if (first + (u + 1) * static_cast<int>(hw) > a.Hq) {  // not query rows alone; the same in all lanes
-          const uint32_t top0 = abs_max8(n), top1 = abs_max8(n + 4), mine = top0 | top1 << 16;
+          // the largest values of the lane's two groups, and of the neighbours that they share scales with, as pairs
+          const uint32_t mine = abs_max8_pair(n, n + 4);
           const uint32_t of0 = __shfl_sync(0xFFFFFFFFu, mine, lane - lr + (other0 & 15u));
           const uint32_t of1 = __shfl_sync(0xFFFFFFFFu, mine, lane - lr + (other1 & 15u));
-          const uint32_t scale0 = scale_of(max(top0, other0 & 16u ? of0 >> 16 : of0 & 0xFFFFu));
-          const uint32_t scale1 = scale_of(max(top1, other1 & 16u ? of1 >> 16 : of1 & 0xFFFFu));
+          const uint32_t top = __vmaxu2(mine, __byte_perm(of0, of1, pair_of));
+          uint32_t codes0, codes1, scale0, scale1;
+          if (!__any_sync(0xFFFFFFFFu, !plain_maxima(top))) {
+            scale0 = plain_codes(n, top << 16, codes0);
+            scale1 = plain_codes(n + 4, top & 0xFFFF0000u, codes1);
+          } else {
+            scale0 = scale_of(top & 0xFFFFu);
+            scale1 = scale_of(top >> 16);
+            codes0 = codes_of(n[0], n[1], n[2], n[3], scale0);
+            codes1 = codes_of(n[4], n[5], n[6], n[7], scale1);
+          }
           if (live && head >= a.Hq && head < last && cache_row >= 0) {
             const int64_t row = cache_row * a.Hkv + head - a.Hq - (is_v ? a.Hkv : 0);
             uint32_t* codes = reinterpret_cast<uint32_t*>(is_v ? a.v_pages : a.k_pages) + row * (D / 8);
             uint8_t* scales = (is_v ? a.v_scales : a.k_scales) + row * (D / 16);
-            codes[g0] = codes_of(n, scale0);
-            codes[g1] = codes_of(n + 4, scale1);
+            codes[g0] = codes0;
+            codes[g1] = codes1;
             if (!(g0 & 1u)) scales[g0 >> 1] = static_cast<uint8_t>(scale0);
             if (!(g1 & 1u)) scales[g1 >> 1] = static_cast<uint8_t>(scale1);
           }
