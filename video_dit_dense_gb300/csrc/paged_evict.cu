@@ -7,9 +7,11 @@
 //
 // First kernel, a cluster of 1 to 8 CTAs a sequence by the cache's room: each CTA
 // holds its part of the weights in shared memory, as integers in their order.  The
-// weight T of the front-th heaviest old token comes from three counting passes over
-// 11, 11 and 10 bits of that order (the CTAs' counts are added up across the cluster), then
-// kept = above T, or equal to it and among the first ones.  Each warp owns a
+// weight T of the front-th heaviest old token comes from counting passes over
+// 8 bits of that order (the CTAs' counts are added up across the cluster), until all
+// tokens that begin like T are kept or no bits are left; then
+// kept = above T, or equal to it and among the first ones.  (11 bits a pass are one pass fewer, but 2048
+// counts from each of 8 CTAs for each of them took longer.)  Each warp owns a
 // contiguous part of the tokens, so that a ballot numbers movers and gaps.  It writes
 // their lists, moves the weights, and looks up the rows that the places are.
 // Weights read again from memory in each pass, a load at a time, took 64 us of one
@@ -28,7 +30,7 @@ namespace h3 {
 namespace {
 
 constexpr int kSelectThreads = 1024, kSelectWarps = kSelectThreads / 32;
-constexpr int kBins = 2048, kPasses = 3;
+constexpr int kBins = 256, kPasses = 4;
 constexpr int kMostHeld = 200 * 1024 / 4;  // weights in a CTA's shared memory
 
 __device__ __forceinline__ uint32_t cluster_rank() {
@@ -113,7 +115,7 @@ __global__ void __launch_bounds__(kSelectThreads) evict_select_kernel(const __gr
   __shared__ uint32_t hist[kPasses][kBins];
   __shared__ uint32_t sums[2][3][kSelectWarps + 1];
   __shared__ uint32_t found[kPasses][3];  // bin, how many of its tokens are still wanted, how many it has
-  __shared__ uint32_t above_of[kSelectWarps];
+  __shared__ uint32_t above_of[kBins / 32];
   const int b = blockIdx.x / ctas, warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const uint32_t rank = ctas > 1 ? cluster_rank() : 0;
   for (int i = threadIdx.x; i < kPasses * kBins; i += kSelectThreads) (&hist[0][0])[i] = 0;
@@ -146,75 +148,67 @@ __global__ void __launch_bounds__(kSelectThreads) evict_select_kernel(const __gr
   auto order = [&](int j) { return HELD ? mine[j] : order_of(weights[j]); };
   __syncthreads();
   // ---- the weight of the front-th heaviest ----
-  uint32_t prefix = 0, want = static_cast<uint32_t>(front);  // of tokens whose order begins with prefix, so many are kept
-  bool all_ties = false;
-  if (front > 0) {
+  uint32_t prefix = 0, seen_bits = 0;               // the bits of T that are known, and which those are
+  uint32_t want = static_cast<uint32_t>(front);  // of tokens that begin with them, so many are kept
+  bool all_ties = front == 0;
+  if (front == 0) prefix = 0xFFFFFFFFu;  // none is kept
 #pragma unroll 1
-    for (int pass = 0; pass < kPasses; ++pass) {
-      const int shift = pass == 0 ? 21 : pass == 1 ? 10 : 0, bits = pass == 2 ? 10 : 11;
-      const uint32_t mask = pass == 0 ? 0u : pass == 1 ? 0xFFE00000u : 0xFFFFFC00u;
+  for (int pass = 0; pass < kPasses && !all_ties; ++pass) {
+    const int shift = 24 - 8 * pass;
 #pragma unroll 4
-      for (int j0 = begin; j0 < end; j0 += 32) {
-        const uint32_t o = j0 + lane < end ? order(j0 + lane) : 0u;
-        const bool counts = j0 + lane < end && (o & mask) == prefix;
-        if (!__any_sync(0xFFFFFFFFu, counts)) continue;
-        // lanes with the same bin add to it once
-        const uint32_t bin = counts ? o >> shift & ((1u << bits) - 1u) : 0xFFFFFFFFu;
-        const uint32_t same = __match_any_sync(0xFFFFFFFFu, bin);
-        if (counts && (same & ((1u << lane) - 1u)) == 0) atomicAdd(&hist[pass][bin], static_cast<uint32_t>(__popc(same)));
-      }
-      if (ctas > 1)
-        cluster_sync();
-      else
-        __syncthreads();
-      // each thread adds up its bins over the cluster, from the last bin on
-      constexpr int kMine = kBins / kSelectThreads;
-      uint32_t of_bin[kMine], sum = 0;
+    for (int j0 = begin; j0 < end; j0 += 32) {
+      const uint32_t o = j0 + lane < end ? order(j0 + lane) : 0u;
+      const bool counts = j0 + lane < end && (o & seen_bits) == prefix;
+      if (!__any_sync(0xFFFFFFFFu, counts)) continue;
+      // lanes with the same bin add to it once
+      const uint32_t bin = counts ? o >> shift & 255u : 0xFFFFFFFFu;
+      const uint32_t same = __match_any_sync(0xFFFFFFFFu, bin);
+      if (counts && (same & ((1u << lane) - 1u)) == 0) atomicAdd(&hist[pass][bin], static_cast<uint32_t>(__popc(same)));
+    }
+    if (ctas > 1)
+      cluster_sync();
+    else
+      __syncthreads();
+    // a thread adds up a bin over the cluster, from the last bin on
+    uint32_t of_bin = 0, above = 0;
+    if (threadIdx.x < kBins) {
+      const int bin = kBins - 1 - static_cast<int>(threadIdx.x);
+      if (ctas > 1) {
 #pragma unroll
-      for (int i = 0; i < kMine; ++i) {
-        const int bin = kBins - 1 - (static_cast<int>(threadIdx.x) * kMine + i);
-        of_bin[i] = hist[pass][bin];
-        if (ctas > 1) {
-          of_bin[i] = 0;
-#pragma unroll
-          for (uint32_t r = 0; r < 8; ++r)
-            if (r < ctas) of_bin[i] += peer_load(&hist[pass][bin], r);
-        }
-        sum += of_bin[i];
+        for (uint32_t r = 0; r < 8; ++r)
+          if (r < ctas) of_bin += peer_load(&hist[pass][bin], r);
+      } else {
+        of_bin = hist[pass][bin];
       }
-      uint32_t above = sum;
+      above = of_bin;
 #pragma unroll
       for (int off = 1; off < 32; off <<= 1) {
         const uint32_t m = __shfl_up_sync(0xFFFFFFFFu, above, off);
         if (lane >= off) above += m;
       }
       if (lane == 31) above_of[warp] = above;
-      __syncthreads();
-      above -= sum;
-      above += __reduce_add_sync(0xFFFFFFFFu, lane < warp ? above_of[lane] : 0u);
-#pragma unroll
-      for (int i = 0; i < kMine; ++i) {
-        if (above < want && want <= above + of_bin[i]) {
-          found[pass][0] = kBins - 1 - (threadIdx.x * kMine + i);
-          found[pass][1] = want - above;
-          found[pass][2] = of_bin[i];
-        }
-        above += of_bin[i];
-      }
-      __syncthreads();
-      prefix |= found[pass][0] << shift;
-      want = found[pass][1];
-      all_ties = want == found[pass][2];
     }
-  } else {
-    prefix = 0xFFFFFFFFu;  // none is kept
-    want = 0;
+    __syncthreads();
+    if (threadIdx.x < kBins) {
+      above -= of_bin;
+      above += __reduce_add_sync(0xFFFFFFFFu, lane < warp && lane < kBins / 32 ? above_of[lane] : 0u);
+      if (above < want && want <= above + of_bin) {
+        found[pass][0] = kBins - 1 - threadIdx.x;
+        found[pass][1] = want - above;
+        found[pass][2] = of_bin;
+      }
+    }
+    __syncthreads();
+    prefix |= found[pass][0] << shift;
+    seen_bits |= 255u << shift;
+    want = found[pass][1];
+    all_ties = want == found[pass][2];
   }
-  // ---- which are kept: above the prefix, or equal and among the first `want` ----
+  // ---- which are kept: above the prefix, or equal and among the first `want` (all_ties: all of those, or none at all) ----
   uint32_t ties_before = 0;
-  if (front > 0 && !all_ties) {
+  if (!all_ties) {
     uint32_t ties = 0;
-    for (int j = begin + lane; j < end; j += 32) ties += order(j) == prefix;
+    for (int j = begin + lane; j < end; j += 32) ties += (order(j) & seen_bits) == prefix;
     ties_before = cluster_scan(__reduce_add_sync(0xFFFFFFFFu, ties), 0, 0, ctas, rank, sums[0]).x;
   }
   auto walk = [&](auto&& each) {
@@ -222,7 +216,7 @@ __global__ void __launch_bounds__(kSelectThreads) evict_select_kernel(const __gr
 #pragma unroll 2
     for (int j0 = begin; j0 < end; j0 += 32) {
       const int j = j0 + lane;
-      const uint32_t o = j < end ? order(j) : 0u;
+      const uint32_t o = (j < end ? order(j) : 0u) & seen_bits;
       const bool tie = j < end && o == prefix;
       const uint32_t tied = all_ties ? 0u : __ballot_sync(0xFFFFFFFFu, tie);
       const bool kept =
