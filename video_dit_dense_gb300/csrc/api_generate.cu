@@ -348,7 +348,7 @@ h3attn_status_t read(const Cache& cache, void* k, void* v, const int32_t* first,
 
 h3attn_status_t evict_size(int B, int64_t capacity, int keep, int recent, size_t* bytes) {
   if (keep < 1 || recent < 0 || recent > keep) return H3ATTN_ERR_INVALID_ARG;
-  *bytes = static_cast<size_t>(B) * h3::evict_ints(h3::evict_most(capacity, keep, recent)) * sizeof(int);
+  *bytes = static_cast<size_t>(B) * static_cast<size_t>(h3::evict_ints(capacity, keep, recent)) * sizeof(int);
   return H3ATTN_OK;
 }
 
@@ -389,6 +389,7 @@ h3attn_status_t evict(const Cache& cache, float* weights, int keep, int recent, 
   a.keep = keep;
   a.recent = recent;
   a.most = h3::evict_most(a.capacity, keep, recent);
+  a.ints = h3::evict_ints(a.capacity, keep, recent);
   a.status = h3::status_word_ptr();
   if (!a.status) return H3ATTN_ERR_LAUNCH;
   return h3::launch_evict(a, static_cast<cudaStream_t>(stream)) == cudaSuccess ? H3ATTN_OK : H3ATTN_ERR_LAUNCH;

@@ -152,9 +152,9 @@ struct EvictArgs {
   const int32_t* kv_len;
   float* weights;        // [B, capacity]
   int32_t* len_out;
-  int* ws;               // [B, 4 + 2 * most]: counts, rows that move, rows they move to
+  int* ws;               // [B, ints]: counts, rows that move, rows they move to, the latter by where chains begin
   FastDiv div_page;
-  int64_t capacity;
+  int64_t capacity, ints;
   int B, page_size, max_pages, num_pages, keep, recent, most;
   int* status;
 };
@@ -165,7 +165,10 @@ inline int evict_most(int64_t capacity, int keep, int recent) {
 }
 // Ints of a sequence's part of the workspace.
 constexpr int kEvictHeader = 4;  // rows that move into gaps, and those of them from below keep
-inline size_t evict_ints(int most) { return kEvictHeader + 2 * static_cast<size_t>(most); }
+inline int64_t evict_ints(int64_t capacity, int keep, int recent) {
+  const int64_t chains = capacity - keep < recent ? capacity - keep : recent;
+  return kEvictHeader + 2 * static_cast<int64_t>(evict_most(capacity, keep, recent)) + (chains > 0 ? chains : 0);
+}
 cudaError_t launch_evict(const EvictArgs& a, cudaStream_t stream);
 
 }  // namespace h3

@@ -5,7 +5,7 @@
 //   the recent ones to front, front + 1, ... in their order.
 // Few rows move where few tokens are evicted: movers and gaps are at most n - keep.
 //
-// First kernel, a cluster of 1 to 8 CTAs a sequence by the cache's room: each CTA
+// First kernel, a cluster of 1 to 16 CTAs a sequence by the cache's room: each CTA
 // holds its part of the weights in shared memory, as integers in their order.  The
 // weight T of the front-th heaviest old token comes from counting passes over
 // 8 bits of that order (the CTAs' counts are added up across the cluster), until all
@@ -17,11 +17,14 @@
 // Weights read again from memory in each pass, a load at a time, took 64 us of one
 // sequence of 104448 tokens.
 //
-// Second kernel: moves the rows.  Movers from beyond `keep` are not in the way of
-// anything: a warp takes a row.  What else moves into [front, keep) or out of it is in order:
-// a CTA owns a column of pieces of all rows of one sequence, and moves first the movers from
-// below `keep`, then the recent rows in tiles from the first on (a row moves
-// down, so what a tile overwrites has been read).
+// Second kernel: moves the rows, d = n - keep places down.  Movers from beyond `keep`
+// are not in the way of anything: a warp takes a row.  The place front + c is read
+// by its mover, if it has one, then written by the recent row from old + c = front + c + d,
+// whose place is then written by the one from old + c + d, and so on: a chain, in which a warp
+// takes one row after the other, so that each of its lanes reads what it later overwrites.
+// There are min(d, recent) chains.  Where they are few and long (d < recent / kLongChain)
+// a CTA owns a column of pieces of all rows instead, and moves the movers first, then the
+// recent rows in tiles from the first on.
 #include <algorithm>
 
 #include "decode_common.cuh"
@@ -31,6 +34,7 @@ namespace {
 
 constexpr int kSelectThreads = 1024, kSelectWarps = kSelectThreads / 32;
 constexpr int kBins = 256, kPasses = 4;
+constexpr uint32_t kMostCtas = 16;  // of a cluster
 constexpr int kMostHeld = 200 * 1024 / 4;  // weights in a CTA's shared memory
 
 __device__ __forceinline__ uint32_t cluster_rank() {
@@ -110,7 +114,7 @@ __device__ __forceinline__ int row_of(const EvictArgs& a, const int32_t* table, 
 
 // HELD: the weights' order is kept in shared memory; otherwise (more tokens than fit) it is read anew in each pass.
 template <bool HELD>
-__global__ void __launch_bounds__(kSelectThreads) evict_select_kernel(const __grid_constant__ EvictArgs a, uint32_t ctas) {
+__global__ void __launch_bounds__(kSelectThreads, 1) evict_select_kernel(const __grid_constant__ EvictArgs a, uint32_t ctas) {
   extern __shared__ uint32_t held[];
   __shared__ uint32_t hist[kPasses][kBins];
   __shared__ uint32_t sums[2][3][kSelectWarps + 1];
@@ -122,7 +126,7 @@ __global__ void __launch_bounds__(kSelectThreads) evict_select_kernel(const __gr
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
   asm volatile("griddepcontrol.wait;" ::: "memory");
   const int n = static_cast<int>(min(static_cast<int64_t>(max(a.kv_len[b], 0)), a.capacity));
-  int* const list = a.ws + static_cast<int64_t>(b) * (kEvictHeader + 2 * static_cast<int64_t>(a.most));
+  int* const list = a.ws + b * a.ints;
   if (rank == 0 && threadIdx.x == 0) a.len_out[b] = min(n, a.keep);
   if (n <= a.keep) return;  // the whole cluster
   float* const weights = a.weights + b * a.capacity;
@@ -175,7 +179,7 @@ __global__ void __launch_bounds__(kSelectThreads) evict_select_kernel(const __gr
       const int bin = kBins - 1 - static_cast<int>(threadIdx.x);
       if (ctas > 1) {
 #pragma unroll
-        for (uint32_t r = 0; r < 8; ++r)
+        for (uint32_t r = 0; r < kMostCtas; ++r)
           if (r < ctas) of_bin += peer_load(&hist[pass][bin], r);
       } else {
         of_bin = hist[pass][bin];
@@ -236,9 +240,12 @@ __global__ void __launch_bounds__(kSelectThreads) evict_select_kernel(const __gr
   });
   const Scan at = cluster_scan(n_movers, n_gaps, n_below, ctas, rank, sums[1]);
   uint32_t to_mover = at.x, to_gap = at.y;
-  int *const from = list + kEvictHeader, *const to = from + a.most;
+  int *const from = list + kEvictHeader, *const to = from + a.most, *const chain = to + a.most;
+  const int chains = min(a.recent, n - a.keep);
   walk([&](int j0, uint32_t movers, uint32_t gaps) {
     const uint32_t before = (1u << lane) - 1u;
+    const int c = j0 + lane - front;  // the chain that begins with this place
+    if (c >= 0 && c < chains && j0 + lane < end && !(movers >> lane & 1u)) chain[c] = -1;
     if (movers >> lane & 1u) from[to_mover + __popc(movers & before)] = j0 + lane;
     if (gaps >> lane & 1u) to[to_gap + __popc(gaps & before)] = j0 + lane;
     to_mover += __popc(movers);
@@ -251,11 +258,26 @@ __global__ void __launch_bounds__(kSelectThreads) evict_select_kernel(const __gr
   }
   cluster_sync();
   // ---- the weights move: gaps are below all movers and recent ones, which are read before they are overwritten ----
-  for (int64_t i = static_cast<int64_t>(rank) * kSelectThreads + threadIdx.x; i < moves; i += ctas * kSelectThreads) {
-    const int f = from[i], t = to[i];
-    weights[t] = weights[f];
-    from[i] = row_of(a, table, f);
-    to[i] = row_of(a, table, t);
+  {
+    constexpr int U = 2;
+    const int64_t step = static_cast<int64_t>(ctas) * kSelectThreads;
+    for (int64_t i0 = static_cast<int64_t>(rank) * kSelectThreads + threadIdx.x; i0 < moves; i0 += U * step) {
+      int f[U], t[U];
+#pragma unroll
+      for (int u = 0; u < U; ++u) {
+        f[u] = i0 + u * step < moves ? from[i0 + u * step] : -1;
+        t[u] = f[u] >= 0 ? to[i0 + u * step] : -1;
+      }
+#pragma unroll
+      for (int u = 0; u < U; ++u) {
+        if (f[u] < 0) continue;
+        weights[t[u]] = weights[f[u]];
+        const int to_row = row_of(a, table, t[u]);
+        from[i0 + u * step] = row_of(a, table, f[u]);
+        to[i0 + u * step] = to_row;
+        if (f[u] < a.keep) chain[f[u] - front] = to_row;
+      }
+    }
   }
   cluster_sync();
   if (rank == 0) {
@@ -282,14 +304,14 @@ __global__ void __launch_bounds__(kSelectThreads) evict_select_kernel(const __gr
 }
 
 constexpr int kMoveThreads = 256;
-constexpr int kLanes = 8;                       // pieces of a row that a CTA of the ordered moves owns
+constexpr int kLongChain = 8;
+constexpr int kLanes = 8;                       // pieces of a row that a CTA owns where chains are long
 constexpr int kAtOnce = kMoveThreads / kLanes;  // rows that it takes at a time
-constexpr int kMoveUnroll = 8;
+constexpr int kMoveUnroll = 4;
 
 struct MovePlan {
   int columns[4];  // CTAs that own kLanes pieces of each array
   int piece[2];    // bytes of a piece of K and V, and of the scales: 16, 8 or 4
-  int ordered;     // all columns; the CTAs from there on take movers from beyond keep
 };
 
 // The moves that are in order: `below` movers, then the recent rows, of the pieces from piece0 on.
@@ -352,28 +374,43 @@ __device__ __forceinline__ void move_row(uint8_t* first, uint8_t* second, int pi
   }
 }
 
-__global__ void __launch_bounds__(kMoveThreads) evict_move_kernel(const __grid_constant__ EvictArgs a, const __grid_constant__ MovePlan p) {
+__global__ void __launch_bounds__(kMoveThreads, 4) evict_move_kernel(const __grid_constant__ EvictArgs a, const __grid_constant__ MovePlan p) {
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
   asm volatile("griddepcontrol.wait;" ::: "memory");
   const int b = blockIdx.y;
   const int n = static_cast<int>(min(static_cast<int64_t>(max(a.kv_len[b], 0)), a.capacity));
   if (n <= a.keep) return;
-  const int* const list = a.ws + static_cast<int64_t>(b) * (kEvictHeader + 2 * static_cast<int64_t>(a.most));
-  if (static_cast<int>(blockIdx.x) >= p.ordered) {  // movers from beyond keep, a warp each
-    const int moves = list[0], below = list[1], step = (gridDim.x - p.ordered) * (kMoveThreads / 32);
-    const int *from = list + kEvictHeader, *to = from + a.most;
-    for (int64_t i = below + static_cast<int64_t>(blockIdx.x - p.ordered) * (kMoveThreads / 32) + (threadIdx.x >> 5); i < moves; i += step) {
-      const int src = from[i], dst = to[i];
-      if (src < 0 || dst < 0) continue;
-      move_row<uint4>(a.row[0], a.row[1], a.row_bytes[0] / 16, src, dst);
-      if (!a.row[2]) continue;
-      if (p.piece[1] == 16)
-        move_row<uint4>(a.row[2], a.row[3], a.row_bytes[1] / 16, src, dst);
-      else
-        move_row<uint32_t>(a.row[2], a.row[3], a.row_bytes[1] / 4, src, dst);
+  const int* const list = a.ws + b * a.ints;
+  const int d = n - a.keep, chains = min(a.recent, d);
+  if (static_cast<int64_t>(d) * kLongChain >= a.recent) {
+    const int *from = list + kEvictHeader, *to = from + a.most, *chain = to + a.most;
+    const int32_t* const table = a.page_table + static_cast<int64_t>(b) * a.max_pages;
+    const int below = list[1], old = n - a.recent, front = a.keep - a.recent;
+    const int64_t items = static_cast<int64_t>(chains) + list[0] - below;
+    for (int64_t i = static_cast<int64_t>(blockIdx.x) * (kMoveThreads / 32) + (threadIdx.x >> 5); i < items;
+         i += gridDim.x * (kMoveThreads / 32)) {
+      // a chain: its first place goes to a gap, if it is a mover's, and each recent row to the place moved or left before
+      const bool in_chain = i < chains;
+      int src = in_chain ? row_of(a, table, front + static_cast<int>(i)) : from[below + i - chains];
+      int dst = in_chain ? chain[i] : to[below + i - chains];
+      int64_t r = in_chain ? i : a.recent;
+      while (true) {
+        if (src >= 0 && dst >= 0) {
+          move_row<uint4>(a.row[0], a.row[1], a.row_bytes[0] / 16, src, dst);
+          if (a.row[2]) move_row<uint32_t>(a.row[2], a.row[3], a.row_bytes[1] / 4, src, dst);
+        }
+        if (r >= a.recent) break;
+        dst = src;
+        src = row_of(a, table, old + static_cast<int>(r));
+        r += d;
+      }
     }
     return;
   }
+  int columns = 0;
+#pragma unroll
+  for (int i = 0; i < 4; ++i) columns += p.columns[i];
+  if (static_cast<int>(blockIdx.x) >= columns) return;
   int column = blockIdx.x, of = 0;
   while (column >= p.columns[of]) column -= p.columns[of++];
   const int bytes = a.row_bytes[of >> 1], piece = p.piece[of >> 1];
@@ -388,24 +425,24 @@ __global__ void __launch_bounds__(kMoveThreads) evict_move_kernel(const __grid_c
 }  // namespace
 
 cudaError_t launch_evict(const EvictArgs& a, cudaStream_t stream) {
-  // One CTA for up to 8192 tokens, which has no cluster to wait for; then as many as leave 4096 each, up to the 8 that
-  // any cluster may have.
+  // One CTA for up to 8192 tokens, which has no cluster to wait for; then as many as leave 4096 each, up to 16.
   uint32_t ctas = 1;
-  while (ctas < 8 && a.capacity > 8192 && a.capacity > 4096 * static_cast<int64_t>(ctas)) ctas *= 2;
+  while (ctas < kMostCtas && a.capacity > 8192 && a.capacity > 4096 * static_cast<int64_t>(ctas)) ctas *= 2;
   const int64_t each = tokens_per_warp(a.capacity - a.recent > 0 ? a.capacity - a.recent : 0, ctas) * kSelectWarps;
   const bool fits = each <= kMostHeld;
   auto* const select = fits ? evict_select_kernel<true> : evict_select_kernel<false>;
-  if (fits) {
-    static std::atomic<bool> attr_set[64];  // calls of several host threads
-    int dev = 0;
-    cudaError_t e = cudaGetDevice(&dev);
+  static std::atomic<bool> attr_set[64];  // calls of several host threads
+  int dev = 0;
+  cudaError_t e = cudaGetDevice(&dev);
+  if (e != cudaSuccess) return e;
+  if (dev < 0 || dev >= 64) return cudaErrorInvalidDevice;
+  if (!attr_set[dev]) {
+    e = cudaFuncSetAttribute(evict_select_kernel<true>, cudaFuncAttributeMaxDynamicSharedMemorySize, kMostHeld * 4);
+    // clusters of more than 8
+    if (e == cudaSuccess) e = cudaFuncSetAttribute(evict_select_kernel<true>, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
+    if (e == cudaSuccess) e = cudaFuncSetAttribute(evict_select_kernel<false>, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
     if (e != cudaSuccess) return e;
-    if (dev < 0 || dev >= 64) return cudaErrorInvalidDevice;
-    if (!attr_set[dev]) {
-      e = cudaFuncSetAttribute(evict_select_kernel<true>, cudaFuncAttributeMaxDynamicSharedMemorySize, kMostHeld * 4);
-      if (e != cudaSuccess) return e;
-      attr_set[dev] = true;
-    }
+    attr_set[dev] = true;
   }
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(static_cast<unsigned>(a.B) * ctas);
@@ -420,24 +457,26 @@ cudaError_t launch_evict(const EvictArgs& a, cudaStream_t stream) {
   attr[1].val.clusterDim.y = attr[1].val.clusterDim.z = 1;
   cfg.attrs = attr;
   cfg.numAttrs = 2;
-  cudaError_t e = cudaLaunchKernelEx(&cfg, select, a, ctas);
+  e = cudaLaunchKernelEx(&cfg, select, a, ctas);
   if (e != cudaSuccess) return e;
   MovePlan p = {};
+  int columns = 0;
   for (int i = 0; i < 4; ++i) {
     const int bytes = a.row_bytes[i >> 1];
     if (!a.row[i]) continue;
     p.piece[i >> 1] = bytes % 16 == 0 ? 16 : bytes % 8 == 0 ? 8 : 4;
     p.columns[i] = (bytes / p.piece[i >> 1] + kLanes - 1) / kLanes;
-    p.ordered += p.columns[i];
+    columns += p.columns[i];
   }
-  // movers from beyond keep: a CTA for each 16 that there may be (two a warp), up to 8 an SM over all sequences
-  const int64_t beyond = std::max<int64_t>(std::min<int64_t>(a.most, a.capacity - a.keep - a.recent), 0);
+  // chains and movers from beyond keep: a warp for each that there may be, up to 8 CTAs an SM over all sequences
+  const int64_t longest = std::max<int64_t>(a.capacity - a.keep, 0);  // d
+  const int64_t items = std::min<int64_t>(a.recent, longest) + std::min<int64_t>(a.most, std::max<int64_t>(longest - a.recent, 0));
   int sms = 0;
   e = sm_count(&sms);
   if (e != cudaSuccess) return e;
-  const int64_t dealt = std::min<int64_t>((beyond + 15) / 16, std::max(8 * sms / a.B, 1));
-  return launch_dependent(evict_move_kernel, dim3(static_cast<unsigned>(p.ordered + dealt), static_cast<unsigned>(a.B)), kMoveThreads,
-                          0, stream, a, p);
+  const int64_t dealt = std::min<int64_t>((items + 7) / 8, std::max(8 * sms / a.B, 1));
+  return launch_dependent(evict_move_kernel, dim3(static_cast<unsigned>(std::max<int64_t>(columns, dealt)), static_cast<unsigned>(a.B)),
+                          kMoveThreads, 0, stream, a, p);
 }
 
 }  // namespace h3
