@@ -344,8 +344,9 @@ inline cudaError_t sm_count(int* sms) {
 }
 
 // The shape of a launch whose CTAs have `warps` warps that take `tile` tokens at a time; the warps of `share` neighbouring
-// tiles of query heads load for one another where there is an even number of those.
-inline DecodePlan make_plan(const DecodeArgs& a, int sms, bool split, int warps, int tile, int share) {
+// tiles of query heads load for one another where there is an even number of those; caches of at most `few` tiles a
+// warp are walked whole.
+inline DecodePlan make_plan(const DecodeArgs& a, int sms, bool split, int warps, int tile, int share, int few) {
   DecodePlan p;
   const int G = a.Hq / a.Hkv;
   p.q_tiles = (G + 15) / 16;
@@ -357,10 +358,11 @@ inline DecodePlan make_plan(const DecodeArgs& a, int sms, bool split, int warps,
   p.share = p.q_tiles % 2 == 0 ? share : 1;
   const int loaders = p.WT * p.share;  // warps that load different tiles
   // Split into one range an SM, unless
-  // - the cache has no room for sequences of more than four tiles a warp: one CTA walks them in less time than the
-  //   second kernel takes (16 query and 4 key-value heads of 128, one sequence: 6.1 us against 6.9 at 128 tokens, 9.0
+  // - the cache has no room for sequences of more than `few` tiles a warp: one CTA walks them in less time than the
+  //   second kernel takes (bf16, four: 16 query and 4 key-value heads of 128, one sequence: 6.1 us against 6.9 at 128 tokens, 9.0
   //   against 7.2 at 256; 24 heads of each: 5.6 against 6.6 at 64, 8.5 against 6.8 at 128; 8 and 1: 6.8 against 7.7 at
-  //   512, 9.7 against 7.8 at 1024);
+  //   512, 9.7 against 7.8 at 1024; 4 bits, two: 16 and 4 heads of 128 5.6 against 6.7 at 120, 8.4 against 6.5 at 250; 8 and 1
+  //   5.9 against 7.0 at 500, 8.5 against 6.8 at 1000);
   // - the batch is too long for the tables in shared memory.  It has sequences enough to fill the GPU then, which is as
   //   good where they are alike and is not where one outlasts the others (16 query and 2 key-value heads of 64; 500 to
   //   1500 tokens: 512 sequences 48 us, 513 48; 0 to 4000 and one of 50000: 512 sequences 91 us, 513 392, 513 in two calls 98);
@@ -371,14 +373,14 @@ inline DecodePlan make_plan(const DecodeArgs& a, int sms, bool split, int warps,
   p.min_tiles = p.WT;  // one a warp: two or more take longer than their partials (7.6 us against 7.0 at 1024 tokens)
   p.start = 2 * loaders;
   const bool whole =
-      capacity <= 4 * p.WT * tile || a.B > kMaxSplitBatch || (capacity / 16 + 1 + p.start) * a.B > INT32_MAX;
+      capacity <= static_cast<int64_t>(few) * p.WT * tile || a.B > kMaxSplitBatch || (capacity / 16 + 1 + p.start) * a.B > INT32_MAX;
   p.ranges = split && !whole ? std::max(1, std::min(sms / p.groups, kMaxRanges)) : 0;
   // Caches without room for a tile a warp, or two where one or two sequences are all, leave half of the SMs to the
   // call's neighbours and have half the partials to join: one sequence of 8000 tokens, 16 query and 4 key-value heads of
   // 128, 9.3 us (on all SMs 10.0), 32 and 1 head 9.3 (11.2); 4 of 2000 tokens, 8 and 1 head, 6.9 (7.6).  With two tiles
   // a warp and many sequences all SMs are better: 48 of 342 tokens, 4 heads of 64, 7.5 (on half of them 8.5).
-  const int64_t tiles = (capacity + tile - 1) / tile * a.B, few = static_cast<int64_t>(p.ranges) * loaders;
-  if (tiles < (a.B <= 2 ? 2 * few : few)) p.ranges = (p.ranges + 1) / 2;
+  const int64_t tiles = (capacity + tile - 1) / tile * a.B, all = static_cast<int64_t>(p.ranges) * loaders;
+  if (tiles < (a.B <= 2 ? 2 * all : all)) p.ranges = (p.ranges + 1) / 2;
   return p;
 }
 

@@ -130,6 +130,7 @@ template <int D, int NT, int WARPS>
 struct Q4Cfg {
   static constexpr int kTile = 32;  // tokens a warp takes at a time, one a lane where pages are looked up
   static constexpr int kWarps = WARPS;
+  static constexpr int kProducts = D * NT <= 256 ? 2 : 1;  // two more than registers hold with 16 heads of 256
   static constexpr int kStages = WARPS == 8 && D * NT <= 128 ? 4 : 2;
   static constexpr int kCodes = kTile * D / 2, kScales = kTile * D / 16;  // bytes of K, and the same of V
   static constexpr int kStage = 2 * (kCodes + kScales);
@@ -160,7 +161,8 @@ __device__ __forceinline__ int token_of(int r) { return r ^ (r >> 2 & 1); }
 template <int D, int NT, int WARPS, bool W>
 __global__ void __launch_bounds__(WARPS * 32, 1) decode_q4_kernel(const __grid_constant__ Kernelargs k) {
   using C = Q4Cfg<D, NT, WARPS>;
-  constexpr int TILE = C::kTile, MT = TILE / 16, STAGES = C::kStages;
+  constexpr int TILE = C::kTile, STAGES = C::kStages;
+  constexpr int MT = C::kProducts;  // products of 16 tokens at a time
   constexpr int CH = D / 32;          // 16-byte pieces of a row's codes
   constexpr int KW = D / 32;          // words of a K row that a lane takes (8 channels each)
   constexpr int VB = D / 16;          // bytes of a V row that a lane takes, and of a row's scales
@@ -391,9 +393,12 @@ __global__ void __launch_bounds__(WARPS * 32, 1) decode_q4_kernel(const __grid_c
         for (int i = 0; i + 1 < STAGES; ++i) mask_of[i] = mask_of[i + 1];
         ++turn;
         const uint32_t stage = ring + st * C::kStage;
-        const uint32_t k_at = stage + (of_k & 0xFFFFu), ks_at = stage + (of_k >> 16);
-        const uint32_t v_at[2] = {stage + (of_v[0] & 0xFFFFu), stage + (of_v[1] & 0xFFFFu)};
-        const uint32_t vs_at[2] = {stage + (of_v[0] >> 16), stage + (of_v[1] >> 16)};
+#pragma unroll 1
+        for (int sub = 0; sub < TILE / 16; sub += MT) {
+        const uint32_t codes_at = stage + sub * (16 * (D / 2)), scales_at = stage + sub * (16 * VB);
+        const uint32_t k_at = codes_at + (of_k & 0xFFFFu), ks_at = scales_at + (of_k >> 16);
+        const uint32_t v_at[2] = {codes_at + (of_v[0] & 0xFFFFu), codes_at + (of_v[1] & 0xFFFFu)};
+        const uint32_t vs_at[2] = {scales_at + (of_v[0] >> 16), scales_at + (of_v[1] >> 16)};
         float s[NT][MT][4];
 #pragma unroll
         for (int mt = 0; mt < MT; ++mt) {
@@ -441,6 +446,7 @@ __global__ void __launch_bounds__(WARPS * 32, 1) decode_q4_kernel(const __grid_c
         }
         // lane: tokens token_of(g) and 8 more of each 16, heads 2 t and 2 t + 1 of each 8
         if (mask != 0xFFFFFFFFu) {
+          const uint32_t here = mask >> (16 * sub);
           asm volatile("" ::: "memory");  // a branch, not selects
 #pragma unroll
           for (int n = 0; n < NT; ++n)
@@ -448,7 +454,7 @@ __global__ void __launch_bounds__(WARPS * 32, 1) decode_q4_kernel(const __grid_c
             for (int mt = 0; mt < MT; ++mt)
 #pragma unroll
               for (int e = 0; e < 4; ++e)
-                if (!((mask >> (mt * 16 + token_of(g) + (e < 2 ? 0 : 8))) & 1u)) s[n][mt][e] = -INFINITY;
+                if (!((here >> (mt * 16 + token_of(g) + (e < 2 ? 0 : 8))) & 1u)) s[n][mt][e] = -INFINITY;
         }
         if constexpr (W) {
 #pragma unroll
@@ -456,7 +462,7 @@ __global__ void __launch_bounds__(WARPS * 32, 1) decode_q4_kernel(const __grid_c
 #pragma unroll
             for (int c = 0; c < 2; ++c) {
               const int h = n * 8 + 2 * t + c;
-              float* row = a.scores + (static_cast<int64_t>(b) * a.Hq + head0 + h) * a.score_stride + tile * TILE + token_of(g);
+              float* row = a.scores + (static_cast<int64_t>(b) * a.Hq + head0 + h) * a.score_stride + tile * TILE + sub * 16 + token_of(g);
 #pragma unroll
               for (int mt = 0; mt < MT; ++mt)
                 if (h < heads) {
@@ -533,6 +539,7 @@ __global__ void __launch_bounds__(WARPS * 32, 1) decode_q4_kernel(const __grid_c
               }
             }
           }
+        }
         }
         __syncwarp();  // the stage is read; the next turn's load may fill it
       }
@@ -645,7 +652,7 @@ int warps_of(const DecodeArgs& a, int sms) {
   const int64_t units = static_cast<int64_t>(a.Hkv) * ((a.Hq / a.Hkv + 15) / 16);
   return (capacity + 31) / 32 * a.B * units >= 160LL * sms ? 16 : 8;
 }
-DecodePlan plan_of(const DecodeArgs& a, int sms, bool split) { return make_plan(a, sms, split, warps_of(a, sms), 32, 1); }
+DecodePlan plan_of(const DecodeArgs& a, int sms, bool split) { return make_plan(a, sms, split, warps_of(a, sms), 32, 1, 2); }
 
 template <int D, int NT, int WARPS, bool W>
 cudaError_t launch_d(const Kernelargs& k, cudaStream_t stream) {
