@@ -187,3 +187,32 @@ def test_refusals(h3):
             call(**bad)
     with pytest.raises(h3.H3AttnError):
         h3.paged_evict_workspace(c.cache, 0, 0)
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("kind", ["plain", "ties"])
+def test_more_weights_than_shared_memory_holds(h3, kind):
+    """A sequence whose weights are read anew in each pass; the tokens numbered in their rows."""
+    n, keep, recent, page = 900001, 500000, 1000, 64
+    pages = -(-n // page)
+    held = [torch.zeros(pages, page, 1, 64 // m, dtype=torch.uint8, device="cuda") for m in (2, 2, 16, 16)]
+    table = torch.randperm(pages, generator=torch.Generator().manual_seed(3)).int()
+    token = torch.arange(pages * page, device="cuda").view(pages, page)[torch.argsort(table).cuda()]  # of each row
+    held[0].view(torch.int64)[..., 0, 0] = token
+    held[2].view(torch.int32)[..., 0, 0] = token.int()
+    cache = h3.PagedKV4(*held, table[None].cuda(), torch.tensor([n], dtype=torch.int32, device="cuda"))
+    w = weights_of(kind, (1, pages * page), 5).cuda()
+    before, out = w.clone(), torch.zeros(1, dtype=torch.int32, device="cuda")
+    h3.h3attn_paged_evict(cache, w, keep, recent, out, h3.paged_evict_workspace(cache, keep, recent))
+    assert out.tolist() == [keep] and h3.h3attn_check_device_status() == 0
+    place = torch.arange(keep, device="cuda")
+    row = table.cuda().long()[place // page], place % page
+    front, old = keep - recent, n - recent
+    stay = torch.sort(before[0, :old], descending=True, stable=True)[1][:front].sort()[0]
+    gaps = torch.ones(front, dtype=torch.bool, device="cuda").index_fill_(0, stay[stay < front], False).nonzero()[:, 0]
+    want = torch.arange(keep, device="cuda")
+    want[gaps] = stay[stay >= front]
+    want[front:] = torch.arange(old, n, device="cuda")
+    assert torch.equal(held[0].view(torch.int64)[..., 0, 0][row], want)
+    assert torch.equal(held[2].view(torch.int32)[..., 0, 0][row], want.int())
+    assert torch.equal(w[0, :keep], before[0, want]) and bool((w[0, keep:n] == 0).all()) and torch.equal(w[0, n:], before[0, n:])
