@@ -44,7 +44,8 @@ __device__ __forceinline__ uint32_t transpose8x8(uint32_t v) {
 // Unit heads and the shape of the launch, the same on the host and in both kernels.
 struct DecodePlan {
   int unit_heads;  // Hkv * tiles of query heads
-  int q_tiles;     // tiles of at most 16 query heads in a group
+  int q_tiles;     // tiles of at most tile_heads query heads in a group
+  int tile_heads;
   int WH, WT;      // warps of a CTA: unit heads x token splits
   int share;       // neighbouring tiles of query heads whose warps load for one another (1 or 2)
   int groups;      // CTAs across the unit heads
@@ -169,7 +170,7 @@ constexpr int kFewParts = 4;  // partials that a warp asks for at a time: a head
 // sit beside a decode CTA.
 template <int D, bool W>
 __global__ void __launch_bounds__(kJoinThreads) __maxnreg__(D == 256 ? 96 : 56)
-    decode_join_kernel(const __grid_constant__ Kernelargs k, int tile, int tile_heads) {
+    decode_join_kernel(const __grid_constant__ Kernelargs k, int tile, int part_heads) {
   constexpr int VEC = D / 32, WARPS = kJoinThreads / 32;
   static_assert((WARPS & (WARPS - 1)) == 0, "warps are shared out to heads in powers of two");
   const DecodeArgs& a = k.a;
@@ -209,7 +210,7 @@ __global__ void __launch_bounds__(kJoinThreads) __maxnreg__(D == 256 ? 96 : 56)
   if (kind >= 0) split[kind][at + __popc(same[kind] & ((1u << lane) - 1u))] = mine;
   __syncthreads();
   const int G = a.Hq / a.Hkv;
-  const int64_t unit_floats = partial_floats(tile_heads, D), stride = 2 * p.unit_heads * unit_floats;  // from range to range
+  const int64_t unit_floats = partial_floats(part_heads, D), stride = 2 * p.unit_heads * unit_floats;  // from range to range
   // A head of a split sequence: its partial of the first range (slot 1 where that range begins in another sequence), the
   // lane's part of it, and the row it goes to.
   struct Head {
@@ -222,11 +223,11 @@ __global__ void __launch_bounds__(kJoinThreads) __maxnreg__(D == 256 ? 96 : 56)
     const int in_list = i / a.Hq, h = i - in_list * a.Hq;
     const uint32_t q = split[list][in_list];
     const int b = q >> 16, r0 = (q >> 8) & 255;
-    const int kvh = h / G, in_group = h - kvh * G, qt = in_group / 16, hh = in_group - qt * 16;
+    const int kvh = h / G, in_group = h - kvh * G, qt = in_group / p.tile_heads, hh = in_group - qt * p.tile_heads;
     const float* part = a.ws + r0 * stride + (kvh * p.q_tiles + qt) * unit_floats;
     Head x;
     x.ml = part + 2 * hh;
-    x.o = part + partial_o(tile_heads) + hh * D + lane * VEC;
+    x.o = part + partial_o(part_heads) + hh * D + lane * VEC;
     x.out = a.o + (static_cast<int64_t>(b) * a.Hq + h) * D + lane * VEC;
     x.slot1 = ranges.begin(r0) >= (b > 0 ? end[b - 1] : 0) ? 0 : stride / 2;
     x.n = static_cast<int>(q & 255) - r0 + 1;
@@ -343,13 +344,16 @@ inline cudaError_t sm_count(int* sms) {
   return e != cudaSuccess ? e : cudaDeviceGetAttribute(sms, cudaDevAttrMultiProcessorCount, dev);
 }
 
-// The shape of a launch whose CTAs have `warps` warps that take `tile` tokens at a time; the warps of `share` neighbouring
+// The shape of a launch whose CTAs have `warps` warps that take `tile` tokens and up to `tile_heads` query heads of a
+// group at a time; the warps of `share` neighbouring
 // tiles of query heads load for one another where there is an even number of those; caches of at most `few` tiles a
 // warp are walked whole.
-inline DecodePlan make_plan(const DecodeArgs& a, int sms, bool split, int warps, int tile, int share, int few) {
+inline DecodePlan make_plan(const DecodeArgs& a, int sms, bool split, int warps, int tile, int tile_heads, int share,
+                             int few) {
   DecodePlan p;
   const int G = a.Hq / a.Hkv;
-  p.q_tiles = (G + 15) / 16;
+  p.tile_heads = tile_heads;
+  p.q_tiles = (G + tile_heads - 1) / tile_heads;
   p.unit_heads = a.Hkv * p.q_tiles;
   p.WH = 1;
   while (p.WH < warps && p.unit_heads % (2 * p.WH) == 0) p.WH *= 2;

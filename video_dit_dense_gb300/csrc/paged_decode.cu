@@ -548,7 +548,7 @@ int tile_of(int D) { return D == 64 ? 32 : 16; }
 // Heads of 64, 9 sequences of 20000 to 40000: 22.9 without, 23.6 with (DRAM 40 %, tensor pipe 29 %).
 int share_of(int D) { return D > 64 ? 2 : 1; }
 DecodePlan plan_of(const DecodeArgs& a, int sms, bool split) {
-  return make_plan(a, sms, split, warps_of(a.D), tile_of(a.D), share_of(a.D), 4);
+  return make_plan(a, sms, split, warps_of(a.D), tile_of(a.D), 16, share_of(a.D), 4);
 }
 
 template <int D, int NT, int SHARE, bool W>

@@ -125,12 +125,12 @@ __device__ __forceinline__ uint32_t high2(uint32_t x, uint32_t k1024, const Scal
   return hfma2((x & 0x00F000F0u) | k1024, s.m, s.c1);
 }
 
-// NT: tiles of 8 query heads (1 or 2).
+// NT: tiles of 8 query heads (1, 2 or 4).
 template <int D, int NT, int WARPS>
 struct Q4Cfg {
   static constexpr int kTile = 32;  // tokens a warp takes at a time, one a lane where pages are looked up
   static constexpr int kWarps = WARPS;
-  static constexpr int kProducts = D * NT <= 256 ? 2 : 1;  // two more than registers hold with 16 heads of 256
+  static constexpr int kProducts = D * NT <= 256 ? 2 : 1;  // two are more than registers hold with 16 heads of 256
   static constexpr int kStages = WARPS == 8 && D * NT <= 128 ? 4 : 2;
   static constexpr int kCodes = kTile * D / 2, kScales = kTile * D / 16;  // bytes of K, and the same of V
   static constexpr int kStage = 2 * (kCodes + kScales);
@@ -189,8 +189,8 @@ __global__ void __launch_bounds__(WARPS * 32, 1) decode_q4_kernel(const __grid_c
   const int unit = (blockIdx.x - r * p.groups) * p.WH + wh;
   const int kvh = unit / p.q_tiles, qt = unit - kvh * p.q_tiles;
   const int G = a.Hq / a.Hkv;
-  const int head0 = kvh * G + qt * 16;            // first query head of the unit
-  const int heads = min(G - qt * 16, C::kHeads);  // its query heads
+  const int head0 = kvh * G + qt * p.tile_heads;            // first query head of the unit
+  const int heads = min(G - qt * p.tile_heads, C::kHeads);  // its query heads
 
   // This CTA's tiles [t0, t1) of all sequences' tiles.  Without a split the range is sequence r.
   int t0, t1, b0;
@@ -643,16 +643,25 @@ __global__ void __launch_bounds__(WARPS * 32, 1) decode_q4_kernel(const __grid_c
   cp_async_wait<0>();
 }
 
+// Query heads that a warp takes at a time, 8, 16 or 32: codes become operands once for all of them.  With heads of 256
+// registers end at 16.
+int heads_of(const DecodeArgs& a) {
+  const int G = a.Hq / a.Hkv;
+  return G <= 8 ? 8 : G <= 16 || a.D == 256 ? 16 : 32;
+}
 // Warps of a CTA.  Heads of 128 and two column tiles, or of 256, leave registers for 8.  Otherwise 16 where each has many
 // tiles (one sequence of 104448 tokens, 24 heads of 128: 75 us, with 8 warps 83), and 8 where they have few, whose registers leave room
 // for the joining kernel beside them (16 sequences of up to 8192, 16 and 4 heads: 23 and 21).
 int warps_of(const DecodeArgs& a, int sms) {
-  if (a.D * (a.Hq / a.Hkv > 8 ? 2 : 1) > 128) return 8;
+  const int heads = heads_of(a), G = a.Hq / a.Hkv;
+  if (a.D * heads > 1024) return 8;
   const int64_t capacity = static_cast<int64_t>(a.max_pages) * a.page_size;
-  const int64_t units = static_cast<int64_t>(a.Hkv) * ((a.Hq / a.Hkv + 15) / 16);
+  const int64_t units = static_cast<int64_t>(a.Hkv) * ((G + heads - 1) / heads);
   return (capacity + 31) / 32 * a.B * units >= 160LL * sms ? 16 : 8;
 }
-DecodePlan plan_of(const DecodeArgs& a, int sms, bool split) { return make_plan(a, sms, split, warps_of(a, sms), 32, 1, 2); }
+DecodePlan plan_of(const DecodeArgs& a, int sms, bool split) {
+  return make_plan(a, sms, split, warps_of(a, sms), 32, heads_of(a), 1, 2);
+}
 
 template <int D, int NT, int WARPS, bool W>
 cudaError_t launch_d(const Kernelargs& k, cudaStream_t stream) {
@@ -685,7 +694,9 @@ cudaError_t launch_warps(const Kernelargs& k, cudaStream_t stream) {
 
 template <int D>
 cudaError_t launch_heads(const Kernelargs& k, cudaStream_t stream) {
-  return k.a.Hq / k.a.Hkv > 8 ? launch_warps<D, 2>(k, stream) : launch_warps<D, 1>(k, stream);
+  if constexpr (D < 256)
+    if (k.p.tile_heads == 32) return launch_warps<D, 4>(k, stream);
+  return k.p.tile_heads == 16 ? launch_warps<D, 2>(k, stream) : launch_warps<D, 1>(k, stream);
 }
 
 }  // namespace
@@ -695,7 +706,7 @@ cudaError_t decode_q4_workspace(const DecodeArgs& a, size_t* bytes) {
   cudaError_t e = sm_count(&sms);
   if (e != cudaSuccess) return e;
   const DecodePlan p = plan_of(a, sms, true);
-  const int heads = std::min(a.Hq / a.Hkv, 16);
+  const int heads = std::min(a.Hq / a.Hkv, p.tile_heads);
   *bytes = static_cast<size_t>(p.ranges) * 2 * p.unit_heads * partial_floats(heads, a.D) * sizeof(float);
   return cudaSuccess;
 }
