@@ -18,7 +18,7 @@
 // sequence of 104448 tokens.
 //
 // Second kernel: moves the rows, d = n - keep places down.  Movers from beyond `keep`
-// are not in the way of anything: a warp takes a row.  The place front + c is read
+// are not in the way of anything: a warp, or as many of its lanes as a short row has pieces, takes a row.  The place front + c is read
 // by its mover, if it has one, then written by the recent row from old + c = front + c + d,
 // whose place is then written by the one from old + c + d, and so on: a chain, in which a warp
 // takes one row after the other, so that each of its lanes reads what it later overwrites.
@@ -311,6 +311,7 @@ constexpr int kMoveUnroll = 4;
 struct MovePlan {
   int columns[4];  // CTAs that own kLanes pieces of each array
   int piece[2];    // bytes of a piece of K and V, and of the scales: 16, 8 or 4
+  int lanes_log2;  // lanes that take a row where columns are not owned
 };
 
 // The moves that are in order: `below` movers, then the recent rows, of the pieces from piece0 on.
@@ -354,20 +355,19 @@ __device__ __forceinline__ void move_column(const EvictArgs& a, uint8_t* base, i
   move(a.recent, [&](int i) { return row_of(a, table, old + i); }, [&](int i) { return row_of(a, table, front + i); });
 }
 
-// `pieces` pieces of each of two arrays, from row src to row dst, by the lanes of a warp.
+// `pieces` pieces of each of two arrays, from row src to row dst, by `lanes` lanes of a warp.
 template <class T>
-__device__ __forceinline__ void move_row(uint8_t* first, uint8_t* second, int pieces, int64_t src, int64_t dst) {
-  const int lane = threadIdx.x & 31;
-  for (int i0 = lane; i0 < 2 * pieces; i0 += 32 * kMoveUnroll) {
+__device__ __forceinline__ void move_row(uint8_t* first, uint8_t* second, int pieces, int64_t src, int64_t dst, int lanes) {
+  for (int i0 = threadIdx.x & (lanes - 1); i0 < 2 * pieces; i0 += lanes * kMoveUnroll) {
     T x[kMoveUnroll];
 #pragma unroll
     for (int u = 0; u < kMoveUnroll; ++u) {
-      const int i = i0 + 32 * u;
+      const int i = i0 + lanes * u;
       if (i < 2 * pieces) x[u] = reinterpret_cast<const T*>(i < pieces ? first : second)[src * pieces + (i < pieces ? i : i - pieces)];
     }
 #pragma unroll
     for (int u = 0; u < kMoveUnroll; ++u) {
-      const int i = i0 + 32 * u;
+      const int i = i0 + lanes * u;
       if (i < 2 * pieces) reinterpret_cast<T*>(i < pieces ? first : second)[dst * pieces + (i < pieces ? i : i - pieces)] = x[u];
     }
   }
@@ -388,8 +388,9 @@ __global__ void __launch_bounds__(kMoveThreads, 4) evict_move_kernel(const __gri
     const int32_t* const table = a.page_table + static_cast<int64_t>(b) * a.max_pages;
     const int below = list[1], old = n - a.recent, front = a.keep - a.recent;
     const int64_t items = static_cast<int64_t>(chains) + list[0] - below;
-    for (int64_t i = static_cast<int64_t>(blockIdx.x) * (kMoveThreads / 32) + (threadIdx.x >> 5); i < items;
-         i += gridDim.x * (kMoveThreads / 32)) {
+    const int lanes = 1 << p.lanes_log2, at_once = kMoveThreads >> p.lanes_log2;
+    for (int64_t i = static_cast<int64_t>(blockIdx.x) * at_once + (threadIdx.x >> p.lanes_log2); i < items;
+         i += static_cast<int64_t>(gridDim.x) * at_once) {
       // a chain: its first place goes to a gap, if it is a mover's, and each recent row to the place moved or left before
       const bool in_chain = i < chains;
       int src = in_chain ? row_of(a, table, front + static_cast<int>(i)) : from[below + i - chains];
@@ -397,8 +398,8 @@ __global__ void __launch_bounds__(kMoveThreads, 4) evict_move_kernel(const __gri
       int64_t r = in_chain ? i : a.recent;
       while (true) {
         if (src >= 0 && dst >= 0) {
-          move_row<uint4>(a.row[0], a.row[1], a.row_bytes[0] / 16, src, dst);
-          if (a.row[2]) move_row<uint32_t>(a.row[2], a.row[3], a.row_bytes[1] / 4, src, dst);
+          move_row<uint4>(a.row[0], a.row[1], a.row_bytes[0] / 16, src, dst, lanes);
+          if (a.row[2]) move_row<uint32_t>(a.row[2], a.row[3], a.row_bytes[1] / 4, src, dst, lanes);
         }
         if (r >= a.recent) break;
         dst = src;
@@ -426,15 +427,24 @@ __global__ void __launch_bounds__(kMoveThreads, 4) evict_move_kernel(const __gri
 }  // namespace
 
 cudaError_t launch_evict(const EvictArgs& a, cudaStream_t stream) {
-  // One CTA for up to 8192 tokens, which has no cluster to wait for; then as many as leave 4096 each, up to 16.
+  int sms = 0;
+  cudaError_t e = sm_count(&sms);
+  if (e != cudaSuccess) return e;
+  // One CTA for up to 8192 tokens, which has no cluster to wait for; then as many as leave 4096 each, up to 16, and up to
+  // one an SM over all sequences (35 of 37518 tokens: 16 each, in four waves, 199 us, 4 each 80), but for weights that
+  // shared memory does not hold otherwise.
+  const int64_t most_old = std::max<int64_t>(a.capacity - a.recent, 0);
+  auto held_by = [&](uint32_t ctas) { return tokens_per_warp(most_old, ctas) * kSelectWarps; };
   uint32_t ctas = 1;
-  while (ctas < kMostCtas && a.capacity > 8192 && a.capacity > 4096 * static_cast<int64_t>(ctas)) ctas *= 2;
-  const int64_t each = tokens_per_warp(a.capacity - a.recent > 0 ? a.capacity - a.recent : 0, ctas) * kSelectWarps;
+  while (ctas < kMostCtas && a.capacity > 8192 && a.capacity > 4096 * static_cast<int64_t>(ctas) &&
+         (static_cast<int64_t>(a.B) * ctas * 2 <= sms || held_by(ctas) > kMostHeld))
+    ctas *= 2;
+  const int64_t each = held_by(ctas);
   const bool fits = each <= kMostHeld;
   auto* const select = fits ? evict_select_kernel<true> : evict_select_kernel<false>;
   static std::atomic<bool> attr_set[64];  // calls of several host threads
   int dev = 0;
-  cudaError_t e = cudaGetDevice(&dev);
+  e = cudaGetDevice(&dev);
   if (e != cudaSuccess) return e;
   if (dev < 0 || dev >= 64) return cudaErrorInvalidDevice;
   if (!attr_set[dev]) {
@@ -469,13 +479,11 @@ cudaError_t launch_evict(const EvictArgs& a, cudaStream_t stream) {
     p.columns[i] = (bytes / p.piece[i >> 1] + kLanes - 1) / kLanes;
     columns += p.columns[i];
   }
-  // chains and movers from beyond keep: a warp for each that there may be, up to 8 CTAs an SM over all sequences
-  const int64_t longest = std::max<int64_t>(a.capacity - a.keep, 0);  // d
+  while (p.lanes_log2 < 5 && (1 << p.lanes_log2) < a.row_bytes[0] / 16 * 2) ++p.lanes_log2;
+  // chains and movers from beyond keep: lanes for each that there may be, up to 8 CTAs an SM over all sequences
+  const int64_t longest = std::max<int64_t>(a.capacity - a.keep, 0), at_once = kMoveThreads >> p.lanes_log2;
   const int64_t items = std::min<int64_t>(a.recent, longest) + std::min<int64_t>(a.most, std::max<int64_t>(longest - a.recent, 0));
-  int sms = 0;
-  e = sm_count(&sms);
-  if (e != cudaSuccess) return e;
-  const int64_t dealt = std::min<int64_t>((items + 7) / 8, std::max(8 * sms / a.B, 1));
+  const int64_t dealt = std::min<int64_t>((items + at_once - 1) / at_once, std::max(8 * sms / a.B, 1));
   return launch_dependent(evict_move_kernel, dim3(static_cast<unsigned>(std::max<int64_t>(columns, dealt)), static_cast<unsigned>(a.B)),
                           kMoveThreads, 0, stream, a, p);
 }
