@@ -534,16 +534,18 @@ h3attn_status_t h3attn_paged_decode_workspace_size(const h3attn_paged_kv_t* cach
  * h3attn_paged_kv_t, a row of D channels held as D / 2 bytes of codes and D / 16
  * scales.  Channel d of a row stands for (c - 8) s, where
  *   c = the lower (d even) or upper (d odd) half of byte d / 2,
- *   s = the binary16 whose bits are byte d / 16 of the row's scales, moved up by 7
- *       (an unsigned float of 5 exponent and 3 mantissa bits: 0, 2^-17 to 3840 in
- *       steps of at most 1/8); bytes above 0xD7 (3840) stand for NaN.
+ *   s = the binary16 whose bits are byte d / 16 of the row's scales, moved up by 7:
+ *       an unsigned float of 5 exponent and 3 mantissa bits, 0 or 2^-17 to 3840
+ *       (0xD7).  0xFF stands for NaN; the bytes between are not stored, and what a
+ *       row with one of them gives is not defined (h3attn_paged_read_q4(): NaN).
  * A row x is stored with, for each 16 neighbouring channels,
  *   s = max |x| / 7 rounded to the nearest scale (ties to the even byte), at most 3840,
  *   c = 8 + min(max(k, -8), 7), k = x / s rounded to the nearest integer, ties away from 0;
  *   c = 8 where s is 0.  An infinity or a NaN among the 16 makes all of them NaN (s = 0xFF).
- * Values are exact in bf16.  Errors are at most s / 2, and at most s where k was
- * cut at -8 or 7, which happens for normal scales (from 2^-14 on) only to x beyond 7.5 s; groups whose
- * maximum lies past 26880 are cut at 7 * 3840.
+ * Values are exact in bf16.  From a maximum of 2^-11 to 26880 errors are at most
+ * s / 2; for rows like noise s is about 0.3 standard deviations and the error 0.09 of
+ * them (root mean square).  Below, scales become coarse (and 0 below 7 * 2^-18);
+ * above, values are cut at -8 * 3840 and 7 * 3840.
  * 4.5 bits a channel.
  */
 typedef struct {
@@ -598,15 +600,16 @@ h3attn_status_t h3attn_paged_read_q4(const h3attn_paged_kv4_t* cache, void* k, v
  * The queries are taken in binary16 after scaling each head's row by a power of
  * two, exact but for channels below 2^-20 of the row's largest, and a weight is
  * kept to 11 bits in the second product; sums are float32, the output is
- * rounded once to bf16.  Results do not depend on timing.
+ * rounded once to bf16.  Results do not depend on timing.  Another workspace size
+ * than for a cache in bf16.
  */
 h3attn_status_t h3attn_paged_decode_q4(const void* q, void* o, const h3attn_paged_kv4_t* cache, int Hq, float scale,
                                        void* workspace, size_t workspace_bytes, h3attn_stream_t stream);
 h3attn_status_t h3attn_paged_decode_q4_workspace_size(const h3attn_paged_kv4_t* cache, int Hq, size_t* bytes);
 
 /*
- * The decode attention, with what each token of the cache was attended to by
- * all query heads added up:
+ * The decode attention, with the weight that each token of the cache was attended
+ * with, summed over the query heads, added up:
  *   weights[b, j] += sum_h softmax_j(scale * q[b, h] . k_j),   j < kv_len[b],
  * o as in h3attn_paged_decode() and h3attn_paged_decode_q4().  The sum over h is
  * in the order of the heads, float32.  Tokens of a page outside [0, num_pages)
@@ -638,19 +641,20 @@ h3attn_status_t h3attn_paged_decode_weights_q4_workspace_size(const h3attn_paged
  *   - the recent ones take places keep - recent to keep - 1 in their order.
  * A decode step does not depend on the order of a cache (a key's position is in
  * its rotation), so few rows move: appends go on at len_out, with their own pos.
- * weights move with their tokens, those of the places from keep to n - 1 become 0,
- * and so does what is appended there; rows and weights of the other places stay as they were.  Sequences of at most keep tokens
- * are left as they are.
+ * weights move with their tokens, and those of the places from keep to n - 1 become
+ * 0, where the next tokens are appended; rows there and all other places stay as they
+ * were.  Sequences of at most keep tokens are left as they are.
  * Pages of the places that change must be the sequence's own.  Rows that lie in a
  * page outside [0, num_pages), or are to go to one, are not moved (and reported).
  *
  * weights: [B, max_pages * page_size] float32, 4-byte aligned.
  * keep >= 1, 0 <= recent <= keep.  len_out: [B] int32, receives min(kv_len, keep)
- *    (at least 0; kv_len is not changed); may not be kv_len.
+ *    (at least 0); it may not be kv_len, which is not changed.
  * workspace: h3attn_paged_evict_workspace_size() bytes for the same sizes, 16-byte
- *    aligned (NULL where that is 0: B == 0); its contents on entry do not matter.  Calls that share one must be ordered.
- * Outputs (pages, weights, len_out, workspace) overlap nothing else.  Stream order as for
- * h3attn_rmsnorm_modulate().
+ *    aligned (NULL where that is 0: B == 0); its contents on entry do not matter.
+ *    Calls that share one must be ordered: one stream, events, or graphs replayed in turn.
+ * B == 0 is a no-op.  Outputs (pages, weights, len_out, workspace) overlap nothing
+ * else.  Stream order as for h3attn_rmsnorm_modulate().
  * Errors: INVALID_ARG, MISALIGNED, UNSUPPORTED_HEAD_DIM, UNSUPPORTED_DEVICE, LAUNCH.
  */
 h3attn_status_t h3attn_paged_evict(const h3attn_paged_kv_t* cache, float* weights, int keep, int recent,

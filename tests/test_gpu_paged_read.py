@@ -96,3 +96,27 @@ def test_refusals(h3):
         with pytest.raises(h3.H3AttnError):
             h3.h3attn_paged_read(*bad)
     h3.h3attn_paged_read(cache, k[:, :0], None)
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("bits", [4, 16])
+@pytest.mark.parametrize("Hkv,D", [(1, 64), (1, 128), (2, 64), (3, 64), (1, 256), (2, 128)])
+def test_many_tokens_of_short_rows(h3, bits, Hkv, D):
+    """Several tokens of a lane at a time: sequences that end at every place among them, starts, bad pages."""
+    lens = [0, 1, 2, 3, 4, 5, 4999, 5003, 5002, 5000, 17, 5001]
+    p = Pages(bits, len(lens), 5003, 24, Hkv, D, 3, poison=False)
+    p.table[7, 3] = -1
+    cache = p.hold().cuda(h3, lens)
+    first = torch.tensor([0, 0, 0, 1, 0, 2, -3, 5, 0, 1, 0, 0], dtype=torch.int32)
+    outs = [torch.full((len(lens), 5003, Hkv, D), 5.0, dtype=torch.bfloat16, device="cuda") for _ in range(2)]
+    h3.h3attn_paged_read(cache, *outs, first=first.cuda())
+    assert h3.h3attn_check_device_status() == h3.H3ATTN_ERR_INVALID_ARG
+    for out, kv in zip(outs, p.kv):
+        want = torch.full(out.shape, 5.0, dtype=torch.bfloat16)
+        for b, n in enumerate(lens):
+            s = torch.arange(5003)
+            j = s + int(first[b])
+            ok = (j >= 0) & (j < n)
+            ok[ok.clone()] &= p.table[b][j[ok] // 24] >= 0
+            want[b, s[ok]] = kv[p.table[b][j[ok] // 24].long(), j[ok] % 24].to(torch.bfloat16)
+        assert torch.equal(out.cpu(), want)
