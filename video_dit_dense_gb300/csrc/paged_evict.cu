@@ -431,7 +431,7 @@ cudaError_t launch_evict(const EvictArgs& a, cudaStream_t stream) {
   cudaError_t e = sm_count(&sms);
   if (e != cudaSuccess) return e;
   // One CTA for up to 8192 tokens, which has no cluster to wait for; then as many as leave 4096 each, up to 16, and up to
-  // one an SM over all sequences (35 of 37518 tokens: 16 each, in four waves, 199 us, 4 each 80), but for weights that
+  // one an SM over all sequences (35 of 37518 tokens: 16 each, in four waves, 124 us, 4 each 49), but for weights that
   // shared memory does not hold otherwise.
   const int64_t most_old = std::max<int64_t>(a.capacity - a.recent, 0);
   auto held_by = [&](uint32_t ctas) { return tokens_per_warp(most_old, ctas) * kSelectWarps; };
