@@ -237,12 +237,16 @@ __global__ void __launch_bounds__(kSelectThreads, 1) evict_select_kernel(const _
     n_gaps += __popc(gaps);
     const int64_t left = static_cast<int64_t>(a.keep) - j0;  // this turn's tokens below keep
     n_below += left >= 32 ? __popc(movers) : left > 0 ? __popc(movers & ((1u << left) - 1u)) : 0;
+    if constexpr (HELD) {  // in the place of the turn's weights, for the second time over them
+      __syncwarp();
+      if (lane < 2) mine[j0 + lane] = lane == 0 ? movers : gaps;
+    }
   });
   const Scan at = cluster_scan(n_movers, n_gaps, n_below, ctas, rank, sums[1]);
   uint32_t to_mover = at.x, to_gap = at.y;
   int *const from = list + kEvictHeader, *const to = from + a.most, *const chain = to + a.most;
   const int chains = min(a.recent, n - a.keep);
-  walk([&](int j0, uint32_t movers, uint32_t gaps) {
+  auto list_turn = [&](int j0, uint32_t movers, uint32_t gaps) {
     const uint32_t before = (1u << lane) - 1u;
     const int c = j0 + lane - front;  // the chain that begins with this place
     if (c >= 0 && c < chains && j0 + lane < end && !(movers >> lane & 1u)) chain[c] = -1;
@@ -250,57 +254,64 @@ __global__ void __launch_bounds__(kSelectThreads, 1) evict_select_kernel(const _
     if (gaps >> lane & 1u) to[to_gap + __popc(gaps & before)] = j0 + lane;
     to_mover += __popc(movers);
     to_gap += __popc(gaps);
-  });
+  };
+  if constexpr (HELD) {
+#pragma unroll 4
+    for (int j0 = begin; j0 < end; j0 += 32) list_turn(j0, mine[j0], mine[j0 + 1]);
+  } else {
+    walk(list_turn);
+  }
   const int moves = static_cast<int>(at.all_x);
   if (rank == 0 && threadIdx.x == 0) {
     list[0] = moves;
     list[1] = static_cast<int>(at.all_z);
   }
   cluster_sync();
-  // ---- the weights move: gaps are below all movers and recent ones, which are read before they are overwritten ----
-  {
-    constexpr int U = 2;
-    const int64_t step = static_cast<int64_t>(ctas) * kSelectThreads;
-    for (int64_t i0 = static_cast<int64_t>(rank) * kSelectThreads + threadIdx.x; i0 < moves; i0 += U * step) {
-      int f[U], t[U];
+  // ---- the weights move: gaps are below all movers and recent ones; the recent ones, from the first on, to where movers
+  // and they themselves have been read ----
+  constexpr int U = 2, R = 4;
+  const int64_t step = static_cast<int64_t>(ctas) * kSelectThreads, me = static_cast<int64_t>(rank) * kSelectThreads + threadIdx.x;
+  float recent_w[R];  // the first CTA's
+  auto read_recent = [&](int64_t i0) {
 #pragma unroll
-      for (int u = 0; u < U; ++u) {
-        f[u] = i0 + u * step < moves ? from[i0 + u * step] : -1;
-        t[u] = f[u] >= 0 ? to[i0 + u * step] : -1;
-      }
+    for (int u = 0; u < R; ++u)
+      if (i0 + u * kSelectThreads < a.recent) recent_w[u] = weights[old + i0 + u * kSelectThreads];
+  };
+  auto write_recent = [&](int64_t i0) {
 #pragma unroll
-      for (int u = 0; u < U; ++u) {
-        if (f[u] < 0) continue;
-        weights[t[u]] = weights[f[u]];
-        const int to_row = row_of(a, table, t[u]);
-        from[i0 + u * step] = row_of(a, table, f[u]);
-        to[i0 + u * step] = to_row;
-        if (f[u] < a.keep) chain[f[u] - front] = to_row;
-      }
+    for (int u = 0; u < R; ++u)
+      if (i0 + u * kSelectThreads < a.recent) weights[front + i0 + u * kSelectThreads] = recent_w[u];
+  };
+  if (rank == 0) read_recent(threadIdx.x);
+  for (int64_t i0 = me; i0 < moves; i0 += U * step) {
+    int f[U], t[U];
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+      f[u] = i0 + u * step < moves ? from[i0 + u * step] : -1;
+      t[u] = f[u] >= 0 ? to[i0 + u * step] : -1;
+    }
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+      if (f[u] < 0) continue;
+      weights[t[u]] = weights[f[u]];
+      const int to_row = row_of(a, table, t[u]);
+      from[i0 + u * step] = row_of(a, table, f[u]);
+      to[i0 + u * step] = to_row;
+      if (f[u] < a.keep) chain[f[u] - front] = to_row;
     }
   }
   cluster_sync();
   if (rank == 0) {
-    constexpr int U = 4;
-    for (int64_t i0 = 0; i0 < a.recent; i0 += U * kSelectThreads) {
-      float w[U];
-#pragma unroll
-      for (int u = 0; u < U; ++u) {
-        const int64_t i = i0 + u * kSelectThreads + threadIdx.x;
-        if (i < a.recent) w[u] = weights[old + i];
-      }
+    write_recent(threadIdx.x);
+    for (int64_t i0 = R * kSelectThreads; i0 < a.recent; i0 += R * kSelectThreads) {
       __syncthreads();
-#pragma unroll
-      for (int u = 0; u < U; ++u) {
-        const int64_t i = i0 + u * kSelectThreads + threadIdx.x;
-        if (i < a.recent) weights[front + i] = w[u];
-      }
+      read_recent(i0 + threadIdx.x);
       __syncthreads();
+      write_recent(i0 + threadIdx.x);
     }
   }
-  cluster_sync();
-  for (int64_t j = a.keep + static_cast<int64_t>(rank) * kSelectThreads + threadIdx.x; j < n; j += ctas * kSelectThreads)
-    weights[j] = 0.0f;
+  if (a.recent > R * kSelectThreads) cluster_sync();  // otherwise all recent ones were read before the last one
+  for (int64_t j = a.keep + me; j < n; j += step) weights[j] = 0.0f;
 }
 
 constexpr int kMoveThreads = 256;
