@@ -288,6 +288,7 @@ h3attn_status_t decode(const void* q, void* o, const Cache& cache, int Hq, float
     uint8_t* const at = static_cast<uint8_t*>(workspace);
     if (space.partials > 0) a.ws = reinterpret_cast<float*>(at);
     if (weighted) {
+      a.weights = weights;
       a.stats = reinterpret_cast<float2*>(at + up(space.partials));
       a.scores = reinterpret_cast<float*>(at + up(space.partials) + space.stats);
       a.score_stride = space.score_stride;
@@ -299,8 +300,7 @@ h3attn_status_t decode(const void* q, void* o, const Cache& cache, int Hq, float
   a.status = h3::status_word_ptr();
   if (!a.status) return H3ATTN_ERR_LAUNCH;
   const cudaStream_t s = static_cast<cudaStream_t>(stream);
-  cudaError_t e = cache.q4 ? h3::launch_decode_q4(a, s) : h3::launch_decode(a, s);
-  if (e == cudaSuccess && weighted) e = h3::launch_add_weights(a, weights, s);
+  const cudaError_t e = cache.q4 ? h3::launch_decode_q4(a, s) : h3::launch_decode(a, s);
   return e == cudaSuccess ? H3ATTN_OK : H3ATTN_ERR_LAUNCH;
 }
 

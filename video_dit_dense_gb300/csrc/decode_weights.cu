@@ -1,14 +1,14 @@
 // What each token of a paged cache was attended to: the sum over the query
-// heads of its softmax weights, added to the caller's sums.
+// heads of its softmax weights, added to the caller's sums, for decode calls that do not split (the
+// others' join does it, see add_split_weights).
 //
-// The decode kernel has left each head's scores (in exponents of two) and its
-// join what they are taken against, m, and 1 / l:
+// The decode kernel has left each head's scores (in exponents of two), what they
+// are taken against, m, and 1 / l:
 //   weights[b, j] += sum_h 2^(score[b, h, j] - m[b, h]) / l[b, h],
 // heads in order, so results do not depend on timing.  A thread takes a token, so that
 // a warp reads 128 bytes of each head's scores, eight heads at a time; those were
-// written by the decode kernel and are mostly still in L2.  Bound by the wait for the join and
-// then three dependent reads (length, scores beside sums, weights): four tokens a thread took 18 us
-// instead of 12 of a cold start (4 sequences of up to 32760 tokens, 24 heads).
+// written by the decode kernel and are mostly still in L2.  Bound by its launch and
+// three dependent reads (length, scores beside sums, weights).
 #include "decode_common.cuh"
 
 namespace h3 {
@@ -16,7 +16,7 @@ namespace {
 
 constexpr int kThreads = 256;
 
-__global__ void __launch_bounds__(kThreads) add_weights_kernel(const __grid_constant__ DecodeArgs a, float* weights) {
+__global__ void __launch_bounds__(kThreads) add_weights_kernel(const __grid_constant__ DecodeArgs a) {
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
   asm volatile("griddepcontrol.wait;" ::: "memory");
   const int64_t capacity = static_cast<int64_t>(a.max_pages) * a.page_size;
@@ -25,22 +25,23 @@ __global__ void __launch_bounds__(kThreads) add_weights_kernel(const __grid_cons
   if (j >= len_of(a, b)) return;
   const float* score = a.scores + static_cast<int64_t>(b) * a.Hq * a.score_stride + j;
   const float2* stats = a.stats + static_cast<int64_t>(b) * a.Hq;
-  const float before = weights[b * capacity + j];
+  float* const to = a.weights + b * capacity + j;
+  const float before = *to;
   float sum = 0.0f;
 #pragma unroll 8
   for (int h = 0; h < a.Hq; ++h) {
     const float2 ml = stats[h];
     sum = fmaf(ex2(score[h * a.score_stride] - ml.x), ml.y, sum);
   }
-  weights[b * capacity + j] = before + sum;
+  *to = before + sum;
 }
 
 }  // namespace
 
-cudaError_t launch_add_weights(const DecodeArgs& a, float* weights, cudaStream_t stream) {
+cudaError_t launch_add_weights(const DecodeArgs& a, cudaStream_t stream) {
   const int64_t capacity = static_cast<int64_t>(a.max_pages) * a.page_size;
   const dim3 grid(static_cast<unsigned>((capacity + kThreads - 1) / kThreads), static_cast<unsigned>(a.B));  // B <= 65535
-  return launch_dependent(add_weights_kernel, grid, kThreads, 0, stream, a, weights);
+  return launch_dependent(add_weights_kernel, grid, kThreads, 0, stream, a);
 }
 
 }  // namespace h3

@@ -113,8 +113,10 @@ struct DecodeArgs {
   // a cache in 4 bits: codes in k_pages and v_pages, and their scales
   const uint8_t* k_scales;
   const uint8_t* v_scales;
-  // for the tokens' weights: scale * log2(e) * score of each query head and token, score_stride tokens a head, and for each
-  // query head what exponents were taken against and 1 / their sum; nullptr: not asked for
+  // for the tokens' weights, [B, capacity]: scale * log2(e) * score of each query head and token, score_stride tokens a
+  // head, and for each query head of a sequence that one range held what exponents were taken against and 1 / their sum;
+  // nullptr: not asked for
+  float* weights;
   float* scores;
   float2* stats;
   int64_t score_stride;
@@ -124,8 +126,8 @@ cudaError_t decode_workspace(const DecodeArgs& a, size_t* bytes);
 cudaError_t launch_decode(const DecodeArgs& a, cudaStream_t stream);
 cudaError_t decode_q4_workspace(const DecodeArgs& a, size_t* bytes);
 cudaError_t launch_decode_q4(const DecodeArgs& a, cudaStream_t stream);
-// weights[b, j] += sum over the heads of 2^(score - stats.x) * stats.y
-cudaError_t launch_add_weights(const DecodeArgs& a, float* weights, cudaStream_t stream);
+// Of a call that does not split: weights[b, j] += sum over the heads of 2^(score - stats.x) * stats.y
+cudaError_t launch_add_weights(const DecodeArgs& a, cudaStream_t stream);
 
 // ---- cached tokens as contiguous rows ----
 struct ReadArgs {

@@ -567,10 +567,12 @@ cudaError_t launch_d(const Kernelargs& k, cudaStream_t stream) {
   const int64_t ranges = k.p.ranges > 0 ? k.p.ranges : k.a.B;
   e = launch_dependent(decode_kernel<D, NT, SHARE, W>, dim3(static_cast<unsigned>(ranges * k.p.groups)), C::kWarps * 32,
                        C::kSmem, stream, k);
-  if (e != cudaSuccess || k.p.ranges == 0) return e;
+  if (e != cudaSuccess) return e;
+  if (k.p.ranges == 0) return W ? launch_add_weights(k.a, stream) : e;
   const int G = k.a.Hq / k.a.Hkv;
-  return launch_dependent(decode_join_kernel<D, W>, dim3(k.p.ranges * k.p.groups), kJoinThreads, 0, stream, k, C::kTile,
-                          std::min(G, C::kHeads));
+  const int joins = k.p.ranges * k.p.groups;
+  return launch_dependent(decode_join_kernel<D, W>, dim3(joins + (W ? adding_ctas(k.a, joins) : 0)), kJoinThreads, 0, stream, k,
+                          C::kTile, std::min(G, C::kHeads), joins);
 }
 
 template <int D, bool W>
