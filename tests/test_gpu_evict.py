@@ -86,6 +86,7 @@ def test_weights_and_budgets(h3, bits, kind, keep, recent):
 
 @pytest.mark.gpu
 @pytest.mark.parametrize("n,keep,recent", [(4097, 4096, 512), (5000, 100, 50), (9000, 8999, 3000), (20000, 15000, 100), (40001, 9000, 4000),
+                                           (8100, 8000, 5000), (30000, 20000, 9000), (30000, 29950, 9000),
                                            (70000, 69999, 1)])
 @pytest.mark.parametrize("kind", ["plain", "ties", "special"])
 def test_long_sequences(h3, n, keep, recent, kind):
@@ -190,10 +191,12 @@ def test_refusals(h3):
 
 
 @pytest.mark.gpu
+@pytest.mark.parametrize("n", [700001, 900001])
 @pytest.mark.parametrize("kind", ["plain", "ties"])
-def test_more_weights_than_shared_memory_holds(h3, kind):
-    """A sequence whose weights are read anew in each pass; the tokens numbered in their rows."""
-    n, keep, recent, page = 900001, 500000, 1000, 64
+def test_as_many_weights_as_shared_memory_holds_and_more(h3, kind, n):
+    """A cluster's shared memory nearly full, and a sequence whose weights are read anew in each pass; the tokens numbered
+    in their rows."""
+    keep, recent, page = 500000, 1000, 64
     pages = -(-n // page)
     held = [torch.zeros(pages, page, 1, 64 // m, dtype=torch.uint8, device="cuda") for m in (2, 2, 16, 16)]
     table = torch.randperm(pages, generator=torch.Generator().manual_seed(3)).int()

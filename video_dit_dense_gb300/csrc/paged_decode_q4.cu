@@ -22,9 +22,16 @@
 //     channels are.  So a lane takes D / 4 neighbouring channels of a K row and D / 8 of a V row, in one
 //     load each, with one or few scales.
 // Both products are exact in their operands but for P, which is rounded to 11 bits
-// (binary16: half a step is 2^-12 of a weight, an eighth of the output's own rounding): P is taken
-// 2^7 times larger than its sum's reference so that weights down to 2^-31 of the largest are normal.
+// (binary16: half a step is 2^-11 of a weight, an eighth of the output's own rounding): P is taken
+// 2^7 times larger than the exponents' reference gives it, so that weights down to 2^-21 of that
+// keep their bits and only those below 2^-32 are lost.
 // Queries are taken in binary16 after a scaling by a power of two for each row.
+//
+// Measured: 104448 tokens, 24 heads of 128, one sequence: 74.5 us, 4.8 TB/s (bf16:
+// 182); the tiles alone run at 88 % of the copy rate, 643 instructions and 914 cycles a scheduler for a
+// tile of 32 tokens of a head, and 14 us lie around them (waits for lengths, pages and
+// rows 5, unequal SMs 2, the join and the launch 6).  16 sequences of 4096 to 8192 tokens, 16 and
+// 4 heads of 128: 21 us of 8.5 (bf16: 36).
 #include <type_traits>
 
 #include "cache4.cuh"

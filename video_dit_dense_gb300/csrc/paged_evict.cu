@@ -10,21 +10,22 @@
 // weight T of the front-th heaviest old token comes from counting passes over
 // 8 bits of that order (the CTAs' counts are added up across the cluster), until all
 // tokens that begin like T are kept or no bits are left; then
-// kept = above T, or equal to it and among the first ones.  (11 bits a pass are one pass fewer, but 2048
-// counts from each of 8 CTAs for each of them took longer.)  Each warp owns a
-// contiguous part of the tokens, so that a ballot numbers movers and gaps.  It writes
-// their lists, moves the weights, and looks up the rows that the places are.
-// Weights read again from memory in each pass, a load at a time, took 64 us of one
-// sequence of 104448 tokens.
+// kept = above T, or equal to it and among the first ones.  (11 bits a pass are one
+// pass fewer, but 2048 counts from each of 8 CTAs for each of them took 12 us longer
+// on the longest case below.)  Each warp owns a contiguous part of the tokens, so that a
+// ballot numbers movers and gaps.  It writes their lists, moves the weights, and
+// looks up the rows that the places are.  Bound by latencies: of 16 sequences of up to
+// 4352 tokens 12 us, of one of 104448 25 (a load at a time from memory in each pass: 64).
 //
 // Second kernel: moves the rows, d = n - keep places down.  Movers from beyond `keep`
-// are not in the way of anything: a warp, or as many of its lanes as a short row has pieces, takes a row.  The place front + c is read
-// by its mover, if it has one, then written by the recent row from old + c = front + c + d,
-// whose place is then written by the one from old + c + d, and so on: a chain, in which a warp
-// takes one row after the other, so that each of its lanes reads what it later overwrites.
-// There are min(d, recent) chains.  Where they are longer than the tiles of the other
-// way would be many (and than two) a CTA owns a column of pieces of all rows instead, and moves the movers first, then the
-// recent rows in tiles from the first on.
+// are not in the way of anything: a warp, or as many of its lanes as a short row has
+// pieces, takes a row.  The place front + c is read by its mover, if it has one, then
+// written by the recent row from old + c = front + c + d, whose place is then written by
+// the one from old + c + d, and so on: a chain, in which a warp takes one row after the
+// other, so that each of its lanes reads what it later overwrites.  There are
+// min(d, recent) chains.  Where they are long and few, a CTA owns a column of pieces of
+// all rows instead, and moves the movers first, then the recent rows in tiles from the
+// first on.  23286 rows of 3456 bytes: 30 us, 5.4 TB/s read and written.
 #include <algorithm>
 
 #include "decode_common.cuh"
