@@ -61,14 +61,14 @@ __device__ __forceinline__ uint32_t plain_codes(const uint32_t* n, uint32_t top,
   return (r >> 20) - (112u << 3);
 }
 // Any group's scale, and the codes of 8 of its values.
-__device__ __noinline__ uint32_t scale_of(uint32_t top) {
+__device__ __forceinline__ uint32_t scale_of(uint32_t top) {
   if (top >= 0x7F80u) return 0xFFu;
   const float t = fminf(__uint_as_float(top << 16) * (1.0f / 7.0f), 3840.0f);
   const uint32_t u = (__float_as_uint(t) + 4u) & ~7u;
   if (u < 0x38800000u) return static_cast<uint32_t>(__float2int_rn(__uint_as_float(u) * 0x1p17f));  // below 2^-14
   return ((u + 0x7FFFFu + ((u >> 20) & 1u)) >> 20) - (112u << 3);
 }
-__device__ __noinline__ uint32_t codes_of(uint32_t n0, uint32_t n1, uint32_t n2, uint32_t n3, uint32_t scale) {
+__device__ __forceinline__ uint32_t codes_of(uint32_t n0, uint32_t n1, uint32_t n2, uint32_t n3, uint32_t scale) {
   if (scale == 0u || scale == 0xFFu) return 0x88888888u;
   const float inv = __fdividef(1.0f + 0x1p-13f, scale_value(scale));
   uint32_t codes = 0;
