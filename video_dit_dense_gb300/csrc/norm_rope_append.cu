@@ -11,7 +11,7 @@
 // operations on other pairs; without weights n = x.  For a cache in 4 bits the
 // K and V rows are rounded to bf16 as for the other, and then to codes and scales
 // (see cache4.cuh); the instructions of that bound it: the case below takes 197 us
-// for 918 MB, 4.7 TB/s, with 70 % of the issue slots busy.
+// for 918 MB, 4.7 TB/s, with 72 % of the issue slots busy.
 //
 // Memory-bound: every row is read once and written once.  A row is one
 // (token, head) vector; D/16 lanes own a row and hold two 16-byte groups of it.
