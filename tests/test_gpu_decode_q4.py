@@ -348,3 +348,20 @@ def test_refusals(h3):
             h3.h3attn_paged_decode_weights(q, q.clone(), c.cache, weights, space)
     with pytest.raises(h3.H3AttnError):
         h3.h3attn_paged_decode_weights(q, q.clone(), None, w, ws)
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("bits", [4, 16])
+@pytest.mark.parametrize("lens,Hq,Hkv,D", [([300, 0, 5000, 1, 256, 257, 900], 6, 2, 128), ([0, 0, 3], 33, 1, 64),
+                                           ([255, 256, 257, 512, 513] * 9, 5, 1, 64), ([1], 40, 40, 64)])
+def test_tables_with_more_room_than_tokens(h3, bits, lens, Hq, Hkv, D):
+    """Weights are added up of the tokens that are there, wherever the tables would end."""
+    check(h3, Case(lens, Hq, Hkv, D, 16, capacity=9000, seed=len(lens), bits=bits))
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("bits", [4, 16])
+def test_more_tokens_than_threads_that_add_weights(h3, bits):
+    """41 sequences of 32 times 256 tokens, split; and 600 of up to ten times 256, each by one CTA, with four that add."""
+    check(h3, Case([8000] * 41, 2, 1, 64, 64, seed=1, bits=bits))
+    check(h3, Case([2600 if b % 200 == 7 else (37 * b) % 90 for b in range(600)], 2, 1, 64, 16, seed=2, bits=bits))

@@ -163,25 +163,45 @@ constexpr int kFewParts = 4;  // partials that a warp asks for at a time: a head
 
 // weights[b, j] += sum_h 2^(score[b, h, j] - m[b, h]) / l[b, h], heads in order, of split sequences beside their join: what
 // the weights need of it, each head's maximum and sum, every CTA works out for itself, 32 heads at a time, eight lanes to
-// a head's ranges.  A thread takes a token; CTA `me` of `all` takes every all-th kJoinThreads tokens of a sequence.
-// (A kernel behind the join instead: 43.1 us against 41.3 of 4 sequences of up to 32760 tokens, 24 and 8 heads of 128 in
-// 4 bits, 47.1 against 45.5 of 16 of up to 8192, 16 and 4 in bf16.)
+// a head's ranges.  A thread takes a token; CTA `me` of `all` takes every all-th chunk of kJoinThreads tokens, counted over the
+// tokens that are there (over all that the tables have room for: 64 sequences of 2000 tokens, 16 and 4 heads of 128, in tables
+// for 131072 118 us, 54 so).  Bound by its chain of reads: lengths; partials' maxima and sums beside the first scores; the
+// other scores.  4 sequences of up to 32760 tokens, 24 and 8 heads of 128 in 4 bits, and 16 of up to 8192, 16 and 4 in bf16:
+// by a kernel behind the join 43.1 and 47.1 us; beside it 42.1 and 45.0; with scores asked for before the maxima and
+// sums, and those in one turn 41.0 and 44.1; these CTAs before the joining ones in the grid 39.1 and
+// 43.7; counted over the tokens 38.5 and 42.7.
+constexpr int kEarly = 16;       // scores asked for before the maxima and sums
+constexpr int kPartsAtOnce = 8;  // partials of a lane
 template <int D>
-__device__ __forceinline__ void add_split_weights(const Kernelargs& k, const Ranges& ranges, const int* end, int part_heads, int me, int all) {
+__device__ __forceinline__ void add_split_weights(const Kernelargs& k, const Ranges& ranges, const int* end, const int* len,
+                                                  int part_heads, int me, int all) {
   const DecodeArgs& a = k.a;
   const DecodePlan& p = k.p;
   __shared__ float2 ml[32];
   const int64_t capacity = static_cast<int64_t>(a.max_pages) * a.page_size;
-  const int64_t chunks = (capacity + kJoinThreads - 1) / kJoinThreads;
+  // chunks of sequences 0 .. b: every warp for itself, all write the same
+  __shared__ int chunks_to[kMaxSplitBatch];
+  int chunks = 0;
+  for (int b0 = 0; b0 < a.B; b0 += 32) {
+    const int lane = threadIdx.x & 31, b = b0 + lane;
+    int upto = b < a.B ? (len[b] + kJoinThreads - 1) / kJoinThreads : 0;
+#pragma unroll
+    for (int off = 1; off < 32; off <<= 1) {
+      const int before = __shfl_up_sync(0xFFFFFFFFu, upto, off);
+      if (lane >= off) upto += before;
+    }
+    if (b < a.B) chunks_to[b] = chunks + upto;
+    chunks += __shfl_sync(0xFFFFFFFFu, upto, 31);
+  }
+  __syncwarp();
+  if (me >= chunks) return;  // the joining CTAs wait for the decode kernel: a kernel that waits for this one waits for both
   const int G = a.Hq / a.Hkv;
   const int64_t unit_floats = partial_floats(part_heads, D), stride = 2 * p.unit_heads * unit_floats;
   asm volatile("griddepcontrol.wait;" ::: "memory");
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
-  for (int64_t item = me; item < a.B * chunks; item += all) {
-    const int b = static_cast<int>(item / chunks);
-    const int64_t j = (item - b * chunks) * kJoinThreads + threadIdx.x;
-    const int n = len_of(a, b);
-    if (j - static_cast<int>(threadIdx.x) >= n) continue;  // the whole CTA
+  for (int chunk = me; chunk < chunks; chunk += all) {
+    const int b = sequence_at(chunks_to, a.B, chunk), n = len[b];
+    const int64_t j = static_cast<int64_t>(chunk - (b > 0 ? chunks_to[b - 1] : 0)) * kJoinThreads + threadIdx.x;
     const int begin = b > 0 ? end[b - 1] : 0, r0 = ranges.of(begin + p.start), parts = ranges.of(end[b] - 1) - r0 + 1;
     const int64_t slot1 = ranges.begin(r0) >= begin ? 0 : stride / 2;
     const float* score = a.scores + static_cast<int64_t>(b) * a.Hq * a.score_stride + j;
@@ -189,17 +209,29 @@ __device__ __forceinline__ void add_split_weights(const Kernelargs& k, const Ran
     const float before = j < n ? *to : 0.0f;
     float sum = 0.0f;
     for (int h0 = 0; h0 < a.Hq; h0 += 32) {
+      const int heads = min(a.Hq - h0, 32);
+      float early[kEarly];  // scores, asked for before what the maxima and sums wait for
+#pragma unroll
+      for (int i = 0; i < kEarly; ++i) early[i] = j < n && i < heads ? score[(h0 + i) * a.score_stride] : 0.0f;
       const int h = h0 + (threadIdx.x >> 3);
       float m = -FLT_MAX, l = 0.0f;
       if (h < a.Hq && parts > 1) {
         const int kvh = h / G, in_group = h - kvh * G, qt = in_group / p.tile_heads, hh = in_group - qt * p.tile_heads;
         const float* part = a.ws + r0 * stride + (kvh * p.q_tiles + qt) * unit_floats + 2 * hh;
-#pragma unroll 4
-        for (int i = threadIdx.x & 7; i < parts; i += 8) {
-          const float2 of = *reinterpret_cast<const float2*>(part + (i == 0 ? slot1 : i * stride));
-          const float to_m = fmaxf(m, of.x);
-          l = l * ex2(m - to_m) + of.y * ex2(of.x - to_m);
-          m = to_m;
+        for (int i0 = threadIdx.x & 7; i0 < parts; i0 += 8 * kPartsAtOnce) {
+          float2 of[kPartsAtOnce];
+#pragma unroll
+          for (int u = 0; u < kPartsAtOnce; ++u) {
+            const int i = i0 + 8 * u;
+            of[u] = make_float2(-FLT_MAX, 0.0f);
+            if (i < parts) of[u] = *reinterpret_cast<const float2*>(part + (i == 0 ? slot1 : i * stride));
+          }
+#pragma unroll
+          for (int u = 0; u < kPartsAtOnce; ++u) {
+            const float to_m = fmaxf(m, of[u].x);
+            l = l * ex2(m - to_m) + of[u].y * ex2(of[u].x - to_m);
+            m = to_m;
+          }
         }
       }
 #pragma unroll
@@ -212,9 +244,11 @@ __device__ __forceinline__ void add_split_weights(const Kernelargs& k, const Ran
         ml[threadIdx.x >> 3] = parts > 1 ? make_float2(m, l == 0.0f ? 0.0f : 1.0f / l) : a.stats[static_cast<int64_t>(b) * a.Hq + h];
       __syncthreads();
       if (j < n) {
-        const int heads = min(a.Hq - h0, 32);
+#pragma unroll
+        for (int i = 0; i < kEarly; ++i)
+          if (i < heads) sum = fmaf(ex2(early[i] - ml[i].x), ml[i].y, sum);
 #pragma unroll 8
-        for (int i = 0; i < heads; ++i) sum = fmaf(ex2(score[(h0 + i) * a.score_stride] - ml[i].x), ml[i].y, sum);
+        for (int i = kEarly; i < heads; ++i) sum = fmaf(ex2(score[(h0 + i) * a.score_stride] - ml[i].x), ml[i].y, sum);
       }
       __syncthreads();
     }
@@ -229,9 +263,10 @@ __device__ __forceinline__ void add_split_weights(const Kernelargs& k, const Ran
 // have to be waited for.  Sequences that one range held are written already;
 // sequences without a key get their zeros here.  One CTA an SM, small enough to
 // sit beside a decode CTA.
-// W: the CTAs from `joins` on add up the tokens' weights.
+// W: the CTAs before the last `joins` ones add up the tokens' weights, in 64 registers, as many CTAs an SM as with 56 but
+// without spills.
 template <int D, bool W>
-__global__ void __launch_bounds__(kJoinThreads) __maxnreg__(D == 256 ? 96 : 56)
+__global__ void __launch_bounds__(kJoinThreads) __maxnreg__(D == 256 ? 96 : W ? 64 : 56)
     decode_join_kernel(const __grid_constant__ Kernelargs k, int tile, int part_heads, int joins) {
   constexpr int VEC = D / 32, WARPS = kJoinThreads / 32;
   static_assert((WARPS & (WARPS - 1)) == 0, "warps are shared out to heads in powers of two");
@@ -242,10 +277,11 @@ __global__ void __launch_bounds__(kJoinThreads) __maxnreg__(D == 256 ? 96 : 56)
   __shared__ int in_warp[2][WARPS];
   __shared__ float part_o[WARPS][D];
   __shared__ float2 part_ml[WARPS];
-  const Ranges ranges = scan_tiles<kJoinThreads>(a, p, tile, end, nullptr);
+  __shared__ int len[W ? kMaxSplitBatch : 1];
+  const Ranges ranges = scan_tiles<kJoinThreads>(a, p, tile, end, W ? len : nullptr);
   if constexpr (W) {
-    if (static_cast<int>(blockIdx.x) >= joins) {
-      add_split_weights<D>(k, ranges, end, part_heads, blockIdx.x - joins, gridDim.x - joins);
+    if (static_cast<int>(blockIdx.x) < static_cast<int>(gridDim.x) - joins) {
+      add_split_weights<D>(k, ranges, end, len, part_heads, blockIdx.x, gridDim.x - joins);
       return;
     }
   }
@@ -352,12 +388,13 @@ __global__ void __launch_bounds__(kJoinThreads) __maxnreg__(D == 256 ? 96 : 56)
     for (int e = 0; e < VEC; e += 2) reinterpret_cast<uint32_t*>(out)[e >> 1] = pack_bf16(o[e] * inv, o[e + 1] * inv);
   };
   // Heads in few ranges: a warp each.  Heads in many: as many warps on each as there are for all of them.
+  const int cta = W ? blockIdx.x - (gridDim.x - joins) : blockIdx.x;
   const int few = n_split[1] * a.Hq, many = n_split[0] * a.Hq;
   int per = WARPS;
   while (per > 2 && many * per > joins * WARPS) per >>= 1;
   const int lead = warp / per * per, at_once = WARPS / per;  // first warp of this one's head, heads a CTA takes at a time
   // the first of each is looked up before the wait
-  int i_few = blockIdx.x * WARPS + warp, i_many = blockIdx.x * at_once + warp / per;
+  int i_few = cta * WARPS + warp, i_many = cta * at_once + warp / per;
   Head x_few{}, x_many{};
   if (i_few < few) x_few = locate(1, i_few);
   if (i_many < many) x_many = locate(0, i_many);
@@ -370,7 +407,7 @@ __global__ void __launch_bounds__(kJoinThreads) __maxnreg__(D == 256 ? 96 : 56)
     i_few += joins * WARPS;
     if (i_few < few) x_few = locate(1, i_few);
   }
-  for (int i0 = blockIdx.x * at_once; i0 < many; i0 += joins * at_once) {
+  for (int i0 = cta * at_once; i0 < many; i0 += joins * at_once) {
     const bool there = i_many < many;
     if (there) {
       gather(x_many, warp - lead, per);
@@ -397,7 +434,7 @@ __global__ void __launch_bounds__(kJoinThreads) __maxnreg__(D == 256 ? 96 : 56)
     i_many += joins * at_once;
     if (i_many < many) x_many = locate(0, i_many);
   }
-  for (int b = blockIdx.x; b < a.B; b += joins) {
+  for (int b = cta; b < a.B; b += joins) {
     if (end[b] == (b > 0 ? end[b - 1] : 0)) {  // no key: zeros
       uint2* row = reinterpret_cast<uint2*>(a.o + static_cast<int64_t>(b) * a.Hq * D);
       for (int i = threadIdx.x; i < a.Hq * (D / 4); i += kJoinThreads) row[i] = make_uint2(0u, 0u);
