@@ -219,3 +219,37 @@ def test_as_many_weights_as_shared_memory_holds_and_more(h3, kind, n):
     assert torch.equal(held[0].view(torch.int64)[..., 0, 0][row], want)
     assert torch.equal(held[2].view(torch.int32)[..., 0, 0][row], want.int())
     assert torch.equal(w[0, :keep], before[0, want]) and bool((w[0, keep:n] == 0).all()) and torch.equal(w[0, n:], before[0, n:])
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("kind", ["plain", "ties", "special"])
+@pytest.mark.parametrize("keep,recent", [(3000, 300), (8193, 5000), (1, 0)])
+def test_unlike_lengths_in_wide_tables(h3, kind, keep, recent):
+    """Sequences of one call that take one CTA of their cluster, some, and all."""
+    check(h3, 4, [5000, 8192, 8193, 20000, 33000, 3000], keep, recent, 1, 64, 64, capacity=70000, kind=kind, seed=keep)
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("kind", ["plain", "ties"])
+@pytest.mark.parametrize("room", [400000, 810000, 900001])
+@pytest.mark.parametrize("n", [3000, 20000, 150000])
+def test_pages_for_the_tokens_in_a_very_wide_table(h3, n, room, kind):
+    """As above where the weights of all the room lie in shared memory, and where they would not; no page behind the tokens."""
+    keep, recent, page = 2000, 64, 64
+    pages, wide = -(-n // page), -(-room // page)
+    held = [torch.zeros(pages, page, 1, 64 // m, dtype=torch.uint8, device="cuda") for m in (2, 2, 16, 16)]
+    held[0].view(torch.int64)[..., 0, 0] = torch.arange(pages * page, device="cuda").view(pages, page)
+    table = torch.full((1, wide), -1, dtype=torch.int32)
+    table[0, :pages] = torch.arange(pages)
+    cache = h3.PagedKV4(*held, table.cuda(), torch.tensor([n], dtype=torch.int32, device="cuda"))
+    w = weights_of(kind, (1, wide * page), n).cuda()
+    before, out = w.clone(), torch.zeros(1, dtype=torch.int32, device="cuda")
+    h3.h3attn_paged_evict(cache, w, keep, recent, out, h3.paged_evict_workspace(cache, keep, recent))
+    assert out.tolist() == [keep] and h3.h3attn_check_device_status() == 0
+    front, old = keep - recent, n - recent
+    stay = torch.sort(before[0, :old], descending=True, stable=True)[1][:front].sort()[0]
+    want = torch.arange(keep, device="cuda")
+    want[torch.ones(front, dtype=torch.bool, device="cuda").index_fill_(0, stay[stay < front], False).nonzero()[:, 0]] = stay[stay >= front]
+    want[front:] = torch.arange(old, n, device="cuda")
+    assert torch.equal(held[0].view(torch.int64).view(-1, 4)[:keep, 0], want)
+    assert torch.equal(w[0, :keep], before[0, want]) and bool((w[0, keep:n] == 0).all()) and torch.equal(w[0, n:], before[0, n:])

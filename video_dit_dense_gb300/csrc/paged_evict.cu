@@ -15,7 +15,7 @@
 // on the longest case below.)  Each warp owns a contiguous part of the tokens, so that a
 // ballot numbers movers and gaps.  It writes their lists, moves the weights, and
 // looks up the rows that the places are.  Bound by latencies: of 16 sequences of up to
-// 4352 tokens 12 us, of one of 104448 25 (a load at a time from memory in each pass: 64).
+// 4352 tokens 11 us, of one of 104448 25 (a load at a time from memory in each pass: 64).
 //
 // Second kernel: moves the rows, d = n - keep places down.  Movers from beyond `keep`
 // are not in the way of anything: a warp, or as many of its lanes as a short row has
@@ -96,6 +96,11 @@ __device__ __forceinline__ Scan cluster_scan(uint32_t x, uint32_t y, uint32_t z,
   return s;
 }
 
+// CTAs that share a sequence of n tokens' select: one up to kAlone, whose barriers are its own; then as many as leave
+// 4096 each.
+constexpr int kAlone = 8192, kShare = 4096;
+__host__ __device__ inline bool more_ctas(int64_t n, uint32_t ctas) { return n > kAlone && n > kShare * static_cast<int64_t>(ctas); }
+
 // Tokens of a warp where a sequence has `old` to choose from: whole turns of 32.
 __host__ __device__ inline int64_t tokens_per_warp(int64_t old, uint32_t ctas) {
   const int64_t warps = static_cast<int64_t>(ctas) * kSelectWarps;
@@ -115,14 +120,15 @@ __device__ __forceinline__ int row_of(const EvictArgs& a, const int32_t* table, 
 
 // HELD: the weights' order is kept in shared memory; otherwise (more tokens than fit) it is read anew in each pass.
 template <bool HELD>
-__global__ void __launch_bounds__(kSelectThreads, 1) evict_select_kernel(const __grid_constant__ EvictArgs a, uint32_t ctas) {
+__global__ void __launch_bounds__(kSelectThreads, 1)
+    evict_select_kernel(const __grid_constant__ EvictArgs a, uint32_t most_ctas, int most_held) {
   extern __shared__ uint32_t held[];
   __shared__ uint32_t hist[kPasses][kBins];
   __shared__ uint32_t sums[2][3][kSelectWarps + 1];
   __shared__ uint32_t found[kPasses][3];  // bin, how many of its tokens are still wanted, how many it has
   __shared__ uint32_t above_of[kBins / 32];
-  const int b = blockIdx.x / ctas, warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const uint32_t rank = ctas > 1 ? cluster_rank() : 0;
+  const int b = blockIdx.x / most_ctas, warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const uint32_t rank = most_ctas > 1 ? cluster_rank() : 0;
   for (int i = threadIdx.x; i < kPasses * kBins; i += kSelectThreads) (&hist[0][0])[i] = 0;
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
   asm volatile("griddepcontrol.wait;" ::: "memory");
@@ -133,6 +139,18 @@ __global__ void __launch_bounds__(kSelectThreads, 1) evict_select_kernel(const _
   float* const weights = a.weights + b * a.capacity;
   const int32_t* const table = a.page_table + static_cast<int64_t>(b) * a.max_pages;
   const int old = n - a.recent, front = a.keep - a.recent;  // front < old
+  // The cluster is as large as the cache has room for; a sequence with fewer tokens takes fewer of its CTAs, and the
+  // barriers do not wait for those that have left (16 sequences of 2000 tokens in tables for 131072: all CTAs 20.0 us, one
+  // 11.9; in tables for 2048 11.2).
+  uint32_t ctas = 1;
+  while (ctas < most_ctas && (more_ctas(n, ctas) || (HELD && tokens_per_warp(old, ctas) * kSelectWarps > most_held))) ctas *= 2;
+  if (rank >= ctas) return;
+  auto all_sync = [&] {
+    if (ctas > 1)
+      cluster_sync();
+    else
+      __syncthreads();
+  };
   // this warp's tokens are neighbours, 32 a turn
   const int64_t per_warp = tokens_per_warp(old, ctas), w0 = (rank * kSelectWarps + warp) * per_warp;
   const int begin = static_cast<int>(min(w0, static_cast<int64_t>(old)));
@@ -170,10 +188,7 @@ __global__ void __launch_bounds__(kSelectThreads, 1) evict_select_kernel(const _
       const uint32_t same = __match_any_sync(0xFFFFFFFFu, bin);
       if (counts && (same & ((1u << lane) - 1u)) == 0) atomicAdd(&hist[pass][bin], static_cast<uint32_t>(__popc(same)));
     }
-    if (ctas > 1)
-      cluster_sync();
-    else
-      __syncthreads();
+    all_sync();
     // a thread adds up a bin over the cluster, from the last bin on
     uint32_t of_bin = 0, above = 0;
     if (threadIdx.x < kBins) {
@@ -267,7 +282,7 @@ __global__ void __launch_bounds__(kSelectThreads, 1) evict_select_kernel(const _
     list[0] = moves;
     list[1] = static_cast<int>(at.all_z);
   }
-  cluster_sync();
+  all_sync();
   // ---- the weights move: gaps are below all movers and recent ones; the recent ones, from the first on, to where movers
   // and they themselves have been read ----
   constexpr int U = 2, R = 4;
@@ -301,7 +316,7 @@ __global__ void __launch_bounds__(kSelectThreads, 1) evict_select_kernel(const _
       if (f[u] < a.keep) chain[f[u] - front] = to_row;
     }
   }
-  cluster_sync();
+  all_sync();
   if (rank == 0) {
     write_recent(threadIdx.x);
     for (int64_t i0 = R * kSelectThreads; i0 < a.recent; i0 += R * kSelectThreads) {
@@ -311,7 +326,7 @@ __global__ void __launch_bounds__(kSelectThreads, 1) evict_select_kernel(const _
       write_recent(i0 + threadIdx.x);
     }
   }
-  if (a.recent > R * kSelectThreads) cluster_sync();  // otherwise all recent ones were read before the last one
+  if (a.recent > R * kSelectThreads) all_sync();  // otherwise all recent ones were read before the last one
   for (int64_t j = a.keep + me; j < n; j += step) weights[j] = 0.0f;
 }
 
@@ -448,7 +463,7 @@ cudaError_t launch_evict(const EvictArgs& a, cudaStream_t stream) {
   const int64_t most_old = std::max<int64_t>(a.capacity - a.recent, 0);
   auto held_by = [&](uint32_t ctas) { return tokens_per_warp(most_old, ctas) * kSelectWarps; };
   uint32_t ctas = 1;
-  while (ctas < kMostCtas && a.capacity > 8192 && a.capacity > 4096 * static_cast<int64_t>(ctas) &&
+  while (ctas < kMostCtas && more_ctas(a.capacity, ctas) &&
          (static_cast<int64_t>(a.B) * ctas * 2 <= sms || held_by(ctas) > kMostHeld))
     ctas *= 2;
   const int64_t each = held_by(ctas);
@@ -480,7 +495,7 @@ cudaError_t launch_evict(const EvictArgs& a, cudaStream_t stream) {
   attr[1].val.clusterDim.y = attr[1].val.clusterDim.z = 1;
   cfg.attrs = attr;
   cfg.numAttrs = 2;
-  e = cudaLaunchKernelEx(&cfg, select, a, ctas);
+  e = cudaLaunchKernelEx(&cfg, select, a, ctas, static_cast<int>(fits ? each : 0));
   if (e != cudaSuccess) return e;
   MovePlan p = {};
   int columns = 0;
