@@ -15,7 +15,7 @@
 // on the longest case below.)  Each warp owns a contiguous part of the tokens, so that a
 // ballot numbers movers and gaps.  It writes their lists, moves the weights, and
 // looks up the rows that the places are.  Bound by latencies: of 16 sequences of up to
-// 4352 tokens 11 us, of one of 104448 25 (a load at a time from memory in each pass: 64).
+// 4352 tokens 11 us, of one of 104448 22 (a load at a time from memory in each pass: 64).
 //
 // Second kernel: moves the rows, d = n - keep places down.  Movers from beyond `keep`
 // are not in the way of anything: a warp, or as many of its lanes as a short row has
@@ -65,7 +65,7 @@ struct Scan {
   uint32_t x, y, all_x, all_z;
 };
 __device__ __forceinline__ Scan cluster_scan(uint32_t x, uint32_t y, uint32_t z, uint32_t ctas, uint32_t rank,
-                                             uint32_t (&sums)[3][kSelectWarps + 1]) {
+                                             uint32_t (&sums)[3][kSelectWarps + 3]) {
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   static_assert(kSelectWarps == 32, "a lane for each warp");
   if (lane < 3) sums[lane][warp] = lane == 0 ? x : lane == 1 ? y : z;
@@ -82,16 +82,20 @@ __device__ __forceinline__ Scan cluster_scan(uint32_t x, uint32_t y, uint32_t z,
   Scan s{before[0], before[1], all[0], all[2]};
   if (ctas > 1) {
     cluster_sync();
-    uint32_t theirs[3] = {0, 0, 0};
-    if (lane < static_cast<int>(ctas)) {
-#pragma unroll
-      for (int i = 0; i < 3; ++i) theirs[i] = peer_load(&sums[i][kSelectWarps], lane);
+    if (warp < 3) {  // asked for once a CTA (by every warp, the longest case below took 58.0 us instead of 54.5 with its rows)
+      const uint32_t theirs = lane < static_cast<int>(ctas) ? peer_load(&sums[warp][kSelectWarps], lane) : 0u;
+      const uint32_t earlier = __reduce_add_sync(0xFFFFFFFFu, lane < static_cast<int>(rank) ? theirs : 0u);
+      const uint32_t of_all = __reduce_add_sync(0xFFFFFFFFu, theirs);
+      if (lane == 0) {
+        sums[warp][kSelectWarps + 1] = earlier;
+        sums[warp][kSelectWarps + 2] = of_all;
+      }
     }
-    const bool earlier = lane < static_cast<int>(rank);
-    s.x += __reduce_add_sync(0xFFFFFFFFu, earlier ? theirs[0] : 0u);
-    s.y += __reduce_add_sync(0xFFFFFFFFu, earlier ? theirs[1] : 0u);
-    s.all_x = __reduce_add_sync(0xFFFFFFFFu, theirs[0]);
-    s.all_z = __reduce_add_sync(0xFFFFFFFFu, theirs[2]);
+    __syncthreads();
+    s.x += sums[0][kSelectWarps + 1];
+    s.y += sums[1][kSelectWarps + 1];
+    s.all_x = sums[0][kSelectWarps + 2];
+    s.all_z = sums[2][kSelectWarps + 2];
   }
   return s;
 }
@@ -124,7 +128,7 @@ __global__ void __launch_bounds__(kSelectThreads, 1)
     evict_select_kernel(const __grid_constant__ EvictArgs a, uint32_t most_ctas, int most_held) {
   extern __shared__ uint32_t held[];
   __shared__ uint32_t hist[kPasses][kBins];
-  __shared__ uint32_t sums[2][3][kSelectWarps + 1];
+  __shared__ uint32_t sums[2][3][kSelectWarps + 3];
   __shared__ uint32_t found[kPasses][3];  // bin, how many of its tokens are still wanted, how many it has
   __shared__ uint32_t above_of[kBins / 32];
   const int b = blockIdx.x / most_ctas, warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
