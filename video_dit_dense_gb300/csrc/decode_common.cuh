@@ -54,9 +54,12 @@ struct DecodePlan {
   int start;       // what starting on a sequence costs a CTA, in tiles
 };
 
+// The plan first, and in both structs what only some calls read last: a kernel's arguments are fetched a line at a time when it
+// starts, and what every call reads lies in as few lines as it can (64 sequences of up to 2048 tokens, 16 and 2 heads of 64 in
+// bf16: 12.04 us, 12.15 with the plan behind the arguments of the tokens' weights; 43 of 520, 20 and 4 of 128: 15.24 and 15.31).
 struct Kernelargs {
-  DecodeArgs a;
   DecodePlan p;
+  DecodeArgs a;
 };
 
 // Tokens attended of sequence b.  From L2: the joining kernel looks before its own wait.

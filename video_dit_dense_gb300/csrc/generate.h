@@ -75,8 +75,6 @@ struct AppendArgs {
   uint16_t* v_pages;
   const int32_t* page_table;  // [B, max_pages]
   const int32_t* kv_len;      // [B] tokens in the cache before the call
-  uint8_t* k_scales;          // a cache in 4 bits: codes in k_pages and v_pages, and their scales; nullptr: bf16
-  uint8_t* v_scales;
   const float* wq;            // [D] or nullptr (no norm)
   const float* wk;
   const float* cos;           // [table_rows, rotary_dim / 2]
@@ -94,6 +92,8 @@ struct AppendArgs {
   int B, S, Hq, Hkv, D, page_size, max_pages, num_pages, table_rows, rotary_dim, interleaved;
   float eps;
   int* status;
+  uint8_t* k_scales;  // a cache in 4 bits: codes in k_pages and v_pages, and their scales; nullptr: bf16
+  uint8_t* v_scales;
 };
 cudaError_t launch_append(const AppendArgs& a, cudaStream_t stream);
 

@@ -602,7 +602,7 @@ cudaError_t launch_decode(const DecodeArgs& a, cudaStream_t stream) {
   int sms = 0;
   cudaError_t e = sm_count(&sms);
   if (e != cudaSuccess) return e;
-  Kernelargs k{a, plan_of(a, sms, a.ws != nullptr)};
+  Kernelargs k{plan_of(a, sms, a.ws != nullptr), a};
   switch (a.D) {
     case 64: return launch_weights<64>(k, stream);
     case 128: return launch_weights<128>(k, stream);

@@ -726,7 +726,7 @@ cudaError_t launch_decode_q4(const DecodeArgs& a, cudaStream_t stream) {
   int sms = 0;
   cudaError_t e = sm_count(&sms);
   if (e != cudaSuccess) return e;
-  Kernelargs k{a, plan_of(a, sms, a.ws != nullptr)};
+  Kernelargs k{plan_of(a, sms, a.ws != nullptr), a};
   switch (a.D) {
     case 64: return launch_heads<64>(k, stream);
     case 128: return launch_heads<128>(k, stream);
