@@ -658,11 +658,7 @@ def h3attn_paged_decode(q, o, cache: PagedKV, scale=None, workspace=None, stream
 
 def h3attn_paged_decode_workspace_size(cache: PagedKV, Hq) -> int:
     """Bytes of workspace h3attn_paged_decode takes for this cache and Hq query heads (0: no split)."""
-    load()
-    out = ctypes.c_size_t(0)
-    st = _lib.h3attn_paged_decode_workspace_size(ctypes.byref(cache._struct), int(Hq), ctypes.byref(out))
-    _raise_if(st, "h3attn_paged_decode_workspace_size")
-    return int(out.value)
+    return _sized("h3attn_paged_decode_workspace_size", ctypes.byref(cache._struct), _int32("Hq", Hq))
 
 
 def paged_decode_workspace(q, cache: PagedKV):
@@ -719,6 +715,14 @@ def h3attn_paged_evict(cache, weights, keep, recent, len_out, workspace, stream=
     return (_bound or _get_step()).evict(cache, weights, keep, recent, len_out, workspace, stream)
 
 
+def _int32(name, n) -> int:
+    """n for the C interface: ctypes would take it modulo 2^32."""
+    n = int(n)
+    if not -2 ** 31 <= n < 2 ** 31:
+        raise H3AttnError(H3ATTN_ERR_INVALID_ARG, f"{name} must fit 32 bits")
+    return n
+
+
 def _sized(entry, *args) -> int:
     out = ctypes.c_size_t(0)
     _raise_if(getattr(load(), entry)(*args, ctypes.byref(out)), entry)
@@ -732,7 +736,7 @@ def _workspace(n, device):
 
 def h3attn_paged_decode_q4_workspace_size(cache: PagedKV4, Hq) -> int:
     """Bytes of workspace h3attn_paged_decode_q4 takes for this cache and Hq query heads (0: no split)."""
-    return _sized("h3attn_paged_decode_q4_workspace_size", ctypes.byref(cache._struct), int(Hq))
+    return _sized("h3attn_paged_decode_q4_workspace_size", ctypes.byref(cache._struct), _int32("Hq", Hq))
 
 
 def paged_decode_q4_workspace(q, cache: PagedKV4):
@@ -744,7 +748,7 @@ def paged_decode_q4_workspace(q, cache: PagedKV4):
 def h3attn_paged_decode_weights_workspace_size(cache, Hq) -> int:
     """Bytes of workspace h3attn_paged_decode_weights takes for this cache (of either kind) and Hq query heads."""
     kind = "_q4" if isinstance(cache, PagedKV4) else ""
-    return _sized(f"h3attn_paged_decode_weights{kind}_workspace_size", ctypes.byref(cache._struct), int(Hq))
+    return _sized(f"h3attn_paged_decode_weights{kind}_workspace_size", ctypes.byref(cache._struct), _int32("Hq", Hq))
 
 
 def paged_decode_weights_workspace(q, cache):
@@ -756,7 +760,7 @@ def paged_decode_weights_workspace(q, cache):
 def h3attn_paged_evict_workspace_size(cache, keep, recent) -> int:
     """Bytes of workspace h3attn_paged_evict takes for this cache (of either kind), keep and recent."""
     s = cache._struct
-    return _sized("h3attn_paged_evict_workspace_size", s.B, s.page_size, s.max_pages, int(keep), int(recent))
+    return _sized("h3attn_paged_evict_workspace_size", s.B, s.page_size, s.max_pages, _int32("keep", keep), _int32("recent", recent))
 
 
 def paged_evict_workspace(cache, keep, recent):
