@@ -197,7 +197,9 @@ __device__ __forceinline__ void add_split_weights(const Kernelargs& k, const Ran
     chunks += __shfl_sync(0xFFFFFFFFu, upto, 31);
   }
   __syncwarp();
-  if (me >= chunks) return;  // the joining CTAs wait for the decode kernel: a kernel that waits for this one waits for both
+  // Nothing to add: these leave without griddepcontrol.wait (they would hold their place for as long as the decode runs),
+  // which is allowed beside the joining CTAs of the same grid only, who wait for it (see launch_dependent).
+  if (me >= chunks) return;
   const int G = a.Hq / a.Hkv;
   const int64_t unit_floats = partial_floats(part_heads, D), stride = 2 * p.unit_heads * unit_floats;
   asm volatile("griddepcontrol.wait;" ::: "memory");

@@ -19,7 +19,10 @@ namespace h3 {
 // because the kernel before it only reads them and lets it start
 // (griddepcontrol.launch_dependents) after its own wait, when they are final.  A kernel
 // that writes lengths or that lets others start before it has waited must not stand
-// there.  What the kernels before may have written (lengths, page tables,
+// there.  Some CTAs of that join leave without waiting: those that would add up tokens' weights and have none.  They
+// touch nothing, and the kernel is not over before its joining CTAs, of which there is always one, have waited, so that
+// a kernel behind it still waits for the decode kernel through it.  A grid of CTAs that may all leave must wait first.
+// What the kernels before may have written (lengths, page tables,
 // rotary tables) is read with ordinary loads, not through the read-only path,
 // which is for data that stays as it is for the whole life of a kernel.
 template <class... P, class... A>
