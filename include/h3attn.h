@@ -506,7 +506,7 @@ h3attn_status_t h3attn_qk_norm_rope_append(const void* q, const void* k, const v
  *    and group of key-value heads (no second kernel).  Calls that share a
  *    workspace must be ordered: one stream, events, or graphs replayed in turn.
  *    Both kernels read the lengths: where several host threads use one stream,
- *    a call that changes them must not fall between the two.
+ *    a call that changes them or uses the same workspace must not fall between the two.
  *    The size is 0 where the page tables have room (max_pages * page_size) for
  *    a few tiles of tokens only, and for more than 512 sequences: with
  *    lengths that are unlike, parts of up to 512 in calls of their own are
@@ -618,7 +618,8 @@ h3attn_status_t h3attn_paged_decode_q4_workspace_size(const h3attn_paged_kv4_t* 
  * weights: [B, max_pages * page_size] float32, 4-byte aligned, overlapping nothing else.
  * workspace: of at least h3attn_paged_decode_weights_workspace_size() bytes, which
  *    is never 0 but for B == 0, so it is required: the scores lie in it between the
- *    kernels, 4 bytes for each query head and token that the page tables have room for.
+ *    kernels, 4 bytes for each query head and token that the page tables have room for (with 32
+ *    query heads to a key-value head of 128 as much as a cache in 4 bits itself).
  * Other arguments, rules and errors as for h3attn_paged_decode().
  */
 h3attn_status_t h3attn_paged_decode_weights(const void* q, void* o, const h3attn_paged_kv_t* cache, int Hq,
@@ -653,6 +654,10 @@ h3attn_status_t h3attn_paged_decode_weights_q4_workspace_size(const h3attn_paged
  * workspace: h3attn_paged_evict_workspace_size() bytes for the same sizes, 16-byte
  *    aligned (NULL where that is 0: B == 0); its contents on entry do not matter.
  *    Calls that share one must be ordered: one stream, events, or graphs replayed in turn.
+ *    Two kernels run, and both read the lengths: where several host threads use one stream, no call that
+ *    changes them, the cache or the weights, or that uses the same workspace, must fall between the two.
+ * The cost hardly depends on how many tokens go: evicting once in several steps, with room for those in
+ * the page tables, is cheaper than at each.
  * B == 0 is a no-op.  Outputs (pages, weights, len_out, workspace) overlap nothing
  * else.  Stream order as for h3attn_rmsnorm_modulate().
  * Errors: INVALID_ARG, MISALIGNED, UNSUPPORTED_HEAD_DIM, UNSUPPORTED_DEVICE, LAUNCH.
