@@ -11,7 +11,7 @@
 // operations on other pairs; without weights n = x.  For a cache in 4 bits the
 // K and V rows are rounded to bf16 as for the other, and then to codes and scales
 // (see cache4.cuh); the instructions of that bound it: the case below takes 197 us
-// for 918 MB, 4.7 TB/s, with 72 % of the issue slots busy.
+// for 918 MB, 4.7 TB/s, with 73 % of the issue slots busy.
 //
 // Memory-bound: every row is read once and written once.  A row is one
 // (token, head) vector; D/16 lanes own a row and hold two 16-byte groups of it.
@@ -63,7 +63,7 @@ enum : int { kHalf = 0, kInterleaved = 1, kStraddling = 2 };
 
 // Q4: a cache in 4 bits.  Its straddling layout runs better in 80 registers, three CTAs an SM (5 prompts of up to 3950 tokens, 20
 // and 4 heads of 128, 66 rotated: 49.4 us in 64, 47.3 in 80), the others in 64, although the half layout stores 28 bytes a
-// thread to local memory then (clip 279 and 280, 13 prompts of 1167, 16 and 2 heads: 37.5 and 41.1).
+// thread to local memory and loads 64 then (clip 279 and 280, 13 prompts of 1167, 16 and 2 heads: 37.5 and 41.1).
 template <int D, int LAYOUT, bool Q4>
 __global__ void __launch_bounds__(kThreads, Q4 && LAYOUT == kStraddling ? 3 : 4) append_kernel(const __grid_constant__ AppendArgs a) {
   constexpr int LPR = D / 16, RPW = 32 / LPR, U = kUnroll;
@@ -293,6 +293,9 @@ __global__ void __launch_bounds__(kThreads, Q4 && LAYOUT == kStraddling ? 3 : 4)
           const uint32_t of1 = __shfl_sync(0xFFFFFFFFu, mine, lane - lr + (other1 & 15u));
           const uint32_t top = __vmaxu2(mine, __byte_perm(of0, of1, pair_of));
           uint32_t codes0, codes1, scale0, scale1;
+          // One way for the whole warp.  Lanes that store nothing (no head, padding: zeros; query rows) count as well, so where a
+          // token's heads are no multiple of a turn's, its last turn goes the long way: 4 prompts of 4096 tokens, 32 and 1 heads
+          // of 128, 34 rows a token, 62.5 us; 34 and 1 heads, 36 rows, 63.3.
           if (!__any_sync(0xFFFFFFFFu, !plain_maxima(top))) {
             scale0 = plain_codes(n, top << 16, codes0);
             scale1 = plain_codes(n + 4, top & 0xFFFF0000u, codes1);

@@ -28,10 +28,10 @@
 // Queries are taken in binary16 after a scaling by a power of two for each row.
 //
 // Measured: 104448 tokens, 24 heads of 128, one sequence: 74.5 us, 4.8 TB/s (bf16:
-// 182); the tiles alone run at 88 % of the copy rate, 643 instructions and 914 cycles a scheduler for a
-// tile of 32 tokens of a head, and 14 us lie around them (waits for lengths, pages and
-// rows 5, unequal SMs 2, the join and the launch 6).  16 sequences of 4096 to 8192 tokens, 16 and
-// 4 heads of 128: 21 us of 8.5 (bf16: 36).
+// 182).  60.7 of them are tiles (by the slope over lengths), at 89 % of the copy rate, 627 instructions and 0.465 us of a
+// scheduler for a tile of 32 tokens of a head; around them lie 4.9 us of waits for lengths, pages and rows, 2.1 of
+// joining a CTA's warps, 2.7 of unequal CTAs and 3.4 of the join and the launch.  16 sequences of 4096 to 8192
+// tokens, 16 and 4 heads of 128: 21 us of 8.5 (bf16: 36).
 #include <type_traits>
 
 #include "cache4.cuh"
@@ -653,14 +653,16 @@ __global__ void __launch_bounds__(WARPS * 32, 1) decode_q4_kernel(const __grid_c
 }
 
 // Query heads that a warp takes at a time, 8, 16 or 32: codes become operands once for all of them.  With heads of 256
-// registers end at 16.
+// registers end at 16; 32 of 128 spill (40 bytes a thread stored and 76 loaded, with weights 48 and 68), and are faster all the
+// same (16 sequences of 30000 tokens, 32 heads to one: 44.4 us, by 16 at a time 47.8).
 int heads_of(const DecodeArgs& a) {
   const int G = a.Hq / a.Hkv;
   return G <= 8 ? 8 : G <= 16 || a.D == 256 ? 16 : 32;
 }
 // Warps of a CTA.  Heads of 128 and two column tiles, or of 256, leave registers for 8.  Otherwise 16 where each has many
-// tiles (one sequence of 104448 tokens, 24 heads of 128: 75 us, with 8 warps 83), and 8 where they have few, whose registers leave room
-// for the joining kernel beside them (16 sequences of up to 8192, 16 and 4 heads: 23 and 21).
+// tiles (one sequence of 104448 tokens, 24 heads of 128: 75 us, with 8 warps 83), although in 128 registers they spill (20 bytes a
+// thread stored and 32 loaded, with weights 32 and 56; two column tiles of heads of 64 24 and 40, 36 and 52), and 8 where they
+// have few, whose registers leave room for the joining kernel beside them (16 sequences of up to 8192, 16 and 4 heads: 23 and 21).
 int warps_of(const DecodeArgs& a, int sms) {
   const int heads = heads_of(a), G = a.Hq / a.Hkv;
   if (a.D * heads > 1024) return 8;

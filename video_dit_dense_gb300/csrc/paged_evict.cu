@@ -15,7 +15,9 @@
 // on the longest case below.)  Each warp owns a contiguous part of the tokens, so that a
 // ballot numbers movers and gaps.  It writes their lists, moves the weights, and
 // looks up the rows that the places are.  Bound by latencies: of 16 sequences of up to
-// 4352 tokens 11 us, of one of 104448 22 (a load at a time from memory in each pass: 64).
+// 4352 tokens 11 us, of one of 104448 22 (a load at a time from memory in each pass: 64).  The recent ones' weights
+// are moved by the first CTA alone, 4096 at a time with two barriers each: with 50000 recent ones of 52224 kept, of the same 104448,
+// the kernel takes 30 us under the profiler, with 1536 of 32760 25.
 //
 // Second kernel: moves the rows, d = n - keep places down.  Movers from beyond `keep`
 // are not in the way of anything: a warp, or as many of its lanes as a short row has
